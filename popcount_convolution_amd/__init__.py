@@ -6,6 +6,10 @@ of ``libbconv.so``, reached through its C ABI (``include/bconv.h``).  This
 package holds the ctypes binding (``_binding``), a small torch-facing wrapper
 (``BinaryConvolution``: torch only provides device memory and the current
 stream) and the seeded synthetic workloads (``workloads``).
+
+Next to the binary layers are the 4-bit operators of a language model's
+decoding step (``include/bconv_q4.h``, ``q4``): ``Q4Linear``, ``KV4Cache`` (its
+``append`` and ``attention``) and ``build_block_tables``.
 """
 
 from __future__ import annotations
@@ -25,7 +29,11 @@ from ._binding import (  # noqa: F401  (re-exported C ABI names)
     bconv_forward_packed_bits, bconv_forward_profiled,
     bconv_get_info, bconv_last_error,
     bconv_main_kernel, bconv_status_string, bconv_validate_desc, bconv_workspace_layout,
-    bconv_workspace_size, load_library, make_desc)
+    bconv_workspace_size, load_library, make_desc,
+    BCONV_BF16, BCONV_F16, BCONV_F32, bconv_block_tables, bconv_kv4_append, bconv_kv4_attention, bconv_kv4_attention_t,
+    bconv_kv4_attention_workspace_size, bconv_kv4_desc_t, bconv_kv4_layout, bconv_q4_linear_create,
+    bconv_q4_linear_destroy, bconv_q4_linear_forward, bconv_q4_linear_workspace_size)
+from .q4 import BlockTables, KV4Cache, Q4Linear, build_block_tables, pack_codes  # noqa: F401
 
 
 def check_tensor(t, name: str, shape, dtypes, device=None) -> None:

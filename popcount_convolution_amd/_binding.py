@@ -72,6 +72,37 @@ class bconv_workspace_layout_t(ctypes.Structure):
                 ("total_bytes", ctypes.c_size_t)]
 
 
+# bconv_dtype_t
+BCONV_F32 = 0
+BCONV_F16 = 1
+BCONV_BF16 = 2
+
+
+class bconv_q4_linear_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("in_features", "out_features", "group")]
+
+
+class bconv_kv4_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("num_blocks", "block_size", "kv_heads", "head_dim", "group")]
+
+
+class bconv_kv4_layout_t(ctypes.Structure):
+    _fields_ = [("pool_bytes", ctypes.c_size_t), ("record_bytes", ctypes.c_size_t), ("row_bytes", ctypes.c_int32),
+                ("dim_padded", ctypes.c_int32), ("groups", ctypes.c_int32), ("reserved", ctypes.c_int32),
+                ("v_codes_offset", ctypes.c_size_t), ("k_scales_offset", ctypes.c_size_t),
+                ("v_scales_offset", ctypes.c_size_t)]
+
+
+class bconv_kv4_attention_t(ctypes.Structure):
+    _fields_ = [("pool", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_token_stride", ctypes.c_int64),
+                ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("context_lens", ctypes.c_void_p), ("q_start", ctypes.c_void_p),
+                ("requests", ctypes.c_int32), ("q_tokens", ctypes.c_int32), ("max_q", ctypes.c_int32),
+                ("heads", ctypes.c_int32), ("table_width", ctypes.c_int32), ("table_stride", ctypes.c_int32),
+                ("max_context", ctypes.c_int32), ("window", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
 _lib = None
 
 
@@ -86,6 +117,7 @@ def load_library(path: Optional[str] = None):
             f"{p} is not built: run __graft_entry__.build() (hipcc --offload-arch=gfx950)")
     lib = ctypes.CDLL(p)
     vp, i32, u32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_uint32, ctypes.c_size_t
+    i64 = ctypes.c_int64
     st = ctypes.c_int
     fp = ctypes.POINTER(ctypes.c_float)
     up = ctypes.POINTER(ctypes.c_uint32)
@@ -111,6 +143,18 @@ def load_library(path: Optional[str] = None):
         "bconv_destroy": (st, [vp]),
         "bconv_status_string": (ctypes.c_char_p, [st]),
         "bconv_last_error": (ctypes.c_char_p, []),
+        "bconv_q4_linear_create": (st, [ctypes.POINTER(bconv_q4_linear_desc_t), up, vp, vp, fp, ctypes.POINTER(vp)]),
+        "bconv_q4_linear_workspace_size": (st, [vp, i32, i32, ctypes.POINTER(sz)]),
+        "bconv_q4_linear_forward": (st, [vp, vp, i32, i32, vp, i64, vp, i64, vp, sz]),
+        "bconv_q4_linear_destroy": (st, [vp]),
+        "bconv_kv4_layout": (st, [ctypes.POINTER(bconv_kv4_desc_t), ctypes.POINTER(bconv_kv4_layout_t)]),
+        "bconv_kv4_append": (st, [ctypes.POINTER(bconv_kv4_desc_t), vp, vp, i32, i32, vp, i64, i64, vp, i64, i64, vp,
+                                  vp, vp]),
+        "bconv_kv4_attention_workspace_size": (st, [ctypes.POINTER(bconv_kv4_desc_t),
+                                                    ctypes.POINTER(bconv_kv4_attention_t), ctypes.POINTER(sz)]),
+        "bconv_kv4_attention": (st, [ctypes.POINTER(bconv_kv4_desc_t), vp, ctypes.POINTER(bconv_kv4_attention_t), vp,
+                                     sz]),
+        "bconv_block_tables": (st, [vp, i32, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -274,3 +318,66 @@ def bconv_status_string(s: int) -> str:
 
 def bconv_last_error() -> str:
     return load_library().bconv_last_error().decode()
+
+
+def bconv_q4_linear_create(in_features: int, out_features: int, group: int, weight_words, scales, zeros=None,
+                           bias=None) -> int:
+    """Host arrays: uint32 words, fp16 scales, uint8 zeros or None, float32 bias or None."""
+    desc = bconv_q4_linear_desc_t(in_features, out_features, group)
+    ww = np.ascontiguousarray(weight_words, dtype=np.uint32)
+    sc = np.ascontiguousarray(scales, dtype=np.float16)
+    zs = None if zeros is None else np.ascontiguousarray(zeros, dtype=np.uint8)
+    b = _host_f32(bias)
+    h = ctypes.c_void_p()
+    _check(load_library().bconv_q4_linear_create(
+        ctypes.byref(desc), ww.ctypes.data_as(ctypes.POINTER(ctypes.c_uint32)), sc.ctypes.data,
+        None if zs is None else zs.ctypes.data, b[1] if b else None, ctypes.byref(h)))
+    return h.value
+
+
+def bconv_q4_linear_workspace_size(h: int, rows: int, dtype: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().bconv_q4_linear_workspace_size(h, rows, dtype, ctypes.byref(b)))
+    return b.value
+
+
+def bconv_q4_linear_forward(h: int, stream, rows: int, dtype: int, x, ldx: int, y, ldy: int, workspace=None,
+                            workspace_bytes: int = 0) -> None:
+    _check(load_library().bconv_q4_linear_forward(h, _ptr(stream), rows, dtype, _ptr(x), ldx, _ptr(y), ldy,
+                                                  _ptr(workspace), workspace_bytes))
+
+
+def bconv_q4_linear_destroy(h: int) -> None:
+    _check(load_library().bconv_q4_linear_destroy(h))
+
+
+def bconv_kv4_layout(desc: bconv_kv4_desc_t) -> bconv_kv4_layout_t:
+    layout = bconv_kv4_layout_t()
+    _check(load_library().bconv_kv4_layout(ctypes.byref(desc), ctypes.byref(layout)))
+    return layout
+
+
+def bconv_kv4_append(desc: bconv_kv4_desc_t, stream, pool, tokens: int, dtype: int, k, k_strides, v, v_strides, slots,
+                     k_out=None, v_out=None) -> None:
+    _check(load_library().bconv_kv4_append(desc, _ptr(stream), _ptr(pool), tokens, dtype, _ptr(k), *k_strides, _ptr(v),
+                                           *v_strides, _ptr(slots), _ptr(k_out), _ptr(v_out)))
+
+
+def bconv_kv4_attention_workspace_size(desc: bconv_kv4_desc_t, args: bconv_kv4_attention_t) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().bconv_kv4_attention_workspace_size(desc, args, ctypes.byref(b)))
+    return b.value
+
+
+def bconv_kv4_attention(desc: bconv_kv4_desc_t, stream, args: bconv_kv4_attention_t, workspace=None,
+                        workspace_bytes: int = 0) -> None:
+    _check(load_library().bconv_kv4_attention(desc, _ptr(stream), args, _ptr(workspace), workspace_bytes))
+
+
+def bconv_block_tables(stream, requests: int, block_size: int, block_table, table_width: int, table_stride: int,
+                       context_lens, new_lens, free_blocks, free_count: int, free_head, free_head_out, tokens: int,
+                       slots=None, positions=None, q_start=None, context_lens_out=None) -> None:
+    _check(load_library().bconv_block_tables(_ptr(stream), requests, block_size, _ptr(block_table), table_width,
+                                             table_stride, _ptr(context_lens), _ptr(new_lens), _ptr(free_blocks),
+                                             free_count, _ptr(free_head), _ptr(free_head_out), tokens, _ptr(slots),
+                                             _ptr(positions), _ptr(q_start), _ptr(context_lens_out)))

@@ -3,16 +3,15 @@
 // kernels of this library; this file only checks, sizes and launches.
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
 #include <cstdint>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
-#include <string>
 #include <vector>
 
 #include "bconv.h"
+#include "host.h"
 #include "internal.h"
 
 struct bconv_handle {
@@ -41,23 +40,11 @@ struct bconv_handle {
 
 namespace {
 
-thread_local std::string g_last_error;
-
-bconv_status_t fail(bconv_status_t s, const char *fmt, ...)
-{
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return s;
-}
-
-bconv_status_t hip_fail(hipError_t e, const char *what)
-{
-    return fail(BCONV_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-}
+using bconv::DeviceGuard;
+using bconv::fail;
+using bconv::hip_fail;
+using bconv::ranges_overlap;
+using bconv::upload;
 
 constexpr int32_t kMaxExtent = 1 << 16;
 constexpr int32_t kMaxChannels = 1 << 20;
@@ -177,37 +164,6 @@ bconv_workspace_layout_t layout_for(const bconv_handle *h, int n)
     return L;
 }
 
-// Runs `fn` with the handle's device current, restoring the caller's device.
-struct DeviceGuard {
-    int prev = -1;
-    hipError_t err = hipSuccess;
-    explicit DeviceGuard(int dev)
-    {
-        err = hipGetDevice(&prev);
-        if (err == hipSuccess && prev != dev) err = hipSetDevice(dev);
-        else if (err == hipSuccess) prev = -1;
-    }
-    ~DeviceGuard()
-    {
-        if (prev >= 0) (void)hipSetDevice(prev);
-    }
-};
-
-template <typename T>
-bconv_status_t upload(const T *host, size_t count, T **dev)
-{
-    *dev = nullptr;
-    if (!host || count == 0) return BCONV_OK;
-    hipError_t e = hipMalloc(reinterpret_cast<void **>(dev), count * sizeof(T));
-    if (e != hipSuccess) {
-        *dev = nullptr;
-        return fail(BCONV_ERR_ALLOC, "hipMalloc(%zu): %s", count * sizeof(T), hipGetErrorString(e));
-    }
-    e = hipMemcpy(*dev, host, count * sizeof(T), hipMemcpyHostToDevice);
-    if (e != hipSuccess) return hip_fail(e, "hipMemcpy");
-    return BCONV_OK;
-}
-
 void release(bconv_handle *h)
 {
     if (!h) return;
@@ -216,12 +172,6 @@ void release(bconv_handle *h)
     for (void *p : ptrs)
         if (p) (void)hipFree(p);
     delete h;
-}
-
-bool ranges_overlap(const void *a, size_t an, const void *b, size_t bn)
-{
-    const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
-    return a0 < b0 + bn && b0 < a0 + an;
 }
 
 // Whether a call with fp32 input takes the single-launch small-layer kernel.
@@ -682,6 +632,6 @@ const char *bconv_status_string(bconv_status_t s)
     return "BCONV_ERR_UNKNOWN";
 }
 
-const char *bconv_last_error(void) { return g_last_error.c_str(); }
+const char *bconv_last_error(void) { return bconv::last_error; }
 
 }  // extern "C"

@@ -1,0 +1,697 @@
+// Attention over the paged 4-bit cache: one pass over the keys and values with
+// a running softmax, all products on the matrix cores straight from the codes.
+//
+// For one request and key/value head, the columns of a product are (query,
+// head of the group) pairs, 16 a tile, and its rows are tokens (S = K Q^T) or
+// channels (O = V^T P).  A wave takes 32 tokens at a time:
+//
+//   S[t][c] = sum_g s_tg (sum_{d in g} (code - 8) q_d) + b_tg sum_{d in g} q_d
+//   O[d][c] += sum_t (code_td - 8) (p_tc s_tg) + sum_t p_tc b_tg
+//
+// so a key's step scales a finished product and a value's step goes into the
+// probability before it is rounded for the matrix cores; the midpoints never
+// meet the matrix cores and stay in fp32.  Rows of the first product are
+// numbered so that a lane ends up with the probabilities of the 8 tokens whose
+// codes it decodes for the second: P never leaves its registers.
+#include <hip/hip_runtime.h>
+
+#include "kv4.h"
+
+namespace bconv {
+
+constexpr int kTile = 32;         // tokens a wave takes at a time
+constexpr int kAttnWaves = 4;     // waves that share a part of a request's tokens
+constexpr float kLowest = -1e30f; // running maximum before the first visible token
+// How far a logit (base 2) may pass the running maximum before the sums are
+// rescaled: 2^8 of headroom costs fp32 sums nothing and saves most rescales.
+constexpr float kSlack = 8.0f;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    const char *pool;
+    const void *q;
+    long long q_token, q_head;
+    void *out;
+    float *lse;
+    const int *table, *context, *q_start;
+    int requests, q_tokens, max_q, heads, ratio;
+    int width;
+    long long stride;
+    int max_context, window;
+    float scale_log2;
+    int vec;
+    int col_blocks, parts, part_tokens;  // part_tokens: a multiple of kTile
+    float *part_o;                       // [column rows][parts][dim_padded]
+    float2 *part_ml;                     // [column rows][parts]
+    Kv4Geom g;
+};
+
+// The columns one workgroup takes and the tokens they see.
+struct Span {
+    int q0, n, j0, c0, c1;   // first query row, queries, first query's index, columns [c0, c1)
+    int last;                // position of the request's query 0 (context - queries)
+    int t0, t1;              // tokens [t0, t1), t0 a multiple of kTile
+    int low;                 // the first of them that any column sees
+};
+
+__device__ __forceinline__ int first_seen(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
+
+__device__ __forceinline__ Span column_span(const AttnArgs &a, int req, int cb, int width_cols)
+{
+    Span s;
+    int q0, n;
+    if (a.q_start) {
+        q0 = a.q_start[req];
+        n = a.q_start[req + 1] - q0;
+    } else {
+        n = a.q_tokens / a.requests;
+        q0 = req * n;
+    }
+    const int ctx = a.context[req] > 0 ? a.context[req] : 0;
+    if (n < 0) n = 0;
+    s.last = ctx - n;
+    if (n > a.max_q) n = a.max_q;
+    if (q0 < 0 || q0 > a.q_tokens) n = 0;
+    else if (n > a.q_tokens - q0) n = a.q_tokens - q0;
+    s.q0 = q0;
+    s.n = n;
+    s.c0 = cb * width_cols;
+    const int cols = s.n * a.ratio;
+    s.c1 = s.c0 + width_cols < cols ? s.c0 + width_cols : cols;
+    s.t0 = s.t1 = s.low = 0;
+    s.j0 = 0;
+    if (s.c0 < s.c1) {
+        s.j0 = s.c0 / a.ratio;
+        const int j1 = (s.c1 - 1) / a.ratio;
+        const int hi = s.last + j1;
+        s.t1 = (hi < a.max_context - 1 ? hi : a.max_context - 1) + 1;
+        s.low = first_seen(s.last + s.j0, a.window);
+        s.t0 = s.low & ~(kTile - 1);
+        if (s.t1 < s.t0) s.t1 = s.t0;
+    }
+    return s;
+}
+
+__device__ __forceinline__ float lane_groups_max(float v)
+{
+    v = fmaxf(v, __shfl_xor(v, 16));
+    return fmaxf(v, __shfl_xor(v, 32));
+}
+
+__device__ __forceinline__ float lane_groups_sum(float v)
+{
+    v += __shfl_xor(v, 16);
+    return v + __shfl_xor(v, 32);
+}
+
+// Parts a probability is rounded into for the matrix cores: one bf16 for bf16
+// results, whose own rounding is as coarse; two (16 bits) for fp16 results,
+// three (24 bits) for fp32.
+template <int DT> constexpr int kProbParts = DT == BCONV_BF16 ? 1 : DT == BCONV_F16 ? 2 : 3;
+
+// Offset of a value code as decoded: 128 + c in bf16 (all of whose 7 mantissa
+// bits it takes, with no shift for the first code); fp32 results use 16 + c,
+// which cancels fewer bits.
+template <int DT> constexpr float kValueOffset = DT == BCONV_F32 ? 24.0f : 136.0f;
+
+// Codes j of two tokens' rows (16 bits of each row's part) as a bf16 pair.
+template <int DT> __device__ __forceinline__ uint32_t value_pair(uint32_t two, int j)
+{
+    if constexpr (DT == BCONV_F32) {
+        const uint32_t t = j == 0 ? two << 3 : two >> (4 * j - 3);
+        return (t & kCodeMask) | kBase16;
+    } else {
+        return ((two >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+    }
+}
+
+template <int DT, int DP, int GROUPS, int NT>
+__global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs a)
+{
+    typedef typename Elem<DT>::type T;
+    constexpr int STEPS = DP / 32;             // 32-channel steps of K Q^T
+    constexpr int PER = STEPS / GROUPS;        // steps a group
+    constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
+    constexpr int VPER = TILES / GROUPS;       // of them a group
+    constexpr int NP = kProbParts<DT>;
+    constexpr int COLS = 16 * NT;
+    constexpr int VW = DP < 128 ? 1 : DP / 128;  // words of a value row's part (16 bits for DP = 64)
+
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = lane & 15, lg = lane >> 4;
+    int id = blockIdx.x;
+    const int part = id % a.parts;
+    id /= a.parts;
+    const int cb = id % a.col_blocks;
+    id /= a.col_blocks;
+    const int head = id % a.g.kv_heads, req = id / a.g.kv_heads;
+    const Span sp = column_span(a, req, cb, COLS);
+    if (sp.c0 >= sp.c1) return;
+    const int span = sp.t1 - sp.t0;
+    const int begin = sp.t0 + part * a.part_tokens;
+    if (part > 0 && begin >= sp.t1) return;
+    const int end = begin + a.part_tokens < sp.t1 ? begin + a.part_tokens : sp.t1;
+    const bool whole = span <= a.part_tokens;
+
+    // this lane's columns: row of q, positions seen
+    Operand<DT> qf[STEPS][NT];
+    int lo[NT], hi[NT];
+    int all_lo = 0, all_hi = 0x7fffffff;  // seen by every column
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = sp.c0 + n * 16 + row;
+        lo[n] = 0;
+        hi[n] = -1;
+        const bool real = c < sp.c1;
+        const int j = real ? c / a.ratio : 0, h = head * a.ratio + (real ? c - j * a.ratio : 0);
+        if (real) {
+            const int pos = sp.last + j;
+            lo[n] = first_seen(pos, a.window);
+            hi[n] = pos < a.max_context ? pos : a.max_context - 1;
+            all_lo = lo[n] > all_lo ? lo[n] : all_lo;
+            all_hi = hi[n] < all_hi ? hi[n] : all_hi;
+        }
+        const T *q = static_cast<const T *>(a.q) + (long long)(sp.q0 + j) * a.q_token + (long long)h * a.q_head;
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int d = s * 32 + lg * 8;
+            if (real && d < a.g.dim) {
+                qf[s][n] = load_operand<DT>(q + d, d, a.g.dim, a.vec != 0);
+            } else {
+#pragma unroll
+                for (int p = 0; p < kSplit<DT>; ++p) qf[s][n].part[p] = u32x4{0, 0, 0, 0};
+            }
+        }
+    }
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        all_lo = max(all_lo, __shfl_xor(all_lo, d));
+        all_hi = min(all_hi, __shfl_xor(all_hi, d));
+    }
+
+    // sums of q over each group, for the midpoints and the codes' offset
+    float qsum[GROUPS][NT];
+    f32x4 qoff[DT == BCONV_BF16 ? GROUPS : 1][NT];
+#pragma unroll
+    for (int g = 0; g < GROUPS; ++g)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            f32x4 x = {0, 0, 0, 0};
+            const u32x4 one = DT == BCONV_F16 ? u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u} : bf16_const(1.0f);
+#pragma unroll
+            for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s][n], x);
+            qsum[g][n] = x[0];
+            if constexpr (DT == BCONV_BF16) qoff[g][n] = x * -24.0f;
+        }
+
+    f32x4 acc[TILES][NT], psum[GROUPS][NT];
+    float mid[GROUPS][NT], m[NT], l[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n] = kLowest;
+        l[n] = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) acc[t][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            psum[g][n] = f32x4{0, 0, 0, 0};
+            mid[g][n] = 0.0f;
+        }
+    }
+    const Zero<DT> eight(8);
+    const u32x4 ones = bf16_const(1.0f);
+    const int *table = a.table + req * a.stride;
+    const int block_mask = (1 << a.g.block_shift) - 1;
+
+    for (int t = begin + wave * kTile; t < end; t += kAttnWaves * kTile) {
+        // Runs of 8 tokens never cross a block.  Row r of S tile u is token
+        // t + 8 (r / 4) + 4 u + r % 4: a lane's eight results are its run's.
+        const int krun = t + (row >> 2) * 8, vrun = t + lg * 8;
+        const int kb = krun >> a.g.block_shift, vb = vrun >> a.g.block_shift;
+        int kid = kb < a.width ? table[kb] : -1, vid = vb < a.width ? table[vb] : -1;
+        const bool known = vid >= 0 && vid < a.g.num_blocks;
+        if (kid < 0 || kid >= a.g.num_blocks) kid = 0;  // read somewhere in the pool, masked below
+        if (!known) vid = 0;
+        const char *krec = a.pool + ((long long)kid * a.g.kv_heads + head) * a.g.record_bytes;
+        const char *vrec = a.pool + ((long long)vid * a.g.kv_heads + head) * a.g.record_bytes;
+        const int koff = krun & block_mask, voff = vrun & block_mask;
+
+        uint32_t kw[2][STEPS];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const char *p = krec + (koff + 4 * u + (row & 3)) * (DP / 2) + lg * (DP / 8);
+            if constexpr (DP == 64) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+                kw[u][0] = w[0];
+                kw[u][1] = w[1];
+            } else {
+#pragma unroll
+                for (int v = 0; v < STEPS / 4; ++v) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(p + 16 * v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) kw[u][4 * v + i] = w[i];
+                }
+            }
+        }
+        uint32_t ks[8 * GROUPS], vs[8 * GROUPS];  // (s, b) of the run's tokens
+#pragma unroll
+        for (int i = 0; i < 2 * GROUPS; ++i) {
+            const u32x4 w = *reinterpret_cast<const u32x4 *>(vrec + a.g.k_scales + voff * GROUPS * 4 + 16 * i);
+            const u32x4 x = *reinterpret_cast<const u32x4 *>(vrec + a.g.v_scales + voff * GROUPS * 4 + 16 * i);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ks[4 * i + e] = w[e];
+                vs[4 * i + e] = x[e];
+            }
+        }
+        uint32_t vw[8][VW];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const char *p = vrec + a.g.v_codes + (voff + i) * (DP / 2) + row * (DP / 32);
+            if constexpr (DP == 64) {
+                vw[i][0] = *reinterpret_cast<const uint16_t *>(p);
+            } else if constexpr (DP == 128) {
+                vw[i][0] = *reinterpret_cast<const uint32_t *>(p);
+            } else {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+                vw[i][0] = w[0];
+                vw[i][1] = w[1];
+            }
+        }
+
+        // S, as base-2 logits
+        f32x4 z[2][NT];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) z[u][n] = f32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            if (g * PER * 32 >= a.g.dim) continue;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                f32x4 d[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if constexpr (DT == BCONV_BF16) d[n] = qoff[g][n];
+                    else d[n] = f32x4{0, 0, 0, 0};
+                }
+#pragma unroll
+                for (int s = 0; s < PER; ++s) {
+                    const u32x4 k = decode<DT>(kw[u][g * PER + s], eight);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) d[n] = mfma_parts<DT>(k, qf[g * PER + s][n], d[n]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const f16x2 sb = __builtin_bit_cast(f16x2, ks[(4 * u + i) * GROUPS + g]);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        z[u][n][i] = __builtin_fmaf((float)sb[0], d[n][i], z[u][n][i]);
+                        z[u][n][i] = __builtin_fmaf((float)sb[1], qsum[g][n], z[u][n][i]);
+                    }
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n) z[u][n] *= a.scale_log2;
+
+        // Tiles that some column does not see in full, or with a block that
+        // does not exist: masked logits are -inf whatever was read, and masked
+        // tokens' steps and midpoints 0, since 0 * NaN would not vanish.
+        if (t < all_lo || t + kTile - 1 > all_hi || __any(!known)) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = vrun + 4 * u + i;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+                        if (!known || pos < lo[n] || pos > hi[n]) z[u][n][i] = -__builtin_inff();
+                    if (!known || pos < sp.low || pos >= sp.t1) {
+#pragma unroll
+                        for (int g = 0; g < GROUPS; ++g) vs[(4 * u + i) * GROUPS + g] = 0;
+                    }
+                }
+        }
+
+        // running softmax
+        float p[NT][8];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float top = fmaxf(fmaxf(fmaxf(z[0][n][0], z[0][n][1]), fmaxf(z[0][n][2], z[0][n][3])),
+                              fmaxf(fmaxf(z[1][n][0], z[1][n][1]), fmaxf(z[1][n][2], z[1][n][3])));
+            if (__any(top > m[n] + kSlack)) {
+                top = fmaxf(m[n], lane_groups_max(top));
+                const float f = __builtin_amdgcn_exp2f(m[n] - top);
+                m[n] = top;
+                l[n] *= f;
+#pragma unroll
+                for (int k = 0; k < TILES; ++k) acc[k][n] *= f;
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) {
+                    psum[g][n] *= f;
+                    mid[g][n] *= f;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                p[n][i] = __builtin_amdgcn_exp2f(z[i >> 2][n][i & 3] - m[n]);
+                l[n] += p[n][i];
+            }
+        }
+
+        // V^T P
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            if (g * VPER * 16 >= a.g.dim) continue;
+            u32x4 pp[NT][NP];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float ps[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const f16x2 sb = __builtin_bit_cast(f16x2, vs[i * GROUPS + g]);
+                    ps[i] = p[n][i] * (float)sb[0];
+                    mid[g][n] = __builtin_fmaf((float)sb[1], p[n][i], mid[g][n]);
+                }
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bf16x2 r = {(__bf16)ps[2 * i], (__bf16)ps[2 * i + 1]};
+                        pp[n][k][i] = __builtin_bit_cast(uint32_t, r);
+                        if (k + 1 < NP) {
+                            ps[2 * i] -= (float)r[0];
+                            ps[2 * i + 1] -= (float)r[1];
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = NP - 1; k >= 0; --k) psum[g][n] = mfma16<BCONV_BF16>(ones, pp[n][k], psum[g][n]);
+            }
+#pragma unroll
+            for (int j = 0; j < VPER; ++j) {
+                const int tile = g * VPER + j, word = tile / 8, half = (tile / 4) & 1;
+                u32x4 v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t two = __builtin_amdgcn_perm(vw[2 * i + 1][word], vw[2 * i][word],
+                                                               half ? 0x07060302u : 0x05040100u);
+                    v[i] = value_pair<DT>(two, tile & 3);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int k = NP - 1; k >= 0; --k) acc[tile][n] = mfma16<BCONV_BF16>(v, pp[n][k], acc[tile][n]);
+            }
+        }
+    }
+
+    // the waves' parts, brought to one maximum and added in wave order
+    extern __shared__ float lds[];
+    float *so = lds;                             // [waves][COLS][DP + 4]
+    float *sm = lds + kAttnWaves * COLS * (DP + 4);  // [waves][COLS]
+    float *sl = sm + kAttnWaves * COLS;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        l[n] = lane_groups_sum(l[n]);
+        if (lg == 0) {
+            sm[wave * COLS + n * 16 + row] = m[n];
+            sl[wave * COLS + n * 16 + row] = l[n];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        float top = kLowest;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm[w * COLS + n * 16 + row]);
+        const float f = __builtin_amdgcn_exp2f(m[n] - top);
+#pragma unroll
+        for (int g = 0; g < GROUPS; ++g) {
+            const float add = lane_groups_sum(mid[g][n]) - kValueOffset<DT> * psum[g][n][0];
+#pragma unroll
+            for (int j = 0; j < VPER; ++j) {
+                const int tile = g * VPER + j;
+                *reinterpret_cast<f32x4 *>(so + (wave * COLS + n * 16 + row) * (DP + 4) + tile * 16 + lg * 4) =
+                    (acc[tile][n] + add) * f;
+            }
+        }
+    }
+    __syncthreads();
+    const int cols = sp.c1 - sp.c0;
+    for (int e = threadIdx.x; e < cols * DP; e += kAttnWaves * 64) {
+        const int c = e / DP, d = e % DP;
+        if (d >= a.g.dim) continue;
+        float top = kLowest, sum = 0.0f, o = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm[w * COLS + c]);
+#pragma unroll
+        for (int w = 0; w < kAttnWaves; ++w) {
+            sum += sl[w * COLS + c] * __builtin_amdgcn_exp2f(sm[w * COLS + c] - top);
+            o += so[(w * COLS + c) * (DP + 4) + d];
+        }
+        const int j = (sp.c0 + c) / a.ratio, h = head * a.ratio + (sp.c0 + c) % a.ratio;
+        const long long at = (long long)(sp.q0 + j) * a.heads + h;
+        if (whole) {
+            static_cast<T *>(a.out)[at * a.g.dim + d] = round_to<DT>(sum > 0.0f || sum != sum ? o / sum : 0.0f);
+            if (a.lse && d == 0) a.lse[at] = sum > 0.0f || sum != sum ? (top + __log2f(sum)) * kLn2 : -__builtin_inff();
+        } else {
+            a.part_o[(at * a.parts + part) * DP + d] = o;
+            if (d == 0) a.part_ml[at * a.parts + part] = float2{top, sum};
+        }
+    }
+}
+
+// Joins the parts of one column (a wave each), in part order.
+template <int DT>
+__global__ __launch_bounds__(256) void kv4_combine_kernel(AttnArgs a, int width_cols)
+{
+    typedef typename Elem<DT>::type T;
+    const int lane = threadIdx.x & 63;
+    const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int per_head = a.max_q * a.ratio;
+    if (id >= (long long)a.requests * a.g.kv_heads * per_head) return;
+    const int c = (int)(id % per_head);
+    const int head = (int)(id / per_head % a.g.kv_heads), req = (int)(id / per_head / a.g.kv_heads);
+    const Span sp = column_span(a, req, c / width_cols, width_cols);
+    const int span = sp.t1 - sp.t0;
+    if (c >= sp.c1 || span <= a.part_tokens) return;
+    const int used = (span + a.part_tokens - 1) / a.part_tokens;
+    const int j = c / a.ratio, h = head * a.ratio + c % a.ratio;
+    const long long at = (long long)(sp.q0 + j) * a.heads + h;
+    const float2 *ml = a.part_ml + at * a.parts;
+    float top = kLowest;
+    for (int p = 0; p < used; ++p) top = fmaxf(top, ml[p].x);
+    float sum = 0.0f;
+    for (int p = 0; p < used; ++p) sum += ml[p].y * __builtin_amdgcn_exp2f(ml[p].x - top);
+    const bool any = sum > 0.0f || sum != sum;
+    for (int d = lane; d < a.g.dim; d += 64) {
+        float o = 0.0f;
+        for (int p = 0; p < used; ++p)
+            o += a.part_o[(at * a.parts + p) * a.g.dim_padded + d] * __builtin_amdgcn_exp2f(ml[p].x - top);
+        static_cast<T *>(a.out)[at * a.g.dim + d] = round_to<DT>(any ? o / sum : 0.0f);
+    }
+    if (a.lse && lane == 0) a.lse[at] = any ? (top + __log2f(sum)) * kLn2 : -__builtin_inff();
+}
+
+// ------------------------------------------------------------------ dispatch
+
+template <int DT, int DP, int GROUPS, int NT>
+hipError_t launch_attention_kernel(const AttnArgs &a, hipStream_t s)
+{
+    const size_t lds = (size_t)kAttnWaves * 16 * NT * (DP + 4 + 2) * sizeof(float);
+    const long long grid = (long long)a.requests * a.g.kv_heads * a.col_blocks * a.parts;
+    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, NT>), dim3((unsigned)grid), dim3(kAttnWaves * 64), lds, s, a);
+    hipError_t e = hipGetLastError();
+    if (e == hipSuccess && a.parts > 1) {
+        const long long cols = (long long)a.requests * a.g.kv_heads * a.max_q * a.ratio;
+        hipLaunchKernelGGL((kv4_combine_kernel<DT>), dim3((unsigned)((cols + 3) / 4)), dim3(256), 0, s, a, 16 * NT);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+template <int DT, int DP>
+hipError_t launch_attention_dim(const AttnArgs &a, int nt, hipStream_t s)
+{
+    (void)nt;
+    switch (a.g.groups) {
+    case 1: if constexpr (DP <= 128) return launch_attention_kernel<DT, DP, 1, 1>(a, s); else break;
+    case 2: return launch_attention_kernel<DT, DP, 2, 1>(a, s);
+    case 4: if constexpr (DP >= 128) return launch_attention_kernel<DT, DP, 4, 1>(a, s); else break;
+    case 8: if constexpr (DP >= 256) return launch_attention_kernel<DT, DP, 8, 1>(a, s); else break;
+    }
+    return hipErrorInvalidValue;
+}
+
+template <int DT>
+hipError_t launch_attention(const AttnArgs &a, int nt, hipStream_t s)
+{
+    switch (a.g.dim_padded) {
+    case 64: return launch_attention_dim<DT, 64>(a, nt, s);
+    case 128: return launch_attention_dim<DT, 128>(a, nt, s);
+    default: return launch_attention_dim<DT, 256>(a, nt, s);
+    }
+}
+
+}  // namespace bconv
+
+namespace {
+
+using bconv::fail;
+
+struct AttnPlan {
+    bconv::AttnArgs a;
+    int nt;
+    size_t o_bytes, bytes;  // partial results: sums, then (maximum, denominator) pairs
+    bool empty;
+};
+
+constexpr long long kMaxContext = 1LL << 30;  // tokens of one request
+
+int compute_units()
+{
+    static thread_local int cached_dev = -1, cached = 0;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return 256;
+    if (dev != cached_dev) {
+        int cus = 0;
+        if (hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || cus < 1) cus = 256;
+        cached = cus;
+        cached_dev = dev;
+    }
+    return cached;
+}
+
+// Everything that follows from the descriptor and the host arguments; no
+// device work.
+bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_attention_t *t, AttnPlan *p)
+{
+    if (!t) return fail(BCONV_ERR_INVALID_ARGUMENT, "args is NULL");
+    *p = AttnPlan{};
+    bconv::AttnArgs &a = p->a;
+    const bconv_status_t st = bconv::kv4_geometry(desc, &a.g);
+    if (st != BCONV_OK) return st;
+    if (!bconv::dtype_size(t->dtype)) return fail(BCONV_ERR_INVALID_ARGUMENT, "unknown dtype %d", t->dtype);
+    if (t->requests < 0 || t->q_tokens < 0) return fail(BCONV_ERR_INVALID_ARGUMENT, "requests and q_tokens must be >= 0");
+    if (t->heads < 1 || t->heads > 65536 || t->heads % a.g.kv_heads)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "heads must be a multiple of kv_heads (%d) up to 65536", a.g.kv_heads);
+    p->empty = t->requests == 0 || t->q_tokens == 0;
+    if (p->empty) return BCONV_OK;
+    if (!t->q_start && t->q_tokens % t->requests)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "without q_start, q_tokens must be a multiple of requests");
+    if (t->max_q < 1) return fail(BCONV_ERR_INVALID_ARGUMENT, "max_q must be >= 1");
+    if (!t->q_start && t->max_q < t->q_tokens / t->requests)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "max_q is below q_tokens / requests");
+    if (t->table_width < 0 || t->table_stride < t->table_width)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "table_width must be >= 0 and table_stride >= table_width");
+    if (t->max_context < 0 || t->max_context > kMaxContext || t->window < 0)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "max_context must be in [0, 2^30] and window >= 0");
+    if (t->q_token_stride < 0 || t->q_head_stride < 0 || t->q_token_stride > (1LL << 40) || t->q_head_stride > (1LL << 40))
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "strides must be in [0, 2^40]");
+    const int es = bconv::dtype_size(t->dtype);
+    a.pool = static_cast<const char *>(t->pool);
+    a.q = t->q;
+    a.q_token = t->q_token_stride;
+    a.q_head = t->q_head_stride;
+    a.out = t->out;
+    a.lse = t->lse;
+    a.table = t->block_table;
+    a.context = t->context_lens;
+    a.q_start = t->q_start;
+    a.requests = t->requests;
+    a.q_tokens = t->q_tokens;
+    a.max_q = t->max_q < t->q_tokens ? t->max_q : t->q_tokens;
+    a.heads = t->heads;
+    a.ratio = t->heads / a.g.kv_heads;
+    a.width = t->table_width;
+    a.stride = t->table_stride;
+    const long long held = (long long)t->table_width << a.g.block_shift;
+    long long most = t->max_context > 0 && t->max_context < held ? t->max_context : held;
+    if (most > kMaxContext) most = kMaxContext;
+    a.max_context = (int)most;
+    a.window = t->window;
+    a.scale_log2 = t->scale * bconv::kLog2e;
+    a.vec = (uintptr_t)t->q % 16 == 0 && t->q_token_stride * es % 16 == 0 && t->q_head_stride * es % 16 == 0;
+
+    p->nt = 1;
+    const int cols = 16 * p->nt;
+    if ((long long)a.max_q * a.ratio >= (1LL << 30)) return fail(BCONV_ERR_INVALID_ARGUMENT, "max_q*heads too large");
+    a.col_blocks = (a.max_q * a.ratio + cols - 1) / cols;
+    const long long tiles = (long long)a.requests * a.g.kv_heads * a.col_blocks;
+    if (tiles >= (1LL << 29)) return fail(BCONV_ERR_INVALID_ARGUMENT, "requests*heads*max_q too large for one call");
+    // tokens that the columns of one workgroup can see, from a multiple of the tile
+    long long seen = most;
+    if (a.window > 0) {
+        const long long w = (long long)a.window + (cols + a.ratio - 1) / a.ratio;
+        if (w < seen) seen = w;
+    }
+    seen += bconv::kTile;
+    // Parts of the long axis until four workgroups a compute unit are there,
+    // none below 512 tokens (128 a wave), which a part's prologue and the join
+    // would outweigh.
+    const long long want = (4LL * compute_units() + tiles - 1) / tiles;
+    long long part = (seen + want - 1) / want;
+    if (part < 512) part = 512;
+    part = (part + bconv::kTile - 1) / bconv::kTile * bconv::kTile;
+    a.part_tokens = (int)part;
+    a.parts = (int)((seen + part - 1) / part);
+    if (a.parts < 1) a.parts = 1;
+    if (tiles * a.parts >= (1LL << 31)) return fail(BCONV_ERR_INVALID_ARGUMENT, "too many parts for one call");
+    if (a.parts > 1) {
+        const size_t rows = (size_t)a.q_tokens * a.heads * a.parts;
+        p->o_bytes = (rows * a.g.dim_padded * 4 + 255) / 256 * 256;
+        p->bytes = p->o_bytes + rows * 8;
+    }
+    return BCONV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+bconv_status_t bconv_kv4_attention_workspace_size(const bconv_kv4_desc_t *desc, const bconv_kv4_attention_t *args,
+                                                  size_t *bytes)
+{
+    if (!bytes) return fail(BCONV_ERR_INVALID_ARGUMENT, "bytes is NULL");
+    AttnPlan p;
+    const bconv_status_t st = plan_attention(desc, args, &p);
+    if (st != BCONV_OK) return st;
+    *bytes = p.bytes;
+    return BCONV_OK;
+}
+
+bconv_status_t bconv_kv4_attention(const bconv_kv4_desc_t *desc, void *stream, const bconv_kv4_attention_t *args,
+                                   void *workspace, size_t workspace_bytes)
+{
+    AttnPlan p;
+    const bconv_status_t st = plan_attention(desc, args, &p);
+    if (st != BCONV_OK) return st;
+    if (p.empty) return BCONV_OK;
+    if (!args->pool || !args->q || !args->out || !args->context_lens || (!args->block_table && args->table_width > 0))
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "pool, q, out, block_table and context_lens must not be NULL");
+    const int es = bconv::dtype_size(args->dtype);
+    if ((uintptr_t)args->pool % 16 || ((uintptr_t)args->q | (uintptr_t)args->out) % es)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "the pool must be 16-byte aligned, q and out aligned to an element");
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+        return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes,
+                    workspace ? workspace_bytes : (size_t)0);
+    if (p.bytes > 0 && (uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+    p.a.part_o = static_cast<float *>(workspace);
+    p.a.part_ml = p.bytes ? reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.o_bytes) : nullptr;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    hipError_t e;
+    switch (args->dtype) {
+    case BCONV_F32: e = bconv::launch_attention<BCONV_F32>(p.a, p.nt, s); break;
+    case BCONV_F16: e = bconv::launch_attention<BCONV_F16>(p.a, p.nt, s); break;
+    default: e = bconv::launch_attention<BCONV_BF16>(p.a, p.nt, s); break;
+    }
+    if (e != hipSuccess) return bconv::hip_fail(e, "cache attention kernel");
+    return BCONV_OK;
+}
+
+}  // extern "C"
