@@ -72,7 +72,7 @@ bconv_status_t bconv_q4_linear_workspace_size(bconv_q4_linear_t h, int32_t rows,
  * row m starts at x + m*ldx (ldx >= in_features) and y + m*ldy (ldy >=
  * out_features), strides in elements; any element alignment is accepted (rows
  * on 16-byte boundaries load wider).  rows == 0 is a no-op.  The workspace is
- * 256-byte aligned.  bf16 products are exact and summed in fp32 after an
+ * 16-byte aligned and overlaps neither.  bf16 products are exact and summed in fp32 after an
  * offset that is taken out again, so a bf16 row with an infinity gives NaN in
  * every output of that row; fp16 and fp32 rows follow IEEE arithmetic.
  * Errors: INVALID_ARGUMENT for a NULL handle or pointer, rows < 0, an unknown
@@ -129,7 +129,7 @@ typedef struct {
 /* Checks a descriptor and gives the layout (host only, no device). */
 bconv_status_t bconv_kv4_layout(const bconv_kv4_desc_t *desc, bconv_kv4_layout_t *layout);
 
-/* Writes `tokens` new rows of keys and values into the pool (device, 256-byte
+/* Writes `tokens` new rows of keys and values into the pool (device, 16-byte
  * aligned, layout.pool_bytes; clear it once before its first use).  k and v
  * hold elements of `dtype`; channel d of head h of token t is at
  * t*token_stride + h*head_stride + d (strides in elements, each side its own;

@@ -15,12 +15,14 @@
 // codes it decodes for the second: P never leaves its registers.
 #include <hip/hip_runtime.h>
 
+#include <cmath>
+#include <cstdlib>
+
 #include "kv4.h"
 
 namespace bconv {
 
 constexpr int kTile = 32;         // tokens a wave takes at a time
-constexpr int kAttnWaves = 4;     // waves that share a part of a request's tokens
 constexpr float kLowest = -1e30f; // running maximum before the first visible token
 // How far a logit (base 2) may pass the running maximum before the sums are
 // rescaled: 2^8 of headroom costs fp32 sums nothing and saves most rescales.
@@ -38,12 +40,20 @@ struct AttnArgs {
     int width;
     long long stride;
     int max_context, window;
-    float scale_log2;
+    float scale_log2;  // |scale| log2 e
+    uint32_t flip;     // sign bits to flip in q: those of a negative scale
     int vec;
     int col_blocks, parts, part_tokens;  // part_tokens: a multiple of kTile
     float *part_o;                       // [column rows][parts][dim_padded]
     float2 *part_ml;                     // [column rows][parts]
     Kv4Geom g;
+};
+
+constexpr int kMaxParts = 512;
+
+// Kernel variant of a call: column tiles and waves a workgroup.
+struct AttnShape {
+    int nt, waves;
 };
 
 // The columns one workgroup takes and the tokens they see.
@@ -109,33 +119,142 @@ __device__ __forceinline__ float lane_groups_sum(float v)
 // three (24 bits) for fp32.
 template <int DT> constexpr int kProbParts = DT == BCONV_BF16 ? 1 : DT == BCONV_F16 ? 2 : 3;
 
-// Offset of a value code as decoded: 128 + c in bf16 (all of whose 7 mantissa
-// bits it takes, with no shift for the first code); fp32 results use 16 + c,
-// which cancels fewer bits.
+// A value code decodes to 128 + c in bf16 (all of whose 7 mantissa bits it
+// takes, with no shift for the first code) or, for fp32 results, to 16 + c,
+// whose offset costs fewer bits.  A product with the constant -(offset + 8)
+// follows each product, so the running sums hold code - 8 and never grow with
+// the offset.
 template <int DT> constexpr float kValueOffset = DT == BCONV_F32 ? 24.0f : 136.0f;
 
-// Codes j of two tokens' rows (16 bits of each row's part) as a bf16 pair.
-template <int DT> __device__ __forceinline__ uint32_t value_pair(uint32_t two, int j)
+// The word that lane N of each 16 lanes holds.
+template <int N> __device__ __forceinline__ uint32_t from_lane(uint32_t v)
 {
-    if constexpr (DT == BCONV_F32) {
-        const uint32_t t = j == 0 ? two << 3 : two >> (4 * j - 3);
-        return (t & kCodeMask) | kBase16;
-    } else {
-        return ((two >> (4 * j)) & 0x000f000fu) | 0x43004300u;
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x150 + N, 0xf, 0xf, true);
+}
+
+// from_lane() of entry e of a table kept 16 entries a register, one a lane: a
+// broadcast inside the 16 lanes, so a table costs them one register and one
+// load instead of 16.
+template <int R> __device__ __forceinline__ uint32_t entry(const uint32_t (&v)[R], int e)
+{
+    switch (e & 15) {
+    case 0: return from_lane<0>(v[e >> 4]);
+    case 1: return from_lane<1>(v[e >> 4]);
+    case 2: return from_lane<2>(v[e >> 4]);
+    case 3: return from_lane<3>(v[e >> 4]);
+    case 4: return from_lane<4>(v[e >> 4]);
+    case 5: return from_lane<5>(v[e >> 4]);
+    case 6: return from_lane<6>(v[e >> 4]);
+    case 7: return from_lane<7>(v[e >> 4]);
+    case 8: return from_lane<8>(v[e >> 4]);
+    case 9: return from_lane<9>(v[e >> 4]);
+    case 10: return from_lane<10>(v[e >> 4]);
+    case 11: return from_lane<11>(v[e >> 4]);
+    case 12: return from_lane<12>(v[e >> 4]);
+    case 13: return from_lane<13>(v[e >> 4]);
+    case 14: return from_lane<14>(v[e >> 4]);
+    default: return from_lane<15>(v[e >> 4]);
     }
 }
 
-template <int DT, int DP, int GROUPS, int NT>
-__global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs a)
+// Codes j of two tokens' rows (16 bits of each row's part) as a bf16 pair.
+template <int DT> __device__ __forceinline__ uint32_t value_pair(uint32_t two, int j, const CodeBits &bits)
+{
+    if constexpr (DT == BCONV_F32) return bits(j == 0 ? two << 3 : two >> (4 * j - 3));
+    else return bits(two >> (4 * j));
+}
+
+template <int DT> __device__ __forceinline__ CodeBits value_bits()
+{
+    return DT == BCONV_F32 ? code_bits<DT>() : opaque_bits(0x000f000fu, 0x43004300u);  // bf16 128
+}
+
+// What a lane holds of 32 tokens: key words of its operand rows, value words of
+// its run of 8 tokens, and entries of the run's (s, b) tables, which the 16
+// lanes of a run share (entry = token of the run * GROUPS + group).
+template <int DP, int GROUPS> struct Tile {
+    static constexpr int STEPS = DP / 32;
+    static constexpr int VW = DP < 128 ? 1 : DP / 128;      // words of a value row's part (16 bits for DP = 64)
+    static constexpr int TABLE = (8 * GROUPS + 15) / 16;
+    uint32_t k[2][STEPS], v[8][VW], ks[TABLE], vs[TABLE];
+    bool known;  // the run's block exists
+
+    // Runs of 8 tokens never cross a block.  Row r of S tile u is token
+    // t + 8 (r / 4) + 4 u + r % 4: a lane's eight results are its run's.
+    // `kid` and `vid` are the block ids of the row's and the lane's run.
+    // `pool` is the head's record of block 0, block_bytes a block of all heads.
+    __device__ __forceinline__ void load(const AttnArgs &a, const char *pool, unsigned block_bytes, int t, int kid, int vid,
+                                         int lane)
+    {
+        const int row = lane & 15, lg = lane >> 4;
+        const int mask = (1 << a.g.block_shift) - 1;
+        known = (unsigned)vid < (unsigned)a.g.num_blocks;
+        // a block that does not exist: read the pool's first, masked later
+        kid = (unsigned)kid < (unsigned)a.g.num_blocks ? kid : 0;
+        vid = known ? vid : 0;
+        const char *krec = pool + (unsigned long long)(unsigned)kid * block_bytes;
+        const char *vrec = pool + (unsigned long long)(unsigned)vid * block_bytes;
+        const int koff = (t + (row >> 2) * 8) & mask, voff = (t + lg * 8) & mask;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const char *p = krec + (koff + 4 * u + (row & 3)) * (DP / 2) + lg * (DP / 8);
+            if constexpr (DP == 64) {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+                k[u][0] = w[0];
+                k[u][1] = w[1];
+            } else {
+#pragma unroll
+                for (int x = 0; x < STEPS / 4; ++x) {
+                    const u32x4 w = *reinterpret_cast<const u32x4 *>(p + 16 * x);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) k[u][4 * x + i] = w[i];
+                }
+            }
+        }
+#pragma unroll
+        for (int x = 0; x < TABLE; ++x) {
+            const int e = (x * 16 + row) & (8 * GROUPS - 1);
+            ks[x] = *reinterpret_cast<const uint32_t *>(vrec + a.g.k_scales + (voff * GROUPS + e) * 4);
+            vs[x] = *reinterpret_cast<const uint32_t *>(vrec + a.g.v_scales + (voff * GROUPS + e) * 4);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const char *p = vrec + a.g.v_codes + (voff + i) * (DP / 2) + row * (DP / 32);
+            if constexpr (DP == 64) {
+                v[i][0] = *reinterpret_cast<const uint16_t *>(p);
+            } else if constexpr (DP == 128) {
+                v[i][0] = *reinterpret_cast<const uint32_t *>(p);
+            } else {
+                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
+                v[i][0] = w[0];
+                v[i][1] = w[1];
+            }
+        }
+    }
+};
+
+// Waves a SIMD that the registers are held to.
+constexpr int min_waves(int dt, int dp, int groups, int nt)
+{
+    return dp == 256 || nt == 2 || dt == BCONV_F32 ? 1 : groups >= 4 ? 2 : 3;
+}
+
+// Whether eight waves a workgroup (at most 256 registers a wave) hold a variant without spills.
+constexpr bool fits_8_waves(int dt, int dp, int groups) { return dp <= 128 || (groups == 2 && dt != BCONV_F32); }
+
+// FULL: no group of channels is padding alone (such groups are skipped).
+template <int DT, int DP, int GROUPS, int NT, int WAVES, bool FULL>
+__global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4_attention_kernel(AttnArgs a)
 {
     typedef typename Elem<DT>::type T;
+    typedef Tile<DP, GROUPS> TileT;
     constexpr int STEPS = DP / 32;             // 32-channel steps of K Q^T
     constexpr int PER = STEPS / GROUPS;        // steps a group
     constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
     constexpr int VPER = TILES / GROUPS;       // of them a group
     constexpr int NP = kProbParts<DT>;
     constexpr int COLS = 16 * NT;
-    constexpr int VW = DP < 128 ? 1 : DP / 128;  // words of a value row's part (16 bits for DP = 64)
+    constexpr int TABLE = TileT::TABLE;
 
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = lane & 15, lg = lane >> 4;
@@ -152,6 +271,28 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
     if (part > 0 && begin >= sp.t1) return;
     const int end = begin + a.part_tokens < sp.t1 ? begin + a.part_tokens : sp.t1;
     const bool whole = span <= a.part_tokens;
+
+    // the first tiles are on their way while the queries are read
+    const int *table = a.table + req * a.stride;
+    const char *pool = a.pool + (long long)head * a.g.record_bytes;
+    const unsigned block_bytes = (unsigned)a.g.kv_heads * (unsigned)a.g.record_bytes;  // below 2^29
+    const int krun = (row >> 2) * 8, vrun = lg * 8;
+    auto block_of = [&](int pos) {
+        const int b = pos >> a.g.block_shift;
+        return b < a.width ? table[b] : -1;
+    };
+    int t = begin + wave * kTile;
+    int kid = -1, vid = -1;
+    TileT next;
+    if (t < end) {
+        kid = block_of(t + krun);
+        vid = block_of(t + vrun);
+        next.load(a, pool, block_bytes, t, kid, vid, lane);
+        if (t + WAVES * kTile < end) {
+            kid = block_of(t + WAVES * kTile + krun);
+            vid = block_of(t + WAVES * kTile + vrun);
+        }
+    }
 
     // this lane's columns: row of q, positions seen
     Operand<DT> qf[STEPS][NT];
@@ -177,6 +318,8 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
             const int d = s * 32 + lg * 8;
             if (real && d < a.g.dim) {
                 qf[s][n] = load_operand<DT>(q + d, d, a.g.dim, a.vec != 0);
+#pragma unroll
+                for (int p = 0; p < kSplit<DT>; ++p) qf[s][n].part[p] ^= a.flip;
             } else {
 #pragma unroll
                 for (int p = 0; p < kSplit<DT>; ++p) qf[s][n].part[p] = u32x4{0, 0, 0, 0};
@@ -204,82 +347,39 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
             if constexpr (DT == BCONV_BF16) qoff[g][n] = x * -24.0f;
         }
 
-    f32x4 acc[TILES][NT], psum[GROUPS][NT];
+    f32x4 acc[TILES][NT];
     float mid[GROUPS][NT], m[NT], l[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = kLowest;
         l[n] = 0.0f;
 #pragma unroll
-        for (int t = 0; t < TILES; ++t) acc[t][n] = f32x4{0, 0, 0, 0};
+        for (int k = 0; k < TILES; ++k) acc[k][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            psum[g][n] = f32x4{0, 0, 0, 0};
-            mid[g][n] = 0.0f;
-        }
+        for (int g = 0; g < GROUPS; ++g) mid[g][n] = 0.0f;
     }
     const Zero<DT> eight(8);
-    const u32x4 ones = bf16_const(1.0f);
-    const int *table = a.table + req * a.stride;
-    const int block_mask = (1 << a.g.block_shift) - 1;
+    const u32x4 offset = bf16_const(-kValueOffset<DT>);
+    const CodeBits kbits = code_bits<DT>(), vbits = value_bits<DT>();
 
-    for (int t = begin + wave * kTile; t < end; t += kAttnWaves * kTile) {
-        // Runs of 8 tokens never cross a block.  Row r of S tile u is token
-        // t + 8 (r / 4) + 4 u + r % 4: a lane's eight results are its run's.
-        const int krun = t + (row >> 2) * 8, vrun = t + lg * 8;
-        const int kb = krun >> a.g.block_shift, vb = vrun >> a.g.block_shift;
-        int kid = kb < a.width ? table[kb] : -1, vid = vb < a.width ? table[vb] : -1;
-        const bool known = vid >= 0 && vid < a.g.num_blocks;
-        if (kid < 0 || kid >= a.g.num_blocks) kid = 0;  // read somewhere in the pool, masked below
-        if (!known) vid = 0;
-        const char *krec = a.pool + ((long long)kid * a.g.kv_heads + head) * a.g.record_bytes;
-        const char *vrec = a.pool + ((long long)vid * a.g.kv_heads + head) * a.g.record_bytes;
-        const int koff = krun & block_mask, voff = vrun & block_mask;
-
-        uint32_t kw[2][STEPS];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const char *p = krec + (koff + 4 * u + (row & 3)) * (DP / 2) + lg * (DP / 8);
-            if constexpr (DP == 64) {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-                kw[u][0] = w[0];
-                kw[u][1] = w[1];
-            } else {
-#pragma unroll
-                for (int v = 0; v < STEPS / 4; ++v) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(p + 16 * v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) kw[u][4 * v + i] = w[i];
-                }
-            }
-        }
-        uint32_t ks[8 * GROUPS], vs[8 * GROUPS];  // (s, b) of the run's tokens
-#pragma unroll
-        for (int i = 0; i < 2 * GROUPS; ++i) {
-            const u32x4 w = *reinterpret_cast<const u32x4 *>(vrec + a.g.k_scales + voff * GROUPS * 4 + 16 * i);
-            const u32x4 x = *reinterpret_cast<const u32x4 *>(vrec + a.g.v_scales + voff * GROUPS * 4 + 16 * i);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                ks[4 * i + e] = w[e];
-                vs[4 * i + e] = x[e];
-            }
-        }
-        uint32_t vw[8][VW];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const char *p = vrec + a.g.v_codes + (voff + i) * (DP / 2) + row * (DP / 32);
-            if constexpr (DP == 64) {
-                vw[i][0] = *reinterpret_cast<const uint16_t *>(p);
-            } else if constexpr (DP == 128) {
-                vw[i][0] = *reinterpret_cast<const uint32_t *>(p);
-            } else {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-                vw[i][0] = w[0];
-                vw[i][1] = w[1];
+    for (; t < end; t += WAVES * kTile) {
+        const TileT cur = next;
+        const int ahead = t + WAVES * kTile;
+        if (ahead < end) {
+            next.load(a, pool, block_bytes, ahead, kid, vid, lane);
+            if (ahead + WAVES * kTile < end) {
+                kid = block_of(ahead + WAVES * kTile + krun);
+                vid = block_of(ahead + WAVES * kTile + vrun);
             }
         }
 
-        // S, as base-2 logits
+        // S; times scale_log2 (not negative: a negative scale is in q) these are base-2 logits
+        uint32_t ks[TABLE], vs[TABLE];
+#pragma unroll
+        for (int x = 0; x < TABLE; ++x) {
+            ks[x] = cur.ks[x];
+            vs[x] = cur.vs[x];
+        }
         f32x4 z[2][NT];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -287,7 +387,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
             for (int n = 0; n < NT; ++n) z[u][n] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            if (g * PER * 32 >= a.g.dim) continue;
+            if (!FULL && g * PER * 32 >= a.g.dim) continue;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 f32x4 d[NT];
@@ -298,13 +398,13 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
                 }
 #pragma unroll
                 for (int s = 0; s < PER; ++s) {
-                    const u32x4 k = decode<DT>(kw[u][g * PER + s], eight);
+                    const u32x4 k = decode<DT>(cur.k[u][g * PER + s], eight, kbits);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) d[n] = mfma_parts<DT>(k, qf[g * PER + s][n], d[n]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const f16x2 sb = __builtin_bit_cast(f16x2, ks[(4 * u + i) * GROUPS + g]);
+                    const f16x2 sb = __builtin_bit_cast(f16x2, entry(ks, (4 * u + i) * GROUPS + g));
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         z[u][n][i] = __builtin_fmaf((float)sb[0], d[n][i], z[u][n][i]);
@@ -313,28 +413,24 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
                 }
             }
         }
-#pragma unroll
-        for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) z[u][n] *= a.scale_log2;
-
         // Tiles that some column does not see in full, or with a block that
         // does not exist: masked logits are -inf whatever was read, and masked
         // tokens' steps and midpoints 0, since 0 * NaN would not vanish.
-        if (t < all_lo || t + kTile - 1 > all_hi || __any(!known)) {
+        if (t < all_lo || t + kTile - 1 > all_hi || __any(!cur.known)) {
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int pos = vrun + 4 * u + i;
+                    const int pos = t + vrun + 4 * u + i;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        if (!known || pos < lo[n] || pos > hi[n]) z[u][n][i] = -__builtin_inff();
-                    if (!known || pos < sp.low || pos >= sp.t1) {
-#pragma unroll
-                        for (int g = 0; g < GROUPS; ++g) vs[(4 * u + i) * GROUPS + g] = 0;
-                    }
+                        if (!cur.known || pos < lo[n] || pos > hi[n]) z[u][n][i] = -__builtin_inff();
                 }
+#pragma unroll
+            for (int x = 0; x < TABLE; ++x) {
+                const int pos = t + vrun + ((x * 16 + row) & (8 * GROUPS - 1)) / GROUPS;
+                if (!cur.known || pos < sp.low || pos >= sp.t1) vs[x] = 0;
+            }
         }
 
         // running softmax
@@ -343,6 +439,7 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
         for (int n = 0; n < NT; ++n) {
             float top = fmaxf(fmaxf(fmaxf(z[0][n][0], z[0][n][1]), fmaxf(z[0][n][2], z[0][n][3])),
                               fmaxf(fmaxf(z[1][n][0], z[1][n][1]), fmaxf(z[1][n][2], z[1][n][3])));
+            top *= a.scale_log2;
             if (__any(top > m[n] + kSlack)) {
                 top = fmaxf(m[n], lane_groups_max(top));
                 const float f = __builtin_amdgcn_exp2f(m[n] - top);
@@ -351,14 +448,11 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
 #pragma unroll
                 for (int k = 0; k < TILES; ++k) acc[k][n] *= f;
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) {
-                    psum[g][n] *= f;
-                    mid[g][n] *= f;
-                }
+                for (int g = 0; g < GROUPS; ++g) mid[g][n] *= f;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[n][i] = __builtin_amdgcn_exp2f(z[i >> 2][n][i & 3] - m[n]);
+                p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i >> 2][n][i & 3], a.scale_log2, -m[n]));
                 l[n] += p[n][i];
             }
         }
@@ -366,16 +460,18 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
         // V^T P
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            if (g * VPER * 16 >= a.g.dim) continue;
+            if (!FULL && g * VPER * 16 >= a.g.dim) continue;
+            f16x2 sb[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sb[i] = __builtin_bit_cast(f16x2, entry(vs, i * GROUPS + g));
             u32x4 pp[NT][NP];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float ps[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    const f16x2 sb = __builtin_bit_cast(f16x2, vs[i * GROUPS + g]);
-                    ps[i] = p[n][i] * (float)sb[0];
-                    mid[g][n] = __builtin_fmaf((float)sb[1], p[n][i], mid[g][n]);
+                    ps[i] = p[n][i] * (float)sb[i][0];
+                    mid[g][n] = __builtin_fmaf((float)sb[i][1], p[n][i], mid[g][n]);
                 }
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
@@ -389,8 +485,6 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
                         }
                     }
                 }
-#pragma unroll
-                for (int k = NP - 1; k >= 0; --k) psum[g][n] = mfma16<BCONV_BF16>(ones, pp[n][k], psum[g][n]);
             }
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
@@ -398,23 +492,26 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
                 u32x4 v;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t two = __builtin_amdgcn_perm(vw[2 * i + 1][word], vw[2 * i][word],
+                    const uint32_t two = __builtin_amdgcn_perm(cur.v[2 * i + 1][word], cur.v[2 * i][word],
                                                                half ? 0x07060302u : 0x05040100u);
-                    v[i] = value_pair<DT>(two, tile & 3);
+                    v[i] = value_pair<DT>(two, tile & 3, vbits);
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = NP - 1; k >= 0; --k) acc[tile][n] = mfma16<BCONV_BF16>(v, pp[n][k], acc[tile][n]);
+                    for (int k = NP - 1; k >= 0; --k) {
+                        acc[tile][n] = mfma16<BCONV_BF16>(offset, pp[n][k], acc[tile][n]);
+                        acc[tile][n] = mfma16<BCONV_BF16>(v, pp[n][k], acc[tile][n]);
+                    }
             }
         }
     }
 
-    // the waves' parts, brought to one maximum and added in wave order
+    // the waves' sums, brought to one maximum and added in wave order
     extern __shared__ float lds[];
     float *so = lds;                             // [waves][COLS][DP + 4]
-    float *sm = lds + kAttnWaves * COLS * (DP + 4);  // [waves][COLS]
-    float *sl = sm + kAttnWaves * COLS;
+    float *sm = lds + WAVES * COLS * (DP + 4);   // [waves][COLS]
+    float *sl = sm + WAVES * COLS;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         l[n] = lane_groups_sum(l[n]);
@@ -428,11 +525,11 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
     for (int n = 0; n < NT; ++n) {
         float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm[w * COLS + n * 16 + row]);
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + n * 16 + row]);
         const float f = __builtin_amdgcn_exp2f(m[n] - top);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const float add = lane_groups_sum(mid[g][n]) - kValueOffset<DT> * psum[g][n][0];
+            const float add = lane_groups_sum(mid[g][n]);
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;
@@ -443,14 +540,14 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
     }
     __syncthreads();
     const int cols = sp.c1 - sp.c0;
-    for (int e = threadIdx.x; e < cols * DP; e += kAttnWaves * 64) {
+    for (int e = threadIdx.x; e < cols * DP; e += WAVES * 64) {
         const int c = e / DP, d = e % DP;
         if (d >= a.g.dim) continue;
         float top = kLowest, sum = 0.0f, o = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) top = fmaxf(top, sm[w * COLS + c]);
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + c]);
 #pragma unroll
-        for (int w = 0; w < kAttnWaves; ++w) {
+        for (int w = 0; w < WAVES; ++w) {
             sum += sl[w * COLS + c] * __builtin_amdgcn_exp2f(sm[w * COLS + c] - top);
             o += so[(w * COLS + c) * (DP + 4) + d];
         }
@@ -466,75 +563,123 @@ __global__ __launch_bounds__(kAttnWaves * 64) void kv4_attention_kernel(AttnArgs
     }
 }
 
-// Joins the parts of one column (a wave each), in part order.
-template <int DT>
+// Joins the parts of one column, a workgroup each: DP / 4 threads take the
+// channels, 1024 / DP slices of them every so-many-th part; the slices are
+// added in order.
+template <int DT, int DP>
 __global__ __launch_bounds__(256) void kv4_combine_kernel(AttnArgs a, int width_cols)
 {
     typedef typename Elem<DT>::type T;
-    const int lane = threadIdx.x & 63;
-    const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    constexpr int THREADS = DP / 4, SLICES = 256 / THREADS;
+    __shared__ float factor[kMaxParts], edge[8];
+    __shared__ f32x4 sums[SLICES][THREADS];
     const int per_head = a.max_q * a.ratio;
-    if (id >= (long long)a.requests * a.g.kv_heads * per_head) return;
-    const int c = (int)(id % per_head);
-    const int head = (int)(id / per_head % a.g.kv_heads), req = (int)(id / per_head / a.g.kv_heads);
+    const int id = blockIdx.x, tid = threadIdx.x;
+    const int c = id % per_head, head = id / per_head % a.g.kv_heads, req = id / per_head / a.g.kv_heads;
     const Span sp = column_span(a, req, c / width_cols, width_cols);
     const int span = sp.t1 - sp.t0;
-    if (c >= sp.c1 || span <= a.part_tokens) return;
+    if (c >= sp.c1 || span <= a.part_tokens) return;  // uniform over the workgroup
     const int used = (span + a.part_tokens - 1) / a.part_tokens;
     const int j = c / a.ratio, h = head * a.ratio + c % a.ratio;
     const long long at = (long long)(sp.q0 + j) * a.heads + h;
     const float2 *ml = a.part_ml + at * a.parts;
-    float top = kLowest;
-    for (int p = 0; p < used; ++p) top = fmaxf(top, ml[p].x);
-    float sum = 0.0f;
-    for (int p = 0; p < used; ++p) sum += ml[p].y * __builtin_amdgcn_exp2f(ml[p].x - top);
-    const bool any = sum > 0.0f || sum != sum;
-    for (int d = lane; d < a.g.dim; d += 64) {
-        float o = 0.0f;
-        for (int p = 0; p < used; ++p)
-            o += a.part_o[(at * a.parts + p) * a.g.dim_padded + d] * __builtin_amdgcn_exp2f(ml[p].x - top);
-        static_cast<T *>(a.out)[at * a.g.dim + d] = round_to<DT>(any ? o / sum : 0.0f);
+    float2 mine[kMaxParts / 256];
+    float top = kLowest, sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 256; ++i) {
+        mine[i] = i * 256 + tid < used ? ml[i * 256 + tid] : float2{kLowest, 0.0f};
+        top = fmaxf(top, mine[i].x);
     }
-    if (a.lse && lane == 0) a.lse[at] = any ? (top + __log2f(sum)) * kLn2 : -__builtin_inff();
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    if ((tid & 63) == 0) edge[tid >> 6] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(edge[0], edge[1]), fmaxf(edge[2], edge[3]));
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 256; ++i) {
+        const float f = __builtin_amdgcn_exp2f(mine[i].x - top);
+        if (i * 256 + tid < used) factor[i * 256 + tid] = f;
+        sum += mine[i].y * f;
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+    if ((tid & 63) == 0) edge[4 + (tid >> 6)] = sum;
+    __syncthreads();
+    sum = edge[4] + edge[5] + edge[6] + edge[7];
+
+    const int d4 = tid % THREADS, slice = tid / THREADS;
+    const f32x4 *o4 = reinterpret_cast<const f32x4 *>(a.part_o + at * a.parts * DP) + d4;
+    f32x4 o = {0, 0, 0, 0};
+#pragma unroll 4
+    for (int p = slice; p < used; p += SLICES) o += o4[(long long)p * THREADS] * factor[p];
+    sums[slice][d4] = o;
+    __syncthreads();
+    if (slice) return;
+#pragma unroll
+    for (int s = 1; s < SLICES; ++s) o += sums[s][d4];
+    const bool any = sum > 0.0f || sum != sum;
+    if (4 * d4 < a.g.dim) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            static_cast<T *>(a.out)[at * a.g.dim + 4 * d4 + i] = round_to<DT>(any ? o[i] / sum : 0.0f);
+    }
+    if (a.lse && tid == 0) a.lse[at] = any ? (top + __log2f(sum)) * kLn2 : -__builtin_inff();
 }
 
 // ------------------------------------------------------------------ dispatch
 
-template <int DT, int DP, int GROUPS, int NT>
-hipError_t launch_attention_kernel(const AttnArgs &a, hipStream_t s)
+template <int DT, int DP, int GROUPS, int NT, int WAVES, bool FULL>
+hipError_t launch_attention_waves(const AttnArgs &a, hipStream_t s)
 {
-    const size_t lds = (size_t)kAttnWaves * 16 * NT * (DP + 4 + 2) * sizeof(float);
+    const size_t lds = (size_t)WAVES * 16 * NT * (DP + 4 + 2) * sizeof(float);
     const long long grid = (long long)a.requests * a.g.kv_heads * a.col_blocks * a.parts;
-    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, NT>), dim3((unsigned)grid), dim3(kAttnWaves * 64), lds, s, a);
+    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, NT, WAVES, FULL>), dim3((unsigned)grid), dim3(WAVES * 64), lds, s, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.parts > 1) {
         const long long cols = (long long)a.requests * a.g.kv_heads * a.max_q * a.ratio;
-        hipLaunchKernelGGL((kv4_combine_kernel<DT>), dim3((unsigned)((cols + 3) / 4)), dim3(256), 0, s, a, 16 * NT);
+        hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3((unsigned)cols), dim3(256), 0, s, a, 16 * NT);
         e = hipGetLastError();
     }
     return e;
 }
 
-template <int DT, int DP>
-hipError_t launch_attention_dim(const AttnArgs &a, int nt, hipStream_t s)
+template <int DT, int DP, int GROUPS, bool FULL>
+hipError_t launch_attention_full(const AttnArgs &a, const AttnShape &h, hipStream_t s)
 {
-    (void)nt;
+    if constexpr (DP <= 128)
+        if (h.nt == 2) return launch_attention_waves<DT, DP, GROUPS, 2, 4, FULL>(a, s);
+    if constexpr (fits_8_waves(DT, DP, GROUPS))
+        if (h.waves == 8) return launch_attention_waves<DT, DP, GROUPS, 1, 8, FULL>(a, s);
+    return launch_attention_waves<DT, DP, GROUPS, 1, 4, FULL>(a, s);
+}
+
+template <int DT, int DP, int GROUPS>
+hipError_t launch_attention_kernel(const AttnArgs &a, const AttnShape &h, hipStream_t s)
+{
+    if (a.g.dim > DP - DP / GROUPS) return launch_attention_full<DT, DP, GROUPS, true>(a, h, s);
+    if constexpr (GROUPS > 1) return launch_attention_full<DT, DP, GROUPS, false>(a, h, s);
+    return hipErrorInvalidValue;  // not reached: one group is never empty
+}
+
+template <int DT, int DP>
+hipError_t launch_attention_dim(const AttnArgs &a, const AttnShape &h, hipStream_t s)
+{
     switch (a.g.groups) {
-    case 1: if constexpr (DP <= 128) return launch_attention_kernel<DT, DP, 1, 1>(a, s); else break;
-    case 2: return launch_attention_kernel<DT, DP, 2, 1>(a, s);
-    case 4: if constexpr (DP >= 128) return launch_attention_kernel<DT, DP, 4, 1>(a, s); else break;
-    case 8: if constexpr (DP >= 256) return launch_attention_kernel<DT, DP, 8, 1>(a, s); else break;
+    case 1: if constexpr (DP <= 128) return launch_attention_kernel<DT, DP, 1>(a, h, s); else break;
+    case 2: return launch_attention_kernel<DT, DP, 2>(a, h, s);
+    case 4: if constexpr (DP >= 128) return launch_attention_kernel<DT, DP, 4>(a, h, s); else break;
+    case 8: if constexpr (DP >= 256) return launch_attention_kernel<DT, DP, 8>(a, h, s); else break;
     }
     return hipErrorInvalidValue;
 }
 
 template <int DT>
-hipError_t launch_attention(const AttnArgs &a, int nt, hipStream_t s)
+hipError_t launch_attention(const AttnArgs &a, const AttnShape &h, hipStream_t s)
 {
     switch (a.g.dim_padded) {
-    case 64: return launch_attention_dim<DT, 64>(a, nt, s);
-    case 128: return launch_attention_dim<DT, 128>(a, nt, s);
-    default: return launch_attention_dim<DT, 256>(a, nt, s);
+    case 64: return launch_attention_dim<DT, 64>(a, h, s);
+    case 128: return launch_attention_dim<DT, 128>(a, h, s);
+    default: return launch_attention_dim<DT, 256>(a, h, s);
     }
 }
 
@@ -546,7 +691,7 @@ using bconv::fail;
 
 struct AttnPlan {
     bconv::AttnArgs a;
-    int nt;
+    bconv::AttnShape shape;
     size_t o_bytes, bytes;  // partial results: sums, then (maximum, denominator) pairs
     bool empty;
 };
@@ -615,11 +760,13 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
     if (most > kMaxContext) most = kMaxContext;
     a.max_context = (int)most;
     a.window = t->window;
-    a.scale_log2 = t->scale * bconv::kLog2e;
+    a.scale_log2 = fabsf(t->scale) * bconv::kLog2e;
+    a.flip = t->scale < 0.0f ? 0x80008000u : 0u;
     a.vec = (uintptr_t)t->q % 16 == 0 && t->q_token_stride * es % 16 == 0 && t->q_head_stride * es % 16 == 0;
 
-    p->nt = 1;
-    const int cols = 16 * p->nt;
+    p->shape.nt = a.max_q * a.ratio > 16 && a.g.dim_padded <= 128 ? 2 : 1;
+    if (getenv("AT_N")) p->shape.nt = atoi(getenv("AT_N"));
+    const int cols = 16 * p->shape.nt;
     if ((long long)a.max_q * a.ratio >= (1LL << 30)) return fail(BCONV_ERR_INVALID_ARGUMENT, "max_q*heads too large");
     a.col_blocks = (a.max_q * a.ratio + cols - 1) / cols;
     const long long tiles = (long long)a.requests * a.g.kv_heads * a.col_blocks;
@@ -631,12 +778,13 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
         if (w < seen) seen = w;
     }
     seen += bconv::kTile;
-    // Parts of the long axis until four workgroups a compute unit are there,
-    // none below 512 tokens (128 a wave), which a part's prologue and the join
-    // would outweigh.
-    const long long want = (4LL * compute_units() + tiles - 1) / tiles;
+    p->shape.waves = tiles >= 512 || p->shape.nt == 2 || !bconv::fits_8_waves(t->dtype, a.g.dim_padded, a.g.groups) ? 4 : 8;
+    if (getenv("AT_W")) p->shape.waves = atoi(getenv("AT_W"));
+    const long long want = ((getenv("AT_T") ? atoi(getenv("AT_T")) : 4LL) * compute_units() + tiles - 1) / tiles;
     long long part = (seen + want - 1) / want;
-    if (part < 512) part = 512;
+    const int least = getenv("AT_P") ? atoi(getenv("AT_P")) : 1024;
+    if (part < least) part = least;
+    if (part < (seen + bconv::kMaxParts - 1) / bconv::kMaxParts) part = (seen + bconv::kMaxParts - 1) / bconv::kMaxParts;
     part = (part + bconv::kTile - 1) / bconv::kTile * bconv::kTile;
     a.part_tokens = (int)part;
     a.parts = (int)((seen + part - 1) / part);
@@ -686,9 +834,9 @@ bconv_status_t bconv_kv4_attention(const bconv_kv4_desc_t *desc, void *stream, c
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     switch (args->dtype) {
-    case BCONV_F32: e = bconv::launch_attention<BCONV_F32>(p.a, p.nt, s); break;
-    case BCONV_F16: e = bconv::launch_attention<BCONV_F16>(p.a, p.nt, s); break;
-    default: e = bconv::launch_attention<BCONV_BF16>(p.a, p.nt, s); break;
+    case BCONV_F32: e = bconv::launch_attention<BCONV_F32>(p.a, p.shape, s); break;
+    case BCONV_F16: e = bconv::launch_attention<BCONV_F16>(p.a, p.shape, s); break;
+    default: e = bconv::launch_attention<BCONV_BF16>(p.a, p.shape, s); break;
     }
     if (e != hipSuccess) return bconv::hip_fail(e, "cache attention kernel");
     return BCONV_OK;

@@ -158,23 +158,39 @@ template <> struct Zero<BCONV_F32> {
     __device__ __forceinline__ explicit Zero(int z) : v(16.0f + (float)z) {}
 };
 
-template <int DT> __device__ __forceinline__ u32x4 decode(uint32_t w, const Zero<DT> &zero)
+// (x & mask) | base is one v_and_or_b32 when one constant is in a scalar
+// register and the other in a vector register (as 32-bit literals they would
+// take two instructions), so both are made opaque here, once a kernel.  The
+// asm is empty on purpose: the compiler writes the registers itself and so
+// keeps the wait states that a write next to a matrix instruction needs.
+struct CodeBits {
+    uint32_t mask, base;
+    __device__ __forceinline__ uint32_t operator()(uint32_t t) const { return (t & mask) | base; }
+};
+__device__ __forceinline__ CodeBits opaque_bits(uint32_t mask, uint32_t base)
+{
+    asm("" : "+s"(mask));
+    asm("" : "+v"(base));
+    return CodeBits{mask, base};
+}
+template <int DT> __device__ __forceinline__ CodeBits code_bits()
+{
+    return opaque_bits(kCodeMask, DT == BCONV_F16 ? kBase128 : kBase16);
+}
+
+template <int DT> __device__ __forceinline__ u32x4 decode(uint32_t w, const Zero<DT> &zero, const CodeBits &bits)
 {
     u32x4 r;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const uint32_t t = e ? rotr(w, 4 * e) : w;
+        const uint32_t c = bits(e ? rotr(w, 4 * e) : w);
         if constexpr (DT == BCONV_F16) {
-            const f16x2 c = __builtin_bit_cast(f16x2, (t & kCodeMask) | kBase128) - zero.v;
-            r[e] = __builtin_bit_cast(uint32_t, c);
+            r[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - zero.v);
+        } else if constexpr (DT == BCONV_BF16) {
+            r[e] = c;
         } else {
-            const uint32_t c = (t & kCodeMask) | kBase16;
-            if constexpr (DT == BCONV_BF16) {
-                r[e] = c;
-            } else {
-                const float lo = __uint_as_float(c << 16) - zero.v, hi = __uint_as_float(c & 0xffff0000u) - zero.v;
-                r[e] = pack_hi16(__float_as_uint(lo), __float_as_uint(hi));
-            }
+            const float lo = __uint_as_float(c << 16) - zero.v, hi = __uint_as_float(c & 0xffff0000u) - zero.v;
+            r[e] = pack_hi16(__float_as_uint(lo), __float_as_uint(hi));
         }
     }
     return r;

@@ -9,7 +9,7 @@
 // read them: one 16-byte load a lane is 16 outputs x 128 inputs.
 #include <hip/hip_runtime.h>
 
-#include <cstring>
+#include <cstdlib>
 #include <new>
 
 #include "host.h"
@@ -18,8 +18,6 @@
 namespace bconv {
 
 constexpr int kChunk = 128;         // inputs of one 16-byte load a lane
-constexpr int kFewWaves = 8;        // waves that split the inputs of one output tile
-constexpr int kGroupsMax = kChunk / 32;
 
 struct Q4Args {
     const uint32_t *codes;   // [tiles][chunks][64 lanes][4]
@@ -76,174 +74,461 @@ __global__ void q4_prepack_scales_kernel(const uint16_t *user_s, const uint8_t *
     if (zeros) zeros[i] = in ? user_z[(long long)o * groups + group] : 8;
 }
 
+// Scales and zero points of one output tile and chunk, as a lane uses them:
+// the scales of its 4 result rows, and for the codes' zero points either those
+// of its result rows (bf16, taken out as a multiple of sum x) or of its operand
+// row (fp16 and fp32, subtracted from the codes).
+template <int DT, bool ZP, int STEPS> struct Scales {
+    static constexpr int N = 4 / STEPS;  // groups a chunk
+    typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+    f16x4 s[N];
+    uint32_t z[ZP ? N : 1];
+    __device__ __forceinline__ void load(const uint16_t *sc, const uint8_t *zp, int lane)
+    {
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            s[g] = *reinterpret_cast<const f16x4 *>(sc + g * 16 + (lane >> 4) * 4);
+            if constexpr (ZP) {
+                if constexpr (DT == BCONV_BF16) z[g] = *reinterpret_cast<const uint32_t *>(zp + g * 16 + (lane >> 4) * 4);
+                else z[g] = zp[g * 16 + (lane & 15)];
+            }
+        }
+    }
+    __device__ __forceinline__ float scale(int g, int i) const { return (float)s[g][i]; }
+    __device__ __forceinline__ Zero<DT> zero(int g) const
+    {
+        if constexpr (ZP && DT != BCONV_BF16) return Zero<DT>((int)z[g]);
+        else return Zero<DT>(8);
+    }
+    // What a group's product starts from: `off` is -24 sum x, or -sum x with
+    // zero points.
+    __device__ __forceinline__ f32x4 start(int g, float off) const
+    {
+        if constexpr (DT != BCONV_BF16) return f32x4{0, 0, 0, 0};
+        if constexpr (!ZP) return f32x4{off, off, off, off};
+        f32x4 r;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r[i] = (float)(16 + ((z[ZP ? g : 0] >> (8 * i)) & 255u)) * off;
+        return r;
+    }
+};
+
 // One chunk (16 RT outputs x 128 inputs) times NT tiles of 16 rows of x, added
 // to acc.  STEPS: 32-input steps a group.  Per group and output tile the exact
 // products of one group are summed first, then scaled once in fp32.
 template <int DT, bool ZP, int STEPS, int RT, int NT>
 __device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operand<DT> (&xf)[4][NT],
-                                              const uint16_t *const (&sc)[RT], const uint8_t *const (&zp)[RT], int lane,
+                                              const Scales<DT, ZP, STEPS> (&sc)[RT], const CodeBits &bits,
                                               f32x4 (&acc)[RT][NT])
 {
-    const int row = lane & 15, lg = lane >> 4;
 #pragma unroll
     for (int g = 0; g < 4 / STEPS; ++g) {
         // bf16: the offset 16 + z of the codes leaves -(16 + z) sum x, on the
         // matrix cores as well (a constant operand times x)
         f32x4 off[NT];
-        if constexpr (DT == BCONV_BF16) {
-            const u32x4 c = bf16_const(ZP ? -1.0f : -24.0f);
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                off[t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < NT; ++t) {
+            off[t] = f32x4{0, 0, 0, 0};
+            if constexpr (DT == BCONV_BF16) {
+                const u32x4 c = bf16_const(ZP ? -1.0f : -24.0f);
 #pragma unroll
                 for (int s = 0; s < STEPS; ++s) off[t] = mfma_parts<DT>(c, xf[g * STEPS + s][t], off[t]);
             }
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-            const f16x4 s4 = *reinterpret_cast<const f16x4 *>(sc[r] + g * 16 + lg * 4);
-            int z = 8;
-            uint32_t z4 = 0;
-            if constexpr (ZP) {
-                if constexpr (DT == BCONV_BF16)
-                    z4 = *reinterpret_cast<const uint32_t *>(zp[r] + g * 16 + lg * 4);
-                else
-                    z = zp[r][g * 16 + row];
-            }
-            const Zero<DT> zero(z);
             f32x4 d[NT];
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                if constexpr (DT == BCONV_BF16) {
-                    if constexpr (ZP) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) d[t][i] = (float)(16 + ((z4 >> (8 * i)) & 255u)) * off[t][i];
-                    } else {
-                        d[t] = off[t];
-                    }
-                } else {
-                    d[t] = f32x4{0, 0, 0, 0};
-                }
-            }
+            for (int t = 0; t < NT; ++t) d[t] = ZP ? sc[r].start(g, off[t][0]) : off[t];
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) {
-                const u32x4 a = decode<DT>(w[r][g * STEPS + s], zero);
+                const u32x4 k = decode<DT>(w[r][g * STEPS + s], sc[r].zero(g), bits);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) d[t] = mfma_parts<DT>(a, xf[g * STEPS + s][t], d[t]);
+                for (int t = 0; t < NT; ++t) d[t] = mfma_parts<DT>(k, xf[g * STEPS + s][t], d[t]);
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf((float)s4[i], d[t][i], acc[r][t][i]);
+                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(sc[r].scale(g, i), d[t][i], acc[r][t][i]);
         }
     }
 }
 
-// Few rows of x.  A workgroup takes 16 RT outputs and 16 NT rows of x; its
-// waves split the inputs chunk by chunk and add their sums in LDS, in a fixed
-// order.
-template <int DT, bool ZP, int STEPS, int RT, int NT>
-__global__ __launch_bounds__(kFewWaves * 64) void q4_few_kernel(Q4Args a)
+// 4 consecutive outputs of a row, with the bias, as far as there are outputs.
+template <int DT> __device__ __forceinline__ void store_outputs(const Q4Args &a, int m, int o0, f32x4 v)
 {
     typedef typename Elem<DT>::type T;
-    __shared__ f32x4 part[kFewWaves][RT * NT][64];
+    T *y = static_cast<T *>(a.y) + (long long)m * a.ldy + o0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (o0 + i < a.n) y[i] = round_to<DT>(v[i] + (a.bias ? a.bias[o0 + i] : 0.0f));
+}
+
+// Few rows of x.  A workgroup takes 16 RT outputs and 16 NT rows of x; its
+// waves split the inputs chunk by chunk and add their sums in LDS, in a fixed
+// order.  UNROLL chunks are requested before the first is used.
+template <int DT, bool ZP, int STEPS, int RT, int NT, int WAVES, int UNROLL>
+__global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
+{
+    typedef typename Elem<DT>::type T;
+    __shared__ f32x4 part[WAVES][RT * NT][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int tile0 = blockIdx.x * RT, m0 = blockIdx.y * 16 * NT;
     const int row = lane & 15, lg = lane >> 4;
     constexpr int per_chunk = 4 / STEPS;
+    const CodeBits bits = code_bits<DT>();
 
     f32x4 acc[RT][NT];
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+    long long first[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
 
-    for (int c = wave; c < a.chunks; c += kFewWaves) {
-        u32x4 w[RT];
-        const uint16_t *sc[RT];
-        const uint8_t *zp[RT];
+    for (int c0 = wave; c0 < a.chunks; c0 += WAVES * UNROLL) {
+        u32x4 w[UNROLL][RT];
+        Scales<DT, ZP, STEPS> sc[UNROLL][RT];
+        Operand<DT> xf[UNROLL][4][NT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const int tile = tile0 + r < a.tiles ? tile0 + r : a.tiles - 1;
-            const long long tc = (long long)tile * a.chunks + c;
-            w[r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
-            sc[r] = a.scales + tc * per_chunk * 16;
-            zp[r] = ZP ? a.zeros + tc * per_chunk * 16 : nullptr;
-        }
-        Operand<DT> xf[4][NT];
+        for (int u = 0; u < UNROLL; ++u) {
+            const int c = c0 + u * WAVES;
+            if (c >= a.chunks) break;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int m = m0 + t * 16 + row;
-            const T *xr = static_cast<const T *>(a.x) + (long long)m * a.ldx;
+            for (int r = 0; r < RT; ++r) {
+                const long long tc = first[r] + c;
+                w[u][r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
+                sc[u][r].load(a.scales + tc * per_chunk * 16, ZP ? a.zeros + tc * per_chunk * 16 : nullptr, lane);
+            }
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const int k = c * kChunk + s * 32 + lg * 8;
-                if (m < a.m && k < a.k) {
-                    xf[s][t] = load_operand<DT>(xr + k, k, a.k, a.vec != 0);
-                } else {
+            for (int t = 0; t < NT; ++t) {
+                const int m = m0 + t * 16 + row;
+                const T *xr = static_cast<const T *>(a.x) + (long long)m * a.ldx;
 #pragma unroll
-                    for (int p = 0; p < kSplit<DT>; ++p) xf[s][t].part[p] = u32x4{0, 0, 0, 0};
+                for (int s = 0; s < 4; ++s) {
+                    const int k = c * kChunk + s * 32 + lg * 8;
+                    if (m < a.m && k < a.k) {
+                        xf[u][s][t] = load_operand<DT>(xr + k, k, a.k, a.vec != 0);
+                    } else {
+#pragma unroll
+                        for (int p = 0; p < kSplit<DT>; ++p) xf[u][s][t].part[p] = u32x4{0, 0, 0, 0};
+                    }
                 }
             }
         }
-        chunk_product<DT, ZP, STEPS, RT, NT>(w, xf, sc, zp, lane, acc);
+#pragma unroll
+        for (int u = 0; u < UNROLL; ++u) {
+            if (c0 + u * WAVES >= a.chunks) break;
+            chunk_product<DT, ZP, STEPS, RT, NT>(w[u], xf[u], sc[u], bits, acc);
+        }
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int t = 0; t < NT; ++t) part[wave][r * NT + t][lane] = acc[r][t];
     __syncthreads();
-    for (int e = threadIdx.x; e < RT * NT * 64; e += kFewWaves * 64) {
+    for (int e = threadIdx.x; e < RT * NT * 64; e += WAVES * 64) {
         const int l = e & 63, rt = e >> 6;
         const int m = m0 + (rt % NT) * 16 + (l & 15);
         const int o0 = (tile0 + rt / NT) * 16 + (l >> 4) * 4;
         if (m >= a.m || o0 >= a.n) continue;
         f32x4 v = part[0][rt][l];
 #pragma unroll
-        for (int w = 1; w < kFewWaves; ++w) v += part[w][rt][l];
-        T *y = static_cast<T *>(a.y) + (long long)m * a.ldy + o0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (o0 + i < a.n) y[i] = round_to<DT>(v[i] + (a.bias ? a.bias[o0 + i] : 0.0f));
+        for (int w = 1; w < WAVES; ++w) v += part[w][rt][l];
+        store_outputs<DT>(a, m, o0, v);
     }
 }
 
-template <int DT, bool ZP, int STEPS, int RT, int NT>
+// ------------------------------------------------------------------ many rows
+
+// What the product of many rows takes besides Q4Args: x laid out as operands
+// and the partial sums of the splits.
+struct Q4Many {
+    u32x4 *xp;       // [column tiles][chunks * 4][parts][64]
+    float *xs;       // bf16: [column tiles][chunks][groups a chunk][16], -sum x (times 24 without zero points)
+    float *sums;     // [splits][column tiles * 16][padded outputs], or nullptr for one split
+    int col_tiles;   // padded to the workgroup's
+    int padded_n;
+    int row_blocks, col_blocks, splits;
+};
+
+// x as operands, a wave a (16 rows, group) pair: converted, split and padded
+// with zeros once instead of once per output tile, with the group's sum that
+// the codes' offset and zero points multiply.
+template <int DT, bool ZP, int STEPS>
+__global__ __launch_bounds__(256) void q4_pack_kernel(Q4Args a, Q4Many q)
+{
+    typedef typename Elem<DT>::type T;
+    const int lane = threadIdx.x & 63;
+    const long long id = (long long)blockIdx.x * 4 + (threadIdx.x >> 6);
+    const int groups = a.chunks * (4 / STEPS);
+    if (id >= (long long)q.col_tiles * groups) return;
+    const int g = (int)(id % groups), tile = (int)(id / groups);
+    const int m = tile * 16 + (lane & 15);
+    f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int step = g * STEPS + s, k = step * 32 + (lane >> 4) * 8;
+        Operand<DT> o;
+        if (m < a.m && k < a.k) {
+            o = load_operand<DT>(static_cast<const T *>(a.x) + (long long)m * a.ldx + k, k, a.k, a.vec != 0);
+        } else {
+#pragma unroll
+            for (int p = 0; p < kSplit<DT>; ++p) o.part[p] = u32x4{0, 0, 0, 0};
+        }
+        u32x4 *dst = q.xp + ((long long)tile * a.chunks * 4 + step) * kSplit<DT> * 64 + lane;
+#pragma unroll
+        for (int p = 0; p < kSplit<DT>; ++p) dst[p * 64] = o.part[p];
+        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(bf16_const(ZP ? -1.0f : -24.0f), o, sum);
+    }
+    if constexpr (DT == BCONV_BF16)
+        if (lane < 16) q.xs[((long long)tile * groups + g) * 16 + lane] = sum[0];
+}
+
+constexpr int kManyRows = 4;  // output tiles a wave
+// column tiles a wave: 64 rows of x, or 32 in fp32, whose operands are three parts
+template <int DT> constexpr int kManyCols = DT == BCONV_F32 ? 2 : 4;
+
+// A workgroup takes 128 outputs and 2 NT column tiles, its four waves a
+// quarter each.  The columns' operands go to LDS, a chunk ahead, by loads that
+// pass no registers; the codes go to registers, a chunk ahead too.
+template <int DT, bool ZP, int STEPS, int NT>
+__global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q4Args a, Q4Many q)
+{
+    constexpr int RT = kManyRows, P = kSplit<DT>, UNITS = 2 * NT * 4 * P;  // 1 KiB units of a stage
+    constexpr int per_chunk = 4 / STEPS;
+    __shared__ u32x4 stage[2][UNITS * 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = lane & 15, lg = lane >> 4;
+    // Blocks go to the XCDs in turn: the splits of the inputs come first, so
+    // that an XCD's L2 sees one slice of x and each code once per column block.
+    int id = blockIdx.x;
+    const int split = id % q.splits;
+    id /= q.splits;
+    const int cb = id % q.col_blocks, rb = id / q.col_blocks;
+    const int c_begin = (int)((long long)a.chunks * split / q.splits), c_end = (int)((long long)a.chunks * (split + 1) / q.splits);
+    const int tile0 = rb * 2 * RT + (wave >> 1) * RT, col0 = cb * 2 * NT;
+    const int mine = col0 + (wave & 1) * NT;
+    const CodeBits bits = code_bits<DT>();
+
+    auto request = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < UNITS / 4; ++i) {
+            const int u = i * 4 + wave, t = u / (4 * P), rest = u % (4 * P);
+            const u32x4 *src = q.xp + (((long long)(col0 + t) * a.chunks + c) * 4 * P + rest) * 64 + lane;
+            __builtin_amdgcn_global_load_lds((const void *)src,
+                                             (__attribute__((address_space(3))) void *)(&stage[c & 1][u * 64]), 16, 0, 0);
+        }
+    };
+    long long first[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
+    u32x4 w[RT], wn[RT];
+    Scales<DT, ZP, STEPS> sc[RT], scn[RT];
+    float xs[per_chunk][NT], xsn[per_chunk][NT];
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const long long tc = first[r] + c;
+            wn[r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
+            scn[r].load(a.scales + tc * per_chunk * 16, ZP ? a.zeros + tc * per_chunk * 16 : nullptr, lane);
+        }
+        if constexpr (DT == BCONV_BF16) {
+#pragma unroll
+            for (int g = 0; g < per_chunk; ++g)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    xsn[g][t] = q.xs[(((long long)(mine + t) * a.chunks + c) * per_chunk + g) * 16 + row];
+        }
+    };
+    f32x4 acc[RT][NT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+
+    if (c_begin < c_end) {
+        request(c_begin);
+        fetch(c_begin);
+    }
+    for (int c = c_begin; c < c_end; ++c) {
+        __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xf << 8));  // vmcnt(0): this chunk's operands and codes are here
+        __syncthreads();                                          // in every wave, and the other stage is read
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            w[r] = wn[r];
+            sc[r] = scn[r];
+        }
+#pragma unroll
+        for (int g = 0; g < per_chunk; ++g)
+#pragma unroll
+            for (int t = 0; t < NT; ++t) xs[g][t] = xsn[g][t];
+        if (c + 1 < c_end) {
+            request(c + 1);
+            fetch(c + 1);
+        }
+        const u32x4 *st = &stage[c & 1][(wave & 1) * NT * 4 * P * 64 + lane];
+#pragma unroll
+        for (int g = 0; g < per_chunk; ++g) {
+            f32x4 d[RT][NT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t) d[r][t] = sc[r].start(g, xs[g][t]);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                Operand<DT> b[NT];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int p = 0; p < P; ++p) b[t].part[p] = st[((t * 4 + g * STEPS + s) * P + p) * 64];
+#pragma unroll
+                for (int r = 0; r < RT; ++r) {
+                    const u32x4 k = decode<DT>(w[r][g * STEPS + s], sc[r].zero(g), bits);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) d[r][t] = mfma_parts<DT>(k, b[t], d[r][t]);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(sc[r].scale(g, i), d[r][t][i], acc[r][t][i]);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int o0 = (tile0 + r) * 16 + lg * 4;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int m = (mine + t) * 16 + row;
+            if (q.splits > 1)
+                *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * q.col_tiles * 16 + m) * q.padded_n + o0) = acc[r][t];
+            else if (m < a.m && o0 < a.n)
+                store_outputs<DT>(a, m, o0, acc[r][t]);
+        }
+    }
+}
+
+// Adds the splits' sums in order.
+template <int DT>
+__global__ __launch_bounds__(256) void q4_reduce_kernel(Q4Args a, Q4Many q)
+{
+    const int per = (a.n + 3) / 4;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (long long)per * a.m) return;
+    const int m = (int)(id / per), o0 = (int)(id % per) * 4;
+    const float *p = q.sums + (long long)m * q.padded_n + o0;
+    const long long step = (long long)q.col_tiles * 16 * q.padded_n;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+    for (int s = 1; s < q.splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * step);
+    store_outputs<DT>(a, m, o0, v);
+}
+
+// ------------------------------------------------------------------ dispatch
+
+// Which kernel a number of rows takes, and what it needs of the workspace.
+struct Q4Plan {
+    bool many;
+    int cols;  // column tiles a workgroup (many) or a wave (few)
+    Q4Many q;
+    size_t xs_offset, sums_offset, bytes;
+};
+
+constexpr int kFewRows = 64;  // rows up to which the waves of a workgroup split the inputs
+
+Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, int cus)
+{
+    Q4Plan p{};
+    const char *ev = getenv("Q4_FEW");
+    p.many = rows > (ev ? atoi(ev) : kFewRows);
+    if (!p.many) return p;
+    const int nt = dtype == BCONV_F32 ? kManyCols<BCONV_F32> : kManyCols<BCONV_BF16>;
+    const int parts = dtype == BCONV_F32 ? 3 : 1;
+    p.q.col_blocks = (rows + 32 * nt - 1) / (32 * nt);
+    p.q.col_tiles = p.q.col_blocks * 2 * nt;
+    p.q.row_blocks = (tiles + 2 * kManyRows - 1) / (2 * kManyRows);
+    p.q.padded_n = p.q.row_blocks * 2 * kManyRows * 16;
+    const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks;
+    long long splits = (2LL * cus + blocks - 1) / blocks;
+    if (const char *e2 = getenv("Q4_SPLITS")) splits = atoi(e2);
+    if (splits > 8) splits = 8;
+    if (splits > chunks / 4) splits = chunks / 4;
+    p.q.splits = splits < 1 ? 1 : (int)splits;
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    p.xs_offset = up((size_t)p.q.col_tiles * chunks * 4 * parts * 1024);
+    p.sums_offset = p.xs_offset + (dtype == BCONV_BF16 ? up((size_t)p.q.col_tiles * chunks * per_chunk * 16 * 4) : 0);
+    p.bytes = p.sums_offset + (p.q.splits > 1 ? (size_t)p.q.splits * p.q.col_tiles * 16 * p.q.padded_n * 4 : 0);
+    return p;
+}
+
+template <int DT, bool ZP, int STEPS, int RT, int NT, int WAVES, int UNROLL>
 hipError_t run_few(const Q4Args &a, hipStream_t s)
 {
     const dim3 grid((a.tiles + RT - 1) / RT, (a.m + 16 * NT - 1) / (16 * NT));
-    hipLaunchKernelGGL((q4_few_kernel<DT, ZP, STEPS, RT, NT>), grid, dim3(kFewWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((q4_few_kernel<DT, ZP, STEPS, RT, NT, WAVES, UNROLL>), grid, dim3(WAVES * 64), 0, s, a);
     return hipGetLastError();
 }
 
 template <int DT, bool ZP, int STEPS>
-hipError_t run_linear(const Q4Args &a, hipStream_t s)
+hipError_t run_linear(const Q4Args &a, const Q4Plan &p, hipStream_t s)
 {
-    return run_few<DT, ZP, STEPS, 1, 1>(a, s);
+    if (p.many) {
+        const long long packs = (long long)p.q.col_tiles * a.chunks * (4 / STEPS);
+        hipLaunchKernelGGL((q4_pack_kernel<DT, ZP, STEPS>), dim3((unsigned)((packs + 3) / 4)), dim3(256), 0, s, a, p.q);
+        hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+        const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks * p.q.splits;
+        hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, kManyCols<DT>>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
+        e = hipGetLastError();
+        if (e != hipSuccess || p.q.splits == 1) return e;
+        const long long outs = (long long)((a.n + 3) / 4) * a.m;
+        hipLaunchKernelGGL((q4_reduce_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
+        return hipGetLastError();
+    }
+    const char *ev = getenv("Q4_VAR");
+    const int v = ev ? atoi(ev) : 0;
+    switch (v) {
+    case 0: return run_few<DT, ZP, STEPS, 1, 1, 8, 1>(a, s);
+    case 1: return run_few<DT, ZP, STEPS, 1, 1, 8, 2>(a, s);
+    case 2: return run_few<DT, ZP, STEPS, 1, 1, 16, 1>(a, s);
+    case 3: return run_few<DT, ZP, STEPS, 1, 1, 16, 2>(a, s);
+    case 4: return run_few<DT, ZP, STEPS, 2, 1, 8, 1>(a, s);
+    case 5: return run_few<DT, ZP, STEPS, 2, 1, 16, 1>(a, s);
+    case 6: return run_few<DT, ZP, STEPS, 4, 1, 8, 1>(a, s);
+    case 7: return run_few<DT, ZP, STEPS, 1, 1, 16, 4>(a, s);
+    case 8: return run_few<DT, ZP, STEPS, 2, 2, 8, 1>(a, s);
+    case 9: return run_few<DT, ZP, STEPS, 1, 2, 16, 1>(a, s);
+    case 10: return run_few<DT, ZP, STEPS, 1, 4, 8, 1>(a, s);
+    case 11: return run_few<DT, ZP, STEPS, 2, 4, 8, 1>(a, s);
+    case 12: return run_few<DT, ZP, STEPS, 4, 1, 16, 1>(a, s);
+    default: return run_few<DT, ZP, STEPS, 1, 4, 16, 1>(a, s);
+    }
 }
 
 template <int DT, bool ZP>
-hipError_t dispatch_group(const Q4Args &a, int group, hipStream_t s)
+hipError_t dispatch_group(const Q4Args &a, const Q4Plan &p, int group, hipStream_t s)
 {
     switch (group) {
-    case 32: return run_linear<DT, ZP, 1>(a, s);
-    case 64: return run_linear<DT, ZP, 2>(a, s);
-    default: return run_linear<DT, ZP, 4>(a, s);
+    case 32: return run_linear<DT, ZP, 1>(a, p, s);
+    case 64: return run_linear<DT, ZP, 2>(a, p, s);
+    default: return run_linear<DT, ZP, 4>(a, p, s);
     }
 }
 
 template <int DT>
-hipError_t dispatch_zero(const Q4Args &a, int group, hipStream_t s)
+hipError_t dispatch_zero(const Q4Args &a, const Q4Plan &p, int group, hipStream_t s)
 {
-    return a.zeros ? dispatch_group<DT, true>(a, group, s) : dispatch_group<DT, false>(a, group, s);
+    return a.zeros ? dispatch_group<DT, true>(a, p, group, s) : dispatch_group<DT, false>(a, p, group, s);
 }
 
 }  // namespace bconv
 
 struct bconv_q4_linear {
     bconv_q4_linear_desc_t desc;
-    int device;
+    int device, cus;
     int tiles, chunks, per_chunk;
     uint32_t *d_codes;
     uint16_t *d_scales;
@@ -319,6 +604,7 @@ bconv_status_t bconv_q4_linear_create(const bconv_q4_linear_desc_t *desc, const 
     h->chunks = (k + bconv::kChunk - 1) / bconv::kChunk;
     h->per_chunk = bconv::kChunk / desc->group;
     hipError_t e = hipGetDevice(&h->device);
+    if (e == hipSuccess) e = hipDeviceGetAttribute(&h->cus, hipDeviceAttributeMultiprocessorCount, h->device);
     if (e != hipSuccess) {
         release(h);
         return hip_fail(e, "hipGetDevice");
@@ -357,7 +643,7 @@ bconv_status_t bconv_q4_linear_workspace_size(bconv_q4_linear_t h, int32_t rows,
     if (!h || !bytes) return fail(BCONV_ERR_INVALID_ARGUMENT, "handle or bytes is NULL");
     if (rows < 0) return fail(BCONV_ERR_INVALID_ARGUMENT, "rows must be >= 0");
     if (!dtype_bytes(dtype)) return fail(BCONV_ERR_INVALID_ARGUMENT, "unknown dtype %d", dtype);
-    *bytes = 0;
+    *bytes = rows ? bconv::plan_linear(rows, dtype, h->tiles, h->chunks, h->per_chunk, h->cus).bytes : 0;
     return BCONV_OK;
 }
 
@@ -376,12 +662,19 @@ bconv_status_t bconv_q4_linear_forward(bconv_q4_linear_t h, void *stream, int32_
     if (((uintptr_t)x | (uintptr_t)y) % es) return fail(BCONV_ERR_INVALID_ARGUMENT, "x/y not aligned to an element");
     const size_t xb = ((size_t)(rows - 1) * ldx + k) * es, yb = ((size_t)(rows - 1) * ldy + n) * es;
     if (ranges_overlap(x, xb, y, yb)) return fail(BCONV_ERR_INVALID_ARGUMENT, "x and y overlap");
-    size_t need = 0;
-    bconv_status_t st = bconv_q4_linear_workspace_size(h, rows, dtype, &need);
-    if (st != BCONV_OK) return st;
-    if (need > 0 && (!workspace || workspace_bytes < need))
-        return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+    bconv::Q4Plan p = bconv::plan_linear(rows, dtype, h->tiles, h->chunks, h->per_chunk, h->cus);
+    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
+        return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes,
                     workspace ? workspace_bytes : (size_t)0);
+    if (p.bytes > 0) {
+        if ((uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+        if (ranges_overlap(workspace, p.bytes, x, xb) || ranges_overlap(workspace, p.bytes, y, yb))
+            return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace overlaps x or y");
+        char *ws = static_cast<char *>(workspace);
+        p.q.xp = reinterpret_cast<bconv::u32x4 *>(ws);
+        p.q.xs = reinterpret_cast<float *>(ws + p.xs_offset);
+        p.q.sums = reinterpret_cast<float *>(ws + p.sums_offset);
+    }
 
     DeviceGuard guard(h->device);
     if (guard.err != hipSuccess) return hip_fail(guard.err, "hipSetDevice");
@@ -403,9 +696,9 @@ bconv_status_t bconv_q4_linear_forward(bconv_q4_linear_t h, void *stream, int32_
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     switch (dtype) {
-    case BCONV_F32: e = bconv::dispatch_zero<BCONV_F32>(a, h->desc.group, s); break;
-    case BCONV_F16: e = bconv::dispatch_zero<BCONV_F16>(a, h->desc.group, s); break;
-    default: e = bconv::dispatch_zero<BCONV_BF16>(a, h->desc.group, s); break;
+    case BCONV_F32: e = bconv::dispatch_zero<BCONV_F32>(a, p, h->desc.group, s); break;
+    case BCONV_F16: e = bconv::dispatch_zero<BCONV_F16>(a, p, h->desc.group, s); break;
+    default: e = bconv::dispatch_zero<BCONV_BF16>(a, p, h->desc.group, s); break;
     }
     if (e != hipSuccess) return hip_fail(e, "4-bit linear kernel");
     return BCONV_OK;
