@@ -186,8 +186,8 @@ def _host_f32(a) -> Optional[ctypes.POINTER(ctypes.c_float)]:
 
 def _ptr(x) -> Optional[int]:
     """Device pointer of a torch tensor or a plain integer address."""
-    if x is None:
-        return None
+    if x is None or type(x) is int:
+        return x
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
     return int(x)
@@ -343,8 +343,10 @@ def bconv_q4_linear_workspace_size(h: int, rows: int, dtype: int) -> int:
 
 def bconv_q4_linear_forward(h: int, stream, rows: int, dtype: int, x, ldx: int, y, ldy: int, workspace=None,
                             workspace_bytes: int = 0) -> None:
-    _check(load_library().bconv_q4_linear_forward(h, _ptr(stream), rows, dtype, _ptr(x), ldx, _ptr(y), ldy,
-                                                  _ptr(workspace), workspace_bytes))
+    st = (_lib or load_library()).bconv_q4_linear_forward(h, stream, rows, dtype, _ptr(x), ldx, _ptr(y), ldy,
+                                                          _ptr(workspace), workspace_bytes)
+    if st:
+        _check(st)
 
 
 def bconv_q4_linear_destroy(h: int) -> None:
@@ -359,8 +361,10 @@ def bconv_kv4_layout(desc: bconv_kv4_desc_t) -> bconv_kv4_layout_t:
 
 def bconv_kv4_append(desc: bconv_kv4_desc_t, stream, pool, tokens: int, dtype: int, k, k_strides, v, v_strides, slots,
                      k_out=None, v_out=None) -> None:
-    _check(load_library().bconv_kv4_append(desc, _ptr(stream), _ptr(pool), tokens, dtype, _ptr(k), *k_strides, _ptr(v),
-                                           *v_strides, _ptr(slots), _ptr(k_out), _ptr(v_out)))
+    st = (_lib or load_library()).bconv_kv4_append(desc, stream, _ptr(pool), tokens, dtype, _ptr(k), *k_strides,
+                                                   _ptr(v), *v_strides, _ptr(slots), _ptr(k_out), _ptr(v_out))
+    if st:
+        _check(st)
 
 
 def bconv_kv4_attention_workspace_size(desc: bconv_kv4_desc_t, args: bconv_kv4_attention_t) -> int:
@@ -371,13 +375,17 @@ def bconv_kv4_attention_workspace_size(desc: bconv_kv4_desc_t, args: bconv_kv4_a
 
 def bconv_kv4_attention(desc: bconv_kv4_desc_t, stream, args: bconv_kv4_attention_t, workspace=None,
                         workspace_bytes: int = 0) -> None:
-    _check(load_library().bconv_kv4_attention(desc, _ptr(stream), args, _ptr(workspace), workspace_bytes))
+    st = (_lib or load_library()).bconv_kv4_attention(desc, stream, args, _ptr(workspace), workspace_bytes)
+    if st:
+        _check(st)
 
 
 def bconv_block_tables(stream, requests: int, block_size: int, block_table, table_width: int, table_stride: int,
                        context_lens, new_lens, free_blocks, free_count: int, free_head, free_head_out, tokens: int,
                        slots=None, positions=None, q_start=None, context_lens_out=None) -> None:
-    _check(load_library().bconv_block_tables(_ptr(stream), requests, block_size, _ptr(block_table), table_width,
-                                             table_stride, _ptr(context_lens), _ptr(new_lens), _ptr(free_blocks),
-                                             free_count, _ptr(free_head), _ptr(free_head_out), tokens, _ptr(slots),
-                                             _ptr(positions), _ptr(q_start), _ptr(context_lens_out)))
+    st = (_lib or load_library()).bconv_block_tables(
+        stream, requests, block_size, _ptr(block_table), table_width, table_stride, _ptr(context_lens),
+        _ptr(new_lens), _ptr(free_blocks), free_count, _ptr(free_head), _ptr(free_head_out), tokens, _ptr(slots),
+        _ptr(positions), _ptr(q_start), _ptr(context_lens_out))
+    if st:
+        _check(st)

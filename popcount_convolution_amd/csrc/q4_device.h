@@ -71,47 +71,66 @@ __device__ __forceinline__ void split3(float x, uint32_t &h, uint32_t &m, uint32
     l = __float_as_uint(r - __uint_as_float(m));
 }
 
-// 8 consecutive elements at p (offset k of a row of length len) as an operand;
-// elements at or past len are 0.  `vec`: p is 16-byte aligned for k % 8 == 0.
+// 8 consecutive elements as loaded.
+template <int DT> struct Raw {
+    u32x4 v[DT == BCONV_F32 ? 2 : 1];
+};
+
+// 16-byte loads; p is 16-byte aligned.
+template <int DT> __device__ __forceinline__ Raw<DT> load_raw(const typename Elem<DT>::type *p)
+{
+    Raw<DT> r;
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+    r.v[0] = q[0];
+    if constexpr (DT == BCONV_F32) r.v[1] = q[1];
+    return r;
+}
+
+// Element loads, for any alignment; elements at or past len (of a row that p is
+// k into) are 0.
 template <int DT>
-__device__ __forceinline__ Operand<DT> load_operand(const typename Elem<DT>::type *p, int k, int len, bool vec)
+__device__ __forceinline__ Raw<DT> load_raw_masked(const typename Elem<DT>::type *p, int k, int len)
+{
+    Raw<DT> r;
+    if constexpr (DT == BCONV_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.v[i >> 2][i & 3] = k + i < len ? __float_as_uint(p[i]) : 0u;
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = k + 2 * i < len ? h[2 * i] : 0u, b = k + 2 * i + 1 < len ? h[2 * i + 1] : 0u;
+            r.v[0][i] = a | (b << 16);
+        }
+    }
+    return r;
+}
+
+template <int DT> __device__ __forceinline__ Operand<DT> to_operand(const Raw<DT> &r)
 {
     Operand<DT> o;
     if constexpr (DT == BCONV_F32) {
-        float v[8];
-        if (vec && k + 8 <= len) {
-            const f32x4 a = *reinterpret_cast<const f32x4 *>(p), b = *reinterpret_cast<const f32x4 *>(p + 4);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = a[i];
-                v[4 + i] = b[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = k + i < len ? p[i] : 0.0f;
-        }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             uint32_t h0, m0, l0, h1, m1, l1;
-            split3(v[2 * i], h0, m0, l0);
-            split3(v[2 * i + 1], h1, m1, l1);
+            split3(__uint_as_float(r.v[i >> 1][2 * (i & 1)]), h0, m0, l0);
+            split3(__uint_as_float(r.v[i >> 1][2 * (i & 1) + 1]), h1, m1, l1);
             o.part[0][i] = pack_hi16(h0, h1);
             o.part[1][i] = pack_hi16(m0, m1);
             o.part[2][i] = pack_hi16(l0, l1);
         }
     } else {
-        if (vec && k + 8 <= len) {
-            o.part[0] = *reinterpret_cast<const u32x4 *>(p);
-        } else {
-            const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t a = k + 2 * i < len ? h[2 * i] : 0u, b = k + 2 * i + 1 < len ? h[2 * i + 1] : 0u;
-                o.part[0][i] = a | (b << 16);
-            }
-        }
+        o.part[0] = r.v[0];
     }
     return o;
+}
+
+// 8 consecutive elements at p (offset k of a row of length len) as an operand;
+// elements at or past len are 0.  `vec`: p is 16-byte aligned for k % 8 == 0.
+template <int DT>
+__device__ __forceinline__ Operand<DT> load_operand(const typename Elem<DT>::type *p, int k, int len, bool vec)
+{
+    return to_operand<DT>(vec && k + 8 <= len ? load_raw<DT>(p) : load_raw_masked<DT>(p, k, len));
 }
 
 template <int DT> __device__ __forceinline__ typename Elem<DT>::type round_to(float x)

@@ -186,11 +186,31 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
     long long first[RT];
 #pragma unroll
     for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
+    // Lanes of columns past the last row load nothing: their operands stay what
+    // they are, and so do only their own, unused results.
+    const T *xr[NT];
+    bool real[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int m = m0 + t * 16 + row;
+        real[t] = m < a.m;
+        xr[t] = static_cast<const T *>(a.x) + (real[t] ? (long long)m * a.ldx : 0) + lg * 8;
+    }
+    Raw<DT> xf[UNROLL][NT][4];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) xf[u][t][s].v[i] = u32x4{0, 0, 0, 0};
+    // chunks whose columns are read in whole 16-byte loads
+    const int whole = a.vec ? a.k / kChunk : 0;
 
     for (int c0 = wave; c0 < a.chunks; c0 += WAVES * UNROLL) {
         u32x4 w[UNROLL][RT];
         Scales<DT, ZP, STEPS> sc[UNROLL][RT];
-        Operand<DT> xf[UNROLL][4][NT];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int c = c0 + u * WAVES;
@@ -203,16 +223,15 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
             }
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
-                const int m = m0 + t * 16 + row;
-                const T *xr = static_cast<const T *>(a.x) + (long long)m * a.ldx;
+                const T *p = xr[t] + c * kChunk;
+                if (real[t]) {
+                    if (c < whole) {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int k = c * kChunk + s * 32 + lg * 8;
-                    if (m < a.m && k < a.k) {
-                        xf[u][s][t] = load_operand<DT>(xr + k, k, a.k, a.vec != 0);
+                        for (int s = 0; s < 4; ++s) xf[u][t][s] = load_raw<DT>(p + s * 32);
                     } else {
 #pragma unroll
-                        for (int p = 0; p < kSplit<DT>; ++p) xf[u][s][t].part[p] = u32x4{0, 0, 0, 0};
+                        for (int s = 0; s < 4; ++s)
+                            xf[u][t][s] = load_raw_masked<DT>(p + s * 32, c * kChunk + s * 32 + lg * 8, a.k);
                     }
                 }
             }
@@ -220,7 +239,12 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             if (c0 + u * WAVES >= a.chunks) break;
-            chunk_product<DT, ZP, STEPS, RT, NT>(w[u], xf[u], sc[u], bits, acc);
+            Operand<DT> op[4][NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int s = 0; s < 4; ++s) op[s][t] = to_operand<DT>(xf[u][t][s]);
+            chunk_product<DT, ZP, STEPS, RT, NT>(w[u], op, sc[u], bits, acc);
         }
     }
 #pragma unroll
@@ -240,10 +264,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
     }
 }
 
-// ------------------------------------------------------------------ many rows
-
-// What the product of many rows takes besides Q4Args: x laid out as operands
-// and the partial sums of the splits.
+// What the products that add up splits of the inputs take besides Q4Args: the
+// partial sums, and for many rows x laid out as operands.
 struct Q4Many {
     u32x4 *xp;       // [column tiles][chunks * 4][parts][64]
     float *xs;       // bf16: [column tiles][chunks][groups a chunk][16], -sum x (times 24 without zero points)
@@ -252,6 +274,119 @@ struct Q4Many {
     int padded_n;
     int row_blocks, col_blocks, splits;
 };
+
+// ------------------------------------------------------------------ up to 16 rows, sliced inputs
+
+constexpr int kSliceWaves = 8, kSliceRows = 2;
+// chunks a slice holds at most: 64 KiB of operands, 96 in fp32
+constexpr int most_slice(int dtype) { return dtype == BCONV_F32 ? 8 : 16; }
+
+// Up to 16 rows of x through a layer whose codes outweigh the join of partial
+// sums.  A workgroup takes one slice of the inputs and 16 x 2 x 8 outputs: x's
+// slice is brought to LDS as operands once for its 16 output tiles (read from
+// global memory by every tile, it would be several times the codes' bytes),
+// then the waves stream codes with no barrier between them.
+template <int DT, bool ZP, int STEPS>
+__global__ __launch_bounds__(kSliceWaves * 64) void q4_slice_kernel(Q4Args a, Q4Many q)
+{
+    typedef typename Elem<DT>::type T;
+    constexpr int RT = kSliceRows, P = kSplit<DT>, G = 4 / STEPS;
+    extern __shared__ u32x4 lds[];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int row = lane & 15, lg = lane >> 4;
+    const int split = blockIdx.x % q.splits, rb = blockIdx.x / q.splits;
+    const int c_begin = (int)((long long)a.chunks * split / q.splits), c_end = (int)((long long)a.chunks * (split + 1) / q.splits);
+    u32x4 *xl = lds;                                                                  // [chunk][4][P][64]
+    float *xs = reinterpret_cast<float *>(lds + (long long)(c_end - c_begin) * 4 * P * 64);  // [chunk][G][16]
+    const int tile0 = (rb * kSliceWaves + wave) * RT;
+    const CodeBits bits = code_bits<DT>();
+    long long first[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
+
+    u32x4 w[2][RT];
+    Scales<DT, ZP, STEPS> sc[2][RT];
+    auto fetch = [&](int b, int c) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const long long tc = first[r] + c;
+            w[b][r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
+            sc[b][r].load(a.scales + tc * G * 16, ZP ? a.zeros + tc * G * 16 : nullptr, lane);
+        }
+    };
+    if (c_begin < c_end) fetch(0, c_begin);
+    if (c_begin + 1 < c_end) fetch(1, c_begin + 1);
+
+    const bool real = row < a.m;
+    const T *xr = static_cast<const T *>(a.x) + (real ? (long long)row * a.ldx : 0);
+    for (int g = wave; g < (c_end - c_begin) * G; g += kSliceWaves) {
+        Operand<DT> o[STEPS];
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+            const int k = (c_begin * 4 + g * STEPS + s) * 32 + lg * 8;
+            if (real && k < a.k) {
+                o[s] = load_operand<DT>(xr + k, k, a.k, a.vec != 0);
+            } else {
+#pragma unroll
+                for (int p = 0; p < P; ++p) o[s].part[p] = u32x4{0, 0, 0, 0};
+            }
+        }
+        f32x4 sum = {0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s) {
+#pragma unroll
+            for (int p = 0; p < P; ++p) xl[((g * STEPS + s) * P + p) * 64 + lane] = o[s].part[p];
+            if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(bf16_const(ZP ? -1.0f : -24.0f), o[s], sum);
+        }
+        if (DT == BCONV_BF16 && lane < 16) xs[g * 16 + lane] = sum[0];
+    }
+    __syncthreads();
+
+    f32x4 acc[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
+    auto product = [&](int b, int c) {
+        const int at = c - c_begin;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const float off = DT == BCONV_BF16 ? xs[(at * G + g) * 16 + row] : 0.0f;
+            f32x4 d[RT];
+#pragma unroll
+            for (int r = 0; r < RT; ++r) d[r] = sc[b][r].start(g, off);
+#pragma unroll
+            for (int s = 0; s < STEPS; ++s) {
+                Operand<DT> x;
+#pragma unroll
+                for (int p = 0; p < P; ++p) x.part[p] = xl[((at * 4 + g * STEPS + s) * P + p) * 64 + lane];
+#pragma unroll
+                for (int r = 0; r < RT; ++r)
+                    d[r] = mfma_parts<DT>(decode<DT>(w[b][r][g * STEPS + s], sc[b][r].zero(g), bits), x, d[r]);
+            }
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sc[b][r].scale(g, i), d[r][i], acc[r][i]);
+        }
+    };
+    for (int c = c_begin; c < c_end; c += 2) {
+        product(0, c);
+        if (c + 2 < c_end) fetch(0, c + 2);
+        if (c + 1 < c_end) {
+            product(1, c + 1);
+            if (c + 3 < c_end) fetch(1, c + 3);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int o0 = (tile0 + r) * 16 + lg * 4;
+        if (q.splits > 1)
+            *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * 16 + row) * q.padded_n + o0) = acc[r];
+        else if (real && o0 < a.n)
+            store_outputs<DT>(a, row, o0, acc[r]);
+    }
+}
+
+// ------------------------------------------------------------------ many rows
 
 // x as operands, a wave a (16 rows, group) pair: converted, split and padded
 // with zeros once instead of once per output tile, with the group's sum that
@@ -287,18 +422,27 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4Args a, Q4Many q)
 }
 
 constexpr int kManyRows = 4;  // output tiles a wave
-// column tiles a wave: 64 rows of x, or 32 in fp32, whose operands are three parts
-template <int DT> constexpr int kManyCols = DT == BCONV_F32 ? 2 : 4;
+
+// Column tiles a wave takes at most: 64 rows of x, or 32 in fp32, whose
+// operands are three parts.
+constexpr int most_cols(int dtype) { return dtype == BCONV_F32 ? 2 : 4; }
 
 // A workgroup takes 128 outputs and 2 NT column tiles, its four waves a
-// quarter each.  The columns' operands go to LDS, a chunk ahead, by loads that
-// pass no registers; the codes go to registers, a chunk ahead too.
+// quarter each.  Everything the waves share (the columns' operands and sums,
+// scales and zero points) goes to LDS a chunk ahead, by loads that pass no
+// registers; the codes go to registers, a chunk ahead too.
 template <int DT, bool ZP, int STEPS, int NT>
 __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q4Args a, Q4Many q)
 {
-    constexpr int RT = kManyRows, P = kSplit<DT>, UNITS = 2 * NT * 4 * P;  // 1 KiB units of a stage
-    constexpr int per_chunk = 4 / STEPS;
-    __shared__ u32x4 stage[2][UNITS * 64];
+    constexpr int RT = kManyRows, P = kSplit<DT>, G = 4 / STEPS;
+    constexpr int UNITS = 2 * NT * 4 * P;  // KiB of operands a chunk
+    struct Stage {
+        u32x4 x[UNITS * 64];
+        uint32_t scales[2 * RT * G * 8];                      // [tile][group][16] fp16
+        float xs[DT == BCONV_BF16 ? 2 * NT * G * 16 : 1];     // [column tile][group][16]
+        uint32_t zeros[ZP ? 2 * RT * G * 4 : 1];              // [tile][group][16] bytes
+    };
+    __shared__ Stage stage[2];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int row = lane & 15, lg = lane >> 4;
     // Blocks go to the XCDs in turn: the splits of the inputs come first, so
@@ -308,39 +452,51 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
     id /= q.splits;
     const int cb = id % q.col_blocks, rb = id / q.col_blocks;
     const int c_begin = (int)((long long)a.chunks * split / q.splits), c_end = (int)((long long)a.chunks * (split + 1) / q.splits);
-    const int tile0 = rb * 2 * RT + (wave >> 1) * RT, col0 = cb * 2 * NT;
-    const int mine = col0 + (wave & 1) * NT;
+    const int tile0 = rb * 2 * RT, col0 = cb * 2 * NT;
+    const int my_row = (wave >> 1) * RT, my_col = (wave & 1) * NT;
     const CodeBits bits = code_bits<DT>();
 
+    auto tile_chunk = [&](int tile, int c) { return (long long)(tile < a.tiles ? tile : a.tiles - 1) * a.chunks + c; };
+    typedef __attribute__((address_space(3))) void *Lds;
     auto request = [&](int c) {
+        Stage &st = stage[c & 1];
 #pragma unroll
         for (int i = 0; i < UNITS / 4; ++i) {
             const int u = i * 4 + wave, t = u / (4 * P), rest = u % (4 * P);
             const u32x4 *src = q.xp + (((long long)(col0 + t) * a.chunks + c) * 4 * P + rest) * 64 + lane;
-            __builtin_amdgcn_global_load_lds((const void *)src,
-                                             (__attribute__((address_space(3))) void *)(&stage[c & 1][u * 64]), 16, 0, 0);
+            __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.x[u * 64]), 16, 0, 0);
         }
-    };
-    long long first[RT];
+        // 4 bytes a lane; a tile's part of a chunk is consecutive
 #pragma unroll
-    for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
-    u32x4 w[RT], wn[RT];
-    Scales<DT, ZP, STEPS> sc[RT], scn[RT];
-    float xs[per_chunk][NT], xsn[per_chunk][NT];
-    auto fetch = [&](int c) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const long long tc = first[r] + c;
-            wn[r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
-            scn[r].load(a.scales + tc * per_chunk * 16, ZP ? a.zeros + tc * per_chunk * 16 : nullptr, lane);
+        for (int i = 0; i < G; ++i) {
+            if ((i & 3) == wave) {
+                const int e = i * 64 + lane, t = e / (G * 8);
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.scales) + tile_chunk(tile0 + t, c) * G * 8 + e % (G * 8);
+                __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.scales[i * 64]), 4, 0, 0);
+            }
+            if (ZP && ((i + 1) & 3) == wave && lane < 32) {
+                const int e = i * 32 + lane, t = e / (G * 4);
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.zeros) + tile_chunk(tile0 + t, c) * G * 4 + e % (G * 4);
+                __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.zeros[i * 32]), 4, 0, 0);
+            }
         }
         if constexpr (DT == BCONV_BF16) {
+            constexpr int LOADS = 2 * NT * G * 16 / 64 > 0 ? 2 * NT * G * 16 / 64 : 1;
 #pragma unroll
-            for (int g = 0; g < per_chunk; ++g)
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    xsn[g][t] = q.xs[(((long long)(mine + t) * a.chunks + c) * per_chunk + g) * 16 + row];
+            for (int i = 0; i < LOADS; ++i) {
+                const int e = i * 64 + lane, t = e / (G * 16);
+                if (((i + 2) & 3) == wave && e < 2 * NT * G * 16) {
+                    const float *src = q.xs + ((long long)(col0 + t) * a.chunks + c) * G * 16 + e % (G * 16);
+                    __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.xs[i * 64]), 4, 0, 0);
+                }
+            }
         }
+    };
+    u32x4 w[RT], wn[RT];
+    auto fetch = [&](int c) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+            wn[r] = *reinterpret_cast<const u32x4 *>(a.codes + tile_chunk(tile0 + my_row + r, c) * 256 + lane * 4);
     };
     f32x4 acc[RT][NT];
 #pragma unroll
@@ -356,54 +512,68 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
         __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xf << 8));  // vmcnt(0): this chunk's operands and codes are here
         __syncthreads();                                          // in every wave, and the other stage is read
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            w[r] = wn[r];
-            sc[r] = scn[r];
-        }
-#pragma unroll
-        for (int g = 0; g < per_chunk; ++g)
-#pragma unroll
-            for (int t = 0; t < NT; ++t) xs[g][t] = xsn[g][t];
+        for (int r = 0; r < RT; ++r) w[r] = wn[r];
         if (c + 1 < c_end) {
             request(c + 1);
             fetch(c + 1);
         }
-        const u32x4 *st = &stage[c & 1][(wave & 1) * NT * 4 * P * 64 + lane];
+        const Stage &st = stage[c & 1];
 #pragma unroll
-        for (int g = 0; g < per_chunk; ++g) {
-            f32x4 d[RT][NT];
+        for (int g = 0; g < G; ++g) {
+            // the group's columns stay in registers for the four output tiles
+            Operand<DT> b[STEPS][NT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int t = 0; t < NT; ++t) d[r][t] = sc[r].start(g, xs[g][t]);
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                Operand<DT> b[NT];
+            for (int s = 0; s < STEPS; ++s)
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) b[t].part[p] = st[((t * 4 + g * STEPS + s) * P + p) * 64];
+                    for (int p = 0; p < P; ++p)
+                        b[s][t].part[p] = st.x[(((my_col + t) * 4 + g * STEPS + s) * P + p) * 64 + lane];
+            float xs[NT];
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    const u32x4 k = decode<DT>(w[r][g * STEPS + s], sc[r].zero(g), bits);
+            for (int t = 0; t < NT; ++t) xs[t] = DT == BCONV_BF16 ? st.xs[((my_col + t) * G + g) * 16 + row] : 0.0f;
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) d[r][t] = mfma_parts<DT>(k, b[t], d[r][t]);
+            for (int r = 0; r < RT; ++r) {
+                typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+                const int at = (my_row + r) * G + g;
+                const f16x4 s4 = *reinterpret_cast<const f16x4 *>(&st.scales[at * 8 + lg * 2]);
+                int z = 8;
+                float z4[4];
+                if constexpr (ZP) {
+                    if constexpr (DT == BCONV_BF16) {
+                        const uint32_t zz = st.zeros[at * 4 + lg];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z4[i] = (float)(16 + ((zz >> (8 * i)) & 255u));
+                    } else {
+                        z = reinterpret_cast<const uint8_t *>(st.zeros)[at * 16 + row];
+                    }
                 }
-            }
+                const Zero<DT> zero(z);
+                f32x4 d[NT];
 #pragma unroll
-            for (int r = 0; r < RT; ++r)
+                for (int t = 0; t < NT; ++t) {
+                    if constexpr (DT == BCONV_BF16 && ZP) d[t] = f32x4{z4[0] * xs[t], z4[1] * xs[t], z4[2] * xs[t], z4[3] * xs[t]};
+                    else d[t] = f32x4{xs[t], xs[t], xs[t], xs[t]};
+                }
+#pragma unroll
+                for (int s = 0; s < STEPS; ++s) {
+                    const u32x4 k = decode<DT>(w[r][g * STEPS + s], zero, bits);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t) d[t] = mfma_parts<DT>(k, b[s][t], d[t]);
+                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(sc[r].scale(g, i), d[r][t][i], acc[r][t][i]);
+                    for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf((float)s4[i], d[t][i], acc[r][t][i]);
+            }
         }
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int o0 = (tile0 + r) * 16 + lg * 4;
+        const int o0 = (tile0 + my_row + r) * 16 + lg * 4;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            const int m = (mine + t) * 16 + row;
+            const int m = (col0 + my_col + t) * 16 + row;
             if (q.splits > 1)
                 *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * q.col_tiles * 16 + m) * q.padded_n + o0) = acc[r][t];
             else if (m < a.m && o0 < a.n)
@@ -430,34 +600,48 @@ __global__ __launch_bounds__(256) void q4_reduce_kernel(Q4Args a, Q4Many q)
 // ------------------------------------------------------------------ dispatch
 
 // Which kernel a number of rows takes, and what it needs of the workspace.
+enum class Q4Kind { Few, Slice, Many };
 struct Q4Plan {
-    bool many;
-    int cols;  // column tiles a workgroup (many) or a wave (few)
+    Q4Kind kind;
+    int nt;    // many: column tiles a wave
     Q4Many q;
     size_t xs_offset, sums_offset, bytes;
 };
 
-constexpr int kFewRows = 64;  // rows up to which the waves of a workgroup split the inputs
-
 Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, int cus)
 {
     Q4Plan p{};
-    const char *ev = getenv("Q4_FEW");
-    p.many = rows > (ev ? atoi(ev) : kFewRows);
-    if (!p.many) return p;
-    const int nt = dtype == BCONV_F32 ? kManyCols<BCONV_F32> : kManyCols<BCONV_BF16>;
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    auto env = [](const char *n, int d) { const char *e = getenv(n); return e ? atoi(e) : d; };
+    const long long codes = (long long)tiles * chunks;  // KiB
+    p.kind = rows > env("Q4_FEW", 16) ? Q4Kind::Many : rows >= env("Q4_SLICE", 2) && codes >= env("Q4_CODES", 4096) ? Q4Kind::Slice : Q4Kind::Few;
+    if (p.kind == Q4Kind::Few) return p;
+    if (p.kind == Q4Kind::Slice) {
+        const int per_block = kSliceWaves * kSliceRows;
+        p.q.col_tiles = p.q.col_blocks = 1;
+        p.q.row_blocks = (tiles + per_block - 1) / per_block;
+        p.q.padded_n = p.q.row_blocks * per_block * 16;
+        long long splits = ((long long)env("Q4_T", 2) * cus + p.q.row_blocks - 1) / p.q.row_blocks;
+        if (splits > chunks / 4) splits = chunks / 4;
+        const int least = (chunks + most_slice(dtype) - 1) / most_slice(dtype);
+        if (splits < least) splits = least;
+        p.q.splits = (int)splits;
+        p.bytes = splits > 1 ? (size_t)splits * 16 * p.q.padded_n * 4 : 0;
+        return p;
+    }
+    int nt = most_cols(dtype);
+    while (nt > 1 && 16 * nt >= rows) nt /= 2;
+    p.nt = nt;
     const int parts = dtype == BCONV_F32 ? 3 : 1;
     p.q.col_blocks = (rows + 32 * nt - 1) / (32 * nt);
     p.q.col_tiles = p.q.col_blocks * 2 * nt;
     p.q.row_blocks = (tiles + 2 * kManyRows - 1) / (2 * kManyRows);
     p.q.padded_n = p.q.row_blocks * 2 * kManyRows * 16;
     const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks;
-    long long splits = (2LL * cus + blocks - 1) / blocks;
-    if (const char *e2 = getenv("Q4_SPLITS")) splits = atoi(e2);
-    if (splits > 8) splits = 8;
+    long long splits = ((long long)env("Q4_T", 2) * cus + blocks - 1) / blocks;
+    if (splits > env("Q4_MAXS", 8)) splits = env("Q4_MAXS", 8);
     if (splits > chunks / 4) splits = chunks / 4;
     p.q.splits = splits < 1 ? 1 : (int)splits;
-    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     p.xs_offset = up((size_t)p.q.col_tiles * chunks * 4 * parts * 1024);
     p.sums_offset = p.xs_offset + (dtype == BCONV_BF16 ? up((size_t)p.q.col_tiles * chunks * per_chunk * 16 * 4) : 0);
     p.bytes = p.sums_offset + (p.q.splits > 1 ? (size_t)p.q.splits * p.q.col_tiles * 16 * p.q.padded_n * 4 : 0);
@@ -475,16 +659,31 @@ hipError_t run_few(const Q4Args &a, hipStream_t s)
 template <int DT, bool ZP, int STEPS>
 hipError_t run_linear(const Q4Args &a, const Q4Plan &p, hipStream_t s)
 {
-    if (p.many) {
+    const long long outs = (long long)((a.n + 3) / 4) * a.m;
+    if (p.kind == Q4Kind::Slice) {
+        const int held = (a.chunks + p.q.splits - 1) / p.q.splits;
+        const size_t lds = (size_t)held * (4 * kSplit<DT> * 1024 + (4 / STEPS) * 64);
+        hipLaunchKernelGGL((q4_slice_kernel<DT, ZP, STEPS>), dim3((unsigned)(p.q.row_blocks * p.q.splits)),
+                           dim3(kSliceWaves * 64), lds, s, a, p.q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.q.splits == 1) return e;
+        hipLaunchKernelGGL((q4_reduce_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
+        return hipGetLastError();
+    }
+    if (p.kind == Q4Kind::Many) {
         const long long packs = (long long)p.q.col_tiles * a.chunks * (4 / STEPS);
         hipLaunchKernelGGL((q4_pack_kernel<DT, ZP, STEPS>), dim3((unsigned)((packs + 3) / 4)), dim3(256), 0, s, a, p.q);
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks * p.q.splits;
-        hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, kManyCols<DT>>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
+        if (p.nt == 1)
+            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, 1>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
+        else if (p.nt == 2)
+            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
+        else
+            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, most_cols(DT)>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
         e = hipGetLastError();
         if (e != hipSuccess || p.q.splits == 1) return e;
-        const long long outs = (long long)((a.n + 3) / 4) * a.m;
         hipLaunchKernelGGL((q4_reduce_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
         return hipGetLastError();
     }

@@ -19,69 +19,81 @@ import numpy as np
 
 from . import _binding as B
 
-_DTYPES: dict = {}
+_torch = None      # the torch module, once a call needs it
+_DTYPES: dict = {}  # torch dtype -> bconv_dtype_t
 
 
-def _dtype_codes() -> dict:
-    if not _DTYPES:
-        import torch
-        _DTYPES.update({torch.float32: B.BCONV_F32, torch.float16: B.BCONV_F16, torch.bfloat16: B.BCONV_BF16})
-    return _DTYPES
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+    _DTYPES.update({torch.float32: B.BCONV_F32, torch.float16: B.BCONV_F16, torch.bfloat16: B.BCONV_BF16})
+    # the current stream's handle without a Stream object around it, where torch has that
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                          lambda index: torch.cuda.current_stream(index).cuda_stream)
+    _torch = torch
+    return torch
 
 
 def _dtype_code(t, name: str) -> int:
-    code = _dtype_codes().get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise ValueError(f"{name}: dtype {t.dtype} is not one of torch.float32, torch.float16, torch.bfloat16")
     return code
 
 
 def _need_tensor(t, name: str) -> None:
-    import torch
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch.Tensor):
         raise ValueError(f"{name}: a torch tensor is required, got {type(t).__name__}")
 
 
 def _need_cuda(t, name: str, device=None) -> None:
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name}: a CUDA (HIP) device tensor is required, got device {t.device}")
     if device is not None and t.device != device:
         raise ValueError(f"{name}: on {t.device}, not on {device}")
 
 
-def _need_int32(t, name: str, shape, device) -> None:
-    """A contiguous int32 device tensor of exactly ``shape``."""
-    import torch
-    _need_tensor(t, name)
-    if t.dtype != torch.int32:
-        raise ValueError(f"{name}: dtype {t.dtype} is not torch.int32")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: the tensor must be contiguous")
-    _need_cuda(t, name, device)
-
-
 def _need_dense(t, name: str, shape, dtype, device) -> None:
+    """A contiguous device tensor of exactly ``shape`` and ``dtype``."""
     _need_tensor(t, name)
     if t.dtype != dtype:
         raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)} != {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: the tensor must be contiguous")
     _need_cuda(t, name, device)
+
+
+def _need_ints(t, name: str, count: int, device) -> None:
+    """A contiguous int32 device tensor [count]."""
+    if not (isinstance(t, _torch.Tensor) and t.dtype is _torch.int32 and t.dim() == 1 and t.numel() == count
+            and t.is_contiguous() and t.is_cuda and t.get_device() == device.index):
+        _need_dense(t, name, (count,), _torch.int32, device)
 
 
 def _need_rows(t, name: str, heads: int, dim: int) -> int:
     """[tokens, heads, dim] with contiguous channels; token and head strides
     are free.  Returns the tokens."""
     _need_tensor(t, name)
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name}: shape {tuple(t.shape)} is not (tokens, {heads}, {dim})")
-    if dim > 1 and t.stride(2) != 1:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
+        raise ValueError(f"{name}: shape {tuple(shape)} is not (tokens, {heads}, {dim})")
+    if t.stride(2) != 1 and dim > 1:
         raise ValueError(f"{name}: channels must be contiguous (stride {t.stride(2)})")
-    return t.shape[0]
+    return shape[0]
+
+
+def _need_table(t) -> tuple:
+    """(requests, width, row stride) of a block table."""
+    _need_tensor(t, "block_table")
+    if t.dtype != _torch.int32 or t.dim() != 2:
+        raise ValueError(f"block_table: {t.dtype} of shape {tuple(t.shape)} is not int32 (requests, width)")
+    requests, width = t.shape
+    stride = t.stride()
+    if width > 1 and stride[1] != 1 or requests > 1 and stride[0] < width:
+        raise ValueError("block_table: rows must be contiguous and must not overlap")
+    return requests, width, stride[0] if requests > 1 else max(width, 1)
 
 
 def _need_workspace(ws, need: int, device) -> None:
@@ -96,8 +108,7 @@ def _need_workspace(ws, need: int, device) -> None:
 
 @contextlib.contextmanager
 def _on(device, stream):
-    import torch
-    with torch.cuda.device(device), torch.cuda.stream(stream):
+    with _torch.cuda.device(device), _torch.cuda.stream(stream):
         yield
 
 
@@ -107,16 +118,13 @@ _STAY = contextlib.nullcontext()
 def _place(device, stream):
     """(context to allocate and launch in, raw stream): nothing to enter when
     the call goes to the current device's current stream."""
-    import torch
     if stream is None:
-        s = torch.cuda.current_stream(device)
-        if device.index == torch.cuda.current_device():
-            return _STAY, s.cuda_stream
-    else:
-        if stream.device != device:
-            raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
-        s = stream
-    return _on(device, s), s.cuda_stream
+        if device.index == _torch.cuda.current_device():
+            return _STAY, _raw_stream(device.index)
+        stream = _torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, the tensors are on {device}")
+    return _on(device, stream), stream.cuda_stream
 
 
 def pack_codes(codes) -> np.ndarray:
@@ -147,6 +155,7 @@ class Q4Linear:
     def __init__(self, *, in_features: int, out_features: int, weight_words, scales, zeros=None, bias=None,
                  group: int = 128):
         self.handle = None
+        self._needs: dict = {}  # workspace bytes by (rows, type)
         if group not in (32, 64, 128):
             raise ValueError(f"group: {group} is not 32, 64 or 128")
         groups = -(-in_features // group)
@@ -165,42 +174,48 @@ class Q4Linear:
         self.handle = B.bconv_q4_linear_create(in_features, out_features, group, weight_words, scales, zeros, bias)
 
     def workspace_bytes(self, rows: int, dtype) -> int:
-        return B.bconv_q4_linear_workspace_size(self.handle, rows, _dtype_codes()[dtype])
+        if _torch is None:
+            _load_torch()
+        return B.bconv_q4_linear_workspace_size(self.handle, rows, _DTYPES[dtype])
 
     def forward(self, x, out=None, workspace=None, stream=None):
         """``[..., in_features]`` -> ``[..., out_features]`` of the same type.
         A 2-d x or out may have any row stride; others must be contiguous."""
-        import torch
+        if _torch is None:
+            _load_torch()
         _need_tensor(x, "input")
-        if x.dim() < 1 or x.shape[-1] != self.in_features:
-            raise ValueError(f"input: shape {tuple(x.shape)} does not end in {self.in_features}")
+        shape = x.shape
+        if not shape or shape[-1] != self.in_features:
+            raise ValueError(f"input: shape {tuple(shape)} does not end in {self.in_features}")
         code = _dtype_code(x, "input")
         rows, ldx = _row_stride(x, "input")
-        device = x.device
         _need_cuda(x, "input")
+        device = x.device
         place, raw = _place(device, stream)
         with place:
+            out_shape = (*shape[:-1], self.out_features)
             if out is None:
-                out = torch.empty(x.shape[:-1] + (self.out_features,), dtype=x.dtype, device=device)
+                out = x.new_empty(out_shape)
                 ldy = self.out_features
             else:
                 _need_tensor(out, "output")
-                if tuple(out.shape) != tuple(x.shape[:-1]) + (self.out_features,):
-                    raise ValueError(f"output: shape {tuple(out.shape)} != "
-                                     f"{tuple(x.shape[:-1]) + (self.out_features,)}")
+                if tuple(out.shape) != out_shape:
+                    raise ValueError(f"output: shape {tuple(out.shape)} != {out_shape}")
                 if out.dtype != x.dtype:
                     raise ValueError(f"output: dtype {out.dtype} is not {x.dtype}")
                 _need_cuda(out, "output", device)
                 ldy = _row_stride(out, "output")[1]
             if rows == 0:
                 return out
-            need = B.bconv_q4_linear_workspace_size(self.handle, rows, code)
-            if workspace is None:
-                if need:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            else:
+            need = self._needs.get((rows, code))
+            if need is None:
+                need = self._needs[rows, code] = B.bconv_q4_linear_workspace_size(self.handle, rows, code)
+            if workspace is not None:
                 _need_workspace(workspace, need, device)
-            B.bconv_q4_linear_forward(self.handle, raw, rows, code, x, ldx, out, ldy, workspace, need)
+            elif need:
+                workspace = _torch.empty(need, dtype=_torch.uint8, device=device)
+            B.bconv_q4_linear_forward(self.handle, raw, rows, code, x.data_ptr(), ldx, out.data_ptr(), ldy,
+                                      workspace.data_ptr() if need else None, need)
         return out
 
     def close(self):
@@ -235,7 +250,7 @@ class KV4Cache:
 
     def __init__(self, num_blocks: int, block_size: int, kv_heads: int, head_dim: int, *, group: int = 64,
                  device=None):
-        import torch
+        torch = _torch or _load_torch()
         self.desc = B.bconv_kv4_desc_t(num_blocks, block_size, kv_heads, head_dim, group)
         self.layout = B.bconv_kv4_layout(self.desc)
         self.num_blocks, self.block_size, self.kv_heads = num_blocks, block_size, kv_heads
@@ -243,36 +258,40 @@ class KV4Cache:
         self.pool = torch.zeros(self.layout.pool_bytes, dtype=torch.uint8, device=device or "cuda")
         _need_cuda(self.pool, "device")
         self.device = self.pool.device
+        self._needs: dict = {}  # workspace bytes of attention by its host arguments
 
     def append(self, k, v, slots, *, values: bool = False, k_out=None, v_out=None, stream=None):
         """Writes new rows ``[tokens, kv_heads, head_dim]`` at ``slots`` (int32
         ``[tokens]``, block * block_size + offset; slots outside the pool are
         skipped).  With ``values`` (or ``k_out`` / ``v_out``) returns the pair of
         dense tensors that the cache now stands for."""
-        import torch
-        tokens = _need_rows(k, "k", self.kv_heads, self.head_dim)
-        if _need_rows(v, "v", self.kv_heads, self.head_dim) != tokens:
+        torch = _torch or _load_torch()
+        heads, dim, device = self.kv_heads, self.head_dim, self.device
+        tokens = _need_rows(k, "k", heads, dim)
+        if _need_rows(v, "v", heads, dim) != tokens:
             raise ValueError(f"v: {v.shape[0]} tokens, k has {tokens}")
         code = _dtype_code(k, "k")
         if v.dtype != k.dtype:
             raise ValueError(f"v: dtype {v.dtype} is not {k.dtype}")
-        _need_cuda(k, "k", self.device)
-        _need_cuda(v, "v", self.device)
-        _need_int32(slots, "slots", (tokens,), self.device)
-        place, raw = _place(self.device, stream)
+        _need_cuda(k, "k", device)
+        _need_cuda(v, "v", device)
+        _need_ints(slots, "slots", tokens, device)
+        place, raw = _place(device, stream)
         with place:
-            shape = (tokens, self.kv_heads, self.head_dim)
+            shape = (tokens, heads, dim)
             if k_out is not None:
-                _need_dense(k_out, "k_out", shape, k.dtype, self.device)
+                _need_dense(k_out, "k_out", shape, k.dtype, device)
             elif values:
-                k_out = torch.empty(shape, dtype=k.dtype, device=self.device)
+                k_out = k.new_empty(shape)
             if v_out is not None:
-                _need_dense(v_out, "v_out", shape, k.dtype, self.device)
+                _need_dense(v_out, "v_out", shape, k.dtype, device)
             elif values:
-                v_out = torch.empty(shape, dtype=k.dtype, device=self.device)
+                v_out = k.new_empty(shape)
             if tokens:
-                B.bconv_kv4_append(self.desc, raw, self.pool, tokens, code, k, k.stride()[:2], v, v.stride()[:2],
-                                   slots, k_out, v_out)
+                B.bconv_kv4_append(self.desc, raw, self.pool.data_ptr(), tokens, code, k.data_ptr(), k.stride()[:2],
+                                   v.data_ptr(), v.stride()[:2], slots.data_ptr(),
+                                   None if k_out is None else k_out.data_ptr(),
+                                   None if v_out is None else v_out.data_ptr())
         return (k_out, v_out) if k_out is not None or v_out is not None else None
 
     def attention(self, q, block_table, context_lens, *, q_start=None, max_q: Optional[int] = None,
@@ -287,27 +306,22 @@ class KV4Cache:
         bounds the context lengths (the table's width by default).  ``scale``
         defaults to ``head_dim ** -0.5``; ``window`` > 0 limits a query to that many
         last positions.  ``lse``: float32 ``[tokens, heads]`` to fill."""
-        import torch
+        torch = _torch or _load_torch()
         _need_tensor(q, "q")
-        if q.dim() != 3 or q.shape[1] % self.kv_heads or not q.shape[1]:
-            raise ValueError(f"q: shape {tuple(q.shape)} is not (tokens, a multiple of {self.kv_heads}, "
+        shape = q.shape
+        if len(shape) != 3 or shape[1] % self.kv_heads or not shape[1]:
+            raise ValueError(f"q: shape {tuple(shape)} is not (tokens, a multiple of {self.kv_heads}, "
                              f"{self.head_dim})")
-        tokens, heads = q.shape[0], q.shape[1]
+        tokens, heads, dim = shape
         _need_rows(q, "q", heads, self.head_dim)
         code = _dtype_code(q, "q")
         device = self.device
         _need_cuda(q, "q", device)
-        _need_tensor(block_table, "block_table")
-        if block_table.dtype != torch.int32 or block_table.dim() != 2:
-            raise ValueError(f"block_table: {block_table.dtype} of shape {tuple(block_table.shape)} is not int32 "
-                             "(requests, width)")
+        requests, width, stride = _need_table(block_table)
         _need_cuda(block_table, "block_table", device)
-        requests, width = block_table.shape
-        if width > 1 and block_table.stride(1) != 1 or requests > 1 and block_table.stride(0) < width:
-            raise ValueError("block_table: rows must be contiguous and must not overlap")
-        _need_int32(context_lens, "context_lens", (requests,), device)
+        _need_ints(context_lens, "context_lens", requests, device)
         if q_start is not None:
-            _need_int32(q_start, "q_start", (requests + 1,), device)
+            _need_ints(q_start, "q_start", requests + 1, device)
             if max_q is None:
                 max_q = max(1, tokens)
         else:
@@ -318,26 +332,31 @@ class KV4Cache:
         place, raw = _place(device, stream)
         with place:
             if out is None:
-                out = torch.empty((tokens, heads, self.head_dim), dtype=q.dtype, device=device)
+                out = q.new_empty(shape)
             else:
-                _need_dense(out, "out", (tokens, heads, self.head_dim), q.dtype, device)
+                _need_dense(out, "out", shape, q.dtype, device)
             if lse is not None:
                 _need_dense(lse, "lse", (tokens, heads), torch.float32, device)
             if not tokens or not requests:
                 return out
-            stride = block_table.stride(0) if requests > 1 else max(width, 1)
+            q_strides = q.stride()
             args = B.bconv_kv4_attention_t(
-                self.pool.data_ptr(), q.data_ptr(), q.stride(0), q.stride(1), out.data_ptr(),
+                self.pool.data_ptr(), q.data_ptr(), q_strides[0], q_strides[1], out.data_ptr(),
                 None if lse is None else lse.data_ptr(), block_table.data_ptr(), context_lens.data_ptr(),
                 None if q_start is None else q_start.data_ptr(), requests, tokens, max_q, heads, width, stride,
-                max_context, window, code, self.head_dim ** -0.5 if scale is None else scale)
-            need = B.bconv_kv4_attention_workspace_size(self.desc, args)
-            if workspace is None:
-                if need:
-                    workspace = torch.empty(need, dtype=torch.uint8, device=device)
-            else:
+                max_context, window, code, dim ** -0.5 if scale is None else scale)
+            key = (requests, tokens, max_q, heads, width, max_context, window, code, q_start is None)
+            need = self._needs.get(key)
+            if need is None:
+                need = B.bconv_kv4_attention_workspace_size(self.desc, args)
+                if len(self._needs) >= 4096:
+                    self._needs.clear()
+                self._needs[key] = need
+            if workspace is not None:
                 _need_workspace(workspace, need, device)
-            B.bconv_kv4_attention(self.desc, raw, args, workspace, need)
+            elif need:
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            B.bconv_kv4_attention(self.desc, raw, args, workspace.data_ptr() if need else None, need)
         return out
 
 
@@ -358,32 +377,27 @@ def build_block_tables(block_table, context_lens, new_lens, free_blocks, free_he
     ``tokens``: entries of the slot map, at least the sum of ``new_lens`` (the
     rest is padded with -1).  All tensors are int32 on one device; ``free_head``
     of the result beyond ``free_blocks`` says that blocks were missing."""
-    import torch
-    _need_tensor(block_table, "block_table")
-    if block_table.dtype != torch.int32 or block_table.dim() != 2:
-        raise ValueError(f"block_table: {block_table.dtype} of shape {tuple(block_table.shape)} is not int32 "
-                         "(requests, width)")
+    torch = _torch or _load_torch()
+    requests, width, stride = _need_table(block_table)
     _need_cuda(block_table, "block_table")
-    requests, width = block_table.shape
-    if width > 1 and block_table.stride(1) != 1 or requests > 1 and block_table.stride(0) < width:
-        raise ValueError("block_table: rows must be contiguous and must not overlap")
     device = block_table.device
-    _need_int32(context_lens, "context_lens", (requests,), device)
-    _need_int32(new_lens, "new_lens", (requests,), device)
+    _need_ints(context_lens, "context_lens", requests, device)
+    _need_ints(new_lens, "new_lens", requests, device)
     _need_tensor(free_blocks, "free_blocks")
-    _need_int32(free_blocks, "free_blocks", (free_blocks.numel(),), device)
-    _need_int32(free_head, "free_head", (1,), device)
+    free_count = free_blocks.numel()
+    _need_ints(free_blocks, "free_blocks", free_count, device)
+    _need_ints(free_head, "free_head", 1, device)
     if tokens < 0:
         raise ValueError(f"tokens: {tokens} is negative")
     place, raw = _place(device, stream)
     with place:
         # one allocation: q_start, lengths, free head, then the token arrays
         flat = torch.empty(2 * requests + 2 + 2 * tokens, dtype=torch.int32, device=device)
-        q_start, lens, head, slots, positions = flat.split((requests + 1, requests, 1, tokens, tokens))
-        stride = block_table.stride(0) if requests > 1 else max(width, 1)
+        q_start, lens, head, slots, positions = flat.split_with_sizes((requests + 1, requests, 1, tokens, tokens))
         base = flat.data_ptr()
-        B.bconv_block_tables(raw, requests, block_size, block_table, width, stride, context_lens, new_lens,
-                             free_blocks, free_blocks.numel(), free_head, base + 4 * (2 * requests + 1), tokens,
+        B.bconv_block_tables(raw, requests, block_size, block_table.data_ptr(), width, stride,
+                             context_lens.data_ptr(), new_lens.data_ptr(), free_blocks.data_ptr(), free_count,
+                             free_head.data_ptr(), base + 4 * (2 * requests + 1), tokens,
                              base + 4 * (2 * requests + 2), base + 4 * (2 * requests + 2 + tokens), base,
                              base + 4 * (requests + 1))
     return BlockTables(slots, positions, q_start, lens, head)
