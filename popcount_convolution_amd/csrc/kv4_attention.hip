@@ -18,11 +18,12 @@
 #include <cmath>
 #include <cstdlib>
 
+#include "internal.h"
 #include "kv4.h"
 
 namespace bconv {
 
-constexpr int kTile = 32;         // tokens a wave takes at a time
+constexpr int kTokens = 32;         // tokens a wave takes at a time
 constexpr float kLowest = -1e30f; // running maximum before the first visible token
 // How far a logit (base 2) may pass the running maximum before the sums are
 // rescaled: 2^8 of headroom costs fp32 sums nothing and saves most rescales.
@@ -37,13 +38,14 @@ struct AttnArgs {
     float *lse;
     const int *table, *context, *q_start;
     int requests, q_tokens, max_q, heads, ratio;
+    FastDiv by_ratio;
     int width;
     long long stride;
     int max_context, window;
     float scale_log2;  // |scale| log2 e
     uint32_t flip;     // sign bits to flip in q: those of a negative scale
     int vec;
-    int col_blocks, parts, part_tokens;  // part_tokens: a multiple of kTile
+    int col_blocks, parts, part_tokens;  // part_tokens: a multiple of kTokens
     float *part_o;                       // [column rows][parts][dim_padded]
     float2 *part_ml;                     // [column rows][parts]
     Kv4Geom g;
@@ -60,7 +62,7 @@ struct AttnShape {
 struct Span {
     int q0, n, j0, c0, c1;   // first query row, queries, first query's index, columns [c0, c1)
     int last;                // position of the request's query 0 (context - queries)
-    int t0, t1;              // tokens [t0, t1), t0 a multiple of kTile
+    int t0, t1;              // tokens [t0, t1), t0 a multiple of kTokens
     int low;                 // the first of them that any column sees
 };
 
@@ -91,12 +93,12 @@ __device__ __forceinline__ Span column_span(const AttnArgs &a, int req, int cb, 
     s.t0 = s.t1 = s.low = 0;
     s.j0 = 0;
     if (s.c0 < s.c1) {
-        s.j0 = s.c0 / a.ratio;
-        const int j1 = (s.c1 - 1) / a.ratio;
+        s.j0 = (int)fastdiv((uint32_t)s.c0, a.by_ratio);
+        const int j1 = (int)fastdiv((uint32_t)(s.c1 - 1), a.by_ratio);
         const int hi = s.last + j1;
         s.t1 = (hi < a.max_context - 1 ? hi : a.max_context - 1) + 1;
         s.low = first_seen(s.last + s.j0, a.window);
-        s.t0 = s.low & ~(kTile - 1);
+        s.t0 = s.low & ~(kTokens - 1);
         if (s.t1 < s.t0) s.t1 = s.t0;
     }
     return s;
@@ -169,74 +171,85 @@ template <int DT> __device__ __forceinline__ CodeBits value_bits()
     return DT == BCONV_F32 ? code_bits<DT>() : opaque_bits(0x000f000fu, 0x43004300u);  // bf16 128
 }
 
-// What a lane holds of 32 tokens: key words of its operand rows, value words of
-// its run of 8 tokens, and entries of the run's (s, b) tables, which the 16
-// lanes of a run share (entry = token of the run * GROUPS + group).
-template <int DP, int GROUPS> struct Tile {
-    static constexpr int STEPS = DP / 32;
-    static constexpr int VW = DP < 128 ? 1 : DP / 128;      // words of a value row's part (16 bits for DP = 64)
-    static constexpr int TABLE = (8 * GROUPS + 15) / 16;
-    uint32_t k[2][STEPS], v[8][VW], ks[TABLE], vs[TABLE];
-    bool known;  // the run's block exists
+// Where a lane's part of 32 tokens is.  Runs of 8 tokens never cross a block,
+// and the 32 tokens from t, a multiple of 32, lie in at most two: `first` and
+// `second` are the records of tokens t and t + 16 for the head.  Row r of S
+// tile u is token t + 8 (r / 4) + 4 u + r % 4: a lane's eight results are the run
+// of 8 tokens from t + 8 (lane / 16), whose values it decodes.
+struct Place {
+    const char *first, *second;
+    int at;  // token t in its block (0 where a block ends inside the tile)
+};
 
-    // Runs of 8 tokens never cross a block.  Row r of S tile u is token
-    // t + 8 (r / 4) + 4 u + r % 4: a lane's eight results are its run's.
-    // `kid` and `vid` are the block ids of the row's and the lane's run.
-    // `pool` is the head's record of block 0, block_bytes a block of all heads.
-    __device__ __forceinline__ void load(const AttnArgs &a, const char *pool, unsigned block_bytes, int t, int kid, int vid,
-                                         int lane)
+template <int GROUPS> constexpr int kTable = (8 * GROUPS + 15) / 16;
+
+// Keys of 32 tokens: words of the lane's two operand rows, and entries of its
+// run's (s, b) table, which the run's 16 lanes share (entry = token of the run
+// * GROUPS + group).
+template <int DP, int GROUPS> struct Keys {
+    uint32_t w[2][DP / 32], table[kTable<GROUPS>];
+    __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int lane)
     {
-        const int row = lane & 15, lg = lane >> 4;
-        const int mask = (1 << a.g.block_shift) - 1;
-        known = (unsigned)vid < (unsigned)a.g.num_blocks;
-        // a block that does not exist: read the pool's first, masked later
-        kid = (unsigned)kid < (unsigned)a.g.num_blocks ? kid : 0;
-        vid = known ? vid : 0;
-        const char *krec = pool + (unsigned long long)(unsigned)kid * block_bytes;
-        const char *vrec = pool + (unsigned long long)(unsigned)vid * block_bytes;
-        const int koff = (t + (row >> 2) * 8) & mask, voff = (t + lg * 8) & mask;
+        const int row = lane & 15, lg = lane >> 4, mask = (1 << a.g.block_shift) - 1;
+        const char *krec = row & 8 ? p.second : p.first, *trec = lg & 2 ? p.second : p.first;
+        const char *k = krec + (p.at + ((row >> 2) * 8 & mask) + (row & 3)) * (DP / 2) + lg * (DP / 8);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const char *p = krec + (koff + 4 * u + (row & 3)) * (DP / 2) + lg * (DP / 8);
             if constexpr (DP == 64) {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-                k[u][0] = w[0];
-                k[u][1] = w[1];
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(k + u * 4 * (DP / 2));
+                w[u][0] = x[0];
+                w[u][1] = x[1];
             } else {
 #pragma unroll
-                for (int x = 0; x < STEPS / 4; ++x) {
-                    const u32x4 w = *reinterpret_cast<const u32x4 *>(p + 16 * x);
+                for (int v = 0; v < DP / 128; ++v) {
+                    const u32x4 x = *reinterpret_cast<const u32x4 *>(k + u * 4 * (DP / 2) + 16 * v);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) k[u][4 * x + i] = w[i];
+                    for (int i = 0; i < 4; ++i) w[u][4 * v + i] = x[i];
                 }
             }
         }
+        const char *t = trec + a.g.k_scales + (p.at + (lg * 8 & mask)) * GROUPS * 4;
 #pragma unroll
-        for (int x = 0; x < TABLE; ++x) {
-            const int e = (x * 16 + row) & (8 * GROUPS - 1);
-            ks[x] = *reinterpret_cast<const uint32_t *>(vrec + a.g.k_scales + (voff * GROUPS + e) * 4);
-            vs[x] = *reinterpret_cast<const uint32_t *>(vrec + a.g.v_scales + (voff * GROUPS + e) * 4);
-        }
+        for (int x = 0; x < kTable<GROUPS>; ++x)
+            table[x] = *reinterpret_cast<const uint32_t *>(t + ((x * 16 + row) & (8 * GROUPS - 1)) * 4);
+    }
+};
+
+// Values of the lane's run: its part of each row (16 bits for DP = 64), and
+// entries of the run's table.
+template <int DP, int GROUPS> struct Values {
+    static constexpr int N = DP < 128 ? 1 : DP / 128;
+    uint32_t w[8][N], table[kTable<GROUPS>];
+    __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int lane)
+    {
+        const int row = lane & 15, lg = lane >> 4, mask = (1 << a.g.block_shift) - 1;
+        const char *rec = lg & 2 ? p.second : p.first;
+        const int at = p.at + (lg * 8 & mask);
+        const char *t = rec + a.g.v_scales + at * GROUPS * 4;
+#pragma unroll
+        for (int x = 0; x < kTable<GROUPS>; ++x)
+            table[x] = *reinterpret_cast<const uint32_t *>(t + ((x * 16 + row) & (8 * GROUPS - 1)) * 4);
+        const char *v = rec + a.g.v_codes + at * (DP / 2) + row * (DP / 32);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const char *p = vrec + a.g.v_codes + (voff + i) * (DP / 2) + row * (DP / 32);
             if constexpr (DP == 64) {
-                v[i][0] = *reinterpret_cast<const uint16_t *>(p);
+                w[i][0] = *reinterpret_cast<const uint16_t *>(v + i * (DP / 2));
             } else if constexpr (DP == 128) {
-                v[i][0] = *reinterpret_cast<const uint32_t *>(p);
+                w[i][0] = *reinterpret_cast<const uint32_t *>(v + i * (DP / 2));
             } else {
-                const u32x2 w = *reinterpret_cast<const u32x2 *>(p);
-                v[i][0] = w[0];
-                v[i][1] = w[1];
+                const u32x2 x = *reinterpret_cast<const u32x2 *>(v + i * (DP / 2));
+                w[i][0] = x[0];
+                w[i][1] = x[1];
             }
         }
     }
 };
 
 // Waves a SIMD that the registers are held to.
-constexpr int min_waves(int dt, int dp, int groups, int nt)
+constexpr int min_waves(int dt, int dp, int groups, int nt, int waves)
 {
-    return dp == 256 || nt == 2 || dt == BCONV_F32 ? 1 : groups >= 4 ? 2 : 3;
+    if (dp == 256 || nt == 2 || dt == BCONV_F32) return 1;
+    return groups >= 4 ? 2 : waves == 8 ? 4 : 3;
 }
 
 // Whether eight waves a workgroup (at most 256 registers a wave) hold a variant without spills.
@@ -244,19 +257,18 @@ constexpr bool fits_8_waves(int dt, int dp, int groups) { return dp <= 128 || (g
 
 // FULL: no group of channels is padding alone (such groups are skipped).
 template <int DT, int DP, int GROUPS, int NT, int WAVES, bool FULL>
-__global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4_attention_kernel(AttnArgs a)
+__global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) void kv4_attention_kernel(AttnArgs a)
 {
     typedef typename Elem<DT>::type T;
-    typedef Tile<DP, GROUPS> TileT;
     constexpr int STEPS = DP / 32;             // 32-channel steps of K Q^T
     constexpr int PER = STEPS / GROUPS;        // steps a group
     constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
     constexpr int VPER = TILES / GROUPS;       // of them a group
     constexpr int NP = kProbParts<DT>;
     constexpr int COLS = 16 * NT;
-    constexpr int TABLE = TileT::TABLE;
+    constexpr int TABLE = kTable<GROUPS>;
 
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, lg = lane >> 4;
     int id = blockIdx.x;
     const int part = id % a.parts;
@@ -264,6 +276,20 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
     const int cb = id % a.col_blocks;
     id /= a.col_blocks;
     const int head = id % a.g.kv_heads, req = id / a.g.kv_heads;
+    // Block ids are the same for a wave's 32 tokens (two of them where blocks are
+    // 16 tokens), so they and the records' addresses stay in scalar registers.
+    const int *table = a.table + req * a.stride;
+    auto block_of = [&](int pos) {
+        const int b = pos >> a.g.block_shift;
+        return __builtin_amdgcn_readfirstlane(b < a.width ? table[b] : -1);
+    };
+    // Without a window the part's tokens follow from its number: the first ids
+    // are read together with the lengths instead of after them.
+    int next0 = -1, next1 = -1;  // block ids of the next tile
+    if (a.window == 0) {
+        next0 = block_of(part * a.part_tokens + wave * kTokens);
+        next1 = block_of(part * a.part_tokens + wave * kTokens + 16);
+    }
     const Span sp = column_span(a, req, cb, COLS);
     if (sp.c0 >= sp.c1) return;
     const int span = sp.t1 - sp.t0;
@@ -272,26 +298,23 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
     const int end = begin + a.part_tokens < sp.t1 ? begin + a.part_tokens : sp.t1;
     const bool whole = span <= a.part_tokens;
 
-    // the first tiles are on their way while the queries are read
-    const int *table = a.table + req * a.stride;
+    // A block that does not exist is read as the pool's first and masked.
     const char *pool = a.pool + (long long)head * a.g.record_bytes;
     const unsigned block_bytes = (unsigned)a.g.kv_heads * (unsigned)a.g.record_bytes;  // below 2^29
-    const int krun = (row >> 2) * 8, vrun = lg * 8;
-    auto block_of = [&](int pos) {
-        const int b = pos >> a.g.block_shift;
-        return b < a.width ? table[b] : -1;
+    auto exists = [&](int block) { return (unsigned)block < (unsigned)a.g.num_blocks; };
+    auto record = [&](int block) { return pool + (unsigned long long)(exists(block) ? (unsigned)block : 0u) * block_bytes; };
+    auto place_of = [&](int pos, int b0, int b1) {
+        return Place{record(b0), record(b1), pos & ((1 << a.g.block_shift) - 1)};
     };
-    int t = begin + wave * kTile;
-    int kid = -1, vid = -1;
-    TileT next;
+    constexpr int STRIDE = WAVES * kTokens;
+    int t = begin + wave * kTokens;
+    Keys<DP, GROUPS> next;
     if (t < end) {
-        kid = block_of(t + krun);
-        vid = block_of(t + vrun);
-        next.load(a, pool, block_bytes, t, kid, vid, lane);
-        if (t + WAVES * kTile < end) {
-            kid = block_of(t + WAVES * kTile + krun);
-            vid = block_of(t + WAVES * kTile + vrun);
+        if (a.window) {
+            next0 = block_of(t);
+            next1 = block_of(t + 16);
         }
+        next.load(a, place_of(t, next0, next1), lane);
     }
 
     // this lane's columns: row of q, positions seen
@@ -304,7 +327,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
         lo[n] = 0;
         hi[n] = -1;
         const bool real = c < sp.c1;
-        const int j = real ? c / a.ratio : 0, h = head * a.ratio + (real ? c - j * a.ratio : 0);
+        const int j = real ? (int)fastdiv((uint32_t)c, a.by_ratio) : 0, h = head * a.ratio + (real ? c - j * a.ratio : 0);
         if (real) {
             const int pos = sp.last + j;
             lo[n] = first_seen(pos, a.window);
@@ -331,6 +354,8 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
         all_lo = max(all_lo, __shfl_xor(all_lo, d));
         all_hi = min(all_hi, __shfl_xor(all_hi, d));
     }
+    all_lo = __builtin_amdgcn_readfirstlane(all_lo);
+    all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
     // sums of q over each group, for the midpoints and the codes' offset
     float qsum[GROUPS][NT];
@@ -362,23 +387,26 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
     const u32x4 offset = bf16_const(-kValueOffset<DT>);
     const CodeBits kbits = code_bits<DT>(), vbits = value_bits<DT>();
 
-    for (; t < end; t += WAVES * kTile) {
-        const TileT cur = next;
-        const int ahead = t + WAVES * kTile;
-        if (ahead < end) {
-            next.load(a, pool, block_bytes, ahead, kid, vid, lane);
-            if (ahead + WAVES * kTile < end) {
-                kid = block_of(ahead + WAVES * kTile + krun);
-                vid = block_of(ahead + WAVES * kTile + vrun);
-            }
+    const int vrun = lg * 8;
+    for (; t < end; t += STRIDE) {
+        // the tile's values are requested now and used after the softmax, the
+        // next tile's keys a tile ahead
+        const int id0 = next0, id1 = next1;
+        const Keys<DP, GROUPS> keys = next;
+        Values<DP, GROUPS> values;
+        values.load(a, place_of(t, id0, id1), lane);
+        if (t + STRIDE < end) {
+            next0 = block_of(t + STRIDE);
+            next1 = block_of(t + STRIDE + 16);
+            next.load(a, place_of(t + STRIDE, next0, next1), lane);
         }
 
         // S; times scale_log2 (not negative: a negative scale is in q) these are base-2 logits
         uint32_t ks[TABLE], vs[TABLE];
 #pragma unroll
         for (int x = 0; x < TABLE; ++x) {
-            ks[x] = cur.ks[x];
-            vs[x] = cur.vs[x];
+            ks[x] = keys.table[x];
+            vs[x] = values.table[x];
         }
         f32x4 z[2][NT];
 #pragma unroll
@@ -398,7 +426,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
                 }
 #pragma unroll
                 for (int s = 0; s < PER; ++s) {
-                    const u32x4 k = decode<DT>(cur.k[u][g * PER + s], eight, kbits);
+                    const u32x4 k = decode<DT>(keys.w[u][g * PER + s], eight, kbits);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) d[n] = mfma_parts<DT>(k, qf[g * PER + s][n], d[n]);
                 }
@@ -416,7 +444,8 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
         // Tiles that some column does not see in full, or with a block that
         // does not exist: masked logits are -inf whatever was read, and masked
         // tokens' steps and midpoints 0, since 0 * NaN would not vanish.
-        if (t < all_lo || t + kTile - 1 > all_hi || __any(!cur.known)) {
+        if (t < all_lo || t + kTokens - 1 > all_hi || !exists(id0) || !exists(id1)) {
+            const bool known = lg & 2 ? exists(id1) : exists(id0);
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
@@ -424,12 +453,12 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
                     const int pos = t + vrun + 4 * u + i;
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
-                        if (!cur.known || pos < lo[n] || pos > hi[n]) z[u][n][i] = -__builtin_inff();
+                        if (!known || pos < lo[n] || pos > hi[n]) z[u][n][i] = -__builtin_inff();
                 }
 #pragma unroll
             for (int x = 0; x < TABLE; ++x) {
                 const int pos = t + vrun + ((x * 16 + row) & (8 * GROUPS - 1)) / GROUPS;
-                if (!cur.known || pos < sp.low || pos >= sp.t1) vs[x] = 0;
+                if (!known || pos < sp.low || pos >= sp.t1) vs[x] = 0;
             }
         }
 
@@ -470,7 +499,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
                 float ps[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    ps[i] = p[n][i] * (float)sb[i][0];
+                    ps[i] = __builtin_fmaf((float)sb[i][0], p[n][i], 0.0f);  // one instruction, with the conversion
                     mid[g][n] = __builtin_fmaf((float)sb[i][1], p[n][i], mid[g][n]);
                 }
 #pragma unroll
@@ -492,7 +521,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
                 u32x4 v;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t two = __builtin_amdgcn_perm(cur.v[2 * i + 1][word], cur.v[2 * i][word],
+                    const uint32_t two = __builtin_amdgcn_perm(values.w[2 * i + 1][word], values.w[2 * i][word],
                                                                half ? 0x07060302u : 0x05040100u);
                     v[i] = value_pair<DT>(two, tile & 3, vbits);
                 }
@@ -533,8 +562,9 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;
-                *reinterpret_cast<f32x4 *>(so + (wave * COLS + n * 16 + row) * (DP + 4) + tile * 16 + lg * 4) =
-                    (acc[tile][n] + add) * f;
+                if (n * 16 + row < sp.c1 - sp.c0)
+                    *reinterpret_cast<f32x4 *>(so + (wave * COLS + n * 16 + row) * (DP + 4) + tile * 16 + lg * 4) =
+                        (acc[tile][n] + add) * f;
             }
         }
     }
@@ -551,7 +581,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
             sum += sl[w * COLS + c] * __builtin_amdgcn_exp2f(sm[w * COLS + c] - top);
             o += so[(w * COLS + c) * (DP + 4) + d];
         }
-        const int j = (sp.c0 + c) / a.ratio, h = head * a.ratio + (sp.c0 + c) % a.ratio;
+        const int j = (int)fastdiv((uint32_t)(sp.c0 + c), a.by_ratio), h = head * a.ratio + (sp.c0 + c - j * a.ratio);
         const long long at = (long long)(sp.q0 + j) * a.heads + h;
         if (whole) {
             static_cast<T *>(a.out)[at * a.g.dim + d] = round_to<DT>(sum > 0.0f || sum != sum ? o / sum : 0.0f);
@@ -564,14 +594,14 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT)) void kv4
 }
 
 // Joins the parts of one column, a workgroup each: DP / 4 threads take the
-// channels, 1024 / DP slices of them every so-many-th part; the slices are
+// channels, 2048 / DP slices of them every so-many-th part; the slices are
 // added in order.
 template <int DT, int DP>
-__global__ __launch_bounds__(256) void kv4_combine_kernel(AttnArgs a, int width_cols)
+__global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a, int width_cols)
 {
     typedef typename Elem<DT>::type T;
-    constexpr int THREADS = DP / 4, SLICES = 256 / THREADS;
-    __shared__ float factor[kMaxParts], edge[8];
+    constexpr int THREADS = DP / 4, SLICES = kMaxParts / THREADS, WAVES = kMaxParts / 64;
+    __shared__ float factor[kMaxParts], edge[2 * WAVES];
     __shared__ f32x4 sums[SLICES][THREADS];
     const int per_head = a.max_q * a.ratio;
     const int id = blockIdx.x, tid = threadIdx.x;
@@ -580,32 +610,26 @@ __global__ __launch_bounds__(256) void kv4_combine_kernel(AttnArgs a, int width_
     const int span = sp.t1 - sp.t0;
     if (c >= sp.c1 || span <= a.part_tokens) return;  // uniform over the workgroup
     const int used = (span + a.part_tokens - 1) / a.part_tokens;
-    const int j = c / a.ratio, h = head * a.ratio + c % a.ratio;
+    const int j = (int)fastdiv((uint32_t)c, a.by_ratio), h = head * a.ratio + (c - j * a.ratio);
     const long long at = (long long)(sp.q0 + j) * a.heads + h;
-    const float2 *ml = a.part_ml + at * a.parts;
-    float2 mine[kMaxParts / 256];
-    float top = kLowest, sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kMaxParts / 256; ++i) {
-        mine[i] = i * 256 + tid < used ? ml[i * 256 + tid] : float2{kLowest, 0.0f};
-        top = fmaxf(top, mine[i].x);
-    }
+    const float2 mine = tid < used ? a.part_ml[at * a.parts + tid] : float2{kLowest, 0.0f};
+    float top = mine.x;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
     if ((tid & 63) == 0) edge[tid >> 6] = top;
     __syncthreads();
-    top = fmaxf(fmaxf(edge[0], edge[1]), fmaxf(edge[2], edge[3]));
 #pragma unroll
-    for (int i = 0; i < kMaxParts / 256; ++i) {
-        const float f = __builtin_amdgcn_exp2f(mine[i].x - top);
-        if (i * 256 + tid < used) factor[i * 256 + tid] = f;
-        sum += mine[i].y * f;
-    }
+    for (int w = 0; w < WAVES; ++w) top = fmaxf(top, edge[w]);
+    const float f = __builtin_amdgcn_exp2f(mine.x - top);
+    factor[tid] = f;
+    float sum = mine.y * f;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-    if ((tid & 63) == 0) edge[4 + (tid >> 6)] = sum;
+    if ((tid & 63) == 0) edge[WAVES + (tid >> 6)] = sum;
     __syncthreads();
-    sum = edge[4] + edge[5] + edge[6] + edge[7];
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) sum += edge[WAVES + w];
 
     const int d4 = tid % THREADS, slice = tid / THREADS;
     const f32x4 *o4 = reinterpret_cast<const f32x4 *>(a.part_o + at * a.parts * DP) + d4;
@@ -637,7 +661,7 @@ hipError_t launch_attention_waves(const AttnArgs &a, hipStream_t s)
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.parts > 1) {
         const long long cols = (long long)a.requests * a.g.kv_heads * a.max_q * a.ratio;
-        hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3((unsigned)cols), dim3(256), 0, s, a, 16 * NT);
+        hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3((unsigned)cols), dim3(kMaxParts), 0, s, a, 16 * NT);
         e = hipGetLastError();
     }
     return e;
@@ -753,6 +777,7 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
     a.max_q = t->max_q < t->q_tokens ? t->max_q : t->q_tokens;
     a.heads = t->heads;
     a.ratio = t->heads / a.g.kv_heads;
+    a.by_ratio = bconv::make_fastdiv((uint32_t)a.ratio);
     a.width = t->table_width;
     a.stride = t->table_stride;
     const long long held = (long long)t->table_width << a.g.block_shift;
@@ -777,7 +802,7 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
         const long long w = (long long)a.window + (cols + a.ratio - 1) / a.ratio;
         if (w < seen) seen = w;
     }
-    seen += bconv::kTile;
+    seen += bconv::kTokens;
     p->shape.waves = tiles >= 512 || p->shape.nt == 2 || !bconv::fits_8_waves(t->dtype, a.g.dim_padded, a.g.groups) ? 4 : 8;
     if (getenv("AT_W")) p->shape.waves = atoi(getenv("AT_W"));
     const long long want = ((getenv("AT_T") ? atoi(getenv("AT_T")) : 4LL) * compute_units() + tiles - 1) / tiles;
@@ -785,7 +810,7 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
     const int least = getenv("AT_P") ? atoi(getenv("AT_P")) : 1024;
     if (part < least) part = least;
     if (part < (seen + bconv::kMaxParts - 1) / bconv::kMaxParts) part = (seen + bconv::kMaxParts - 1) / bconv::kMaxParts;
-    part = (part + bconv::kTile - 1) / bconv::kTile * bconv::kTile;
+    part = (part + bconv::kTokens - 1) / bconv::kTokens * bconv::kTokens;
     a.part_tokens = (int)part;
     a.parts = (int)((seen + part - 1) / part);
     if (a.parts < 1) a.parts = 1;

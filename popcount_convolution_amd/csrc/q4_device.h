@@ -59,13 +59,13 @@ __device__ __forceinline__ uint32_t pack_hi16(uint32_t lo, uint32_t hi)
 }
 
 // Three bf16 parts of x, by truncation: their sum is x exactly (8 significant
-// bits each).  Infinities and NaN sit in the first part alone.
+// bits each).  An infinity or NaN sits in the first part alone.
 __device__ __forceinline__ void split3(float x, uint32_t &h, uint32_t &m, uint32_t &l)
 {
     const uint32_t u = __float_as_uint(x);
-    const bool finite = (u & 0x7f800000u) != 0x7f800000u;
-    h = u & 0xffff0000u;
-    if (x != x) h = 0x7fc00000u;
+    const bool finite = __builtin_isfinite(x);
+    // a NaN whose bits all sit below the first part must not become an infinity
+    h = x != x ? 0x7fc00000u : u & 0xffff0000u;
     const float r = finite ? x - __uint_as_float(h) : 0.0f;
     m = __float_as_uint(r) & 0xffff0000u;
     l = __float_as_uint(r - __uint_as_float(m));
@@ -92,6 +92,9 @@ template <int DT>
 __device__ __forceinline__ Raw<DT> load_raw_masked(const typename Elem<DT>::type *p, int k, int len)
 {
     Raw<DT> r;
+#pragma unroll
+    for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) r.v[i] = u32x4{0, 0, 0, 0};
+    if (k >= len) return r;
     if constexpr (DT == BCONV_F32) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) r.v[i >> 2][i & 3] = k + i < len ? __float_as_uint(p[i]) : 0u;
@@ -148,7 +151,10 @@ template <int DT> __device__ __forceinline__ typename Elem<DT>::type round_to(fl
 // What is left of the offset:
 //   bf16: 16 (the products are exact; the caller takes 16 * sum x out);
 //   fp16: none: a packed subtraction of `zero` leaves the integer itself;
-//   fp32: none: exact fp32 subtraction, so that no cancellation costs bits.
+//   fp32: none, so that no cancellation costs bits: the codes are spread to
+//         bytes, `zero` is taken off four at a time (a byte holds 128 + c - z
+//         and never borrows; with the top bit flipped it is c - z, signed), and
+//         each byte converts to an exact float, whose upper half is the bf16.
 constexpr uint32_t kCodeMask = 0x00780078u;
 constexpr uint32_t kBase16 = 0x41804180u;   // bf16 16, 16
 constexpr uint32_t kBase128 = 0x58005800u;  // fp16 128, 128
@@ -159,7 +165,7 @@ __device__ __forceinline__ uint32_t rotr(uint32_t w, int n)
 }
 
 // `zero` is subtracted from the codes where the type allows (see above): fp32
-// takes it as a float, fp16 as a pair of halves holding 128 + zero.
+// takes it as four bytes of 128 - zero, fp16 as a pair of halves holding 128 + zero.
 template <int DT> struct Zero;
 template <> struct Zero<BCONV_BF16> {
     __device__ __forceinline__ explicit Zero(int) {}
@@ -173,8 +179,8 @@ template <> struct Zero<BCONV_F16> {
     }
 };
 template <> struct Zero<BCONV_F32> {
-    float v;
-    __device__ __forceinline__ explicit Zero(int z) : v(16.0f + (float)z) {}
+    uint32_t v;
+    __device__ __forceinline__ explicit Zero(int z) : v((uint32_t)(128 - z) * 0x01010101u) {}
 };
 
 // (x & mask) | base is one v_and_or_b32 when one constant is in a scalar
@@ -200,16 +206,23 @@ template <int DT> __device__ __forceinline__ CodeBits code_bits()
 template <int DT> __device__ __forceinline__ u32x4 decode(uint32_t w, const Zero<DT> &zero, const CodeBits &bits)
 {
     u32x4 r;
+    if constexpr (DT == BCONV_F32) {
+        // nibbles (rotated by 3) at even and odd places: bytes b of `even` are
+        // nibbles 2b, of `odd` nibbles 2b + 1; codes 2e, 2e + 1 are nibbles e, 4 + e
+        const uint32_t even = ((rotr(w, 3) & 0x0f0f0f0fu) + zero.v) ^ 0x80808080u;
+        const uint32_t odd = ((rotr(w, 7) & 0x0f0f0f0fu) + zero.v) ^ 0x80808080u;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const uint32_t c = bits(e ? rotr(w, 4 * e) : w);
-        if constexpr (DT == BCONV_F16) {
-            r[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - zero.v);
-        } else if constexpr (DT == BCONV_BF16) {
-            r[e] = c;
-        } else {
-            const float lo = __uint_as_float(c << 16) - zero.v, hi = __uint_as_float(c & 0xffff0000u) - zero.v;
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t src = e & 1 ? odd : even;
+            const float lo = (float)(int8_t)(src >> (8 * (e >> 1))), hi = (float)(int8_t)(src >> (8 * (2 + (e >> 1))));
             r[e] = pack_hi16(__float_as_uint(lo), __float_as_uint(hi));
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t c = bits(e ? rotr(w, 4 * e) : w);
+            if constexpr (DT == BCONV_F16) r[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - zero.v);
+            else r[e] = c;
         }
     }
     return r;

@@ -9,7 +9,6 @@
 // read them: one 16-byte load a lane is 16 outputs x 128 inputs.
 #include <hip/hip_runtime.h>
 
-#include <cstdlib>
 #include <new>
 
 #include "host.h"
@@ -113,43 +112,47 @@ template <int DT, bool ZP, int STEPS> struct Scales {
     }
 };
 
-// One chunk (16 RT outputs x 128 inputs) times NT tiles of 16 rows of x, added
-// to acc.  STEPS: 32-input steps a group.  Per group and output tile the exact
-// products of one group are summed first, then scaled once in fp32.
-template <int DT, bool ZP, int STEPS, int RT, int NT>
-__device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operand<DT> (&xf)[4][NT],
+// One chunk (16 RT outputs x 128 inputs) times 16 rows of x, added to acc.
+// STEPS: 32-input steps a group.  Per group and output tile the exact products
+// of one group are summed first, then scaled once in fp32.
+template <int DT, bool ZP, int STEPS, int RT>
+__device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operand<DT> (&x)[4],
                                               const Scales<DT, ZP, STEPS> (&sc)[RT], const CodeBits &bits,
-                                              f32x4 (&acc)[RT][NT])
+                                              f32x4 (&acc)[RT])
 {
+    constexpr int P = kSplit<DT>;
 #pragma unroll
     for (int g = 0; g < 4 / STEPS; ++g) {
         // bf16: the offset 16 + z of the codes leaves -(16 + z) sum x, on the
         // matrix cores as well (a constant operand times x)
-        f32x4 off[NT];
+        f32x4 off = {0, 0, 0, 0};
+        if constexpr (DT == BCONV_BF16) {
+            const u32x4 c = bf16_const(ZP ? -1.0f : -24.0f);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            off[t] = f32x4{0, 0, 0, 0};
-            if constexpr (DT == BCONV_BF16) {
-                const u32x4 c = bf16_const(ZP ? -1.0f : -24.0f);
-#pragma unroll
-                for (int s = 0; s < STEPS; ++s) off[t] = mfma_parts<DT>(c, xf[g * STEPS + s][t], off[t]);
-            }
+            for (int s = 0; s < STEPS; ++s) off = mfma_parts<DT>(c, x[g * STEPS + s], off);
         }
+        // step by step over all tiles, an fp32 row's parts in sums of their
+        // own: a product waits for the one before that adds to the same sum
+        f32x4 d[RT][P];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            f32x4 d[NT];
+            d[r][0] = ZP ? sc[r].start(g, off[0]) : off;
 #pragma unroll
-            for (int t = 0; t < NT; ++t) d[t] = ZP ? sc[r].start(g, off[t][0]) : off[t];
+            for (int p = 1; p < P; ++p) d[r][p] = f32x4{0, 0, 0, 0};
+        }
 #pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
                 const u32x4 k = decode<DT>(w[r][g * STEPS + s], sc[r].zero(g), bits);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) d[t] = mfma_parts<DT>(k, xf[g * STEPS + s][t], d[t]);
+                for (int p = 0; p < P; ++p) d[r][p] = mfma16<DT>(k, x[g * STEPS + s].part[p], d[r][p]);
             }
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+        for (int r = 0; r < RT; ++r) {
+            if constexpr (P == 3) d[r][0] += d[r][1] + d[r][2];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf(sc[r].scale(g, i), d[t][i], acc[r][t][i]);
+            for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sc[r].scale(g, i), d[r][0][i], acc[r][i]);
         }
     }
 }
@@ -164,108 +167,85 @@ template <int DT> __device__ __forceinline__ void store_outputs(const Q4Args &a,
         if (o0 + i < a.n) y[i] = round_to<DT>(v[i] + (a.bias ? a.bias[o0 + i] : 0.0f));
 }
 
-// Few rows of x.  A workgroup takes 16 RT outputs and 16 NT rows of x; its
-// waves split the inputs chunk by chunk and add their sums in LDS, in a fixed
-// order.  UNROLL chunks are requested before the first is used.
-template <int DT, bool ZP, int STEPS, int RT, int NT, int WAVES, int UNROLL>
+// Few rows of x.  A workgroup takes 16 RT outputs and 16 rows of x; its waves
+// split the inputs chunk by chunk and add their sums in LDS, in a fixed order:
+// one launch, and with one output tile a workgroup every compute unit has codes
+// to stream from about 4096 outputs on.
+template <int DT, bool ZP, int STEPS, int RT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
 {
     typedef typename Elem<DT>::type T;
-    __shared__ f32x4 part[WAVES][RT * NT][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int tile0 = blockIdx.x * RT, m0 = blockIdx.y * 16 * NT;
-    const int row = lane & 15, lg = lane >> 4;
     constexpr int per_chunk = 4 / STEPS;
+    __shared__ f32x4 part[WAVES][RT][64];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int tile0 = blockIdx.x * RT, m0 = blockIdx.y * 16;
+    const int row = lane & 15, lg = lane >> 4;
     const CodeBits bits = code_bits<DT>();
 
-    f32x4 acc[RT][NT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+    f32x4 acc[RT];
     long long first[RT];
 #pragma unroll
-    for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
-    // Lanes of columns past the last row load nothing: their operands stay what
-    // they are, and so do only their own, unused results.
-    const T *xr[NT];
-    bool real[NT];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int m = m0 + t * 16 + row;
-        real[t] = m < a.m;
-        xr[t] = static_cast<const T *>(a.x) + (real[t] ? (long long)m * a.ldx : 0) + lg * 8;
+    for (int r = 0; r < RT; ++r) {
+        acc[r] = f32x4{0, 0, 0, 0};
+        first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
     }
-    Raw<DT> xf[UNROLL][NT][4];
+    // Lanes of columns past the last row load nothing: their operands stay 0,
+    // and their results are not stored.
+    const bool real = m0 + row < a.m;
+    const T *xr = static_cast<const T *>(a.x) + (real ? (long long)(m0 + row) * a.ldx : 0) + lg * 8;
+    Raw<DT> xf[4];
 #pragma unroll
-    for (int u = 0; u < UNROLL; ++u)
+    for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) xf[u][t][s].v[i] = u32x4{0, 0, 0, 0};
-    // chunks whose columns are read in whole 16-byte loads
-    const int whole = a.vec ? a.k / kChunk : 0;
+        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) xf[s].v[i] = u32x4{0, 0, 0, 0};
+    const int whole = a.vec ? a.k / kChunk : 0;  // chunks whose columns are 16-byte loads throughout
 
-    for (int c0 = wave; c0 < a.chunks; c0 += WAVES * UNROLL) {
-        u32x4 w[UNROLL][RT];
-        Scales<DT, ZP, STEPS> sc[UNROLL][RT];
+    for (int c = wave; c < a.chunks; c += WAVES) {
+        u32x4 w[RT];
+        Scales<DT, ZP, STEPS> sc[RT];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            const int c = c0 + u * WAVES;
-            if (c >= a.chunks) break;
+        for (int r = 0; r < RT; ++r) {
+            const long long tc = first[r] + c;
+            w[r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
+            sc[r].load(a.scales + tc * per_chunk * 16, ZP ? a.zeros + tc * per_chunk * 16 : nullptr, lane);
+        }
+        if (real) {
+            const T *p = xr + c * kChunk;
+            if (c < whole) {
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
-                const long long tc = first[r] + c;
-                w[u][r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
-                sc[u][r].load(a.scales + tc * per_chunk * 16, ZP ? a.zeros + tc * per_chunk * 16 : nullptr, lane);
-            }
+                for (int s = 0; s < 4; ++s) xf[s] = load_raw<DT>(p + s * 32);
+            } else {
 #pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const T *p = xr[t] + c * kChunk;
-                if (real[t]) {
-                    if (c < whole) {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s) xf[u][t][s] = load_raw<DT>(p + s * 32);
-                    } else {
-#pragma unroll
-                        for (int s = 0; s < 4; ++s)
-                            xf[u][t][s] = load_raw_masked<DT>(p + s * 32, c * kChunk + s * 32 + lg * 8, a.k);
-                    }
+                for (int s = 0; s < 4; ++s) {
+                    const int k = c * kChunk + s * 32 + lg * 8;
+                    if (a.vec && k + 8 <= a.k) xf[s] = load_raw<DT>(p + s * 32);
+                    else xf[s] = load_raw_masked<DT>(p + s * 32, k, a.k);
                 }
             }
         }
+        Operand<DT> x[4];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-            if (c0 + u * WAVES >= a.chunks) break;
-            Operand<DT> op[4][NT];
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-#pragma unroll
-                for (int s = 0; s < 4; ++s) op[s][t] = to_operand<DT>(xf[u][t][s]);
-            chunk_product<DT, ZP, STEPS, RT, NT>(w[u], op, sc[u], bits, acc);
-        }
+        for (int s = 0; s < 4; ++s) x[s] = to_operand<DT>(xf[s]);
+        chunk_product<DT, ZP, STEPS, RT>(w, x, sc, bits, acc);
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) part[wave][r * NT + t][lane] = acc[r][t];
+    for (int r = 0; r < RT; ++r) part[wave][r][lane] = acc[r];
     __syncthreads();
-    for (int e = threadIdx.x; e < RT * NT * 64; e += WAVES * 64) {
-        const int l = e & 63, rt = e >> 6;
-        const int m = m0 + (rt % NT) * 16 + (l & 15);
-        const int o0 = (tile0 + rt / NT) * 16 + (l >> 4) * 4;
+    for (int e = threadIdx.x; e < RT * 64; e += WAVES * 64) {
+        const int l = e & 63, r = e >> 6;
+        const int m = m0 + (l & 15), o0 = (tile0 + r) * 16 + (l >> 4) * 4;
         if (m >= a.m || o0 >= a.n) continue;
-        f32x4 v = part[0][rt][l];
+        f32x4 v = part[0][r][l];
 #pragma unroll
-        for (int w = 1; w < WAVES; ++w) v += part[w][rt][l];
+        for (int w = 1; w < WAVES; ++w) v += part[w][r][l];
         store_outputs<DT>(a, m, o0, v);
     }
 }
 
-// What the products that add up splits of the inputs take besides Q4Args: the
-// partial sums, and for many rows x laid out as operands.
+// ------------------------------------------------------------------ many rows
+
+// What the product of many rows takes besides Q4Args: x laid out as operands
+// and the partial sums of the splits.
 struct Q4Many {
     u32x4 *xp;       // [column tiles][chunks * 4][parts][64]
     float *xs;       // bf16: [column tiles][chunks][groups a chunk][16], -sum x (times 24 without zero points)
@@ -274,119 +254,6 @@ struct Q4Many {
     int padded_n;
     int row_blocks, col_blocks, splits;
 };
-
-// ------------------------------------------------------------------ up to 16 rows, sliced inputs
-
-constexpr int kSliceWaves = 8, kSliceRows = 2;
-// chunks a slice holds at most: 64 KiB of operands, 96 in fp32
-constexpr int most_slice(int dtype) { return dtype == BCONV_F32 ? 8 : 16; }
-
-// Up to 16 rows of x through a layer whose codes outweigh the join of partial
-// sums.  A workgroup takes one slice of the inputs and 16 x 2 x 8 outputs: x's
-// slice is brought to LDS as operands once for its 16 output tiles (read from
-// global memory by every tile, it would be several times the codes' bytes),
-// then the waves stream codes with no barrier between them.
-template <int DT, bool ZP, int STEPS>
-__global__ __launch_bounds__(kSliceWaves * 64) void q4_slice_kernel(Q4Args a, Q4Many q)
-{
-    typedef typename Elem<DT>::type T;
-    constexpr int RT = kSliceRows, P = kSplit<DT>, G = 4 / STEPS;
-    extern __shared__ u32x4 lds[];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = lane & 15, lg = lane >> 4;
-    const int split = blockIdx.x % q.splits, rb = blockIdx.x / q.splits;
-    const int c_begin = (int)((long long)a.chunks * split / q.splits), c_end = (int)((long long)a.chunks * (split + 1) / q.splits);
-    u32x4 *xl = lds;                                                                  // [chunk][4][P][64]
-    float *xs = reinterpret_cast<float *>(lds + (long long)(c_end - c_begin) * 4 * P * 64);  // [chunk][G][16]
-    const int tile0 = (rb * kSliceWaves + wave) * RT;
-    const CodeBits bits = code_bits<DT>();
-    long long first[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) first[r] = (long long)(tile0 + r < a.tiles ? tile0 + r : a.tiles - 1) * a.chunks;
-
-    u32x4 w[2][RT];
-    Scales<DT, ZP, STEPS> sc[2][RT];
-    auto fetch = [&](int b, int c) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const long long tc = first[r] + c;
-            w[b][r] = *reinterpret_cast<const u32x4 *>(a.codes + tc * 256 + lane * 4);
-            sc[b][r].load(a.scales + tc * G * 16, ZP ? a.zeros + tc * G * 16 : nullptr, lane);
-        }
-    };
-    if (c_begin < c_end) fetch(0, c_begin);
-    if (c_begin + 1 < c_end) fetch(1, c_begin + 1);
-
-    const bool real = row < a.m;
-    const T *xr = static_cast<const T *>(a.x) + (real ? (long long)row * a.ldx : 0);
-    for (int g = wave; g < (c_end - c_begin) * G; g += kSliceWaves) {
-        Operand<DT> o[STEPS];
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-            const int k = (c_begin * 4 + g * STEPS + s) * 32 + lg * 8;
-            if (real && k < a.k) {
-                o[s] = load_operand<DT>(xr + k, k, a.k, a.vec != 0);
-            } else {
-#pragma unroll
-                for (int p = 0; p < P; ++p) o[s].part[p] = u32x4{0, 0, 0, 0};
-            }
-        }
-        f32x4 sum = {0, 0, 0, 0};
-#pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-#pragma unroll
-            for (int p = 0; p < P; ++p) xl[((g * STEPS + s) * P + p) * 64 + lane] = o[s].part[p];
-            if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(bf16_const(ZP ? -1.0f : -24.0f), o[s], sum);
-        }
-        if (DT == BCONV_BF16 && lane < 16) xs[g * 16 + lane] = sum[0];
-    }
-    __syncthreads();
-
-    f32x4 acc[RT];
-#pragma unroll
-    for (int r = 0; r < RT; ++r) acc[r] = f32x4{0, 0, 0, 0};
-    auto product = [&](int b, int c) {
-        const int at = c - c_begin;
-#pragma unroll
-        for (int g = 0; g < G; ++g) {
-            const float off = DT == BCONV_BF16 ? xs[(at * G + g) * 16 + row] : 0.0f;
-            f32x4 d[RT];
-#pragma unroll
-            for (int r = 0; r < RT; ++r) d[r] = sc[b][r].start(g, off);
-#pragma unroll
-            for (int s = 0; s < STEPS; ++s) {
-                Operand<DT> x;
-#pragma unroll
-                for (int p = 0; p < P; ++p) x.part[p] = xl[((at * 4 + g * STEPS + s) * P + p) * 64 + lane];
-#pragma unroll
-                for (int r = 0; r < RT; ++r)
-                    d[r] = mfma_parts<DT>(decode<DT>(w[b][r][g * STEPS + s], sc[b][r].zero(g), bits), x, d[r]);
-            }
-#pragma unroll
-            for (int r = 0; r < RT; ++r)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sc[b][r].scale(g, i), d[r][i], acc[r][i]);
-        }
-    };
-    for (int c = c_begin; c < c_end; c += 2) {
-        product(0, c);
-        if (c + 2 < c_end) fetch(0, c + 2);
-        if (c + 1 < c_end) {
-            product(1, c + 1);
-            if (c + 3 < c_end) fetch(1, c + 3);
-        }
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int o0 = (tile0 + r) * 16 + lg * 4;
-        if (q.splits > 1)
-            *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * 16 + row) * q.padded_n + o0) = acc[r];
-        else if (real && o0 < a.n)
-            store_outputs<DT>(a, row, o0, acc[r]);
-    }
-}
-
-// ------------------------------------------------------------------ many rows
 
 // x as operands, a wave a (16 rows, group) pair: converted, split and padded
 // with zeros once instead of once per output tile, with the group's sum that
@@ -600,10 +467,10 @@ __global__ __launch_bounds__(256) void q4_reduce_kernel(Q4Args a, Q4Many q)
 // ------------------------------------------------------------------ dispatch
 
 // Which kernel a number of rows takes, and what it needs of the workspace.
-enum class Q4Kind { Few, Slice, Many };
 struct Q4Plan {
-    Q4Kind kind;
-    int nt;    // many: column tiles a wave
+    bool many;
+    int rt, waves;  // few: output tiles and waves a workgroup
+    int nt;         // many: column tiles a wave
     Q4Many q;
     size_t xs_offset, sums_offset, bytes;
 };
@@ -611,24 +478,28 @@ struct Q4Plan {
 Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, int cus)
 {
     Q4Plan p{};
-    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    auto env = [](const char *n, int d) { const char *e = getenv(n); return e ? atoi(e) : d; };
+    // The few-row kernel reads the codes once for 16 rows of x; the many-row
+    // kernel's three launches cost about 8 us more and pay from 32 MiB of codes
+    // read that way on (16 in fp32, where the few-row kernel converts x again
+    // for every 64 outputs).  bf16, 2048 x 2048: 64 rows 7.0 us against 14.0,
+    // 300 rows 25.2 against 23.2; 4096 x 4096: 32 rows 11.2 against 14.5, 128
+    // rows 40.3 against 26.8; fp32, 2048 x 2048: 64 rows 12.0 against 18.3, 128
+    // rows 20.6 against 19.9.
     const long long codes = (long long)tiles * chunks;  // KiB
-    p.kind = rows > env("Q4_FEW", 16) ? Q4Kind::Many : rows >= env("Q4_SLICE", 2) && codes >= env("Q4_CODES", 4096) ? Q4Kind::Slice : Q4Kind::Few;
-    if (p.kind == Q4Kind::Few) return p;
-    if (p.kind == Q4Kind::Slice) {
-        const int per_block = kSliceWaves * kSliceRows;
-        p.q.col_tiles = p.q.col_blocks = 1;
-        p.q.row_blocks = (tiles + per_block - 1) / per_block;
-        p.q.padded_n = p.q.row_blocks * per_block * 16;
-        long long splits = ((long long)env("Q4_T", 2) * cus + p.q.row_blocks - 1) / p.q.row_blocks;
-        if (splits > chunks / 4) splits = chunks / 4;
-        const int least = (chunks + most_slice(dtype) - 1) / most_slice(dtype);
-        if (splits < least) splits = least;
-        p.q.splits = (int)splits;
-        p.bytes = splits > 1 ? (size_t)splits * 16 * p.q.padded_n * 4 : 0;
+    p.many = rows > 16 && (rows + 15) / 16 * codes > (dtype == BCONV_F32 ? 16384 : 32768);
+    if (!p.many) {
+        // With several rows, x's operands are shared by as many output tiles as
+        // still leave a workgroup for every compute unit (13 x 5000 -> 11003,
+        // bf16: four tiles 12.3 us, one 15.0).  One row shares nothing worth it
+        // (11.6 against 11.0).  Where one tile a workgroup is left and the inputs
+        // are long, sixteen waves split them instead of eight (1 x 25088 -> 4096:
+        // 12.8 us against 14.6; 1 x 4096 -> 12000: 10.1 against 8.4).
+        p.rt = rows > 1 ? (tiles + cus - 1) / cus : 1;
+        if (p.rt > 4) p.rt = 4;
+        p.waves = p.rt == 1 && chunks >= 64 && tiles <= 2 * cus ? 16 : 8;
         return p;
     }
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     int nt = most_cols(dtype);
     while (nt > 1 && 16 * nt >= rows) nt /= 2;
     p.nt = nt;
@@ -638,8 +509,9 @@ Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, in
     p.q.row_blocks = (tiles + 2 * kManyRows - 1) / (2 * kManyRows);
     p.q.padded_n = p.q.row_blocks * 2 * kManyRows * 16;
     const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks;
-    long long splits = ((long long)env("Q4_T", 2) * cus + blocks - 1) / blocks;
-    if (splits > env("Q4_MAXS", 8)) splits = env("Q4_MAXS", 8);
+    // two workgroups a compute unit; a slice holds at least 4 chunks
+    long long splits = (2LL * cus + blocks - 1) / blocks;
+    if (splits > 8) splits = 8;
     if (splits > chunks / 4) splits = chunks / 4;
     p.q.splits = splits < 1 ? 1 : (int)splits;
     p.xs_offset = up((size_t)p.q.col_tiles * chunks * 4 * parts * 1024);
@@ -648,29 +520,18 @@ Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, in
     return p;
 }
 
-template <int DT, bool ZP, int STEPS, int RT, int NT, int WAVES, int UNROLL>
+template <int DT, bool ZP, int STEPS, int RT, int WAVES>
 hipError_t run_few(const Q4Args &a, hipStream_t s)
 {
-    const dim3 grid((a.tiles + RT - 1) / RT, (a.m + 16 * NT - 1) / (16 * NT));
-    hipLaunchKernelGGL((q4_few_kernel<DT, ZP, STEPS, RT, NT, WAVES, UNROLL>), grid, dim3(WAVES * 64), 0, s, a);
+    const dim3 grid((a.tiles + RT - 1) / RT, (a.m + 15) / 16);
+    hipLaunchKernelGGL((q4_few_kernel<DT, ZP, STEPS, RT, WAVES>), grid, dim3(WAVES * 64), 0, s, a);
     return hipGetLastError();
 }
 
 template <int DT, bool ZP, int STEPS>
 hipError_t run_linear(const Q4Args &a, const Q4Plan &p, hipStream_t s)
 {
-    const long long outs = (long long)((a.n + 3) / 4) * a.m;
-    if (p.kind == Q4Kind::Slice) {
-        const int held = (a.chunks + p.q.splits - 1) / p.q.splits;
-        const size_t lds = (size_t)held * (4 * kSplit<DT> * 1024 + (4 / STEPS) * 64);
-        hipLaunchKernelGGL((q4_slice_kernel<DT, ZP, STEPS>), dim3((unsigned)(p.q.row_blocks * p.q.splits)),
-                           dim3(kSliceWaves * 64), lds, s, a, p.q);
-        const hipError_t e = hipGetLastError();
-        if (e != hipSuccess || p.q.splits == 1) return e;
-        hipLaunchKernelGGL((q4_reduce_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
-        return hipGetLastError();
-    }
-    if (p.kind == Q4Kind::Many) {
+    if (p.many) {
         const long long packs = (long long)p.q.col_tiles * a.chunks * (4 / STEPS);
         hipLaunchKernelGGL((q4_pack_kernel<DT, ZP, STEPS>), dim3((unsigned)((packs + 3) / 4)), dim3(256), 0, s, a, p.q);
         hipError_t e = hipGetLastError();
@@ -684,26 +545,17 @@ hipError_t run_linear(const Q4Args &a, const Q4Plan &p, hipStream_t s)
             hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, most_cols(DT)>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
         e = hipGetLastError();
         if (e != hipSuccess || p.q.splits == 1) return e;
+        const long long outs = (long long)((a.n + 3) / 4) * a.m;
         hipLaunchKernelGGL((q4_reduce_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
         return hipGetLastError();
     }
-    const char *ev = getenv("Q4_VAR");
-    const int v = ev ? atoi(ev) : 0;
-    switch (v) {
-    case 0: return run_few<DT, ZP, STEPS, 1, 1, 8, 1>(a, s);
-    case 1: return run_few<DT, ZP, STEPS, 1, 1, 8, 2>(a, s);
-    case 2: return run_few<DT, ZP, STEPS, 1, 1, 16, 1>(a, s);
-    case 3: return run_few<DT, ZP, STEPS, 1, 1, 16, 2>(a, s);
-    case 4: return run_few<DT, ZP, STEPS, 2, 1, 8, 1>(a, s);
-    case 5: return run_few<DT, ZP, STEPS, 2, 1, 16, 1>(a, s);
-    case 6: return run_few<DT, ZP, STEPS, 4, 1, 8, 1>(a, s);
-    case 7: return run_few<DT, ZP, STEPS, 1, 1, 16, 4>(a, s);
-    case 8: return run_few<DT, ZP, STEPS, 2, 2, 8, 1>(a, s);
-    case 9: return run_few<DT, ZP, STEPS, 1, 2, 16, 1>(a, s);
-    case 10: return run_few<DT, ZP, STEPS, 1, 4, 8, 1>(a, s);
-    case 11: return run_few<DT, ZP, STEPS, 2, 4, 8, 1>(a, s);
-    case 12: return run_few<DT, ZP, STEPS, 4, 1, 16, 1>(a, s);
-    default: return run_few<DT, ZP, STEPS, 1, 4, 16, 1>(a, s);
+    switch (p.rt) {
+    case 1:
+        if (p.waves == 16) return run_few<DT, ZP, STEPS, 1, 16>(a, s);
+        return run_few<DT, ZP, STEPS, 1, 8>(a, s);
+    case 2: return run_few<DT, ZP, STEPS, 2, 8>(a, s);
+    case 3: return run_few<DT, ZP, STEPS, 3, 8>(a, s);
+    default: return run_few<DT, ZP, STEPS, 4, 8>(a, s);
     }
 }
 
