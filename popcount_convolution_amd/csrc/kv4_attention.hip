@@ -16,14 +16,14 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <cstdlib>
 
 #include "internal.h"
 #include "kv4.h"
 
 namespace bconv {
 
-constexpr int kTokens = 32;         // tokens a wave takes at a time
+constexpr int kTokens = 32;       // tokens a wave takes at a time
+constexpr int kCols = 16;         // (query, head) columns a workgroup takes
 constexpr float kLowest = -1e30f; // running maximum before the first visible token
 // How far a logit (base 2) may pass the running maximum before the sums are
 // rescaled: 2^8 of headroom costs fp32 sums nothing and saves most rescales.
@@ -53,11 +53,6 @@ struct AttnArgs {
 
 constexpr int kMaxParts = 512;
 
-// Kernel variant of a call: column tiles and waves a workgroup.
-struct AttnShape {
-    int nt, waves;
-};
-
 // The columns one workgroup takes and the tokens they see.
 struct Span {
     int q0, n, j0, c0, c1;   // first query row, queries, first query's index, columns [c0, c1)
@@ -68,7 +63,7 @@ struct Span {
 
 __device__ __forceinline__ int first_seen(int pos, int window) { return window > 0 && pos >= window ? pos - window + 1 : 0; }
 
-__device__ __forceinline__ Span column_span(const AttnArgs &a, int req, int cb, int width_cols)
+__device__ __forceinline__ Span column_span(const AttnArgs &a, int req, int cb)
 {
     Span s;
     int q0, n;
@@ -87,9 +82,9 @@ __device__ __forceinline__ Span column_span(const AttnArgs &a, int req, int cb, 
     else if (n > a.q_tokens - q0) n = a.q_tokens - q0;
     s.q0 = q0;
     s.n = n;
-    s.c0 = cb * width_cols;
+    s.c0 = cb * kCols;
     const int cols = s.n * a.ratio;
-    s.c1 = s.c0 + width_cols < cols ? s.c0 + width_cols : cols;
+    s.c1 = s.c0 + kCols < cols ? s.c0 + kCols : cols;
     s.t0 = s.t1 = s.low = 0;
     s.j0 = 0;
     if (s.c0 < s.c1) {
@@ -245,19 +240,21 @@ template <int DP, int GROUPS> struct Values {
     }
 };
 
+// Waves that share a part of a request's tokens: eight, or four where eight (at
+// most 256 registers a wave) would spill.
+constexpr int attn_waves(int dt, int dp, int groups) { return dp <= 128 || (groups == 2 && dt != BCONV_F32) ? 8 : 4; }
+
 // Waves a SIMD that the registers are held to.
-constexpr int min_waves(int dt, int dp, int groups, int nt, int waves)
+constexpr int min_waves(int dt, int dp, int groups)
 {
-    if (dp == 256 || nt == 2 || dt == BCONV_F32) return 1;
-    return groups >= 4 ? 2 : waves == 8 ? 4 : 3;
+    if (dp == 256 || dt == BCONV_F32) return 1;
+    return groups >= 4 ? 2 : 4;
 }
 
-// Whether eight waves a workgroup (at most 256 registers a wave) hold a variant without spills.
-constexpr bool fits_8_waves(int dt, int dp, int groups) { return dp <= 128 || (groups == 2 && dt != BCONV_F32); }
-
 // FULL: no group of channels is padding alone (such groups are skipped).
-template <int DT, int DP, int GROUPS, int NT, int WAVES, bool FULL>
-__global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) void kv4_attention_kernel(AttnArgs a)
+template <int DT, int DP, int GROUPS, bool FULL>
+__global__ __launch_bounds__(attn_waves(DT, DP, GROUPS) * 64, min_waves(DT, DP, GROUPS)) void
+kv4_attention_kernel(AttnArgs a)
 {
     typedef typename Elem<DT>::type T;
     constexpr int STEPS = DP / 32;             // 32-channel steps of K Q^T
@@ -265,7 +262,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
     constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
     constexpr int VPER = TILES / GROUPS;       // of them a group
     constexpr int NP = kProbParts<DT>;
-    constexpr int COLS = 16 * NT;
+    constexpr int WAVES = attn_waves(DT, DP, GROUPS), COLS = kCols;
     constexpr int TABLE = kTable<GROUPS>;
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -290,7 +287,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
         next0 = block_of(part * a.part_tokens + wave * kTokens);
         next1 = block_of(part * a.part_tokens + wave * kTokens + 16);
     }
-    const Span sp = column_span(a, req, cb, COLS);
+    const Span sp = column_span(a, req, cb);
     if (sp.c0 >= sp.c1) return;
     const int span = sp.t1 - sp.t0;
     const int begin = sp.t0 + part * a.part_tokens;
@@ -318,34 +315,33 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
     }
 
     // this lane's columns: row of q, positions seen
-    Operand<DT> qf[STEPS][NT];
-    int lo[NT], hi[NT];
+    Operand<DT> qf[STEPS];
+    int lo, hi;
     int all_lo = 0, all_hi = 0x7fffffff;  // seen by every column
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int c = sp.c0 + n * 16 + row;
-        lo[n] = 0;
-        hi[n] = -1;
+    {
+        const int c = sp.c0 + row;
+        lo = 0;
+        hi = -1;
         const bool real = c < sp.c1;
         const int j = real ? (int)fastdiv((uint32_t)c, a.by_ratio) : 0, h = head * a.ratio + (real ? c - j * a.ratio : 0);
         if (real) {
             const int pos = sp.last + j;
-            lo[n] = first_seen(pos, a.window);
-            hi[n] = pos < a.max_context ? pos : a.max_context - 1;
-            all_lo = lo[n] > all_lo ? lo[n] : all_lo;
-            all_hi = hi[n] < all_hi ? hi[n] : all_hi;
+            lo = first_seen(pos, a.window);
+            hi = pos < a.max_context ? pos : a.max_context - 1;
+            all_lo = lo > all_lo ? lo : all_lo;
+            all_hi = hi < all_hi ? hi : all_hi;
         }
         const T *q = static_cast<const T *>(a.q) + (long long)(sp.q0 + j) * a.q_token + (long long)h * a.q_head;
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int d = s * 32 + lg * 8;
             if (real && d < a.g.dim) {
-                qf[s][n] = load_operand<DT>(q + d, d, a.g.dim, a.vec != 0);
+                qf[s] = load_operand<DT>(q + d, d, a.g.dim, a.vec != 0);
 #pragma unroll
-                for (int p = 0; p < kSplit<DT>; ++p) qf[s][n].part[p] ^= a.flip;
+                for (int p = 0; p < kSplit<DT>; ++p) qf[s].part[p] ^= a.flip;
             } else {
 #pragma unroll
-                for (int p = 0; p < kSplit<DT>; ++p) qf[s][n].part[p] = u32x4{0, 0, 0, 0};
+                for (int p = 0; p < kSplit<DT>; ++p) qf[s].part[p] = u32x4{0, 0, 0, 0};
             }
         }
     }
@@ -358,30 +354,28 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
     // sums of q over each group, for the midpoints and the codes' offset
-    float qsum[GROUPS][NT];
-    f32x4 qoff[DT == BCONV_BF16 ? GROUPS : 1][NT];
+    float qsum[GROUPS];
+    f32x4 qoff[DT == BCONV_BF16 ? GROUPS : 1];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g)
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        {
             f32x4 x = {0, 0, 0, 0};
             const u32x4 one = DT == BCONV_F16 ? u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u} : bf16_const(1.0f);
 #pragma unroll
-            for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s][n], x);
-            qsum[g][n] = x[0];
-            if constexpr (DT == BCONV_BF16) qoff[g][n] = x * -24.0f;
+            for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s], x);
+            qsum[g] = x[0];
+            if constexpr (DT == BCONV_BF16) qoff[g] = x * -24.0f;
         }
 
-    f32x4 acc[TILES][NT];
-    float mid[GROUPS][NT], m[NT], l[NT];
+    f32x4 acc[TILES];
+    float mid[GROUPS], m, l;
+    {
+        m = kLowest;
+        l = 0.0f;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n] = kLowest;
-        l[n] = 0.0f;
+        for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int k = 0; k < TILES; ++k) acc[k][n] = f32x4{0, 0, 0, 0};
-#pragma unroll
-        for (int g = 0; g < GROUPS; ++g) mid[g][n] = 0.0f;
+        for (int g = 0; g < GROUPS; ++g) mid[g] = 0.0f;
     }
     const Zero<DT> eight(8);
     const u32x4 offset = bf16_const(-kValueOffset<DT>);
@@ -408,35 +402,31 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
             ks[x] = keys.table[x];
             vs[x] = values.table[x];
         }
-        f32x4 z[2][NT];
+        f32x4 z[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-#pragma unroll
-            for (int n = 0; n < NT; ++n) z[u][n] = f32x4{0, 0, 0, 0};
+             z[u] = f32x4{0, 0, 0, 0};
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             if (!FULL && g * PER * 32 >= a.g.dim) continue;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                f32x4 d[NT];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    if constexpr (DT == BCONV_BF16) d[n] = qoff[g][n];
-                    else d[n] = f32x4{0, 0, 0, 0};
+                f32x4 d;
+                {
+                    if constexpr (DT == BCONV_BF16) d = qoff[g];
+                    else d = f32x4{0, 0, 0, 0};
                 }
 #pragma unroll
                 for (int s = 0; s < PER; ++s) {
                     const u32x4 k = decode<DT>(keys.w[u][g * PER + s], eight, kbits);
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) d[n] = mfma_parts<DT>(k, qf[g * PER + s][n], d[n]);
+                     d = mfma_parts<DT>(k, qf[g * PER + s], d);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const f16x2 sb = __builtin_bit_cast(f16x2, entry(ks, (4 * u + i) * GROUPS + g));
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        z[u][n][i] = __builtin_fmaf((float)sb[0], d[n][i], z[u][n][i]);
-                        z[u][n][i] = __builtin_fmaf((float)sb[1], qsum[g][n], z[u][n][i]);
+                    {
+                        z[u][i] = __builtin_fmaf((float)sb[0], d[i], z[u][i]);
+                        z[u][i] = __builtin_fmaf((float)sb[1], qsum[g], z[u][i]);
                     }
                 }
             }
@@ -451,9 +441,8 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const int pos = t + vrun + 4 * u + i;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        if (!known || pos < lo[n] || pos > hi[n]) z[u][n][i] = -__builtin_inff();
+                    
+                        if (!known || pos < lo || pos > hi) z[u][i] = -__builtin_inff();
                 }
 #pragma unroll
             for (int x = 0; x < TABLE; ++x) {
@@ -463,26 +452,25 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
         }
 
         // running softmax
-        float p[NT][8];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float top = fmaxf(fmaxf(fmaxf(z[0][n][0], z[0][n][1]), fmaxf(z[0][n][2], z[0][n][3])),
-                              fmaxf(fmaxf(z[1][n][0], z[1][n][1]), fmaxf(z[1][n][2], z[1][n][3])));
+        float p[8];
+        {
+            float top = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
+                              fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
             top *= a.scale_log2;
-            if (__any(top > m[n] + kSlack)) {
-                top = fmaxf(m[n], lane_groups_max(top));
-                const float f = __builtin_amdgcn_exp2f(m[n] - top);
-                m[n] = top;
-                l[n] *= f;
+            if (__any(top > m + kSlack)) {
+                top = fmaxf(m, lane_groups_max(top));
+                const float f = __builtin_amdgcn_exp2f(m - top);
+                m = top;
+                l *= f;
 #pragma unroll
-                for (int k = 0; k < TILES; ++k) acc[k][n] *= f;
+                for (int k = 0; k < TILES; ++k) acc[k] *= f;
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) mid[g][n] *= f;
+                for (int g = 0; g < GROUPS; ++g) mid[g] *= f;
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                p[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i >> 2][n][i & 3], a.scale_log2, -m[n]));
-                l[n] += p[n][i];
+                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i >> 2][i & 3], a.scale_log2, -m));
+                l += p[i];
             }
         }
 
@@ -493,21 +481,20 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
             f16x2 sb[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) sb[i] = __builtin_bit_cast(f16x2, entry(vs, i * GROUPS + g));
-            u32x4 pp[NT][NP];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
+            u32x4 pp[NP];
+            {
                 float ps[8];
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    ps[i] = __builtin_fmaf((float)sb[i][0], p[n][i], 0.0f);  // one instruction, with the conversion
-                    mid[g][n] = __builtin_fmaf((float)sb[i][1], p[n][i], mid[g][n]);
+                    ps[i] = __builtin_fmaf((float)sb[i][0], p[i], 0.0f);  // one instruction, with the conversion
+                    mid[g] = __builtin_fmaf((float)sb[i][1], p[i], mid[g]);
                 }
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const bf16x2 r = {(__bf16)ps[2 * i], (__bf16)ps[2 * i + 1]};
-                        pp[n][k][i] = __builtin_bit_cast(uint32_t, r);
+                        pp[k][i] = __builtin_bit_cast(uint32_t, r);
                         if (k + 1 < NP) {
                             ps[2 * i] -= (float)r[0];
                             ps[2 * i + 1] -= (float)r[1];
@@ -525,12 +512,11 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
                                                                half ? 0x07060302u : 0x05040100u);
                     v[i] = value_pair<DT>(two, tile & 3, vbits);
                 }
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
+                
 #pragma unroll
                     for (int k = NP - 1; k >= 0; --k) {
-                        acc[tile][n] = mfma16<BCONV_BF16>(offset, pp[n][k], acc[tile][n]);
-                        acc[tile][n] = mfma16<BCONV_BF16>(v, pp[n][k], acc[tile][n]);
+                        acc[tile] = mfma16<BCONV_BF16>(offset, pp[k], acc[tile]);
+                        acc[tile] = mfma16<BCONV_BF16>(v, pp[k], acc[tile]);
                     }
             }
         }
@@ -541,30 +527,28 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
     float *so = lds;                             // [waves][COLS][DP + 4]
     float *sm = lds + WAVES * COLS * (DP + 4);   // [waves][COLS]
     float *sl = sm + WAVES * COLS;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        l[n] = lane_groups_sum(l[n]);
+    {
+        l = lane_groups_sum(l);
         if (lg == 0) {
-            sm[wave * COLS + n * 16 + row] = m[n];
-            sl[wave * COLS + n * 16 + row] = l[n];
+            sm[wave * COLS + row] = m;
+            sl[wave * COLS + row] = l;
         }
     }
     __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    {
         float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + n * 16 + row]);
-        const float f = __builtin_amdgcn_exp2f(m[n] - top);
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + row]);
+        const float f = __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const float add = lane_groups_sum(mid[g][n]);
+            const float add = lane_groups_sum(mid[g]);
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;
-                if (n * 16 + row < sp.c1 - sp.c0)
-                    *reinterpret_cast<f32x4 *>(so + (wave * COLS + n * 16 + row) * (DP + 4) + tile * 16 + lg * 4) =
-                        (acc[tile][n] + add) * f;
+                if (row < sp.c1 - sp.c0)
+                    *reinterpret_cast<f32x4 *>(so + (wave * COLS + row) * (DP + 4) + tile * 16 + lg * 4) =
+                        (acc[tile] + add) * f;
             }
         }
     }
@@ -597,7 +581,7 @@ __global__ __launch_bounds__(WAVES * 64, min_waves(DT, DP, GROUPS, NT, WAVES)) v
 // channels, 2048 / DP slices of them every so-many-th part; the slices are
 // added in order.
 template <int DT, int DP>
-__global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a, int width_cols)
+__global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a)
 {
     typedef typename Elem<DT>::type T;
     constexpr int THREADS = DP / 4, SLICES = kMaxParts / THREADS, WAVES = kMaxParts / 64;
@@ -606,7 +590,7 @@ __global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a, int 
     const int per_head = a.max_q * a.ratio;
     const int id = blockIdx.x, tid = threadIdx.x;
     const int c = id % per_head, head = id / per_head % a.g.kv_heads, req = id / per_head / a.g.kv_heads;
-    const Span sp = column_span(a, req, c / width_cols, width_cols);
+    const Span sp = column_span(a, req, c / kCols);
     const int span = sp.t1 - sp.t0;
     if (c >= sp.c1 || span <= a.part_tokens) return;  // uniform over the workgroup
     const int used = (span + a.part_tokens - 1) / a.part_tokens;
@@ -652,58 +636,49 @@ __global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a, int 
 
 // ------------------------------------------------------------------ dispatch
 
-template <int DT, int DP, int GROUPS, int NT, int WAVES, bool FULL>
-hipError_t launch_attention_waves(const AttnArgs &a, hipStream_t s)
+template <int DT, int DP, int GROUPS, bool FULL>
+hipError_t launch_attention_full(const AttnArgs &a, hipStream_t s)
 {
-    const size_t lds = (size_t)WAVES * 16 * NT * (DP + 4 + 2) * sizeof(float);
+    constexpr int WAVES = attn_waves(DT, DP, GROUPS);
+    const size_t lds = (size_t)WAVES * kCols * (DP + 4 + 2) * sizeof(float);
     const long long grid = (long long)a.requests * a.g.kv_heads * a.col_blocks * a.parts;
-    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, NT, WAVES, FULL>), dim3((unsigned)grid), dim3(WAVES * 64), lds, s, a);
+    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, FULL>), dim3((unsigned)grid), dim3(WAVES * 64), lds, s, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.parts > 1) {
         const long long cols = (long long)a.requests * a.g.kv_heads * a.max_q * a.ratio;
-        hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3((unsigned)cols), dim3(kMaxParts), 0, s, a, 16 * NT);
+        hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3((unsigned)cols), dim3(kMaxParts), 0, s, a);
         e = hipGetLastError();
     }
     return e;
 }
 
-template <int DT, int DP, int GROUPS, bool FULL>
-hipError_t launch_attention_full(const AttnArgs &a, const AttnShape &h, hipStream_t s)
-{
-    if constexpr (DP <= 128)
-        if (h.nt == 2) return launch_attention_waves<DT, DP, GROUPS, 2, 4, FULL>(a, s);
-    if constexpr (fits_8_waves(DT, DP, GROUPS))
-        if (h.waves == 8) return launch_attention_waves<DT, DP, GROUPS, 1, 8, FULL>(a, s);
-    return launch_attention_waves<DT, DP, GROUPS, 1, 4, FULL>(a, s);
-}
-
 template <int DT, int DP, int GROUPS>
-hipError_t launch_attention_kernel(const AttnArgs &a, const AttnShape &h, hipStream_t s)
+hipError_t launch_attention_kernel(const AttnArgs &a, hipStream_t s)
 {
-    if (a.g.dim > DP - DP / GROUPS) return launch_attention_full<DT, DP, GROUPS, true>(a, h, s);
-    if constexpr (GROUPS > 1) return launch_attention_full<DT, DP, GROUPS, false>(a, h, s);
+    if (a.g.dim > DP - DP / GROUPS) return launch_attention_full<DT, DP, GROUPS, true>(a, s);
+    if constexpr (GROUPS > 1) return launch_attention_full<DT, DP, GROUPS, false>(a, s);
     return hipErrorInvalidValue;  // not reached: one group is never empty
 }
 
 template <int DT, int DP>
-hipError_t launch_attention_dim(const AttnArgs &a, const AttnShape &h, hipStream_t s)
+hipError_t launch_attention_dim(const AttnArgs &a, hipStream_t s)
 {
     switch (a.g.groups) {
-    case 1: if constexpr (DP <= 128) return launch_attention_kernel<DT, DP, 1>(a, h, s); else break;
-    case 2: return launch_attention_kernel<DT, DP, 2>(a, h, s);
-    case 4: if constexpr (DP >= 128) return launch_attention_kernel<DT, DP, 4>(a, h, s); else break;
-    case 8: if constexpr (DP >= 256) return launch_attention_kernel<DT, DP, 8>(a, h, s); else break;
+    case 1: if constexpr (DP <= 128) return launch_attention_kernel<DT, DP, 1>(a, s); else break;
+    case 2: return launch_attention_kernel<DT, DP, 2>(a, s);
+    case 4: if constexpr (DP >= 128) return launch_attention_kernel<DT, DP, 4>(a, s); else break;
+    case 8: if constexpr (DP >= 256) return launch_attention_kernel<DT, DP, 8>(a, s); else break;
     }
     return hipErrorInvalidValue;
 }
 
 template <int DT>
-hipError_t launch_attention(const AttnArgs &a, const AttnShape &h, hipStream_t s)
+hipError_t launch_attention(const AttnArgs &a, hipStream_t s)
 {
     switch (a.g.dim_padded) {
-    case 64: return launch_attention_dim<DT, 64>(a, h, s);
-    case 128: return launch_attention_dim<DT, 128>(a, h, s);
-    default: return launch_attention_dim<DT, 256>(a, h, s);
+    case 64: return launch_attention_dim<DT, 64>(a, s);
+    case 128: return launch_attention_dim<DT, 128>(a, s);
+    default: return launch_attention_dim<DT, 256>(a, s);
     }
 }
 
@@ -715,7 +690,6 @@ using bconv::fail;
 
 struct AttnPlan {
     bconv::AttnArgs a;
-    bconv::AttnShape shape;
     size_t o_bytes, bytes;  // partial results: sums, then (maximum, denominator) pairs
     bool empty;
 };
@@ -789,27 +763,34 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
     a.flip = t->scale < 0.0f ? 0x80008000u : 0u;
     a.vec = (uintptr_t)t->q % 16 == 0 && t->q_token_stride * es % 16 == 0 && t->q_head_stride * es % 16 == 0;
 
-    p->shape.nt = a.max_q * a.ratio > 16 && a.g.dim_padded <= 128 ? 2 : 1;
-    if (getenv("AT_N")) p->shape.nt = atoi(getenv("AT_N"));
-    const int cols = 16 * p->shape.nt;
     if ((long long)a.max_q * a.ratio >= (1LL << 30)) return fail(BCONV_ERR_INVALID_ARGUMENT, "max_q*heads too large");
-    a.col_blocks = (a.max_q * a.ratio + cols - 1) / cols;
+    a.col_blocks = (a.max_q * a.ratio + bconv::kCols - 1) / bconv::kCols;
     const long long tiles = (long long)a.requests * a.g.kv_heads * a.col_blocks;
     if (tiles >= (1LL << 29)) return fail(BCONV_ERR_INVALID_ARGUMENT, "requests*heads*max_q too large for one call");
     // tokens that the columns of one workgroup can see, from a multiple of the tile
     long long seen = most;
     if (a.window > 0) {
-        const long long w = (long long)a.window + (cols + a.ratio - 1) / a.ratio;
+        const long long w = (long long)a.window + (bconv::kCols + a.ratio - 1) / a.ratio;
         if (w < seen) seen = w;
     }
     seen += bconv::kTokens;
-    p->shape.waves = tiles >= 512 || p->shape.nt == 2 || !bconv::fits_8_waves(t->dtype, a.g.dim_padded, a.g.groups) ? 4 : 8;
-    if (getenv("AT_W")) p->shape.waves = atoi(getenv("AT_W"));
-    const long long want = ((getenv("AT_T") ? atoi(getenv("AT_T")) : 4LL) * compute_units() + tiles - 1) / tiles;
-    long long part = (seen + want - 1) / want;
-    const int least = getenv("AT_P") ? atoi(getenv("AT_P")) : 1024;
-    if (part < least) part = least;
-    if (part < (seen + bconv::kMaxParts - 1) / bconv::kMaxParts) part = (seen + bconv::kMaxParts - 1) / bconv::kMaxParts;
+    // Parts of the long axis: two workgroups a compute unit, a part no shorter
+    // than 64 tokens a wave and no more than 128 parts a row, which their join
+    // would outweigh, and none longer than 1056 a wave, so that one long request
+    // among short ones is shared.  Up to 136 tokens a wave stay whole: the join's
+    // launch costs more than the second half of the tokens (777 tokens, two
+    // key/value heads: 7.8 us whole, 10.4 in two; 4 requests of 8192 tokens,
+    // eight heads: 17 us in parts of 512, 21 in parts of 1024).
+    const int waves = bconv::attn_waves(t->dtype, a.g.dim_padded, a.g.groups);
+    long long part = seen;
+    if (seen > 136 * waves) {
+        const long long want = (2LL * compute_units() + tiles - 1) / tiles;
+        part = (seen + want - 1) / want;
+        if (part < 64 * waves) part = 64 * waves;
+        if (part < (seen + 127) / 128) part = (seen + 127) / 128;
+        if (part > 1056 * waves) part = 1056 * waves;
+        if (part < (seen + bconv::kMaxParts - 1) / bconv::kMaxParts) part = (seen + bconv::kMaxParts - 1) / bconv::kMaxParts;
+    }
     part = (part + bconv::kTokens - 1) / bconv::kTokens * bconv::kTokens;
     a.part_tokens = (int)part;
     a.parts = (int)((seen + part - 1) / part);
@@ -859,9 +840,9 @@ bconv_status_t bconv_kv4_attention(const bconv_kv4_desc_t *desc, void *stream, c
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e;
     switch (args->dtype) {
-    case BCONV_F32: e = bconv::launch_attention<BCONV_F32>(p.a, p.shape, s); break;
-    case BCONV_F16: e = bconv::launch_attention<BCONV_F16>(p.a, p.shape, s); break;
-    default: e = bconv::launch_attention<BCONV_BF16>(p.a, p.shape, s); break;
+    case BCONV_F32: e = bconv::launch_attention<BCONV_F32>(p.a, s); break;
+    case BCONV_F16: e = bconv::launch_attention<BCONV_F16>(p.a, s); break;
+    default: e = bconv::launch_attention<BCONV_BF16>(p.a, s); break;
     }
     if (e != hipSuccess) return bconv::hip_fail(e, "cache attention kernel");
     return BCONV_OK;
