@@ -288,39 +288,49 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4Args a, Q4Many q)
         if (lane < 16) q.xs[((long long)tile * groups + g) * 16 + lane] = sum[0];
 }
 
-constexpr int kManyRows = 4;  // output tiles a wave
+// Rows of x a workgroup takes: 128 (64 in fp32, whose operands are three
+// parts), or the 64 or 32 that hold them all.
+constexpr int most_cols(int dtype) { return dtype == BCONV_F32 ? 64 : 128; }
 
-// Column tiles a wave takes at most: 64 rows of x, or 32 in fp32, whose
-// operands are three parts.
-constexpr int most_cols(int dtype) { return dtype == BCONV_F32 ? 2 : 4; }
+// Shape of a workgroup of the many-row kernel: its four waves take 64 outputs
+// each and, for 32 rows of x, lie along the outputs; otherwise two by two.
+template <int COLS> struct ManyShape {
+    static constexpr int WC = COLS == 32 ? 1 : 2;     // waves along the rows of x
+    static constexpr int CB = COLS / (32 * WC);       // blocks of 32 rows of x a wave
+    static constexpr int TILES = 4 / WC * 4;          // output tiles a workgroup
+};
 
-// A workgroup takes 128 outputs and 2 NT column tiles, its four waves a
-// quarter each.  Everything the waves share (the columns' operands and sums,
-// scales and zero points) goes to LDS a chunk ahead, by loads that pass no
-// registers; the codes go to registers, a chunk ahead too.
-template <int DT, bool ZP, int STEPS, int NT>
+// Everything the waves share (the operands and sums of x, scales and zero
+// points) goes to LDS a chunk ahead, by loads that pass no registers; the codes
+// go to registers, a chunk ahead too.  v_mfma_f32_32x32x16 rather than
+// 16x16x32: vector instructions issue beside a matrix instruction for all but
+// some 10 of its cycles, whatever its size, and the larger one does twice the
+// work in them (measured: 12 vector instructions with one 32x32x16, 58 cycles;
+// 6 with one 16x16x32, twice, 68).
+template <int DT, bool ZP, int STEPS, int COLS>
 __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q4Args a, Q4Many q)
 {
-    constexpr int RT = kManyRows, P = kSplit<DT>, G = 4 / STEPS;
-    constexpr int UNITS = 2 * NT * 4 * P;  // KiB of operands a chunk
+    typedef ManyShape<COLS> S;
+    constexpr int P = kSplit<DT>, G = 4 / STEPS, CB = S::CB, CT = COLS / 16, RT = S::TILES;
+    constexpr int UNITS = CT * 4 * P;  // KiB of operands a chunk
     struct Stage {
         u32x4 x[UNITS * 64];
-        uint32_t scales[2 * RT * G * 8];                      // [tile][group][16] fp16
-        float xs[DT == BCONV_BF16 ? 2 * NT * G * 16 : 1];     // [column tile][group][16]
-        uint32_t zeros[ZP ? 2 * RT * G * 4 : 1];              // [tile][group][16] bytes
+        uint32_t scales[RT * G * 8];                      // [tile][group][16] fp16
+        float xs[DT == BCONV_BF16 ? CT * G * 16 : 4];     // [column tile][group][16]
+        uint32_t zeros[ZP ? RT * G * 4 : 4];              // [tile][group][16] bytes
     };
     __shared__ Stage stage[2];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int row = lane & 15, lg = lane >> 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane & 31, half = lane >> 5;
     // Blocks go to the XCDs in turn: the splits of the inputs come first, so
     // that an XCD's L2 sees one slice of x and each code once per column block.
     int id = blockIdx.x;
     const int split = id % q.splits;
     id /= q.splits;
-    const int cb = id % q.col_blocks, rb = id / q.col_blocks;
+    const int cb0 = id % q.col_blocks, rb0 = id / q.col_blocks;
     const int c_begin = (int)((long long)a.chunks * split / q.splits), c_end = (int)((long long)a.chunks * (split + 1) / q.splits);
-    const int tile0 = rb * 2 * RT, col0 = cb * 2 * NT;
-    const int my_row = (wave >> 1) * RT, my_col = (wave & 1) * NT;
+    const int tile0 = rb0 * RT, col0 = cb0 * CT;
+    const int my_row = wave / S::WC * 4, my_col = wave % S::WC * CB * 2;  // first output and column tile of the wave
     const CodeBits bits = code_bits<DT>();
 
     auto tile_chunk = [&](int tile, int c) { return (long long)(tile < a.tiles ? tile : a.tiles - 1) * a.chunks + c; };
@@ -333,43 +343,56 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
             const u32x4 *src = q.xp + (((long long)(col0 + t) * a.chunks + c) * 4 * P + rest) * 64 + lane;
             __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.x[u * 64]), 16, 0, 0);
         }
-        // 4 bytes a lane; a tile's part of a chunk is consecutive
+        // 4 bytes a lane, the waves in turn; a tile's part of a chunk is consecutive
 #pragma unroll
-        for (int i = 0; i < G; ++i) {
-            if ((i & 3) == wave) {
-                const int e = i * 64 + lane, t = e / (G * 8);
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.scales) + tile_chunk(tile0 + t, c) * G * 8 + e % (G * 8);
+        for (int i = 0; i < (RT * G * 8 + 63) / 64; ++i) {
+            const int e = i * 64 + lane;
+            if ((i & 3) == wave && e < RT * G * 8) {
+                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.scales) +
+                                      tile_chunk(tile0 + e / (G * 8), c) * G * 8 + e % (G * 8);
                 __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.scales[i * 64]), 4, 0, 0);
             }
-            if (ZP && ((i + 1) & 3) == wave && lane < 32) {
-                const int e = i * 32 + lane, t = e / (G * 4);
-                const uint32_t *src = reinterpret_cast<const uint32_t *>(a.zeros) + tile_chunk(tile0 + t, c) * G * 4 + e % (G * 4);
-                __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.zeros[i * 32]), 4, 0, 0);
+        }
+        if constexpr (ZP) {
+#pragma unroll
+            for (int i = 0; i < (RT * G * 4 + 63) / 64; ++i) {
+                const int e = i * 64 + lane;
+                if (((i + 1) & 3) == wave && e < RT * G * 4) {
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>(a.zeros) +
+                                          tile_chunk(tile0 + e / (G * 4), c) * G * 4 + e % (G * 4);
+                    __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.zeros[i * 64]), 4, 0, 0);
+                }
             }
         }
         if constexpr (DT == BCONV_BF16) {
-            constexpr int LOADS = 2 * NT * G * 16 / 64 > 0 ? 2 * NT * G * 16 / 64 : 1;
 #pragma unroll
-            for (int i = 0; i < LOADS; ++i) {
-                const int e = i * 64 + lane, t = e / (G * 16);
-                if (((i + 2) & 3) == wave && e < 2 * NT * G * 16) {
-                    const float *src = q.xs + ((long long)(col0 + t) * a.chunks + c) * G * 16 + e % (G * 16);
+            for (int i = 0; i < (CT * G * 16 + 63) / 64; ++i) {
+                const int e = i * 64 + lane;
+                if (((i + 2) & 3) == wave && e < CT * G * 16) {
+                    const float *src = q.xs + ((long long)(col0 + e / (G * 16)) * a.chunks + c) * G * 16 + e % (G * 16);
                     __builtin_amdgcn_global_load_lds((const void *)src, (Lds)(&st.xs[i * 64]), 4, 0, 0);
                 }
             }
         }
     };
-    u32x4 w[RT], wn[RT];
+    // Row `row` of a 32 x 16 operand of step (s, j), k = 32 s + 16 j + 8 half on,
+    // is word s of lane 16 (2 j + half) + row % 16 of output tile row / 16.
+    u32x4 w[2][2], wn[2][2];
     auto fetch = [&](int c) {
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
-            wn[r] = *reinterpret_cast<const u32x4 *>(a.codes + tile_chunk(tile0 + my_row + r, c) * 256 + lane * 4);
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+                wn[r][j] = *reinterpret_cast<const u32x4 *>(
+                    a.codes + tile_chunk(tile0 + my_row + r * 2 + (row >> 4), c) * 256 + ((2 * j + half) * 16 + (row & 15)) * 4);
     };
-    f32x4 acc[RT][NT];
+    f32x16 acc[2][CB];
 #pragma unroll
-    for (int r = 0; r < RT; ++r)
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[r][t] = f32x4{0, 0, 0, 0};
+        for (int t = 0; t < CB; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[r][t][i] = 0.0f;
 
     if (c_begin < c_end) {
         request(c_begin);
@@ -379,7 +402,9 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
         __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xf << 8));  // vmcnt(0): this chunk's operands and codes are here
         __syncthreads();                                          // in every wave, and the other stage is read
 #pragma unroll
-        for (int r = 0; r < RT; ++r) w[r] = wn[r];
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) w[r][j] = wn[r][j];
         if (c + 1 < c_end) {
             request(c + 1);
             fetch(c + 1);
@@ -387,66 +412,85 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
         const Stage &st = stage[c & 1];
 #pragma unroll
         for (int g = 0; g < G; ++g) {
-            // the group's columns stay in registers for the four output tiles
-            Operand<DT> b[STEPS][NT];
+            // the group's columns stay in registers for the 64 outputs
+            u32x4 b[STEPS][2][CB][P];
 #pragma unroll
             for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                for (int j = 0; j < 2; ++j)
 #pragma unroll
-                    for (int p = 0; p < P; ++p)
-                        b[s][t].part[p] = st.x[(((my_col + t) * 4 + g * STEPS + s) * P + p) * 64 + lane];
-            float xs[NT];
+                    for (int t = 0; t < CB; ++t)
 #pragma unroll
-            for (int t = 0; t < NT; ++t) xs[t] = DT == BCONV_BF16 ? st.xs[((my_col + t) * G + g) * 16 + row] : 0.0f;
+                        for (int p = 0; p < P; ++p)
+                            b[s][j][t][p] = st.x[(((my_col + t * 2 + (row >> 4)) * 4 + g * STEPS + s) * P + p) * 64 +
+                                                 (2 * j + half) * 16 + (row & 15)];
+            f32x16 off[CB];  // bf16 without zero points: every sum starts from -24 sum x
+            float xs[CB];
 #pragma unroll
-            for (int r = 0; r < RT; ++r) {
+            for (int t = 0; t < CB; ++t) {
+                xs[t] = DT == BCONV_BF16 ? st.xs[((my_col + t * 2 + (row >> 4)) * G + g) * 16 + (row & 15)] : 0.0f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) off[t][i] = xs[t];
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
                 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
-                const int at = (my_row + r) * G + g;
-                const f16x4 s4 = *reinterpret_cast<const f16x4 *>(&st.scales[at * 8 + lg * 2]);
-                int z = 8;
-                float z4[4];
-                if constexpr (ZP) {
-                    if constexpr (DT == BCONV_BF16) {
-                        const uint32_t zz = st.zeros[at * 4 + lg];
+                // results 4 v + i are rows 8 v + 4 half + i of the 32
+                f16x4 s4[4];
+                uint32_t z4[4];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) z4[i] = (float)(16 + ((zz >> (8 * i)) & 255u));
+                for (int v = 0; v < 4; ++v) {
+                    const int at = (my_row + r * 2 + (v >> 1)) * G + g, four = (v & 1) * 2 + half;
+                    s4[v] = *reinterpret_cast<const f16x4 *>(&st.scales[at * 8 + four * 2]);
+                    if constexpr (ZP && DT == BCONV_BF16) z4[v] = st.zeros[at * 4 + four];
+                }
+                int z = 8;
+                if constexpr (ZP && DT != BCONV_BF16)
+                    z = reinterpret_cast<const uint8_t *>(st.zeros)[((my_row + r * 2 + (row >> 4)) * G + g) * 16 + (row & 15)];
+                const Zero<DT> zero(z);
+                f32x16 d[CB];
+#pragma unroll
+                for (int t = 0; t < CB; ++t) {
+                    if constexpr (ZP && DT == BCONV_BF16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) d[t][i] = (float)(16 + ((z4[i >> 2] >> (8 * (i & 3))) & 255u)) * xs[t];
                     } else {
-                        z = reinterpret_cast<const uint8_t *>(st.zeros)[at * 16 + row];
+                        d[t] = off[t];
                     }
                 }
-                const Zero<DT> zero(z);
-                f32x4 d[NT];
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    if constexpr (DT == BCONV_BF16 && ZP) d[t] = f32x4{z4[0] * xs[t], z4[1] * xs[t], z4[2] * xs[t], z4[3] * xs[t]};
-                    else d[t] = f32x4{xs[t], xs[t], xs[t], xs[t]};
-                }
+                for (int s = 0; s < STEPS; ++s)
 #pragma unroll
-                for (int s = 0; s < STEPS; ++s) {
-                    const u32x4 k = decode<DT>(w[r][g * STEPS + s], zero, bits);
+                    for (int j = 0; j < 2; ++j) {
+                        const u32x4 k = decode<DT>(w[r][j][g * STEPS + s], zero, bits);
 #pragma unroll
-                    for (int t = 0; t < NT; ++t) d[t] = mfma_parts<DT>(k, b[s][t], d[t]);
-                }
+                        for (int t = 0; t < CB; ++t)
 #pragma unroll
-                for (int t = 0; t < NT; ++t)
+                            for (int p = P - 1; p >= 0; --p) d[t] = mfma32<DT>(k, b[s][j][t][p], d[t]);
+                    }
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) acc[r][t][i] = __builtin_fmaf((float)s4[i], d[t][i], acc[r][t][i]);
+                for (int t = 0; t < CB; ++t)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        acc[r][t][i] = __builtin_fmaf((float)s4[i >> 2][i & 3], d[t][i], acc[r][t][i]);
             }
         }
     }
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int o0 = (tile0 + my_row + r) * 16 + lg * 4;
+    for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int m = (col0 + my_col + t) * 16 + row;
-            if (q.splits > 1)
-                *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * q.col_tiles * 16 + m) * q.padded_n + o0) = acc[r][t];
-            else if (m < a.m && o0 < a.n)
-                store_outputs<DT>(a, m, o0, acc[r][t]);
+        for (int t = 0; t < CB; ++t) {
+            const int m = (col0 + my_col + t * 2) * 16 + row;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int o0 = (tile0 + my_row + r * 2) * 16 + v * 8 + half * 4;
+                const f32x4 sum = {acc[r][t][4 * v], acc[r][t][4 * v + 1], acc[r][t][4 * v + 2], acc[r][t][4 * v + 3]};
+                if (q.splits > 1)
+                    *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * q.col_tiles * 16 + m) * q.padded_n + o0) = sum;
+                else if (m < a.m && o0 < a.n)
+                    store_outputs<DT>(a, m, o0, sum);
+            }
         }
-    }
 }
 
 // Adds the splits' sums in order.
@@ -470,7 +514,7 @@ __global__ __launch_bounds__(256) void q4_reduce_kernel(Q4Args a, Q4Many q)
 struct Q4Plan {
     bool many;
     int rt, waves;  // few: output tiles and waves a workgroup
-    int nt;         // many: column tiles a wave
+    int cols;       // many: rows of x a workgroup
     Q4Many q;
     size_t xs_offset, sums_offset, bytes;
 };
@@ -500,14 +544,13 @@ Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, in
         return p;
     }
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
-    int nt = most_cols(dtype);
-    while (nt > 1 && 16 * nt >= rows) nt /= 2;
-    p.nt = nt;
+    p.cols = rows <= 32 ? 32 : rows <= 64 ? 64 : most_cols(dtype);
     const int parts = dtype == BCONV_F32 ? 3 : 1;
-    p.q.col_blocks = (rows + 32 * nt - 1) / (32 * nt);
-    p.q.col_tiles = p.q.col_blocks * 2 * nt;
-    p.q.row_blocks = (tiles + 2 * kManyRows - 1) / (2 * kManyRows);
-    p.q.padded_n = p.q.row_blocks * 2 * kManyRows * 16;
+    const int block_tiles = p.cols == 32 ? ManyShape<32>::TILES : ManyShape<64>::TILES;
+    p.q.col_blocks = (rows + p.cols - 1) / p.cols;
+    p.q.col_tiles = p.q.col_blocks * (p.cols / 16);
+    p.q.row_blocks = (tiles + block_tiles - 1) / block_tiles;
+    p.q.padded_n = p.q.row_blocks * block_tiles * 16;
     const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks;
     // two workgroups a compute unit; a slice holds at least 4 chunks
     long long splits = (2LL * cus + blocks - 1) / blocks;
@@ -537,12 +580,13 @@ hipError_t run_linear(const Q4Args &a, const Q4Plan &p, hipStream_t s)
         hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
         const long long blocks = (long long)p.q.row_blocks * p.q.col_blocks * p.q.splits;
-        if (p.nt == 1)
-            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, 1>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
-        else if (p.nt == 2)
-            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
+        const dim3 grid((unsigned)blocks);
+        if (p.cols == 32)
+            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, 32>), grid, dim3(256), 0, s, a, p.q);
+        else if (p.cols == 64)
+            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, 64>), grid, dim3(256), 0, s, a, p.q);
         else
-            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, most_cols(DT)>), dim3((unsigned)blocks), dim3(256), 0, s, a, p.q);
+            hipLaunchKernelGGL((q4_many_kernel<DT, ZP, STEPS, most_cols(DT)>), grid, dim3(256), 0, s, a, p.q);
         e = hipGetLastError();
         if (e != hipSuccess || p.q.splits == 1) return e;
         const long long outs = (long long)((a.n + 3) / 4) * a.m;

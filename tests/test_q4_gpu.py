@@ -95,6 +95,54 @@ def test_linear(dev, dtype, rows, k, n, group, zeros, bias):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,k,n,group,zeros,bias", [
+    (17, 8200, 4100, 64, True, True),
+    (33, 5000, 4400, 32, False, False),
+    (50, 4100, 4111, 128, True, False),
+    (65, 3333, 4000, 128, False, True),
+    (130, 2049, 3500, 64, False, False),
+    (130, 2049, 3500, 32, True, True),
+    (300, 1100, 3100, 128, True, False),
+    (300, 1100, 3100, 64, True, True),
+    (2000, 300, 1400, 32, False, True),   # inputs too short to split
+    (2000, 300, 1400, 128, True, False),
+])
+def test_linear_many_rows(dev, dtype, rows, k, n, group, zeros, bias):
+    """Products large enough for the many-row kernel: each width of its column
+    blocks, split and whole inputs, ragged last tiles and chunks."""
+    say("linear many", dtype, rows, k, n, group, zeros, bias)
+    rng = np.random.default_rng(rows * 1000003 + k * 1009 + n)
+    layer, *w = make_linear(rng, k, n, group, zeros, bias)
+    assert layer.workspace_bytes(rows, DT[dtype]) > 0  # it takes that kernel
+    x = torch.from_numpy(rng.normal(0, 1, (rows, k)).astype(np.float32)).to(dev).to(DT[dtype])
+    buf = torch.full((rows, n + 3), 7.0, device=dev, dtype=DT[dtype])
+    ws = torch.full((layer.workspace_bytes(rows, DT[dtype]),), 0xff, dtype=torch.uint8, device=dev)
+    y = layer.forward(x, out=buf[:, :n], workspace=ws)
+    torch.cuda.synchronize()
+    check_linear(layer, w, x, y, group, dtype)
+    assert bool((buf[:, n:] == 7.0).all())
+    # strided, misaligned rows give the same
+    wide = torch.zeros((rows, k + 3), device=dev, dtype=DT[dtype])
+    wide[:, 1:k + 1] = x
+    assert torch.equal(layer.forward(wide[:, 1:k + 1]), y)
+    layer.close()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32", "bf16"])
+def test_linear_many_rows_nonfinite(dev, dtype):
+    """A bad row leaves the others alone in the many-row kernel too."""
+    rng = np.random.default_rng(15)
+    layer, *_ = make_linear(rng, 1100, 3100, 64, True, False)
+    x = rng.normal(0, 1, (300, 1100)).astype(np.float32)
+    clean = x.copy()
+    x[100, 7], x[101, 1099] = np.inf, np.nan
+    y = host(layer.forward(torch.from_numpy(x).to(dev).to(DT[dtype])))
+    z = host(layer.forward(torch.from_numpy(clean).to(dev).to(DT[dtype])))
+    assert not np.isfinite(y[100]).any() and np.isnan(y[101]).all()
+    assert np.array_equal(np.delete(y, [100, 101], 0), np.delete(z, [100, 101], 0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("rows", [1, 7, 40, 150])
 @pytest.mark.parametrize("ldx,offset,ldy", [(211, 0, 77), (208, 0, 80), (217, 3, 90), (224, 1, 71)])
 def test_linear_strides(dev, dtype, rows, ldx, offset, ldy):
@@ -122,7 +170,7 @@ def test_linear_same_sign(dev):
     for dtype in DT:
         for rows in (1, 20, 100):
             say("same sign", dtype, rows)
-            layer, *w = make_linear(rng, 2000, 64, 128, True, False)
+            layer, *w = make_linear(rng, 2000, 64 if rows < 100 else 5000, 128, True, False)
             x = torch.from_numpy(np.abs(rng.normal(0, 1, (rows, 2000))).astype(np.float32)).to(dev).to(DT[dtype])
             check_linear(layer, w, x, layer.forward(x), 128, dtype)
 
@@ -159,7 +207,7 @@ def test_linear_rows_agree(dev):
     """A row's result does not depend on its place in a batch of the same size."""
     rng = np.random.default_rng(13)
     layer, *_ = make_linear(rng, 1000, 100, 64, False, True)
-    for rows in (40, 300):
+    for rows in (40, 300, 3000):
         x = torch.from_numpy(rng.normal(0, 1, (rows, 1000)).astype(np.float32)).to(dev).bfloat16()
         perm = torch.randperm(rows, device=dev)
         assert torch.equal(layer.forward(x)[perm], layer.forward(x[perm].contiguous()))
@@ -179,10 +227,7 @@ def test_linear_shapes_and_streams(dev):
     y = layer.forward(big, stream=s)
     torch.cuda.current_stream().wait_stream(s)
     assert torch.equal(y, layer.forward(big))
-    ws = torch.empty(max(1, layer.workspace_bytes(150, torch.bfloat16)), dtype=torch.uint8, device=dev)
-    xb = torch.randn(150, 96, device=dev).bfloat16()
-    ws.fill_(0xff)
-    assert torch.equal(layer.forward(xb, workspace=ws), layer.forward(xb))
+    assert layer.workspace_bytes(150, torch.bfloat16) == 0  # few rows for so small a layer: no workspace
 
 
 # ------------------------------------------------------------------- cache
