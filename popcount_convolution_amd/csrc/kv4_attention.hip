@@ -118,9 +118,14 @@ template <int DT> constexpr int kProbParts = DT == BCONV_BF16 ? 1 : DT == BCONV_
 
 // A value code decodes to 128 + c in bf16 (all of whose 7 mantissa bits it
 // takes, with no shift for the first code) or, for fp32 results, to 16 + c,
-// whose offset costs fewer bits.  A product with the constant -(offset + 8)
-// follows each product, so the running sums hold code - 8 and never grow with
-// the offset.
+// whose offset costs fewer bits.  A product with the constant -(offset + 8) goes
+// with each product, so the running sums hold code - 8 and never grow with the
+// offset.  For bf16 results, whose own rounding hides what the offset costs an
+// fp32 sum, the sums of the probabilities are kept instead (one product a group
+// in place of one a channel tile) and taken out at the end: 128 channels in one
+// group, 32 requests of up to 8192 tokens 51.9 -> 50.3 us.  With two groups the
+// sums' registers would spill (58.3 -> 65.2 us).
+constexpr bool sums_probs(int dt, int dp, int groups) { return dt == BCONV_BF16 && !(dp == 128 && groups == 2); }
 template <int DT> constexpr float kValueOffset = DT == BCONV_F32 ? 24.0f : 136.0f;
 
 // The word that lane N of each 16 lanes holds.
@@ -264,6 +269,7 @@ kv4_attention_kernel(AttnArgs a)
     constexpr int NP = kProbParts<DT>;
     constexpr int WAVES = attn_waves(DT, DP, GROUPS), COLS = kCols;
     constexpr int TABLE = kTable<GROUPS>;
+    constexpr bool SUMS = sums_probs(DT, DP, GROUPS);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, lg = lane >> 4;
@@ -367,7 +373,7 @@ kv4_attention_kernel(AttnArgs a)
             if constexpr (DT == BCONV_BF16) qoff[g] = x * -24.0f;
         }
 
-    f32x4 acc[TILES];
+    f32x4 acc[TILES], psum[SUMS ? GROUPS : 1];
     float mid[GROUPS], m, l;
     {
         m = kLowest;
@@ -375,10 +381,13 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
         for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) mid[g] = 0.0f;
+        for (int g = 0; g < GROUPS; ++g) {
+            mid[g] = 0.0f;
+            if constexpr (SUMS) psum[g] = f32x4{0, 0, 0, 0};
+        }
     }
     const Zero<DT> eight(8);
-    const u32x4 offset = bf16_const(-kValueOffset<DT>);
+    const u32x4 offset = bf16_const(SUMS ? 1.0f : -kValueOffset<DT>);
     const CodeBits kbits = code_bits<DT>(), vbits = value_bits<DT>();
 
     const int vrun = lg * 8;
@@ -465,7 +474,10 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
                 for (int k = 0; k < TILES; ++k) acc[k] *= f;
 #pragma unroll
-                for (int g = 0; g < GROUPS; ++g) mid[g] *= f;
+                for (int g = 0; g < GROUPS; ++g) {
+                    mid[g] *= f;
+                    if constexpr (SUMS) psum[g] *= f;
+                }
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
@@ -502,6 +514,7 @@ kv4_attention_kernel(AttnArgs a)
                     }
                 }
             }
+            if constexpr (SUMS) psum[g] = mfma16<BCONV_BF16>(offset, pp[0], psum[g]);
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j, word = tile / 8, half = (tile / 4) & 1;
@@ -515,7 +528,7 @@ kv4_attention_kernel(AttnArgs a)
                 
 #pragma unroll
                     for (int k = NP - 1; k >= 0; --k) {
-                        acc[tile] = mfma16<BCONV_BF16>(offset, pp[k], acc[tile]);
+                        if constexpr (!SUMS) acc[tile] = mfma16<BCONV_BF16>(offset, pp[k], acc[tile]);
                         acc[tile] = mfma16<BCONV_BF16>(v, pp[k], acc[tile]);
                     }
             }
@@ -542,7 +555,8 @@ kv4_attention_kernel(AttnArgs a)
         const float f = __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            const float add = lane_groups_sum(mid[g]);
+            float add = lane_groups_sum(mid[g]);
+            if constexpr (SUMS) add -= kValueOffset<DT> * psum[g][0];
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;
