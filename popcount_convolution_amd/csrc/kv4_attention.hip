@@ -780,7 +780,7 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
     if ((long long)a.max_q * a.ratio >= (1LL << 30)) return fail(BCONV_ERR_INVALID_ARGUMENT, "max_q*heads too large");
     a.col_blocks = (a.max_q * a.ratio + bconv::kCols - 1) / bconv::kCols;
     const long long tiles = (long long)a.requests * a.g.kv_heads * a.col_blocks;
-    if (tiles >= (1LL << 29)) return fail(BCONV_ERR_INVALID_ARGUMENT, "requests*heads*max_q too large for one call");
+    if (tiles >= (1LL << 27)) return fail(BCONV_ERR_INVALID_ARGUMENT, "requests*heads*max_q too large for one call");
     // tokens that the columns of one workgroup can see, from a multiple of the tile
     long long seen = most;
     if (a.window > 0) {
@@ -802,7 +802,7 @@ bconv_status_t plan_attention(const bconv_kv4_desc_t *desc, const bconv_kv4_atte
         part = (seen + want - 1) / want;
         if (part < 64 * waves) part = 64 * waves;
         if (part < (seen + 127) / 128) part = (seen + 127) / 128;
-        if (part > 1056 * waves) part = 1056 * waves;
+        if (part > 1056 * waves && a.col_blocks <= 4) part = 1056 * waves;
         if (part < (seen + bconv::kMaxParts - 1) / bconv::kMaxParts) part = (seen + bconv::kMaxParts - 1) / bconv::kMaxParts;
     }
     part = (part + bconv::kTokens - 1) / bconv::kTokens * bconv::kTokens;

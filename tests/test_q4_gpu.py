@@ -230,6 +230,31 @@ def test_linear_shapes_and_streams(dev):
     assert layer.workspace_bytes(150, torch.bfloat16) == 0  # few rows for so small a layer: no workspace
 
 
+def test_linear_columns_of_one_buffer(dev):
+    """x and y as columns of one buffer share no element; columns that do are
+    refused."""
+    rng = np.random.default_rng(16)
+    layer, *w = make_linear(rng, 64, 48, 32, False, False)
+    buf = torch.randn(5, 200, device=dev)
+    x = buf[:, :64].clone()
+    for left, right in ((buf[:, :64], buf[:, 64:112]), (buf[:, 60:124], buf[:, 5:53])):
+        left.copy_(x)
+        assert torch.equal(layer.forward(left, out=right), layer.forward(x))
+    for left, right in ((buf[:, :64], buf[:, 63:111]), (buf[:, 40:104], buf[:, 0:48])):
+        with pytest.raises(pca.BconvError):
+            layer.forward(left, out=right)
+
+
+def test_linear_rows_past_32_bits(dev):
+    """Row offsets beyond 2^32 bytes and 2^31 elements."""
+    rng = np.random.default_rng(17)
+    layer, *w = make_linear(rng, 300, 40, 64, True, False)
+    buf = torch.empty((3, (1 << 30) + 64), dtype=torch.bfloat16, device=dev)
+    x = buf[:, :300]
+    x.copy_(torch.randn(3, 300, device=dev))
+    check_linear(layer, w, x, layer.forward(x), 64, "bf16")
+
+
 # ------------------------------------------------------------------- cache
 
 def rows_of(rng, tokens, heads, dim, kind):
@@ -389,6 +414,7 @@ def check_attention(rng, dev, dtype, lens, counts, heads, kv_heads, dim, group, 
     ([100, 50], 8, 4, 200, 32, 16),
     ([140], 4, 2, 256, 128, 256),
     ([2300, 700], 40, 1, 104, 128, 1024),
+    ([20000, 3, 9000], 16, 1, 64, 64, 64),     # dozens of parts
 ])
 def test_attention_decode(dev, dtype, lens, heads, kv_heads, dim, group, block):
     """One query a request: lengths of zero, one and odd ones, pages that end
@@ -471,6 +497,22 @@ def test_attention_bounds_and_offsets(dev):
     cache.attention(q, torch.from_numpy(table).to(dev), torch.tensor(lens, dtype=torch.int32, device=dev),
                     q_start=starts, max_q=2, out=out)
     assert bool((out[0] == 3).all()) and bool((out[4] == 3).all()) and not bool((out[1:4] == 3).any())
+
+
+def test_cache_past_32_bits(dev):
+    """Blocks beyond 4 GiB of the pool: written and read where they are."""
+    rng = np.random.default_rng(18)
+    blocks = (5 << 30) // pca.bconv_kv4_layout(pca.bconv_kv4_desc_t(1, 64, 8, 128, 64)).record_bytes // 8
+    high, low = pca.KV4Cache(blocks, 64, 8, 128), pca.KV4Cache(4, 64, 8, 128)
+    k, v = torch.randn(150, 8, 128, device=dev), torch.randn(150, 8, 128, device=dev)
+    pos = torch.arange(150, dtype=torch.int32, device=dev)
+    ids = torch.tensor([[2, 0, 3]], dtype=torch.int32, device=dev)
+    far = ids + (blocks - 4)
+    for cache, table in ((high, far), (low, ids)):
+        cache.append(k, v, table[0][pos // 64] * 64 + pos % 64)
+    q, lens = torch.randn(1, 32, 128, device=dev), torch.tensor([150], dtype=torch.int32, device=dev)
+    assert torch.equal(high.attention(q, far, lens), low.attention(q, ids, lens))
+    assert not high.pool[:1 << 30].any() and float(low.attention(q, ids, lens).abs().sum()) > 0
 
 
 def test_attention_nan_query(dev):
