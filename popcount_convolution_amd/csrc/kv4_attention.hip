@@ -13,6 +13,17 @@
 // meet the matrix cores and stay in fp32.  Rows of the first product are
 // numbered so that a lane ends up with the probabilities of the 8 tokens whose
 // codes it decodes for the second: P never leaves its registers.
+//
+// Bound by instruction issue, not by the cache's bytes: 128 channels in groups
+// of 64 take about 350 vector and 24 matrix instructions a tile (decoding 120,
+// steps and midpoints 128, softmax 40) for 4.6 KB.  32 requests of up to 8192
+// tokens, 32 heads over 8, bf16: 53 us for 183 MB (3.5 TB/s; a large read
+// reaches 6.05), and 5.7 us for the join of their parts; vector units busy 60%,
+// the rest is the requests' uneven lengths and a workgroup's first loads.  Two
+// requests of 131071 tokens, 16 heads over one, fp16: 15.5 us and 5.1 us for the
+// join (floor 5.5 us).  One of 777 tokens: 7.6 us, a chain of loads (lengths,
+// block ids, keys, values).  Registers decide the rest: 128 a wave and four waves
+// a SIMD; spilling 15 of them costs 58 -> 84 us, three waves at 168 registers 66.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -593,7 +604,7 @@ kv4_attention_kernel(AttnArgs a)
 
 // Joins the parts of one column, a workgroup each: DP / 4 threads take the
 // channels, 2048 / DP slices of them every so-many-th part; the slices are
-// added in order.
+// added in order.  Bound by its launch and three dependent loads (5 us).
 template <int DT, int DP>
 __global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a)
 {
