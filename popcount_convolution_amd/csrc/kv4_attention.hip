@@ -35,7 +35,7 @@ namespace bconv {
 
 constexpr int kTokens = 32;       // tokens a wave takes at a time
 constexpr int kCols = 16;         // (query, head) columns a workgroup takes
-constexpr float kLowest = -1e30f; // running maximum before the first visible token
+constexpr float kLowest = -3e38f; // running maximum before the first visible token
 // How far a logit (base 2) may pass the running maximum before the sums are
 // rescaled: 2^8 of headroom costs fp32 sums nothing and saves most rescales.
 constexpr float kSlack = 8.0f;
@@ -194,11 +194,109 @@ struct Place {
 
 template <int GROUPS> constexpr int kTable = (8 * GROUPS + 15) / 16;
 
-// Keys of 32 tokens: words of the lane's two operand rows, and entries of its
-// run's (s, b) table, which the run's 16 lanes share (entry = token of the run
-// * GROUPS + group).
-template <int DP, int GROUPS> struct Keys {
-    uint32_t w[2][DP / 32], table[kTable<GROUPS>];
+// Where a workgroup has at most four columns, each stands REP = 4 times next to
+// itself in the 16, and its copies share its softmax, three quarters of whose
+// lanes would be idle: of a run of 8 tokens, numbered 4 u + i, copy r takes those
+// with i % REP == r.  It reads their (s, b) itself.
+template <int GROUPS, int REP> struct Steps {
+    static constexpr int E = 4 / REP;
+    uint32_t v[2][E][GROUPS];
+    // `t`: the run's (s, b) table
+    __device__ __forceinline__ void load(const char *t, int lane)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                const char *at = t + (4 * u + e * REP + lane % REP) * GROUPS * 4;
+                if constexpr (GROUPS == 1) {
+                    v[u][e][0] = *reinterpret_cast<const uint32_t *>(at);
+                } else {
+#pragma unroll
+                    for (int g = 0; g < GROUPS; g += 2) {
+                        const u32x2 x = *reinterpret_cast<const u32x2 *>(at + 4 * g);
+                        v[u][e][g] = x[0];
+                        v[u][e][g + 1] = x[1];
+                    }
+                }
+            }
+    }
+    __device__ __forceinline__ f16x2 at(int u, int e, int g) const { return __builtin_bit_cast(f16x2, v[u][e][g]); }
+    // drops the tokens that `keep` (of a token's number in the run) denies
+    template <typename F> __device__ __forceinline__ void mask(int lane, F keep)
+    {
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (!keep(4 * u + e * REP + lane % REP)) {
+#pragma unroll
+                    for (int g = 0; g < GROUPS; ++g) v[u][e][g] = 0;
+                }
+    }
+};
+
+// One copy reads every token's: 16 lanes share the run's table, an entry (token
+// * GROUPS + group) a lane.
+template <int GROUPS> struct Steps<GROUPS, 1> {
+    static constexpr int E = 4;
+    uint32_t v[kTable<GROUPS>];
+    __device__ __forceinline__ static int entry_of(int lane, int x) { return (x * 16 + (lane & 15)) & (8 * GROUPS - 1); }
+    __device__ __forceinline__ void load(const char *t, int lane)
+    {
+#pragma unroll
+        for (int x = 0; x < kTable<GROUPS>; ++x) v[x] = *reinterpret_cast<const uint32_t *>(t + entry_of(lane, x) * 4);
+    }
+    __device__ __forceinline__ f16x2 at(int u, int e, int g) const
+    {
+        return __builtin_bit_cast(f16x2, entry(v, (4 * u + e) * GROUPS + g));
+    }
+    template <typename F> __device__ __forceinline__ void mask(int lane, F keep)
+    {
+#pragma unroll
+        for (int x = 0; x < kTable<GROUPS>; ++x)
+            if (!keep(entry_of(lane, x) / GROUPS)) v[x] = 0;
+    }
+};
+
+// Result e of a copy: of the four results of a product, number e REP + r.
+template <int REP> __device__ __forceinline__ float own(f32x4 d, int e, int lane)
+{
+    if constexpr (REP == 1) return d[e];
+    const float even = lane & 1 ? d[1] : d[0], odd = lane & 1 ? d[3] : d[2];
+    return lane & 2 ? odd : even;
+}
+
+// A word of copy r of the lane's column.
+template <int REP> __device__ __forceinline__ uint32_t from_copy(uint32_t v, int r)
+{
+    if constexpr (REP == 1) return v;
+    switch (r) {  // the same lane of each four
+    case 0: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x00, 0xf, 0xf, true);
+    case 1: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x55, 0xf, 0xf, true);
+    case 2: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xaa, 0xf, 0xf, true);
+    default: return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xff, 0xf, 0xf, true);
+    }
+}
+
+template <int REP> __device__ __forceinline__ float copies_max(float v)
+{
+    if constexpr (REP == 1) return v;
+    v = fmaxf(v, __shfl_xor(v, 1));
+    return fmaxf(v, __shfl_xor(v, 2));
+}
+
+template <int REP> __device__ __forceinline__ float copies_sum(float v)
+{
+    if constexpr (REP == 1) return v;
+    v += __shfl_xor(v, 1);
+    return v + __shfl_xor(v, 2);
+}
+
+// Keys of 32 tokens: words of the lane's two operand rows, and (s, b) of its run.
+template <int DP, int GROUPS, int REP> struct Keys {
+    uint32_t w[2][DP / 32];
+    Steps<GROUPS, REP> steps;
     __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int lane)
     {
         const int row = lane & 15, lg = lane >> 4, mask = (1 << a.g.block_shift) - 1;
@@ -219,27 +317,21 @@ template <int DP, int GROUPS> struct Keys {
                 }
             }
         }
-        const char *t = trec + a.g.k_scales + (p.at + (lg * 8 & mask)) * GROUPS * 4;
-#pragma unroll
-        for (int x = 0; x < kTable<GROUPS>; ++x)
-            table[x] = *reinterpret_cast<const uint32_t *>(t + ((x * 16 + row) & (8 * GROUPS - 1)) * 4);
+        steps.load(trec + a.g.k_scales + (p.at + (lg * 8 & mask)) * GROUPS * 4, lane);
     }
 };
 
-// Values of the lane's run: its part of each row (16 bits for DP = 64), and
-// entries of the run's table.
-template <int DP, int GROUPS> struct Values {
+// Values of the lane's run: its part of each row (16 bits for DP = 64), and (s, b).
+template <int DP, int GROUPS, int REP> struct Values {
     static constexpr int N = DP < 128 ? 1 : DP / 128;
-    uint32_t w[8][N], table[kTable<GROUPS>];
+    uint32_t w[8][N];
+    Steps<GROUPS, REP> steps;
     __device__ __forceinline__ void load(const AttnArgs &a, const Place &p, int lane)
     {
         const int row = lane & 15, lg = lane >> 4, mask = (1 << a.g.block_shift) - 1;
         const char *rec = lg & 2 ? p.second : p.first;
         const int at = p.at + (lg * 8 & mask);
-        const char *t = rec + a.g.v_scales + at * GROUPS * 4;
-#pragma unroll
-        for (int x = 0; x < kTable<GROUPS>; ++x)
-            table[x] = *reinterpret_cast<const uint32_t *>(t + ((x * 16 + row) & (8 * GROUPS - 1)) * 4);
+        steps.load(rec + a.g.v_scales + at * GROUPS * 4, lane);
         const char *v = rec + a.g.v_codes + at * (DP / 2) + row * (DP / 32);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -268,7 +360,8 @@ constexpr int min_waves(int dt, int dp, int groups)
 }
 
 // FULL: no group of channels is padding alone (such groups are skipped).
-template <int DT, int DP, int GROUPS, bool FULL>
+// REP: copies of a column (see Steps).
+template <int DT, int DP, int GROUPS, bool FULL, int REP>
 __global__ __launch_bounds__(attn_waves(DT, DP, GROUPS) * 64, min_waves(DT, DP, GROUPS)) void
 kv4_attention_kernel(AttnArgs a)
 {
@@ -278,12 +371,12 @@ kv4_attention_kernel(AttnArgs a)
     constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
     constexpr int VPER = TILES / GROUPS;       // of them a group
     constexpr int NP = kProbParts<DT>;
-    constexpr int WAVES = attn_waves(DT, DP, GROUPS), COLS = kCols;
-    constexpr int TABLE = kTable<GROUPS>;
+    constexpr int WAVES = attn_waves(DT, DP, GROUPS), COLS = kCols / REP;
+    constexpr int E = 4 / REP;                 // tokens of four that a copy takes
     constexpr bool SUMS = sums_probs(DT, DP, GROUPS);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row = lane & 15, lg = lane >> 4;
+    const int row = lane & 15, lg = lane >> 4, col = row / REP;
     int id = blockIdx.x;
     const int part = id % a.parts;
     id /= a.parts;
@@ -322,7 +415,7 @@ kv4_attention_kernel(AttnArgs a)
     };
     constexpr int STRIDE = WAVES * kTokens;
     int t = begin + wave * kTokens;
-    Keys<DP, GROUPS> next;
+    Keys<DP, GROUPS, REP> next;
     if (t < end) {
         if (a.window) {
             next0 = block_of(t);
@@ -336,7 +429,7 @@ kv4_attention_kernel(AttnArgs a)
     int lo, hi;
     int all_lo = 0, all_hi = 0x7fffffff;  // seen by every column
     {
-        const int c = sp.c0 + row;
+        const int c = sp.c0 + col;
         lo = 0;
         hi = -1;
         const bool real = c < sp.c1;
@@ -370,32 +463,30 @@ kv4_attention_kernel(AttnArgs a)
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
-    // sums of q over each group, for the midpoints and the codes' offset
+    // sums of q over each group, for the midpoints and the codes' offset: a
+    // product starts from -24 of them or, where a copy takes few of its results,
+    // each of those gets them afterwards (three registers a group fewer)
+    constexpr bool START = DT == BCONV_BF16 && REP == 1;
     float qsum[GROUPS];
-    f32x4 qoff[DT == BCONV_BF16 ? GROUPS : 1];
+    f32x4 qoff[START ? GROUPS : 1];
 #pragma unroll
-    for (int g = 0; g < GROUPS; ++g)
-        {
-            f32x4 x = {0, 0, 0, 0};
-            const u32x4 one = DT == BCONV_F16 ? u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u} : bf16_const(1.0f);
+    for (int g = 0; g < GROUPS; ++g) {
+        f32x4 x = {0, 0, 0, 0};
+        const u32x4 one = DT == BCONV_F16 ? u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u} : bf16_const(1.0f);
 #pragma unroll
-            for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s], x);
-            qsum[g] = x[0];
-            if constexpr (DT == BCONV_BF16) qoff[g] = x * -24.0f;
-        }
+        for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s], x);
+        qsum[g] = x[0];
+        if constexpr (START) qoff[g] = x * -24.0f;
+    }
 
     f32x4 acc[TILES], psum[SUMS ? GROUPS : 1];
-    float mid[GROUPS], m, l;
-    {
-        m = kLowest;
-        l = 0.0f;
+    float mid[GROUPS], m = kLowest, l = 0.0f;
 #pragma unroll
-        for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
+    for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
-        for (int g = 0; g < GROUPS; ++g) {
-            mid[g] = 0.0f;
-            if constexpr (SUMS) psum[g] = f32x4{0, 0, 0, 0};
-        }
+    for (int g = 0; g < GROUPS; ++g) {
+        mid[g] = 0.0f;
+        if constexpr (SUMS) psum[g] = f32x4{0, 0, 0, 0};
     }
     const Zero<DT> eight(8);
     const u32x4 offset = bf16_const(SUMS ? 1.0f : -kValueOffset<DT>);
@@ -406,8 +497,8 @@ kv4_attention_kernel(AttnArgs a)
         // the tile's values are requested now and used after the softmax, the
         // next tile's keys a tile ahead
         const int id0 = next0, id1 = next1;
-        const Keys<DP, GROUPS> keys = next;
-        Values<DP, GROUPS> values;
+        const Keys<DP, GROUPS, REP> keys = next;
+        Values<DP, GROUPS, REP> values;
         values.load(a, place_of(t, id0, id1), lane);
         if (t + STRIDE < end) {
             next0 = block_of(t + STRIDE);
@@ -415,39 +506,32 @@ kv4_attention_kernel(AttnArgs a)
             next.load(a, place_of(t + STRIDE, next0, next1), lane);
         }
 
-        // S; times scale_log2 (not negative: a negative scale is in q) these are base-2 logits
-        uint32_t ks[TABLE], vs[TABLE];
-#pragma unroll
-        for (int x = 0; x < TABLE; ++x) {
-            ks[x] = keys.table[x];
-            vs[x] = values.table[x];
-        }
-        f32x4 z[2];
+        // S; times scale_log2 (a negative scale is in q) these are base-2 logits
+        float z[2][E];
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-             z[u] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[u][e] = 0.0f;
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             if (!FULL && g * PER * 32 >= a.g.dim) continue;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
                 f32x4 d;
-                {
-                    if constexpr (DT == BCONV_BF16) d = qoff[g];
-                    else d = f32x4{0, 0, 0, 0};
-                }
+                if constexpr (START) d = qoff[g];
+                else d = f32x4{0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < PER; ++s) {
                     const u32x4 k = decode<DT>(keys.w[u][g * PER + s], eight, kbits);
-                     d = mfma_parts<DT>(k, qf[g * PER + s], d);
+                    d = mfma_parts<DT>(k, qf[g * PER + s], d);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f16x2 sb = __builtin_bit_cast(f16x2, entry(ks, (4 * u + i) * GROUPS + g));
-                    {
-                        z[u][i] = __builtin_fmaf((float)sb[0], d[i], z[u][i]);
-                        z[u][i] = __builtin_fmaf((float)sb[1], qsum[g], z[u][i]);
-                    }
+                for (int e = 0; e < E; ++e) {
+                    const f16x2 sb = keys.steps.at(u, e, g);
+                    float mine = own<REP>(d, e, lane);
+                    if constexpr (DT == BCONV_BF16 && !START) mine = __builtin_fmaf(-24.0f, qsum[g], mine);
+                    z[u][e] = __builtin_fmaf((float)sb[0], mine, z[u][e]);
+                    z[u][e] = __builtin_fmaf((float)sb[1], qsum[g], z[u][e]);
                 }
             }
         }
@@ -459,26 +543,31 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = t + vrun + 4 * u + i;
-                    
-                        if (!known || pos < lo || pos > hi) z[u][i] = -__builtin_inff();
+                for (int e = 0; e < E; ++e) {
+                    const int pos = t + vrun + 4 * u + e * REP + lane % REP;
+                    if (!known || pos < lo || pos > hi) z[u][e] = -__builtin_inff();
                 }
-#pragma unroll
-            for (int x = 0; x < TABLE; ++x) {
-                const int pos = t + vrun + ((x * 16 + row) & (8 * GROUPS - 1)) / GROUPS;
-                if (!known || pos < sp.low || pos >= sp.t1) vs[x] = 0;
-            }
+            values.steps.mask(lane, [&](int i) {
+                const int pos = t + vrun + i;
+                return known && pos >= sp.low && pos < sp.t1;
+            });
         }
 
-        // running softmax
-        float p[8];
+        // Running softmax.  The logits are rounded before the maximum is taken
+        // off: fused with the subtraction, a logit beyond 2^31 would differ from
+        // itself, as the maximum, by more than exp2 holds.
+        float p[2][E];
         {
-            float top = fmaxf(fmaxf(fmaxf(z[0][0], z[0][1]), fmaxf(z[0][2], z[0][3])),
-                              fmaxf(fmaxf(z[1][0], z[1][1]), fmaxf(z[1][2], z[1][3])));
-            top *= a.scale_log2;
+#pragma clang fp contract(off)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) z[u][e] *= a.scale_log2;
+            float top = fmaxf(z[0][0], z[1][0]);
+#pragma unroll
+            for (int e = 1; e < E; ++e) top = fmaxf(top, fmaxf(z[0][e], z[1][e]));
             if (__any(top > m + kSlack)) {
-                top = fmaxf(m, lane_groups_max(top));
+                top = fmaxf(m, copies_max<REP>(lane_groups_max(top)));
                 const float f = __builtin_amdgcn_exp2f(m - top);
                 m = top;
                 l *= f;
@@ -491,37 +580,37 @@ kv4_attention_kernel(AttnArgs a)
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                p[i] = __builtin_amdgcn_exp2f(__builtin_fmaf(z[i >> 2][i & 3], a.scale_log2, -m));
-                l += p[i];
-            }
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    p[u][e] = __builtin_amdgcn_exp2f(z[u][e] - m);
+                    l += p[u][e];
+                }
         }
 
-        // V^T P
+        // V^T P; word i of an operand is tokens i and i + 4 of the run
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             if (!FULL && g * VPER * 16 >= a.g.dim) continue;
-            f16x2 sb[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sb[i] = __builtin_bit_cast(f16x2, entry(vs, i * GROUPS + g));
             u32x4 pp[NP];
-            {
-                float ps[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    ps[i] = __builtin_fmaf((float)sb[i][0], p[i], 0.0f);  // one instruction, with the conversion
-                    mid[g] = __builtin_fmaf((float)sb[i][1], p[i], mid[g]);
+            for (int e = 0; e < E; ++e) {
+                float ps[2];
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const f16x2 sb = values.steps.at(u, e, g);
+                    ps[u] = __builtin_fmaf((float)sb[0], p[u][e], 0.0f);  // one instruction, with the conversion
+                    mid[g] = __builtin_fmaf((float)sb[1], p[u][e], mid[g]);
                 }
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
+                    const bf16x2 r = {(__bf16)ps[0], (__bf16)ps[1]};
+                    const uint32_t two = __builtin_bit_cast(uint32_t, r);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bf16x2 r = {(__bf16)ps[2 * i], (__bf16)ps[2 * i + 1]};
-                        pp[k][i] = __builtin_bit_cast(uint32_t, r);
-                        if (k + 1 < NP) {
-                            ps[2 * i] -= (float)r[0];
-                            ps[2 * i + 1] -= (float)r[1];
-                        }
+                    for (int c = 0; c < REP; ++c) pp[k][e * REP + c] = from_copy<REP>(two, c);
+                    if (k + 1 < NP) {
+                        ps[0] -= (float)r[0];
+                        ps[1] -= (float)r[1];
                     }
                 }
             }
@@ -532,16 +621,15 @@ kv4_attention_kernel(AttnArgs a)
                 u32x4 v;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const uint32_t two = __builtin_amdgcn_perm(values.w[2 * i + 1][word], values.w[2 * i][word],
+                    const uint32_t two = __builtin_amdgcn_perm(values.w[i + 4][word], values.w[i][word],
                                                                half ? 0x07060302u : 0x05040100u);
                     v[i] = value_pair<DT>(two, tile & 3, vbits);
                 }
-                
 #pragma unroll
-                    for (int k = NP - 1; k >= 0; --k) {
-                        if constexpr (!SUMS) acc[tile] = mfma16<BCONV_BF16>(offset, pp[k], acc[tile]);
-                        acc[tile] = mfma16<BCONV_BF16>(v, pp[k], acc[tile]);
-                    }
+                for (int k = NP - 1; k >= 0; --k) {
+                    if constexpr (!SUMS) acc[tile] = mfma16<BCONV_BF16>(offset, pp[k], acc[tile]);
+                    acc[tile] = mfma16<BCONV_BF16>(v, pp[k], acc[tile]);
+                }
             }
         }
     }
@@ -551,28 +639,26 @@ kv4_attention_kernel(AttnArgs a)
     float *so = lds;                             // [waves][COLS][DP + 4]
     float *sm = lds + WAVES * COLS * (DP + 4);   // [waves][COLS]
     float *sl = sm + WAVES * COLS;
-    {
-        l = lane_groups_sum(l);
-        if (lg == 0) {
-            sm[wave * COLS + row] = m;
-            sl[wave * COLS + row] = l;
-        }
+    l = copies_sum<REP>(lane_groups_sum(l));
+    if (lg == 0 && row % REP == 0) {
+        sm[wave * COLS + col] = m;
+        sl[wave * COLS + col] = l;
     }
     __syncthreads();
     {
         float top = kLowest;
 #pragma unroll
-        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + row]);
+        for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + col]);
         const float f = __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            float add = lane_groups_sum(mid[g]);
+            float add = copies_sum<REP>(lane_groups_sum(mid[g]));
             if constexpr (SUMS) add -= kValueOffset<DT> * psum[g][0];
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;
-                if (row < sp.c1 - sp.c0)
-                    *reinterpret_cast<f32x4 *>(so + (wave * COLS + row) * (DP + 4) + tile * 16 + lg * 4) =
+                if (col < sp.c1 - sp.c0 && row % REP == 0)
+                    *reinterpret_cast<f32x4 *>(so + (wave * COLS + col) * (DP + 4) + tile * 16 + lg * 4) =
                         (acc[tile] + add) * f;
             }
         }
@@ -661,13 +747,13 @@ __global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a)
 
 // ------------------------------------------------------------------ dispatch
 
-template <int DT, int DP, int GROUPS, bool FULL>
+template <int DT, int DP, int GROUPS, bool FULL, int REP>
 hipError_t launch_attention_full(const AttnArgs &a, hipStream_t s)
 {
     constexpr int WAVES = attn_waves(DT, DP, GROUPS);
-    const size_t lds = (size_t)WAVES * kCols * (DP + 4 + 2) * sizeof(float);
+    const size_t lds = (size_t)WAVES * (kCols / REP) * (DP + 4 + 2) * sizeof(float);
     const long long grid = (long long)a.requests * a.g.kv_heads * a.col_blocks * a.parts;
-    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, FULL>), dim3((unsigned)grid), dim3(WAVES * 64), lds, s, a);
+    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, FULL, REP>), dim3((unsigned)grid), dim3(WAVES * 64), lds, s, a);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && a.parts > 1) {
         const long long cols = (long long)a.requests * a.g.kv_heads * a.max_q * a.ratio;
@@ -680,8 +766,15 @@ hipError_t launch_attention_full(const AttnArgs &a, hipStream_t s)
 template <int DT, int DP, int GROUPS>
 hipError_t launch_attention_kernel(const AttnArgs &a, hipStream_t s)
 {
-    if (a.g.dim > DP - DP / GROUPS) return launch_attention_full<DT, DP, GROUPS, true>(a, s);
-    if constexpr (GROUPS > 1) return launch_attention_full<DT, DP, GROUPS, false>(a, s);
+    if (a.g.dim > DP - DP / GROUPS) {
+        // 32 requests of up to 8192 tokens, 32 heads over 8: groups of 64 bf16
+        // 54.5 us against 58.4, groups of 32 65 against 77, fp32 89 against 105;
+        // 777 tokens 7.1 against 7.8.  Two copies of up to eight columns take
+        // more registers than they save (64 heads: 72 against 60).
+        if (a.max_q * a.ratio <= 4) return launch_attention_full<DT, DP, GROUPS, true, 4>(a, s);
+        return launch_attention_full<DT, DP, GROUPS, true, 1>(a, s);
+    }
+    if constexpr (GROUPS > 1) return launch_attention_full<DT, DP, GROUPS, false, 1>(a, s);
     return hipErrorInvalidValue;  // not reached: one group is never empty
 }
 

@@ -450,6 +450,33 @@ def test_attention_large_logits(dev, dtype):
         check_attention(rng, dev, dtype, [400, 33], [1, 1], 8, 2, 64, 32, 16, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 128), (120, 64), (128, 32), (256, 128), (200, 64), (256, 32)])
+@pytest.mark.parametrize("heads,counts,window", [
+    (1, [1, 1, 1], 0), (2, [2, 0, 1], 0), (1, [4, 3, 2], 0), (3, [1, 1, 1], 9), (4, [1, 1, 1], 0), (1, [4, 2, 4], 5),
+    (1, [5, 1, 3], 0),
+])
+def test_attention_few_columns(dev, dtype, dim, group, heads, counts, window):
+    """One to five (query, head) pairs a request and key/value head: up to four
+    of them share their softmax between lanes."""
+    say("few columns", dtype, dim, group, heads, counts, window)
+    rng = np.random.default_rng(dim * 100 + group + heads * 10 + sum(counts))
+    check_attention(rng, dev, dtype, [703, 2, 45], counts, 2 * heads, 2, dim, group, 16, window)
+
+
+def test_attention_lowest_logits(dev):
+    """Logits far below any mask's usual value are still those of a softmax: a
+    lone token has probability one."""
+    for heads in (1, 8):
+        cache = pca.KV4Cache(2, 16, 1, 64, group=64)
+        k, v = torch.ones(1, 1, 64, device=dev), torch.randn(1, 1, 64, device=dev)
+        _, value = cache.append(k, v, torch.zeros(1, dtype=torch.int32, device=dev), values=True)
+        q = torch.full((1, heads, 64), -1e35, device=dev)
+        out = cache.attention(q, torch.zeros(1, 1, dtype=torch.int32, device=dev),
+                              torch.ones(1, dtype=torch.int32, device=dev))
+        assert float((out - value).abs().max()) <= 2.0 ** -20 * float(value.abs().max())
+
+
 def test_attention_missing_blocks(dev):
     """Blocks outside the pool and positions past the table are masked; a
     request all of whose blocks are missing sees nothing."""
