@@ -74,7 +74,9 @@ bconv_status_t bconv_q4_linear_workspace_size(bconv_q4_linear_t h, int32_t rows,
  * on 16-byte boundaries load wider).  rows == 0 is a no-op.  The workspace is
  * 16-byte aligned and overlaps neither.  bf16 products are exact and summed in fp32 after an
  * offset that is taken out again, so a bf16 row with an infinity gives NaN in
- * every output of that row; fp16 and fp32 rows follow IEEE arithmetic.
+ * every output of that row; fp16 and fp32 rows follow IEEE arithmetic.  An fp32
+ * element enters its products to 2^-24 of itself or 2^-39 of the largest in its
+ * 128 inputs, whichever is more.
  * Errors: INVALID_ARGUMENT for a NULL handle or pointer, rows < 0, an unknown
  * dtype, a short stride or overlapping buffers; WORKSPACE for a missing or
  * short workspace; HIP when a launch fails. */

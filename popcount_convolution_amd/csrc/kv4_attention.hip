@@ -122,22 +122,32 @@ __device__ __forceinline__ float lane_groups_sum(float v)
     return v + __shfl_xor(v, 32);
 }
 
-// Parts a probability is rounded into for the matrix cores: one bf16 for bf16
-// results, whose own rounding is as coarse; two (16 bits) for fp16 results,
-// three (24 bits) for fp32.
-template <int DT> constexpr int kProbParts = DT == BCONV_BF16 ? 1 : DT == BCONV_F16 ? 2 : 3;
+// Type of the operands of V^T P, and parts that a probability, times its value's
+// step, is rounded into: one bf16 for bf16 results, whose own rounding is as
+// coarse; two (16 bits) for fp16 results; two fp16 parts (24 bits) for fp32 results.
+//
+// fp16's exponents need these products near 1: they are taken times a power of
+// two a column and group of channels, which is chosen anew when the column's
+// maximum moves or a product would pass fp16's largest.  The products stay below
+// 2^(kUnitBits + 1) at a choice and have room to grow until the next.  Against three
+// bf16 parts and exact bf16 codes, for keys as well: 32 requests of up to 8192
+// tokens, 32 heads over 8, 88 -> 72 us; 64 heads 108 -> 87.  fp16 results gain
+// nothing from it (64 heads: 74 us with bf16 parts, 80 with fp16).
+template <int DT> constexpr int kValueType = DT == BCONV_F32 ? BCONV_F16 : BCONV_BF16;
+template <int DT> constexpr int kProbParts = DT == BCONV_BF16 ? 1 : 2;
+constexpr int kUnitBits = 8;
+typedef Range<kUnitBits, -40> Unit;  // so that a change of unit keeps fp32 sums in range
 
-// A value code decodes to 128 + c in bf16 (all of whose 7 mantissa bits it
-// takes, with no shift for the first code) or, for fp32 results, to 16 + c,
-// whose offset costs fewer bits.  A product with the constant -(offset + 8) goes
-// with each product, so the running sums hold code - 8 and never grow with the
-// offset.  For bf16 results, whose own rounding hides what the offset costs an
-// fp32 sum, the sums of the probabilities are kept instead (one product a group
-// in place of one a channel tile) and taken out at the end: 128 channels in one
-// group, 32 requests of up to 8192 tokens 51.9 -> 50.3 us.  With two groups the
-// sums' registers would spill (58.3 -> 65.2 us).
+// A value code decodes to code - 8 in fp16 or, in bf16 (which has no packed
+// subtraction), to 128 + c, with no shift for the first code.  There a product
+// with the constant -136 goes with each product, so that the running sums hold
+// code - 8 as well and never grow with the offset.  For bf16 results, whose own
+// rounding hides what the offset costs an fp32 sum, the sums of the probabilities
+// are kept instead (one product a group in place of one a channel tile) and taken
+// out at the end: 128 channels in one group, 32 requests of up to 8192 tokens 51.9
+// -> 50.3 us.  With two groups the sums' registers would spill (58.3 -> 65.2 us).
 constexpr bool sums_probs(int dt, int dp, int groups) { return dt == BCONV_BF16 && !(dp == 128 && groups == 2); }
-template <int DT> constexpr float kValueOffset = DT == BCONV_F32 ? 24.0f : 136.0f;
+constexpr float kValueOffset = 136.0f;
 
 // The word that lane N of each 16 lanes holds.
 template <int N> __device__ __forceinline__ uint32_t from_lane(uint32_t v)
@@ -170,16 +180,18 @@ template <int R> __device__ __forceinline__ uint32_t entry(const uint32_t (&v)[R
     }
 }
 
-// Codes j of two tokens' rows (16 bits of each row's part) as a bf16 pair.
+// Codes j of two tokens' rows (16 bits of each row's part) as a pair: 128 + c in
+// bf16, c - 8 in fp16.
 template <int DT> __device__ __forceinline__ uint32_t value_pair(uint32_t two, int j, const CodeBits &bits)
 {
-    if constexpr (DT == BCONV_F32) return bits(j == 0 ? two << 3 : two >> (4 * j - 3));
-    else return bits(two >> (4 * j));
+    const uint32_t c = bits(two >> (4 * j));
+    if constexpr (kValueType<DT> == BCONV_BF16) return c;
+    return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - f16x2{(_Float16)1032.0f, (_Float16)1032.0f});
 }
 
 template <int DT> __device__ __forceinline__ CodeBits value_bits()
 {
-    return DT == BCONV_F32 ? code_bits<DT>() : opaque_bits(0x000f000fu, 0x43004300u);  // bf16 128
+    return opaque_bits(0x000f000fu, kValueType<DT> == BCONV_BF16 ? 0x43004300u : 0x64006400u);  // bf16 128, fp16 1024
 }
 
 // Where a lane's part of 32 tokens is.  Runs of 8 tokens never cross a block,
@@ -370,7 +382,8 @@ kv4_attention_kernel(AttnArgs a)
     constexpr int PER = STEPS / GROUPS;        // steps a group
     constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
     constexpr int VPER = TILES / GROUPS;       // of them a group
-    constexpr int NP = kProbParts<DT>;
+    constexpr int NP = kProbParts<DT>, VT = kValueType<DT>;
+    constexpr bool UNITS = VT == BCONV_F16;
     constexpr int WAVES = attn_waves(DT, DP, GROUPS), COLS = kCols / REP;
     constexpr int E = 4 / REP;                 // tokens of four that a copy takes
     constexpr bool SUMS = sums_probs(DT, DP, GROUPS);
@@ -426,6 +439,7 @@ kv4_attention_kernel(AttnArgs a)
 
     // this lane's columns: row of q, positions seen
     Operand<DT> qf[STEPS];
+    float scale = a.scale_log2;
     int lo, hi;
     int all_lo = 0, all_hi = 0x7fffffff;  // seen by every column
     {
@@ -442,18 +456,18 @@ kv4_attention_kernel(AttnArgs a)
             all_hi = hi < all_hi ? hi : all_hi;
         }
         const T *q = static_cast<const T *>(a.q) + (long long)(sp.q0 + j) * a.q_token + (long long)h * a.q_head;
+        Raw<DT> raw[STEPS];
 #pragma unroll
         for (int s = 0; s < STEPS; ++s) {
             const int d = s * 32 + lg * 8;
-            if (real && d < a.g.dim) {
-                qf[s] = load_operand<DT>(q + d, d, a.g.dim, a.vec != 0);
-#pragma unroll
-                for (int p = 0; p < kSplit<DT>; ++p) qf[s].part[p] ^= a.flip;
-            } else {
-#pragma unroll
-                for (int p = 0; p < kSplit<DT>; ++p) qf[s].part[p] = u32x4{0, 0, 0, 0};
-            }
+            if (real && d < a.g.dim) raw[s] = load_eight<DT>(q + d, d, a.g.dim, a.vec != 0);
+            else raw[s] = zero_raw<DT>();
         }
+        scale *= to_operands<DT>(raw, qf);
+#pragma unroll
+        for (int s = 0; s < STEPS; ++s)
+#pragma unroll
+            for (int p = 0; p < kSplit<DT>; ++p) qf[s].part[p] ^= a.flip;
     }
 #pragma unroll
     for (int d = 1; d < 16; d *= 2) {
@@ -472,7 +486,7 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
         f32x4 x = {0, 0, 0, 0};
-        const u32x4 one = DT == BCONV_F16 ? u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u} : bf16_const(1.0f);
+        const u32x4 one = DT == BCONV_BF16 ? bf16_const(1.0f) : u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
 #pragma unroll
         for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s], x);
         qsum[g] = x[0];
@@ -481,15 +495,17 @@ kv4_attention_kernel(AttnArgs a)
 
     f32x4 acc[TILES], psum[SUMS ? GROUPS : 1];
     float mid[GROUPS], m = kLowest, l = 0.0f;
+    float unit[UNITS ? GROUPS : 1];  // what the group's products are multiplied by
 #pragma unroll
     for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
         mid[g] = 0.0f;
+        if constexpr (UNITS) unit[g] = 1.0f;
         if constexpr (SUMS) psum[g] = f32x4{0, 0, 0, 0};
     }
     const Zero<DT> eight(8);
-    const u32x4 offset = bf16_const(SUMS ? 1.0f : -kValueOffset<DT>);
+    const u32x4 offset = bf16_const(SUMS ? 1.0f : -kValueOffset);  // bf16
     const CodeBits kbits = code_bits<DT>(), vbits = value_bits<DT>();
 
     const int vrun = lg * 8;
@@ -557,18 +573,20 @@ kv4_attention_kernel(AttnArgs a)
         // off: fused with the subtraction, a logit beyond 2^31 would differ from
         // itself, as the maximum, by more than exp2 holds.
         float p[2][E];
+        bool moved = false;  // this column's maximum
         {
 #pragma clang fp contract(off)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int e = 0; e < E; ++e) z[u][e] *= a.scale_log2;
+                for (int e = 0; e < E; ++e) z[u][e] *= scale;
             float top = fmaxf(z[0][0], z[1][0]);
 #pragma unroll
             for (int e = 1; e < E; ++e) top = fmaxf(top, fmaxf(z[0][e], z[1][e]));
             if (__any(top > m + kSlack)) {
                 top = fmaxf(m, copies_max<REP>(lane_groups_max(top)));
                 const float f = __builtin_amdgcn_exp2f(m - top);
+                moved = top > m;
                 m = top;
                 l *= f;
 #pragma unroll
@@ -592,29 +610,53 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             if (!FULL && g * VPER * 16 >= a.g.dim) continue;
-            u32x4 pp[NP];
+            float ps[2][E];
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                float ps[2];
+            for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
+                for (int e = 0; e < E; ++e) {
                     const f16x2 sb = values.steps.at(u, e, g);
-                    ps[u] = __builtin_fmaf((float)sb[0], p[u][e], 0.0f);  // one instruction, with the conversion
+                    ps[u][e] = __builtin_fmaf((float)sb[0], p[u][e], 0.0f);  // one instruction, with the conversion
                     mid[g] = __builtin_fmaf((float)sb[1], p[u][e], mid[g]);
                 }
+            if constexpr (UNITS) {
+                float top = fmaxf(ps[0][0], ps[1][0]);
 #pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    const bf16x2 r = {(__bf16)ps[0], (__bf16)ps[1]};
-                    const uint32_t two = __builtin_bit_cast(uint32_t, r);
+                for (int e = 1; e < E; ++e) top = fmaxf(top, fmaxf(ps[0][e], ps[1][e]));
+                const bool over = top * unit[g] >= 32768.0f;
+                if (__any(moved || over)) {
+                    top = copies_max<REP>(lane_groups_max(top));
+                    // a column keeps its unit unless its own products ask for one
+                    if (moved || top * unit[g] >= 32768.0f) {
+                        const Unit next(__float_as_uint(top));
+                        const float f = next.to * (1.0f / unit[g]);
+                        unit[g] = next.to;
 #pragma unroll
-                    for (int c = 0; c < REP; ++c) pp[k][e * REP + c] = from_copy<REP>(two, c);
-                    if (k + 1 < NP) {
-                        ps[0] -= (float)r[0];
-                        ps[1] -= (float)r[1];
+                        for (int j = 0; j < VPER; ++j) acc[g * VPER + j] *= f;
                     }
                 }
             }
-            if constexpr (SUMS) psum[g] = mfma16<BCONV_BF16>(offset, pp[0], psum[g]);
+            u32x4 pp[NP];
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                uint32_t two[NP];
+                if constexpr (UNITS) {
+                    split_pair(ps[0][e], ps[1][e], unit[g], two[0], two[1]);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) {
+                        const bf16x2 r = {(__bf16)ps[0][e], (__bf16)ps[1][e]};
+                        two[k] = __builtin_bit_cast(uint32_t, r);
+                        ps[0][e] -= (float)r[0];
+                        ps[1][e] -= (float)r[1];
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+#pragma unroll
+                    for (int c = 0; c < REP; ++c) pp[k][e * REP + c] = from_copy<REP>(two[k], c);
+            }
+            if constexpr (SUMS) psum[g] = mfma16<VT>(offset, pp[0], psum[g]);
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j, word = tile / 8, half = (tile / 4) & 1;
@@ -627,8 +669,8 @@ kv4_attention_kernel(AttnArgs a)
                 }
 #pragma unroll
                 for (int k = NP - 1; k >= 0; --k) {
-                    if constexpr (!SUMS) acc[tile] = mfma16<BCONV_BF16>(offset, pp[k], acc[tile]);
-                    acc[tile] = mfma16<BCONV_BF16>(v, pp[k], acc[tile]);
+                    if constexpr (VT == BCONV_BF16 && !SUMS) acc[tile] = mfma16<VT>(offset, pp[k], acc[tile]);
+                    acc[tile] = mfma16<VT>(v, pp[k], acc[tile]);
                 }
             }
         }
@@ -653,13 +695,14 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             float add = copies_sum<REP>(lane_groups_sum(mid[g]));
-            if constexpr (SUMS) add -= kValueOffset<DT> * psum[g][0];
+            if constexpr (SUMS) add -= kValueOffset * psum[g][0];
+            const float from = UNITS ? 1.0f / unit[g] : 1.0f;  // exact
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;
                 if (col < sp.c1 - sp.c0 && row % REP == 0)
                     *reinterpret_cast<f32x4 *>(so + (wave * COLS + col) * (DP + 4) + tile * 16 + lg * 4) =
-                        (acc[tile] + add) * f;
+                        (acc[tile] * from + add) * f;
             }
         }
     }

@@ -25,9 +25,9 @@ template <> struct Elem<BCONV_F32> { typedef float type; };
 template <> struct Elem<BCONV_F16> { typedef _Float16 type; };
 template <> struct Elem<BCONV_BF16> { typedef __bf16 type; };
 
-// 16-byte matrix-core operands an fp32 value takes: three bf16 parts hold its
-// 24 significant bits exactly; 16-bit types are operands as they are.
-template <int DT> constexpr int kSplit = DT == BCONV_F32 ? 3 : 1;
+// 16-byte matrix-core operands a value takes: fp32 two fp16 parts (see Range),
+// 16-bit types one, as they are.
+template <int DT> constexpr int kSplit = DT == BCONV_F32 ? 2 : 1;
 
 // One lane's operand of v_mfma_f32_16x16x32: 8 consecutive k of one row or
 // column, for each part of the split.
@@ -37,7 +37,7 @@ template <int DT> struct Operand {
 
 template <int DT> __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c)
 {
-    if constexpr (DT == BCONV_F16)
+    if constexpr (DT != BCONV_BF16)
         return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
     else
@@ -47,7 +47,7 @@ template <int DT> __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x
 
 template <int DT> __device__ __forceinline__ f32x16 mfma32(u32x4 a, u32x4 b, f32x16 c)
 {
-    if constexpr (DT == BCONV_F16)
+    if constexpr (DT != BCONV_BF16)
         return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0,
                                                       0, 0);
     else
@@ -63,23 +63,47 @@ template <int DT> __device__ __forceinline__ f32x4 mfma_parts(u32x4 a, const Ope
     return c;
 }
 
-__device__ __forceinline__ uint32_t pack_hi16(uint32_t lo, uint32_t hi)
+// The largest of four lanes' bits 16 apart (of non-negative floats as well).
+__device__ __forceinline__ uint32_t lane_groups_max_bits(uint32_t v)
 {
-    // bytes 2,3 of lo, then bytes 2,3 of hi
-    return __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+    const auto a = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    v = a[0] > a[1] ? a[0] : a[1];
+    const auto b = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return b[0] > b[1] ? b[0] : b[1];
 }
 
-// Three bf16 parts of x, by truncation: their sum is x exactly (8 significant
-// bits each).  An infinity or NaN sits in the first part alone.
-__device__ __forceinline__ void split3(float x, uint32_t &h, uint32_t &m, uint32_t &l)
+// The power of two `to` that brings values up to a largest magnitude below
+// 2^(BITS + 1), for splitting them, and its inverse `from`.  Multiplying by either is
+// exact.  Below 2^LEAST the largest magnitude is taken as that (so that both stay
+// normal numbers).
+//
+// A value x times `to` is split into h = fp16(x), l = fp16(x - h): x - h is
+// exact and at most 2^-12 x, so h + l is x to 2^-24, fp32's own rounding, as long
+// as l is a normal number; below that its error is at most 2^-25, that is
+// 2^-(25 + BITS) of the largest value.  Two products then stand for an
+// fp32 product (exact bf16 parts would take three, and 8 instructions a value
+// instead of 3).
+template <int BITS, int LEAST = BITS - 126> struct Range {
+    static_assert(LEAST >= BITS - 126 && BITS < 16);
+    float to, from;
+    __device__ __forceinline__ explicit Range(uint32_t top)
+    {
+        uint32_t e = top >> 23;
+        e = e < 127 + LEAST ? 127 + LEAST : e;
+        to = __uint_as_float((254 + BITS - e) << 23);
+        from = __uint_as_float((e - BITS) << 23);
+    }
+};
+
+// A pair of values times `to`, split as above.
+__device__ __forceinline__ void split_pair(float x0, float x1, float to, uint32_t &h, uint32_t &l)
 {
-    const uint32_t u = __float_as_uint(x);
-    const bool finite = __builtin_isfinite(x);
-    // a NaN whose bits all sit below the first part must not become an infinity
-    h = x != x ? 0x7fc00000u : u & 0xffff0000u;
-    const float r = finite ? x - __uint_as_float(h) : 0.0f;
-    m = __float_as_uint(r) & 0xffff0000u;
-    l = __float_as_uint(r - __uint_as_float(m));
+    const f16x2 r = {(_Float16)(x0 * to), (_Float16)(x1 * to)};
+    h = __builtin_bit_cast(uint32_t, r);
+    asm("" : "+v"(h));  // or the compiler converts each value once more
+    const f16x2 q = __builtin_bit_cast(f16x2, h);
+    const f16x2 d = {(_Float16)__builtin_fmaf(x0, to, -(float)q[0]), (_Float16)__builtin_fmaf(x1, to, -(float)q[1])};
+    l = __builtin_bit_cast(uint32_t, d);
 }
 
 // 8 consecutive elements as loaded.
@@ -120,31 +144,64 @@ __device__ __forceinline__ Raw<DT> load_raw_masked(const typename Elem<DT>::type
     return r;
 }
 
-template <int DT> __device__ __forceinline__ Operand<DT> to_operand(const Raw<DT> &r)
+// 8 consecutive elements at p (offset k of a row of length len); elements at or
+// past len are 0.  `vec`: p is 16-byte aligned for k % 8 == 0.
+template <int DT>
+__device__ __forceinline__ Raw<DT> load_eight(const typename Elem<DT>::type *p, int k, int len, bool vec)
 {
-    Operand<DT> o;
-    if constexpr (DT == BCONV_F32) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t h0, m0, l0, h1, m1, l1;
-            split3(__uint_as_float(r.v[i >> 1][2 * (i & 1)]), h0, m0, l0);
-            split3(__uint_as_float(r.v[i >> 1][2 * (i & 1) + 1]), h1, m1, l1);
-            o.part[0][i] = pack_hi16(h0, h1);
-            o.part[1][i] = pack_hi16(m0, m1);
-            o.part[2][i] = pack_hi16(l0, l1);
-        }
-    } else {
-        o.part[0] = r.v[0];
-    }
-    return o;
+    return vec && k + 8 <= len ? load_raw<DT>(p) : load_raw_masked<DT>(p, k, len);
 }
 
-// 8 consecutive elements at p (offset k of a row of length len) as an operand;
-// elements at or past len are 0.  `vec`: p is 16-byte aligned for k % 8 == 0.
-template <int DT>
-__device__ __forceinline__ Operand<DT> load_operand(const typename Elem<DT>::type *p, int k, int len, bool vec)
+template <int DT> __device__ __forceinline__ Raw<DT> zero_raw()
 {
-    return to_operand<DT>(vec && k + 8 <= len ? load_raw<DT>(p) : load_raw_masked<DT>(p, k, len));
+    Raw<DT> r;
+#pragma unroll
+    for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) r.v[i] = u32x4{0, 0, 0, 0};
+    return r;
+}
+
+// N runs of 8 elements as operands.  fp32: times a power of two common to the
+// four lanes that hold a row or column, and `from` to take it out of a product (1
+// for other types).  An infinity is one in the first part alone, so products
+// follow IEEE arithmetic.
+template <int DT, int N>
+__device__ __forceinline__ float to_operands(const Raw<DT> (&r)[N], Operand<DT> (&o)[N])
+{
+    if constexpr (DT == BCONV_F32) {
+        float top = 0.0f;
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(__uint_as_float(r[s].v[i >> 2][i & 3])));
+        const uint32_t bits = lane_groups_max_bits(__float_as_uint(top));
+        const Range<14> range(bits);
+#pragma unroll
+        for (int s = 0; s < N; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t h, l;
+                split_pair(__uint_as_float(r[s].v[i >> 1][2 * (i & 1)]), __uint_as_float(r[s].v[i >> 1][2 * (i & 1) + 1]),
+                           range.to, h, l);
+                o[s].part[0][i] = h;
+                o[s].part[1][i] = l;
+            }
+        if (__any(bits >= 0x7f800000u)) {
+            // the second part of an infinity (infinity - infinity) becomes 0
+#pragma unroll
+            for (int s = 0; s < N; ++s)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t h = o[s].part[0][i];
+                    if ((h & 0x7fffu) == 0x7c00u) o[s].part[1][i] &= 0xffff0000u;
+                    if ((h & 0x7fff0000u) == 0x7c000000u) o[s].part[1][i] &= 0xffffu;
+                }
+        }
+        return range.from;
+    } else {
+#pragma unroll
+        for (int s = 0; s < N; ++s) o[s].part[0] = r[s].v[0];
+        return 1.0f;
+    }
 }
 
 template <int DT> __device__ __forceinline__ typename Elem<DT>::type round_to(float x)
@@ -161,11 +218,8 @@ template <int DT> __device__ __forceinline__ typename Elem<DT>::type round_to(fl
 //
 // What is left of the offset:
 //   bf16: 16 (the products are exact; the caller takes 16 * sum x out);
-//   fp16: none: a packed subtraction of `zero` leaves the integer itself;
-//   fp32: none, so that no cancellation costs bits: the codes are spread to
-//         bytes, `zero` is taken off four at a time (a byte holds 128 + c - z
-//         and never borrows; with the top bit flipped it is c - z, signed), and
-//         each byte converts to an exact float, whose upper half is the bf16.
+//   fp16 and fp32: none: a packed subtraction of `zero` leaves the integer
+//         itself, so that no cancellation costs bits.
 constexpr uint32_t kCodeMask = 0x00780078u;
 constexpr uint32_t kBase16 = 0x41804180u;   // bf16 16, 16
 constexpr uint32_t kBase128 = 0x58005800u;  // fp16 128, 128
@@ -175,13 +229,8 @@ __device__ __forceinline__ uint32_t rotr(uint32_t w, int n)
     return __builtin_amdgcn_alignbit(w, w, n);
 }
 
-// `zero` is subtracted from the codes where the type allows (see above): fp32
-// takes it as four bytes of 128 - zero, fp16 as a pair of halves holding 128 + zero.
-template <int DT> struct Zero;
-template <> struct Zero<BCONV_BF16> {
-    __device__ __forceinline__ explicit Zero(int) {}
-};
-template <> struct Zero<BCONV_F16> {
+// `zero` is subtracted from fp16 codes as a pair of halves holding 128 + zero.
+template <int DT> struct Zero {
     f16x2 v;
     __device__ __forceinline__ explicit Zero(int z)
     {
@@ -189,9 +238,8 @@ template <> struct Zero<BCONV_F16> {
         v = f16x2{h, h};
     }
 };
-template <> struct Zero<BCONV_F32> {
-    uint32_t v;
-    __device__ __forceinline__ explicit Zero(int z) : v((uint32_t)(128 - z) * 0x01010101u) {}
+template <> struct Zero<BCONV_BF16> {
+    __device__ __forceinline__ explicit Zero(int) {}
 };
 
 // (x & mask) | base is one v_and_or_b32 when one constant is in a scalar
@@ -211,31 +259,18 @@ __device__ __forceinline__ CodeBits opaque_bits(uint32_t mask, uint32_t base)
 }
 template <int DT> __device__ __forceinline__ CodeBits code_bits()
 {
-    return opaque_bits(kCodeMask, DT == BCONV_F16 ? kBase128 : kBase16);
+    return opaque_bits(kCodeMask, DT == BCONV_BF16 ? kBase16 : kBase128);
 }
 
 template <int DT> __device__ __forceinline__ u32x4 decode(uint32_t w, const Zero<DT> &zero, const CodeBits &bits)
 {
     u32x4 r;
-    if constexpr (DT == BCONV_F32) {
-        // nibbles (rotated by 3) at even and odd places: bytes b of `even` are
-        // nibbles 2b, of `odd` nibbles 2b + 1; codes 2e, 2e + 1 are nibbles e, 4 + e
-        const uint32_t even = ((rotr(w, 3) & 0x0f0f0f0fu) + zero.v) ^ 0x80808080u;
-        const uint32_t odd = ((rotr(w, 7) & 0x0f0f0f0fu) + zero.v) ^ 0x80808080u;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t src = e & 1 ? odd : even;
-            const float lo = (float)(int8_t)(src >> (8 * (e >> 1))), hi = (float)(int8_t)(src >> (8 * (2 + (e >> 1))));
-            r[e] = pack_hi16(__float_as_uint(lo), __float_as_uint(hi));
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            // only the last pair wraps around; a plain shift issues twice as fast
-            const uint32_t c = bits(e == 0 ? w : e < 3 ? w >> (4 * e) : rotr(w, 12));
-            if constexpr (DT == BCONV_F16) r[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - zero.v);
-            else r[e] = c;
-        }
+    for (int e = 0; e < 4; ++e) {
+        // only the last pair wraps around; a plain shift issues twice as fast
+        const uint32_t c = bits(e == 0 ? w : e < 3 ? w >> (4 * e) : rotr(w, 12));
+        if constexpr (DT == BCONV_BF16) r[e] = c;
+        else r[e] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - zero.v);
     }
     return r;
 }

@@ -113,14 +113,20 @@ template <int DT, bool ZP, int STEPS> struct Scales {
 };
 
 // One chunk (16 RT outputs x 128 inputs) times 16 rows of x, added to acc.
-// STEPS: 32-input steps a group.  Per group and output tile the exact products
-// of one group are summed first, then scaled once in fp32.
+// STEPS: 32-input steps a group.  Per group and output tile the products of one
+// group are summed first, then scaled once in fp32; `from` takes the power of
+// two of an fp32 row's operands out of the chunk's sum.
 template <int DT, bool ZP, int STEPS, int RT>
 __device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operand<DT> (&x)[4],
                                               const Scales<DT, ZP, STEPS> (&sc)[RT], const CodeBits &bits,
-                                              f32x4 (&acc)[RT])
+                                              float from, f32x4 (&acc)[RT])
 {
     constexpr int P = kSplit<DT>;
+    f32x4 sum[RT];
+    if constexpr (P > 1) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) sum[r] = f32x4{0, 0, 0, 0};
+    }
 #pragma unroll
     for (int g = 0; g < 4 / STEPS; ++g) {
         // bf16: the offset 16 + z of the codes leaves -(16 + z) sum x, on the
@@ -150,10 +156,17 @@ __device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operan
             }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            if constexpr (P == 3) d[r][0] += d[r][1] + d[r][2];
+            if constexpr (P > 1) d[r][0] += d[r][1];
+            f32x4 &to = P > 1 ? sum[r] : acc[r];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sc[r].scale(g, i), d[r][0][i], acc[r][i]);
+            for (int i = 0; i < 4; ++i) to[i] = __builtin_fmaf(sc[r].scale(g, i), d[r][0][i], to[i]);
         }
+    }
+    if constexpr (P > 1) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[r][i] = __builtin_fmaf(sum[r][i], from, acc[r][i]);
     }
 }
 
@@ -175,10 +188,11 @@ template <int DT> __device__ __forceinline__ void store_outputs(const Q4Args &a,
 // Bound by the codes' bytes for one row of x (1 x 25088 -> 4096 bf16: 12.6 us for
 // 53 MB, 4.2 TB/s with 2.8 us of launch among them; a large read reaches 6.05),
 // by x's operands, which every output tile reads again, for 16 rows (29.6 us).
-// 13 x 5000 -> 11003 bf16 10.5 us; fp32 19.3 us, by the instructions that make
-// exact bf16 codes (20 a word) and the three parts of x (8 a value).  Requesting
-// a wave's next chunk before working on this one was slower (13 rows bf16 13.8
-// us against 12.3): other waves hide the latency, and the registers cost waves.
+// 13 x 5000 -> 11003 bf16 10.5 us; fp32 15.0 us, by the instructions that split x
+// (19.8 with exact bf16 codes and three bf16 parts of x; 1 x 25088 -> 4096 26
+// against 39).  Requesting a wave's next chunk before working on this one was
+// slower (13 rows bf16 13.8 us against 12.3): other waves hide the latency, and
+// the registers cost waves.
 template <int DT, bool ZP, int STEPS, int RT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
 {
@@ -203,9 +217,7 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
     const T *xr = static_cast<const T *>(a.x) + (real ? (long long)(m0 + row) * a.ldx : 0) + lg * 8;
     Raw<DT> xf[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) xf[s].v[i] = u32x4{0, 0, 0, 0};
+    for (int s = 0; s < 4; ++s) xf[s] = zero_raw<DT>();
     const int whole = a.vec ? a.k / kChunk : 0;  // chunks whose columns are 16-byte loads throughout
 
     for (int c = wave; c < a.chunks; c += WAVES) {
@@ -224,17 +236,12 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
                 for (int s = 0; s < 4; ++s) xf[s] = load_raw<DT>(p + s * 32);
             } else {
 #pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const int k = c * kChunk + s * 32 + lg * 8;
-                    if (a.vec && k + 8 <= a.k) xf[s] = load_raw<DT>(p + s * 32);
-                    else xf[s] = load_raw_masked<DT>(p + s * 32, k, a.k);
-                }
+                for (int s = 0; s < 4; ++s) xf[s] = load_eight<DT>(p + s * 32, c * kChunk + s * 32 + lg * 8, a.k, a.vec != 0);
             }
         }
         Operand<DT> x[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) x[s] = to_operand<DT>(xf[s]);
-        chunk_product<DT, ZP, STEPS, RT>(w, x, sc, bits, acc);
+        const float from = to_operands<DT>(xf, x);
+        chunk_product<DT, ZP, STEPS, RT>(w, x, sc, bits, from, acc);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) part[wave][r][lane] = acc[r];
@@ -256,7 +263,8 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
 // and the partial sums of the splits.
 struct Q4Many {
     u32x4 *xp;       // [column tiles][chunks * 4][parts][64]
-    float *xs;       // bf16: [column tiles][chunks][groups a chunk][16], -sum x (times 24 without zero points)
+    float *xs;       // [column tiles][chunks][groups a chunk][16]; bf16: -sum x (times 24 without zero points),
+                     // fp32: the power of two to take out of a group's products
     float *sums;     // [splits][column tiles * 16][padded outputs], or nullptr for one split
     int col_tiles;   // padded to the workgroup's
     int padded_n;
@@ -277,28 +285,31 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4Args a, Q4Many q)
     if (id >= (long long)q.col_tiles * groups) return;
     const int g = (int)(id % groups), tile = (int)(id / groups);
     const int m = tile * 16 + (lane & 15);
+    Raw<DT> raw[STEPS];
+    Operand<DT> o[STEPS];
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int k = (g * STEPS + s) * 32 + (lane >> 4) * 8;
+        if (m < a.m && k < a.k)
+            raw[s] = load_eight<DT>(static_cast<const T *>(a.x) + (long long)m * a.ldx + k, k, a.k, a.vec != 0);
+        else raw[s] = zero_raw<DT>();
+    }
+    float xs = to_operands<DT>(raw, o);
     f32x4 sum = {0, 0, 0, 0};
 #pragma unroll
     for (int s = 0; s < STEPS; ++s) {
-        const int step = g * STEPS + s, k = step * 32 + (lane >> 4) * 8;
-        Operand<DT> o;
-        if (m < a.m && k < a.k) {
-            o = load_operand<DT>(static_cast<const T *>(a.x) + (long long)m * a.ldx + k, k, a.k, a.vec != 0);
-        } else {
+        u32x4 *dst = q.xp + ((long long)tile * a.chunks * 4 + g * STEPS + s) * kSplit<DT> * 64 + lane;
 #pragma unroll
-            for (int p = 0; p < kSplit<DT>; ++p) o.part[p] = u32x4{0, 0, 0, 0};
-        }
-        u32x4 *dst = q.xp + ((long long)tile * a.chunks * 4 + step) * kSplit<DT> * 64 + lane;
-#pragma unroll
-        for (int p = 0; p < kSplit<DT>; ++p) dst[p * 64] = o.part[p];
-        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(bf16_const(ZP ? -1.0f : -24.0f), o, sum);
+        for (int p = 0; p < kSplit<DT>; ++p) dst[p * 64] = o[s].part[p];
+        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(bf16_const(ZP ? -1.0f : -24.0f), o[s], sum);
     }
-    if constexpr (DT == BCONV_BF16)
-        if (lane < 16) q.xs[((long long)tile * groups + g) * 16 + lane] = sum[0];
+    if constexpr (DT == BCONV_BF16) xs = sum[0];
+    if constexpr (DT != BCONV_F16)
+        if (lane < 16) q.xs[((long long)tile * groups + g) * 16 + lane] = xs;
 }
 
-// Rows of x a workgroup takes: 128 (64 in fp32, whose operands are three
-// parts), or the 64 or 32 that hold them all.
+// Rows of x a workgroup takes: 128 (64 in fp32, whose operands are two parts),
+// or the 64 or 32 that hold them all.
 constexpr int most_cols(int dtype) { return dtype == BCONV_F32 ? 64 : 128; }
 
 // Shape of a workgroup of the many-row kernel: its four waves take 64 outputs
@@ -320,9 +331,10 @@ template <int COLS> struct ManyShape {
 // Bound by instruction issue: 256 x 25088 -> 4096 bf16, 71 us (742 TFLOP/s; a
 // large library product reaches 1206), matrix cores busy 39% of the cycles and
 // the vector instructions that decode and scale 55%.  Groups of 32 scale four
-// times as often as groups of 128: 124 us.
+// times as often as groups of 128: 124 us.  fp32, two products for each,
+// with the other two launches: 137 us (200 with three bf16 parts; bf16 83).
 template <int DT, bool ZP, int STEPS, int COLS>
-__global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q4Args a, Q4Many q)
+__global__ __launch_bounds__(256, 2) void q4_many_kernel(Q4Args a, Q4Many q)
 {
     typedef ManyShape<COLS> S;
     constexpr int P = kSplit<DT>, G = 4 / STEPS, CB = S::CB, CT = COLS / 16, RT = S::TILES;
@@ -330,7 +342,7 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
     struct Stage {
         u32x4 x[UNITS * 64];
         uint32_t scales[RT * G * 8];                      // [tile][group][16] fp16
-        float xs[DT == BCONV_BF16 ? CT * G * 16 : 4];     // [column tile][group][16]
+        float xs[DT == BCONV_F16 ? 4 : CT * G * 16];      // [column tile][group][16]
         uint32_t zeros[ZP ? RT * G * 4 : 4];              // [tile][group][16] bytes
     };
     __shared__ Stage stage[2];
@@ -378,7 +390,7 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
                 }
             }
         }
-        if constexpr (DT == BCONV_BF16) {
+        if constexpr (DT != BCONV_F16) {
 #pragma unroll
             for (int i = 0; i < (CT * G * 16 + 63) / 64; ++i) {
                 const int e = i * 64 + lane;
@@ -442,9 +454,9 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
             float xs[CB];
 #pragma unroll
             for (int t = 0; t < CB; ++t) {
-                xs[t] = DT == BCONV_BF16 ? st.xs[((my_col + t * 2 + (row >> 4)) * G + g) * 16 + (row & 15)] : 0.0f;
+                xs[t] = DT != BCONV_F16 ? st.xs[((my_col + t * 2 + (row >> 4)) * G + g) * 16 + (row & 15)] : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 16; ++i) off[t][i] = xs[t];
+                for (int i = 0; i < 16; ++i) off[t][i] = DT == BCONV_BF16 ? xs[t] : 0.0f;
             }
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -485,8 +497,11 @@ __global__ __launch_bounds__(256, DT == BCONV_F32 ? 1 : 2) void q4_many_kernel(Q
 #pragma unroll
                 for (int t = 0; t < CB; ++t)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        acc[r][t][i] = __builtin_fmaf((float)s4[i >> 2][i & 3], d[t][i], acc[r][t][i]);
+                    for (int i = 0; i < 16; ++i) {
+                        float scale = (float)s4[i >> 2][i & 3];
+                        if constexpr (DT == BCONV_F32) scale *= xs[t];
+                        acc[r][t][i] = __builtin_fmaf(scale, d[t][i], acc[r][t][i]);
+                    }
             }
         }
     }
@@ -539,28 +554,29 @@ Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, in
     Q4Plan p{};
     // The few-row kernel reads the codes once for 16 rows of x; the many-row
     // kernel's three launches cost about 8 us more and pay from 32 MiB of codes
-    // read that way on (16 in fp32, where the few-row kernel converts x again
+    // read that way on (12 in fp32, where the few-row kernel converts x again
     // for every 64 outputs).  bf16, 2048 x 2048: 64 rows 7.0 us against 14.0,
     // 300 rows 25.2 against 23.2; 4096 x 4096: 32 rows 11.2 against 14.5, 128
-    // rows 40.3 against 26.8; fp32, 2048 x 2048: 64 rows 12.0 against 18.3, 128
-    // rows 20.6 against 19.9.
+    // rows 40.3 against 26.8; fp32, 2048 x 2048: 64 rows 11.6 against 16.5, 100
+    // rows 19.6 against 17.2; 4096 x 4096: 32 rows 20.0 against 18.1.
     const long long codes = (long long)tiles * chunks;  // KiB
-    p.many = rows > 16 && (rows + 15) / 16 * codes > (dtype == BCONV_F32 ? 16384 : 32768);
+    p.many = rows > 16 && (rows + 15) / 16 * codes > (dtype == BCONV_F32 ? 12288 : 32768);
     if (!p.many) {
         // With several rows, x's operands are shared by as many output tiles as
         // still leave a workgroup for every compute unit (13 x 5000 -> 11003,
         // bf16: four tiles 12.3 us, one 15.0).  One row shares nothing worth it
-        // (11.6 against 11.0).  Where one tile a workgroup is left and the inputs
+        // (11.6 against 11.0), except in fp32, which converts it (three tiles 13.6,
+        // one 18.8).  Where one tile a workgroup is left and the inputs
         // are long, sixteen waves split them instead of eight (1 x 25088 -> 4096:
         // 12.8 us against 14.6; 1 x 4096 -> 12000: 10.1 against 8.4).
-        p.rt = rows > 1 ? (tiles + cus - 1) / cus : 1;
+        p.rt = rows > 1 || dtype == BCONV_F32 ? (tiles + cus - 1) / cus : 1;
         if (p.rt > 4) p.rt = 4;
         p.waves = p.rt == 1 && chunks >= 64 && tiles <= 2 * cus ? 16 : 8;
         return p;
     }
     auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     p.cols = rows <= 32 ? 32 : rows <= 64 ? 64 : most_cols(dtype);
-    const int parts = dtype == BCONV_F32 ? 3 : 1;
+    const int parts = dtype == BCONV_F32 ? 2 : 1;
     const int block_tiles = p.cols == 32 ? ManyShape<32>::TILES : ManyShape<64>::TILES;
     p.q.col_blocks = (rows + p.cols - 1) / p.cols;
     p.q.col_tiles = p.q.col_blocks * (p.cols / 16);
@@ -573,7 +589,7 @@ Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, in
     if (splits > chunks / 4) splits = chunks / 4;
     p.q.splits = splits < 1 ? 1 : (int)splits;
     p.xs_offset = up((size_t)p.q.col_tiles * chunks * 4 * parts * 1024);
-    p.sums_offset = p.xs_offset + (dtype == BCONV_BF16 ? up((size_t)p.q.col_tiles * chunks * per_chunk * 16 * 4) : 0);
+    p.sums_offset = p.xs_offset + (dtype == BCONV_F16 ? 0 : up((size_t)p.q.col_tiles * chunks * per_chunk * 16 * 4));
     p.bytes = p.sums_offset + (p.q.splits > 1 ? (size_t)p.q.splits * p.q.col_tiles * 16 * p.q.padded_n * 4 : 0);
     return p;
 }

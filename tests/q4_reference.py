@@ -33,7 +33,7 @@ def linear_bound(y, mass, bias, k, group, dtype):
     """Every fp32 rounding of the kernel is of a partial sum no larger than the
     sum of |x| (code + offset <= 31 + 31) |s|: at most two products a weight
     within its group, then one a group and wave, then the join of the waves and
-    the bias.  Three bf16 parts of an fp32 x triple the products of a group."""
+    the bias.  The parts of an fp32 x (up to three) multiply the products of a group."""
     steps = 2 * group * (3 if dtype == "f32" else 1) + -(-k // 32) + 64
     b = np.abs(bias).max() if bias is not None and bias.size else 0.0
     return ROUND[dtype] * (1 + 2.0 ** -8) * np.abs(y) + 2.0 * EPS * steps * (mass + b) + TINY[dtype]
@@ -146,7 +146,7 @@ def attention_bound(out, terms, dim, longest, dtype):
     offset of 24 against codes of up to 8 around the middle, plus the
     midpoints): zerr.  Probabilities carry zerr twice (numerator and
     denominator) and the rounding of exp2; they are rounded for the matrix
-    cores to one, two or three bf16 parts (8, 16 or 24 bits) times a code of at most 8 steps, and the value
+    cores to parts of 8, 16 or 24 bits together times a code of at most 8 steps, and the value
     sums run with an offset of 136 steps (24 in fp32) in fp32."""
     zmass, vmax, pstep = (t[..., None] for t in terms)
     parts = 3 if dtype == "f32" else 1

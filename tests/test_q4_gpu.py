@@ -192,6 +192,26 @@ def test_linear_nonfinite(dev, dtype, rows):
     assert np.array_equal(np.delete(y, 1, 0), np.delete(z, 1, 0))
 
 
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("rows,n", [(1, 80), (13, 5000), (70, 300), (70, 9000)])
+def test_linear_fp32_range(dev, rows, n, zeros):
+    """fp32 rows from 1e-30 to 1e30 with values of one row 2^20 apart: a value is
+    split to 2^-24 of itself or 2^-39 of its row's largest, whichever is more."""
+    say("fp32 range", rows, n, zeros)
+    rng = np.random.default_rng(rows + n)
+    layer, *w = make_linear(rng, 2000, n, 64, zeros, False)
+    x = rng.normal(0, 1, (rows, 2000)) * 2.0 ** rng.integers(-20, 1, (rows, 2000))
+    x = (x * 10.0 ** np.linspace(-30, 30, rows)[:, None]).astype(np.float32)
+    y = layer.forward(torch.from_numpy(x).to(dev))
+    xh = x.astype(np.float64)
+    want, mass = ref.linear(xh, *w, 64)
+    weights = ref.linear(np.ones((1, 2000)), *w, 64)[1]
+    bound = (ref.linear_bound(want, mass, None, 2000, 64, "f32") + 2.0 ** -24 * mass +
+             2.0 ** -39 * np.abs(xh).max(1, keepdims=True) * weights)
+    bad = ~(np.abs(host(y) - want) <= bound)
+    assert not bad.any(), f"{bad.sum()} of {bad.size} off"
+
+
 @pytest.mark.parametrize("rows", [2, 70])
 def test_linear_nonfinite_bf16(dev, rows):
     """A bf16 row with an infinity gives NaN in that row alone."""
@@ -462,6 +482,29 @@ def test_attention_few_columns(dev, dtype, dim, group, heads, counts, window):
     say("few columns", dtype, dim, group, heads, counts, window)
     rng = np.random.default_rng(dim * 100 + group + heads * 10 + sum(counts))
     check_attention(rng, dev, dtype, [703, 2, 45], counts, 2 * heads, 2, dim, group, 16, window)
+
+
+@pytest.mark.parametrize("heads", [2, 32])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (200, 64)])
+def test_attention_fp32_steps(dev, dim, group, heads):
+    """Values whose steps span 1e-3 to 1e3, growing and shrinking along the
+    context, under queries of 1e-15 to 1e15 with the scale that undoes it."""
+    rng = np.random.default_rng(dim + heads)
+    for order in (1, -1):
+        for size in (1e-15, 1.0, 1e15):
+            n, block = 900, 16
+            cache, table, kx, vx, vs = make_cache(rng, dev, [n], 2, dim, group, block)
+            slots = (table[0, np.arange(n) // block].astype(np.int64) * block + np.arange(n) % block)
+            k = rng.normal(0, 1, (n, 2, dim)).astype(np.float32)
+            v = (rng.normal(0, 1, k.shape) * 10.0 ** np.linspace(-3, 3, n)[::order, None, None]).astype(np.float32)
+            cache.append(torch.from_numpy(k).to(dev), torch.from_numpy(v).to(dev),
+                         torch.from_numpy(slots.astype(np.int32)).to(dev))
+            kx[slots] = ref.quantise(k, group)[3]
+            _, s, _, val = ref.quantise(v, group)
+            vx[slots], vs[slots] = val, s.astype(np.float64).max(-1)
+            q = torch.from_numpy((rng.normal(0, 1, (1, heads, dim)) * size).astype(np.float32)).to(dev)
+            check_attention(rng, dev, "f32", [n], [1], heads, 2, dim, group, block, uniform=True, q=q,
+                            made=(cache, table, kx, vx, vs), scale=dim ** -0.5 / size)
 
 
 def test_attention_lowest_logits(dev):
