@@ -16,14 +16,15 @@
 //
 // Bound by instruction issue, not by the cache's bytes: 128 channels in groups
 // of 64 take about 350 vector and 24 matrix instructions a tile (decoding 120,
-// steps and midpoints 128, softmax 40) for 4.6 KB.  32 requests of up to 8192
-// tokens, 32 heads over 8, bf16: 53 us for 183 MB (3.5 TB/s; a large read
-// reaches 6.05), and 5.7 us for the join of their parts; vector units busy 60%,
-// the rest is the requests' uneven lengths and a workgroup's first loads.  Two
-// requests of 131071 tokens, 16 heads over one, fp16: 15.5 us and 5.1 us for the
-// join (floor 5.5 us).  One of 777 tokens: 7.6 us, a chain of loads (lengths,
-// block ids, keys, values).  Registers decide the rest: 128 a wave and four waves
-// a SIMD; spilling 15 of them costs 58 -> 84 us, three waves at 168 registers 66.
+// steps and midpoints 128, softmax 40) for 4.6 KB, 270 vector ones where few
+// columns share their softmax (see Steps).  32 requests of up to 8192 tokens, 32
+// heads over 8, bf16: 48.3 us for 183 MB (3.8 TB/s; 4.6 where all lengths are 8192;
+// a large read reaches 6.05), and 5.7 us for the join of their parts; the rest is
+// the requests' uneven lengths and a workgroup's first loads.  Two requests of
+// 131071 tokens, 16 heads over one, fp16: 15.1 us and 5.1 us for the join (floor
+// 5.5 us).  One of 777 tokens: 7.0 us, a chain of loads (lengths, block ids, keys,
+// values).  Registers decide the rest: 128 a wave and four waves a SIMD; spilling
+// 15 of them costs 58 -> 84 us, three waves at 168 registers 66.
 #include <hip/hip_runtime.h>
 
 #include <cmath>
@@ -123,31 +124,43 @@ __device__ __forceinline__ float lane_groups_sum(float v)
 }
 
 // Type of the operands of V^T P, and parts that a probability, times its value's
-// step, is rounded into: one bf16 for bf16 results, whose own rounding is as
-// coarse; two (16 bits) for fp16 results; two fp16 parts (24 bits) for fp32 results.
+// step, is rounded into: one fp16 (11 bits) for bf16 results, two bf16 (16 bits) for
+// fp16 results, two fp16 (24 bits) for fp32 results.
 //
-// fp16's exponents need these products near 1: they are taken times a power of
-// two a column and group of channels, which is chosen anew when the column's
-// maximum moves or a product would pass fp16's largest.  The products stay below
-// 2^(kUnitBits + 1) at a choice and have room to grow until the next.  Against three
-// bf16 parts and exact bf16 codes, for keys as well: 32 requests of up to 8192
-// tokens, 32 heads over 8, 88 -> 72 us; 64 heads 108 -> 87.  fp16 results gain
-// nothing from it (64 heads: 74 us with bf16 parts, 80 with fp16).
-template <int DT> constexpr int kValueType = DT == BCONV_F32 ? BCONV_F16 : BCONV_BF16;
+// fp16's exponents need these products near 1.
+//   bf16 results: m, what is taken off the logits, is the running maximum less a
+//     lead that a wave chooses by the largest step it has met, so that no product
+//     passes 2^14; it changes when a larger step comes.  Steps down to 2^-22 of
+//     the largest keep all 11 bits, down to 2^-25 the 8 that a bf16 part would.
+//     One bf16 part costs the same and adds an error as large as the result's own
+//     rounding (2.4e-3 against 1.7e-3 on 32 ragged requests).
+//   fp32 results: they are taken times a power of two a column and group of
+//     channels, which is chosen anew when the column's maximum moves or a product
+//     would pass fp16's largest.  The products stay below 2^(kUnitBits + 1) at a
+//     choice and have room to grow until the next.  Against three bf16 parts and
+//     exact bf16 codes, for keys as well: 32 requests of up to 8192 tokens, 32
+//     heads over 8, 88 -> 72 us; 64 heads 108 -> 87.
+// fp16 results gain nothing from either (64 heads: 74 us with bf16 parts, 80 with
+// fp16).
+template <int DT> constexpr int kValueType = DT == BCONV_F16 ? BCONV_BF16 : BCONV_F16;
 template <int DT> constexpr int kProbParts = DT == BCONV_BF16 ? 1 : 2;
 constexpr int kUnitBits = 8;
 typedef Range<kUnitBits, -40> Unit;  // so that a change of unit keeps fp32 sums in range
 
-// A value code decodes to code - 8 in fp16 or, in bf16 (which has no packed
-// subtraction), to 128 + c, with no shift for the first code.  There a product
-// with the constant -136 goes with each product, so that the running sums hold
-// code - 8 as well and never grow with the offset.  For bf16 results, whose own
+// The lead for steps below fp16 `limit` = e << 10, that is below 2^(e - 15): times
+// them, probabilities of up to 2^(kSlack + lead) stay up to 2^14.
+__device__ __forceinline__ float lead_of(uint32_t limit) { return 29.0f - kSlack - (float)(limit >> 10); }
+
+// A value code decodes to 128 + c in bf16 or 1024 + c in fp16, with no shift for
+// the first code.  For fp32 results 1032 is subtracted at once; for fp16 results a
+// product with the constant -136 goes with each product, so that the running sums
+// hold code - 8 as well and never grow with the offset.  For bf16 results, whose own
 // rounding hides what the offset costs an fp32 sum, the sums of the probabilities
 // are kept instead (one product a group in place of one a channel tile) and taken
 // out at the end: 128 channels in one group, 32 requests of up to 8192 tokens 51.9
 // -> 50.3 us.  With two groups the sums' registers would spill (58.3 -> 65.2 us).
 constexpr bool sums_probs(int dt, int dp, int groups) { return dt == BCONV_BF16 && !(dp == 128 && groups == 2); }
-constexpr float kValueOffset = 136.0f;
+template <int DT> constexpr float kValueOffset = DT == BCONV_F16 ? 136.0f : 1032.0f;
 
 // The word that lane N of each 16 lanes holds.
 template <int N> __device__ __forceinline__ uint32_t from_lane(uint32_t v)
@@ -180,12 +193,11 @@ template <int R> __device__ __forceinline__ uint32_t entry(const uint32_t (&v)[R
     }
 }
 
-// Codes j of two tokens' rows (16 bits of each row's part) as a pair: 128 + c in
-// bf16, c - 8 in fp16.
+// Codes j of two tokens' rows (16 bits of each row's part) as a pair.
 template <int DT> __device__ __forceinline__ uint32_t value_pair(uint32_t two, int j, const CodeBits &bits)
 {
     const uint32_t c = bits(two >> (4 * j));
-    if constexpr (kValueType<DT> == BCONV_BF16) return c;
+    if constexpr (DT != BCONV_F32) return c;
     return __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, c) - f16x2{(_Float16)1032.0f, (_Float16)1032.0f});
 }
 
@@ -234,6 +246,18 @@ template <int GROUPS, int REP> struct Steps {
             }
     }
     __device__ __forceinline__ f16x2 at(int u, int e, int g) const { return __builtin_bit_cast(f16x2, v[u][e][g]); }
+    // the largest step's bits among the lane's
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t t = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+#pragma unroll
+                for (int g = 0; g < GROUPS; ++g) t = max(t, v[u][e][g] & 0xffffu);
+        return t;
+    }
     // drops the tokens that `keep` (of a token's number in the run) denies
     template <typename F> __device__ __forceinline__ void mask(int lane, F keep)
     {
@@ -262,6 +286,13 @@ template <int GROUPS> struct Steps<GROUPS, 1> {
     __device__ __forceinline__ f16x2 at(int u, int e, int g) const
     {
         return __builtin_bit_cast(f16x2, entry(v, (4 * u + e) * GROUPS + g));
+    }
+    __device__ __forceinline__ uint32_t top() const
+    {
+        uint32_t t = v[0] & 0xffffu;
+#pragma unroll
+        for (int x = 1; x < kTable<GROUPS>; ++x) t = max(t, v[x] & 0xffffu);
+        return t;
     }
     template <typename F> __device__ __forceinline__ void mask(int lane, F keep)
     {
@@ -383,7 +414,7 @@ kv4_attention_kernel(AttnArgs a)
     constexpr int TILES = DP / 16;             // 16-channel tiles of V^T P
     constexpr int VPER = TILES / GROUPS;       // of them a group
     constexpr int NP = kProbParts<DT>, VT = kValueType<DT>;
-    constexpr bool UNITS = VT == BCONV_F16;
+    constexpr bool UNITS = DT == BCONV_F32, LEAD = DT == BCONV_BF16;
     constexpr int WAVES = attn_waves(DT, DP, GROUPS), COLS = kCols / REP;
     constexpr int E = 4 / REP;                 // tokens of four that a copy takes
     constexpr bool SUMS = sums_probs(DT, DP, GROUPS);
@@ -477,25 +508,25 @@ kv4_attention_kernel(AttnArgs a)
     all_lo = __builtin_amdgcn_readfirstlane(all_lo);
     all_hi = __builtin_amdgcn_readfirstlane(all_hi);
 
-    // sums of q over each group, for the midpoints and the codes' offset: a
-    // product starts from -24 of them or, where a copy takes few of its results,
-    // each of those gets them afterwards (three registers a group fewer)
-    constexpr bool START = DT == BCONV_BF16 && REP == 1;
+    // sums of q over each group, for the midpoints and the codes' offset (16 in
+    // bf16: a product gets -24 of them once it is a lane's own, which takes fewer
+    // registers than starting from them)
     float qsum[GROUPS];
-    f32x4 qoff[START ? GROUPS : 1];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
         f32x4 x = {0, 0, 0, 0};
-        const u32x4 one = DT == BCONV_BF16 ? bf16_const(1.0f) : u32x4{0x3c003c00u, 0x3c003c00u, 0x3c003c00u, 0x3c003c00u};
+        const u32x4 one = constant<DT>(1.0f);
 #pragma unroll
         for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s], x);
         qsum[g] = x[0];
-        if constexpr (START) qoff[g] = x * -24.0f;
     }
 
     f32x4 acc[TILES], psum[SUMS ? GROUPS : 1];
     float mid[GROUPS], m = kLowest, l = 0.0f;
     float unit[UNITS ? GROUPS : 1];  // what the group's products are multiplied by
+    // LEAD: steps' bits stay below `limit`, and m is the maximum less slack - kSlack
+    uint32_t limit = LEAD ? 0u : 1u;
+    float slack = kSlack;
 #pragma unroll
     for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -505,7 +536,7 @@ kv4_attention_kernel(AttnArgs a)
         if constexpr (SUMS) psum[g] = f32x4{0, 0, 0, 0};
     }
     const Zero<DT> eight(8);
-    const u32x4 offset = bf16_const(SUMS ? 1.0f : -kValueOffset);  // bf16
+    const u32x4 offset = constant<VT>(SUMS ? 1.0f : -kValueOffset<DT>);
     const CodeBits kbits = code_bits<DT>(), vbits = value_bits<DT>();
 
     const int vrun = lg * 8;
@@ -533,9 +564,7 @@ kv4_attention_kernel(AttnArgs a)
             if (!FULL && g * PER * 32 >= a.g.dim) continue;
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                f32x4 d;
-                if constexpr (START) d = qoff[g];
-                else d = f32x4{0, 0, 0, 0};
+                f32x4 d = {0, 0, 0, 0};
 #pragma unroll
                 for (int s = 0; s < PER; ++s) {
                     const u32x4 k = decode<DT>(keys.w[u][g * PER + s], eight, kbits);
@@ -545,7 +574,7 @@ kv4_attention_kernel(AttnArgs a)
                 for (int e = 0; e < E; ++e) {
                     const f16x2 sb = keys.steps.at(u, e, g);
                     float mine = own<REP>(d, e, lane);
-                    if constexpr (DT == BCONV_BF16 && !START) mine = __builtin_fmaf(-24.0f, qsum[g], mine);
+                    if constexpr (DT == BCONV_BF16) mine = __builtin_fmaf(-24.0f, qsum[g], mine);
                     z[u][e] = __builtin_fmaf((float)sb[0], mine, z[u][e]);
                     z[u][e] = __builtin_fmaf((float)sb[1], qsum[g], z[u][e]);
                 }
@@ -583,8 +612,20 @@ kv4_attention_kernel(AttnArgs a)
             float top = fmaxf(z[0][0], z[1][0]);
 #pragma unroll
             for (int e = 1; e < E; ++e) top = fmaxf(top, fmaxf(z[0][e], z[1][e]));
-            if (__any(top > m + kSlack)) {
-                top = fmaxf(m, copies_max<REP>(lane_groups_max(top)));
+            const uint32_t step = LEAD ? values.steps.top() : 0u;
+            if (__any(top > m + slack || step >= limit)) {
+                top = fmaxf(m + (slack - kSlack), copies_max<REP>(lane_groups_max(top)));
+                if constexpr (LEAD) {
+                    uint32_t most = lane_groups_max_bits(step);
+#pragma unroll
+                    for (int d = 1; d < 16; d *= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
+                    most = __builtin_amdgcn_readfirstlane(most);
+                    if (most >= limit) {
+                        limit = ((most >> 10) + 1) << 10;
+                        slack = kSlack + lead_of(limit);
+                    }
+                    top -= slack - kSlack;
+                }
                 const float f = __builtin_amdgcn_exp2f(m - top);
                 moved = top > m;
                 m = top;
@@ -642,6 +683,9 @@ kv4_attention_kernel(AttnArgs a)
                 uint32_t two[NP];
                 if constexpr (UNITS) {
                     split_pair(ps[0][e], ps[1][e], unit[g], two[0], two[1]);
+                } else if constexpr (LEAD) {
+                    const f16x2 r = {(_Float16)ps[0][e], (_Float16)ps[1][e]};
+                    two[0] = __builtin_bit_cast(uint32_t, r);
                 } else {
 #pragma unroll
                     for (int k = 0; k < NP; ++k) {
@@ -669,7 +713,7 @@ kv4_attention_kernel(AttnArgs a)
                 }
 #pragma unroll
                 for (int k = NP - 1; k >= 0; --k) {
-                    if constexpr (VT == BCONV_BF16 && !SUMS) acc[tile] = mfma16<VT>(offset, pp[k], acc[tile]);
+                    if constexpr (DT != BCONV_F32 && !SUMS) acc[tile] = mfma16<VT>(offset, pp[k], acc[tile]);
                     acc[tile] = mfma16<VT>(v, pp[k], acc[tile]);
                 }
             }
@@ -694,9 +738,9 @@ kv4_attention_kernel(AttnArgs a)
         const float f = __builtin_amdgcn_exp2f(m - top);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
-            float add = copies_sum<REP>(lane_groups_sum(mid[g]));
-            if constexpr (SUMS) add -= kValueOffset * psum[g][0];
             const float from = UNITS ? 1.0f / unit[g] : 1.0f;  // exact
+            float add = copies_sum<REP>(lane_groups_sum(mid[g]));
+            if constexpr (SUMS) add -= kValueOffset<DT> * psum[g][0];
 #pragma unroll
             for (int j = 0; j < VPER; ++j) {
                 const int tile = g * VPER + j;

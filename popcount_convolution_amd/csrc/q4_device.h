@@ -275,10 +275,11 @@ template <int DT> __device__ __forceinline__ u32x4 decode(uint32_t w, const Zero
     return r;
 }
 
-// The constant operand of bf16 value v in every position.
-__device__ __forceinline__ u32x4 bf16_const(float v)
+// The constant operand of value v (in bf16 or, other types, fp16) in every position.
+template <int DT> __device__ __forceinline__ u32x4 constant(float v)
 {
-    const uint32_t h = __float_as_uint(v) >> 16, w = h | (h << 16);
+    const uint16_t h = DT == BCONV_BF16 ? (uint16_t)(__float_as_uint(v) >> 16) : __builtin_bit_cast(uint16_t, (_Float16)v);
+    const uint32_t w = h | ((uint32_t)h << 16);
     return u32x4{w, w, w, w};
 }
 

@@ -133,7 +133,7 @@ __device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operan
         // matrix cores as well (a constant operand times x)
         f32x4 off = {0, 0, 0, 0};
         if constexpr (DT == BCONV_BF16) {
-            const u32x4 c = bf16_const(ZP ? -1.0f : -24.0f);
+            const u32x4 c = constant<DT>(ZP ? -1.0f : -24.0f);
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) off = mfma_parts<DT>(c, x[g * STEPS + s], off);
         }
@@ -301,7 +301,7 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4Args a, Q4Many q)
         u32x4 *dst = q.xp + ((long long)tile * a.chunks * 4 + g * STEPS + s) * kSplit<DT> * 64 + lane;
 #pragma unroll
         for (int p = 0; p < kSplit<DT>; ++p) dst[p * 64] = o[s].part[p];
-        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(bf16_const(ZP ? -1.0f : -24.0f), o[s], sum);
+        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(constant<DT>(ZP ? -1.0f : -24.0f), o[s], sum);
     }
     if constexpr (DT == BCONV_BF16) xs = sum[0];
     if constexpr (DT != BCONV_F16)

@@ -507,6 +507,33 @@ def test_attention_fp32_steps(dev, dim, group, heads):
                             made=(cache, table, kx, vx, vs), scale=dim ** -0.5 / size)
 
 
+@pytest.mark.parametrize("heads", [4, 32])
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 64), (128, 128), (256, 32)])
+def test_attention_bf16_probabilities(dev, dim, group, heads):
+    """A bf16 result's error is its own rounding's, to a quarter: probabilities
+    have 11 bits, an eighth of bf16's error, on the sum of terms up to a few times
+    the result.  One token's steps are 2^12 of the others', early or late."""
+    rng = np.random.default_rng(dim + heads + group)
+    n, block = 700, 32
+    for at in (None, 3, 650):
+        cache, table, kx, vx, vs = make_cache(rng, dev, [n], 2, dim, group, block)
+        slots = (table[0, np.arange(n) // block].astype(np.int64) * block + np.arange(n) % block)
+        k = rng.normal(0, 1, (n, 2, dim)).astype(np.float32)
+        v = rng.normal(0, 1, k.shape).astype(np.float32)
+        if at is not None:
+            v[at] *= 2.0 ** 12
+        cache.append(torch.from_numpy(k).to(dev), torch.from_numpy(v).to(dev),
+                     torch.from_numpy(slots.astype(np.int32)).to(dev))
+        kx[slots], vx[slots] = ref.quantise(k, group)[3], ref.quantise(v, group)[3]
+        q = torch.from_numpy(rng.normal(0, 1.5, (1, heads, dim)).astype(np.float32)).to(dev).bfloat16()
+        out = cache.attention(q, torch.from_numpy(table).to(dev), torch.tensor([n], dtype=torch.int32, device=dev))
+        want = ref.attention(host(q), kx, vx, vs, table, [n], [1], block_size=block, kv_heads=2, scale=dim ** -0.5,
+                             num_blocks=cache.num_blocks)[0]
+        best = torch.from_numpy(want).bfloat16().double().numpy()
+        rms = lambda e: np.sqrt((e ** 2).mean(-1)).mean()  # noqa: E731
+        assert rms(host(out) - want) <= 1.25 * rms(best - want)
+
+
 def test_attention_lowest_logits(dev):
     """Logits far below any mask's usual value are still those of a softmax: a
     lone token has probability one."""
