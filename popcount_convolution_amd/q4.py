@@ -72,6 +72,12 @@ def _need_ints(t, name: str, count: int, device) -> None:
         _need_dense(t, name, (count,), _torch.int32, device)
 
 
+def _need_int32(value, name: str) -> None:
+    """A number that the C side's int32 holds (ctypes would wrap others)."""
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError(f"{name}: {value} is not a 32-bit number")
+
+
 def _need_rows(t, name: str, heads: int, dim: int) -> int:
     """[tokens, heads, dim] with contiguous channels; token and head strides
     are free.  Returns the tokens."""
@@ -251,6 +257,9 @@ class KV4Cache:
     def __init__(self, num_blocks: int, block_size: int, kv_heads: int, head_dim: int, *, group: int = 64,
                  device=None):
         torch = _torch or _load_torch()
+        for name, value in (("num_blocks", num_blocks), ("block_size", block_size), ("kv_heads", kv_heads),
+                            ("head_dim", head_dim), ("group", group)):
+            _need_int32(value, name)
         self.desc = B.bconv_kv4_desc_t(num_blocks, block_size, kv_heads, head_dim, group)
         self.layout = B.bconv_kv4_layout(self.desc)
         self.num_blocks, self.block_size, self.kv_heads = num_blocks, block_size, kv_heads
@@ -329,6 +338,9 @@ class KV4Cache:
                 raise ValueError(f"q: {tokens} tokens are not a multiple of {requests} requests (pass q_start)")
             if max_q is None:
                 max_q = max(1, tokens // requests if requests else 1)
+        _need_int32(max_q, "max_q")
+        _need_int32(max_context, "max_context")
+        _need_int32(window, "window")
         place, raw = _place(device, stream)
         with place:
             if out is None:
@@ -389,6 +401,8 @@ def build_block_tables(block_table, context_lens, new_lens, free_blocks, free_he
     _need_ints(free_head, "free_head", 1, device)
     if tokens < 0:
         raise ValueError(f"tokens: {tokens} is negative")
+    _need_int32(tokens, "tokens")
+    _need_int32(block_size, "block_size")
     place, raw = _place(device, stream)
     with place:
         # one allocation: q_start, lengths, free head, then the token arrays

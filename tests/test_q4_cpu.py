@@ -245,3 +245,11 @@ def test_reference_attention_invariants():
     out, *_ = ref.attention(q, kx, vx, np.ones((32, 1)), table, [20], [1], block_size=16, kv_heads=1, scale=0.5,
                             window=1)
     assert np.allclose(out[0, 0], vx[3, 0])
+
+
+def test_numbers_past_32_bits():
+    """Numbers that an int32 does not hold are refused, not wrapped."""
+    with pytest.raises(ValueError, match="num_blocks"):
+        pca.KV4Cache(2 ** 32 + 1, 16, 1, 64)
+    with pytest.raises(ValueError, match="block_size"):
+        pca.KV4Cache(1, 2 ** 32 + 16, 1, 64)

@@ -612,6 +612,17 @@ def test_cache_past_32_bits(dev):
     assert not high.pool[:1 << 30].any() and float(low.attention(q, ids, lens).abs().sum()) > 0
 
 
+def test_attention_numbers_past_32_bits(dev):
+    """Bounds that an int32 does not hold are refused, not wrapped."""
+    cache, q = pca.KV4Cache(2, 16, 1, 64), torch.zeros(1, 1, 64, device=dev)
+    table, lens = torch.zeros(1, 2, dtype=torch.int32, device=dev), torch.ones(1, dtype=torch.int32, device=dev)
+    for name in ("max_context", "window", "max_q"):
+        with pytest.raises(ValueError, match=name):
+            cache.attention(q, table, lens, **{name: 2 ** 32 + 5})
+    with pytest.raises(ValueError, match="block_size"):
+        pca.build_block_tables(table, lens, lens, lens, lens, block_size=2 ** 32 + 16, tokens=1)
+
+
 def test_attention_nan_query(dev):
     """A NaN query gives NaN for its own head alone."""
     rng = np.random.default_rng(9)
