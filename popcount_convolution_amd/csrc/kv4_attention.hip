@@ -18,9 +18,9 @@
 // of 64 take about 350 vector and 24 matrix instructions a tile (decoding 120,
 // steps and midpoints 128, softmax 40) for 4.6 KB, 270 vector ones where few
 // columns share their softmax (see Steps).  32 requests of up to 8192 tokens, 32
-// heads over 8, bf16: 48.3 us for 183 MB (3.8 TB/s; 4.6 where all lengths are 8192;
-// a large read reaches 6.05), and 5.7 us for the join of their parts; the rest is
-// the requests' uneven lengths and a workgroup's first loads.  Two requests of
+// heads over 8, bf16: 48.3 us for 183 MB (3.8 TB/s; a large read reaches 6.05), and
+// 5.7 us for the join of their parts (all of 8192 tokens: 4.4 TB/s with the join); the
+// rest is the requests' uneven lengths and a workgroup's first loads.  Two requests of
 // 131071 tokens, 16 heads over one, fp16: 15.1 us and 5.1 us for the join (floor
 // 5.5 us).  One of 777 tokens: 7.0 us, a chain of loads (lengths, block ids, keys,
 // values).  Registers decide the rest: 128 a wave and four waves a SIMD; spilling
