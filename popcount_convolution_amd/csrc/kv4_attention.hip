@@ -128,10 +128,13 @@ __device__ __forceinline__ float lane_groups_sum(float v)
 // fp16 results, two fp16 (24 bits) for fp32 results.
 //
 // fp16's exponents need these products near 1.
-//   bf16 results: m, what is taken off the logits, is the running maximum less a
-//     lead that a wave chooses by the largest step it has met, so that no product
-//     passes 2^14; it changes when a larger step comes.  Steps down to 2^-22 of
-//     the largest keep all 11 bits, down to 2^-25 the 8 that a bf16 part would.
+//   bf16 results: they are taken times 2^lead, a lead that a wave chooses by the
+//     largest step it has met, so that no product passes 2^14; it changes when a
+//     larger step comes.  A new maximum's largest product is 2^5 to 2^6, so steps
+//     down to 2^-19 of the largest keep all 11 bits, down to 2^-22 the 8 that a
+//     bf16 part would.  The lead is added to a logit's distance from the maximum,
+//     which is exact where it matters, and not taken off the maximum itself: from
+//     2^26 on that would round to more than the lead, and products to infinity.
 //     One bf16 part costs the same and adds an error as large as the result's own
 //     rounding (2.4e-3 against 1.7e-3 on 32 ragged requests).
 //   fp32 results: they are taken times a power of two a column and group of
@@ -524,9 +527,9 @@ kv4_attention_kernel(AttnArgs a)
     f32x4 acc[TILES], psum[SUMS ? GROUPS : 1];
     float mid[GROUPS], m = kLowest, l = 0.0f;
     float unit[UNITS ? GROUPS : 1];  // what the group's products are multiplied by
-    // LEAD: steps' bits stay below `limit`, and m is the maximum less slack - kSlack
+    // LEAD: steps' bits stay below `limit`, probabilities are times 2^lead
     uint32_t limit = LEAD ? 0u : 1u;
-    float slack = kSlack;
+    float lead = 0.0f;
 #pragma unroll
     for (int k = 0; k < TILES; ++k) acc[k] = f32x4{0, 0, 0, 0};
 #pragma unroll
@@ -613,8 +616,10 @@ kv4_attention_kernel(AttnArgs a)
 #pragma unroll
             for (int e = 1; e < E; ++e) top = fmaxf(top, fmaxf(z[0][e], z[1][e]));
             const uint32_t step = LEAD ? values.steps.top() : 0u;
-            if (__any(top > m + slack || step >= limit)) {
-                top = fmaxf(m + (slack - kSlack), copies_max<REP>(lane_groups_max(top)));
+            // (m + kSlack would round up to a logit that is further away)
+            if (__any(top - m > kSlack || step >= limit)) {
+                top = fmaxf(m, copies_max<REP>(lane_groups_max(top)));
+                float grown = 0.0f;
                 if constexpr (LEAD) {
                     uint32_t most = lane_groups_max_bits(step);
 #pragma unroll
@@ -622,11 +627,11 @@ kv4_attention_kernel(AttnArgs a)
                     most = __builtin_amdgcn_readfirstlane(most);
                     if (most >= limit) {
                         limit = ((most >> 10) + 1) << 10;
-                        slack = kSlack + lead_of(limit);
+                        grown = lead_of(limit) - lead;
+                        lead += grown;
                     }
-                    top -= slack - kSlack;
                 }
-                const float f = __builtin_amdgcn_exp2f(m - top);
+                const float f = __builtin_amdgcn_exp2f(m - top + grown);
                 moved = top > m;
                 m = top;
                 l *= f;
@@ -642,7 +647,7 @@ kv4_attention_kernel(AttnArgs a)
             for (int u = 0; u < 2; ++u)
 #pragma unroll
                 for (int e = 0; e < E; ++e) {
-                    p[u][e] = __builtin_amdgcn_exp2f(z[u][e] - m);
+                    p[u][e] = __builtin_amdgcn_exp2f(LEAD ? z[u][e] - m + lead : z[u][e] - m);
                     l += p[u][e];
                 }
         }
@@ -728,14 +733,14 @@ kv4_attention_kernel(AttnArgs a)
     l = copies_sum<REP>(lane_groups_sum(l));
     if (lg == 0 && row % REP == 0) {
         sm[wave * COLS + col] = m;
-        sl[wave * COLS + col] = l;
+        sl[wave * COLS + col] = LEAD ? l * __builtin_amdgcn_exp2f(-lead) : l;
     }
     __syncthreads();
     {
         float top = kLowest;
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) top = fmaxf(top, sm[w * COLS + col]);
-        const float f = __builtin_amdgcn_exp2f(m - top);
+        const float f = __builtin_amdgcn_exp2f(m - top - lead);
 #pragma unroll
         for (int g = 0; g < GROUPS; ++g) {
             const float from = UNITS ? 1.0f / unit[g] : 1.0f;  // exact
