@@ -106,7 +106,8 @@ __device__ __forceinline__ Span column_span(const AttnArgs &a, int req, int cb)
         s.t1 = (hi < a.max_context - 1 ? hi : a.max_context - 1) + 1;
         s.low = first_seen(s.last + s.j0, a.window);
         s.t0 = s.low & ~(kTokens - 1);
-        if (s.t1 < s.t0) s.t1 = s.t0;
+        // nothing to see: from 0, so that no part's first token passes 32 bits
+        if (s.t1 <= s.t0) s.t0 = s.t1 = 0;
     }
     return s;
 }

@@ -93,3 +93,39 @@ def test_attention_extreme_logits(dev, dtype, dim, group, heads, length, first, 
     assert not bad.any(), [cases[i] for i in np.flatnonzero(bad.any((1, 2)))]
     top = (z.max(1) + np.log2(p.sum(1)))[:, None] * np.log(2)
     assert (np.abs(host(lse) - top) <= 2.0 ** -21 * np.abs(top)).all()
+
+
+# ------------------------------------------------------------ long lengths
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("heads", [1, 8])
+@pytest.mark.parametrize("window", [5090, 100, 0])
+def test_attention_lengths_near_32_bits(dev, dtype, heads, window):
+    """Lengths up to 2^31 - 1 over a table of 8000 tokens: a query whose window
+    lies past the table sees nothing, in one part or eleven (whose last starts past
+    2^31 where the first starts at the window), and the requests
+    beside it are as they are alone."""
+    print("lengths", dtype, heads, window, flush=True)
+    rng = np.random.default_rng(window)
+    lens = [7000, 2 ** 31 - 1, 2 ** 31 - 40, 2 ** 31 - 700, 2 ** 30, 8000 + 5000, 0]
+    block, width, dim = 16, 500, 64
+    cache = pca.KV4Cache(width, block, 1, dim, group=64)
+    x = [torch.from_numpy(rng.normal(0, 1, (width * block, 1, dim)).astype(np.float32)).to(dev) for _ in range(2)]
+    cache.append(*x, torch.arange(width * block, dtype=torch.int32, device=dev))
+    table = torch.arange(width, dtype=torch.int32, device=dev).repeat(len(lens), 1)
+    q = torch.from_numpy(rng.normal(0, 1, (len(lens), heads, dim)).astype(np.float32)).to(dev).to(DT[dtype])
+    lse = torch.empty(len(lens), heads, device=dev)
+    n = torch.tensor(lens, dtype=torch.int32, device=dev)
+    out = cache.attention(q, table, n, window=window, lse=lse)
+    alone = cache.attention(q[:1], table[:1], n[:1], window=window)
+    whole = cache.attention(q, table, n.clamp(max=width * block))  # without a window all of the table is seen
+    bound = {"bf16": 2.0 ** -7, "f32": 2.0 ** -16}[dtype]  # parts end elsewhere; values are below 4
+    assert float((out[:1] - alone).abs().max()) <= 4 * bound
+    for r, length in enumerate(lens):
+        if length == 0 or window and length - window >= width * block:
+            assert not out[r].any() and bool(torch.isneginf(lse[r]).all())
+        else:
+            assert bool(out[r].any()) and bool(lse[r].isfinite().all())
+            if not window:
+                assert float((out[r] - whole[r]).abs().max()) <= 4 * bound
