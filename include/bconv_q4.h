@@ -182,7 +182,8 @@ bconv_status_t bconv_kv4_attention_workspace_size(const bconv_kv4_desc_t *desc, 
 
 /* The attention.  max_context and max_q bound device values that the host does
  * not see: keys past max_context are not read, so a bound that is too small
- * loses keys.  requests == 0 or q_tokens == 0 is a no-op; without q_start,
+ * loses keys, and workgroups are launched for max_q queries in every request.
+ * requests == 0 or q_tokens == 0 is a no-op; without q_start,
  * q_tokens must be a multiple of requests.  Rows of `out` that no request owns
  * are left as they were. */
 bconv_status_t bconv_kv4_attention(const bconv_kv4_desc_t *desc, void *stream, const bconv_kv4_attention_t *args,

@@ -63,6 +63,22 @@ inline bconv_status_t upload(const T *host, size_t count, T **dev)
     return BCONV_OK;
 }
 
+// Workgroups that one launch takes: the runtime counts a dimension's threads in
+// 32 bits, and no workgroup here has more than 512 threads.
+constexpr long long kMaxGroups = 1LL << 22;
+
+// Calls launch(first, count) for `total` workgroups, as many launches as they
+// take (one, but for extreme sizes); the first error ends it.
+template <typename F> inline hipError_t launch_slices(long long total, F launch)
+{
+    for (long long first = 0; first < total; first += kMaxGroups) {
+        launch(first, (unsigned)(total - first < kMaxGroups ? total - first : kMaxGroups));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 inline bool ranges_overlap(const void *a, size_t an, const void *b, size_t bn)
 {
     const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;

@@ -52,6 +52,7 @@ struct AppendArgs {
     const int *slots;
     int tokens;
     Kv4Geom g;
+    long long first_row;  // of the launch
 };
 
 // DP / 8 lanes a row (token, head, side), 8 channels a lane; since head_dim is
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(AppendArgs a)
     const bool is_v = blockIdx.y != 0;
     const AppendSide &side = a.side[is_v ? 1 : 0];
     const long long rows = (long long)a.tokens * a.g.kv_heads;
-    const long long row = (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const long long row = a.first_row + (long long)blockIdx.x * (256 / L) + threadIdx.x / L;
     const bool live = row < rows;  // every lane stays for the exchanges
     const int token = live ? (int)(row / a.g.kv_heads) : 0, head = live ? (int)(row % a.g.kv_heads) : 0;
     const bool real = live && 8 * p < a.g.dim;
@@ -188,18 +189,21 @@ __global__ __launch_bounds__(256) void kv4_append_kernel(AppendArgs a)
 }
 
 template <int DT, int DP>
-hipError_t launch_append_dim(const AppendArgs &a, int group, hipStream_t s)
+hipError_t launch_append_dim(AppendArgs a, int group, hipStream_t s)
 {
+    constexpr int ROWS = 256 / (DP / 8);  // a workgroup
     const long long rows = (long long)a.tokens * a.g.kv_heads;
-    const dim3 grid((unsigned)((rows + 256 / (DP / 8) - 1) / (256 / (DP / 8))), 2);
     const int lanes = (group < DP ? group : DP) / 8;
-    if (lanes == 4)
-        hipLaunchKernelGGL((kv4_append_kernel<DT, DP, 4>), grid, dim3(256), 0, s, a);
-    else if (lanes == 8)
-        hipLaunchKernelGGL((kv4_append_kernel<DT, DP, 8>), grid, dim3(256), 0, s, a);
-    else if constexpr (DP >= 128)
-        hipLaunchKernelGGL((kv4_append_kernel<DT, DP, 16>), grid, dim3(256), 0, s, a);
-    return hipGetLastError();
+    return launch_slices((rows + ROWS - 1) / ROWS, [&](long long first, unsigned count) {
+        a.first_row = first * ROWS;
+        const dim3 grid(count, 2);
+        if (lanes == 4)
+            hipLaunchKernelGGL((kv4_append_kernel<DT, DP, 4>), grid, dim3(256), 0, s, a);
+        else if (lanes == 8)
+            hipLaunchKernelGGL((kv4_append_kernel<DT, DP, 8>), grid, dim3(256), 0, s, a);
+        else if constexpr (DP >= 128)
+            hipLaunchKernelGGL((kv4_append_kernel<DT, DP, 16>), grid, dim3(256), 0, s, a);
+    });
 }
 
 template <int DT>

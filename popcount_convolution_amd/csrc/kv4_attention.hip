@@ -61,6 +61,7 @@ struct AttnArgs {
     float *part_o;                       // [column rows][parts][dim_padded]
     float2 *part_ml;                     // [column rows][parts]
     Kv4Geom g;
+    int first;  // number of the launch's first workgroup
 };
 
 constexpr int kMaxParts = 512;
@@ -425,7 +426,7 @@ kv4_attention_kernel(AttnArgs a)
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 15, lg = lane >> 4, col = row / REP;
-    int id = blockIdx.x;
+    int id = a.first + (int)blockIdx.x;
     const int part = id % a.parts;
     id /= a.parts;
     const int cb = id % a.col_blocks;
@@ -792,7 +793,7 @@ __global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a)
     __shared__ float factor[kMaxParts], edge[2 * WAVES];
     __shared__ f32x4 sums[SLICES][THREADS];
     const int per_head = a.max_q * a.ratio;
-    const int id = blockIdx.x, tid = threadIdx.x;
+    const int id = a.first + (int)blockIdx.x, tid = threadIdx.x;
     const int c = id % per_head, head = id / per_head % a.g.kv_heads, req = id / per_head / a.g.kv_heads;
     const Span sp = column_span(a, req, c / kCols);
     const int span = sp.t1 - sp.t0;
@@ -841,17 +842,21 @@ __global__ __launch_bounds__(kMaxParts) void kv4_combine_kernel(AttnArgs a)
 // ------------------------------------------------------------------ dispatch
 
 template <int DT, int DP, int GROUPS, bool FULL, int REP>
-hipError_t launch_attention_full(const AttnArgs &a, hipStream_t s)
+hipError_t launch_attention_full(AttnArgs a, hipStream_t s)
 {
     constexpr int WAVES = attn_waves(DT, DP, GROUPS);
     const size_t lds = (size_t)WAVES * (kCols / REP) * (DP + 4 + 2) * sizeof(float);
     const long long grid = (long long)a.requests * a.g.kv_heads * a.col_blocks * a.parts;
-    hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, FULL, REP>), dim3((unsigned)grid), dim3(WAVES * 64), lds, s, a);
-    hipError_t e = hipGetLastError();
+    hipError_t e = launch_slices(grid, [&](long long first, unsigned count) {
+        a.first = (int)first;
+        hipLaunchKernelGGL((kv4_attention_kernel<DT, DP, GROUPS, FULL, REP>), dim3(count), dim3(WAVES * 64), lds, s, a);
+    });
     if (e == hipSuccess && a.parts > 1) {
         const long long cols = (long long)a.requests * a.g.kv_heads * a.max_q * a.ratio;
-        hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3((unsigned)cols), dim3(kMaxParts), 0, s, a);
-        e = hipGetLastError();
+        e = launch_slices(cols, [&](long long first, unsigned count) {
+            a.first = (int)first;
+            hipLaunchKernelGGL((kv4_combine_kernel<DT, DP>), dim3(count), dim3(kMaxParts), 0, s, a);
+        });
     }
     return e;
 }

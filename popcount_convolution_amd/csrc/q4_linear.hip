@@ -549,6 +549,15 @@ struct Q4Plan {
     size_t xs_offset, sums_offset, bytes;
 };
 
+// Rows that one set of launches takes: a call of more is several, so that no
+// launch passes 32 bits of threads (the packing kernel's waves are (16 rows,
+// group) pairs) and the operands' workspace does not grow with the rows for ever.
+int slab_rows(int chunks, int per_chunk)
+{
+    const long long tiles = (1LL << 25) / ((long long)chunks * per_chunk) / 8 * 8;  // chunks * per_chunk <= 2^15
+    return tiles < (1 << 14) ? (int)tiles * 16 : 1 << 18;
+}
+
 Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, int cus)
 {
     Q4Plan p{};
@@ -592,6 +601,14 @@ Q4Plan plan_linear(int rows, int dtype, int tiles, int chunks, int per_chunk, in
     p.sums_offset = p.xs_offset + (dtype == BCONV_F16 ? 0 : up((size_t)p.q.col_tiles * chunks * per_chunk * 16 * 4));
     p.bytes = p.sums_offset + (p.q.splits > 1 ? (size_t)p.q.splits * p.q.col_tiles * 16 * p.q.padded_n * 4 : 0);
     return p;
+}
+
+// The same plan, and workspace, for the last slab's fewer rows.
+void fewer_rows(Q4Plan &p, int rows)
+{
+    if (!p.many) return;
+    p.q.col_blocks = (rows + p.cols - 1) / p.cols;
+    p.q.col_tiles = p.q.col_blocks * (p.cols / 16);
 }
 
 template <int DT, bool ZP, int STEPS, int RT, int WAVES>
@@ -783,7 +800,8 @@ bconv_status_t bconv_q4_linear_workspace_size(bconv_q4_linear_t h, int32_t rows,
     if (!h || !bytes) return fail(BCONV_ERR_INVALID_ARGUMENT, "handle or bytes is NULL");
     if (rows < 0) return fail(BCONV_ERR_INVALID_ARGUMENT, "rows must be >= 0");
     if (!dtype_bytes(dtype)) return fail(BCONV_ERR_INVALID_ARGUMENT, "unknown dtype %d", dtype);
-    *bytes = rows ? bconv::plan_linear(rows, dtype, h->tiles, h->chunks, h->per_chunk, h->cus).bytes : 0;
+    const int slab = bconv::slab_rows(h->chunks, h->per_chunk);
+    *bytes = rows ? bconv::plan_linear(rows < slab ? rows : slab, dtype, h->tiles, h->chunks, h->per_chunk, h->cus).bytes : 0;
     return BCONV_OK;
 }
 
@@ -802,7 +820,8 @@ bconv_status_t bconv_q4_linear_forward(bconv_q4_linear_t h, void *stream, int32_
     if (((uintptr_t)x | (uintptr_t)y) % es) return fail(BCONV_ERR_INVALID_ARGUMENT, "x/y not aligned to an element");
     const size_t xb = ((size_t)(rows - 1) * ldx + k) * es, yb = ((size_t)(rows - 1) * ldy + n) * es;
     if (rows_overlap(x, ldx, k, y, ldy, n, rows, es)) return fail(BCONV_ERR_INVALID_ARGUMENT, "x and y overlap");
-    bconv::Q4Plan p = bconv::plan_linear(rows, dtype, h->tiles, h->chunks, h->per_chunk, h->cus);
+    const int slab = bconv::slab_rows(h->chunks, h->per_chunk);
+    bconv::Q4Plan p = bconv::plan_linear(rows < slab ? rows : slab, dtype, h->tiles, h->chunks, h->per_chunk, h->cus);
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
         return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes,
                     workspace ? workspace_bytes : (size_t)0);
@@ -823,24 +842,27 @@ bconv_status_t bconv_q4_linear_forward(bconv_q4_linear_t h, void *stream, int32_
     a.scales = h->d_scales;
     a.zeros = h->d_zeros;
     a.bias = h->d_bias;
-    a.x = x;
-    a.y = y;
     a.ldx = ldx;
     a.ldy = ldy;
-    a.m = rows;
     a.n = n;
     a.k = k;
     a.tiles = h->tiles;
     a.chunks = h->chunks;
     a.vec = ((uintptr_t)x % 16 == 0) && (ldx * es % 16 == 0);
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e;
-    switch (dtype) {
-    case BCONV_F32: e = bconv::dispatch_zero<BCONV_F32>(a, p, h->desc.group, s); break;
-    case BCONV_F16: e = bconv::dispatch_zero<BCONV_F16>(a, p, h->desc.group, s); break;
-    default: e = bconv::dispatch_zero<BCONV_BF16>(a, p, h->desc.group, s); break;
+    for (int64_t first = 0; first < rows; first += slab) {
+        a.x = static_cast<const char *>(x) + first * ldx * es;
+        a.y = static_cast<char *>(y) + first * ldy * es;
+        a.m = (int)(rows - first < slab ? rows - first : slab);
+        if (first > 0) bconv::fewer_rows(p, a.m);
+        hipError_t e;
+        switch (dtype) {
+        case BCONV_F32: e = bconv::dispatch_zero<BCONV_F32>(a, p, h->desc.group, s); break;
+        case BCONV_F16: e = bconv::dispatch_zero<BCONV_F16>(a, p, h->desc.group, s); break;
+        default: e = bconv::dispatch_zero<BCONV_BF16>(a, p, h->desc.group, s); break;
+        }
+        if (e != hipSuccess) return hip_fail(e, "4-bit linear kernel");
     }
-    if (e != hipSuccess) return hip_fail(e, "4-bit linear kernel");
     return BCONV_OK;
 }
 

@@ -311,7 +311,9 @@ class KV4Cache:
         ``block_table``: int32 ``[requests, width]``; ``context_lens``: int32
         ``[requests]``, cached tokens with the new ones; ``q_start``: int32
         ``[requests + 1]`` prefix sums of the requests' queries, with ``max_q`` the
-        most of one request, or None for the same number each.  ``max_context``
+        most of one request (all tokens by default, which launches workgroups for
+        that many in every request: give it where it is known), or None for the same
+        number each.  ``max_context``
         bounds the context lengths (the table's width by default).  ``scale``
         defaults to ``head_dim ** -0.5``; ``window`` > 0 limits a query to that many
         last positions.  ``lse``: float32 ``[tokens, heads]`` to fill."""

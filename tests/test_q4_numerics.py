@@ -129,3 +129,88 @@ def test_attention_lengths_near_32_bits(dev, dtype, heads, window):
             assert bool(out[r].any()) and bool(lse[r].isfinite().all())
             if not window:
                 assert float((out[r] - whole[r]).abs().max()) <= 4 * bound
+
+
+# ------------------------------------------- more than one launch can take
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("k,n,dtype", [(40, 5, "bf16"), (300, 20, "f32"), (300, 40, "f16")])
+def test_linear_more_rows_than_a_launch(dev, k, n, dtype):
+    """2^18 rows and some: every row is computed, rows of the last launch like
+    the same rows of the first."""
+    print("linear rows", k, n, dtype, flush=True)
+    rng = np.random.default_rng(k + n)
+    rows, tail = (1 << 18) + 1037, 1037
+    codes = rng.integers(0, 16, (n, k))
+    scales = (rng.uniform(0.3, 1.5, (n, -(-k // 64))) * 0.02).astype(np.float16)
+    words = pca.pack_codes(codes)
+    layer = pca.Q4Linear(in_features=k, out_features=n, weight_words=words, scales=scales, group=64)
+    x = torch.randn(rows, k, device=dev).to(DT[dtype])
+    x[-tail:] = x[:tail]
+    buf = torch.full((rows, n + 1), 7.0, device=dev, dtype=DT[dtype])
+    y = layer.forward(x, out=buf[:, :n])
+    assert torch.equal(y[-tail:], y[:tail]) and bool((buf[:, n] == 7.0).all())
+    some = torch.cat([torch.arange(0, rows, 997), torch.arange((1 << 18) - 50, (1 << 18) + 50)]).to(dev)
+    want, mass = ref.linear(host(x[some]), words, scales, None, None, 64)
+    assert (np.abs(host(y[some]) - want) <= ref.linear_bound(want, mass, None, k, 64, dtype)).all()
+    assert layer.workspace_bytes(2 ** 31 - 1, DT[dtype]) == layer.workspace_bytes(1 << 20, DT[dtype])
+
+
+@pytest.mark.gpu
+def test_attention_more_workgroups_than_a_launch(dev):
+    """2^24 workgroups: 256 requests, one with 32768 - 255 queries and the others
+    with one, and no max_q.  The same as with each request's own."""
+    print("attention workgroups", flush=True)
+    requests, total, heads, kv, dim, block = 256, 32768, 32, 8, 64, 16
+    lens = torch.full((requests,), 40, dtype=torch.int32, device=dev)
+    lens[200] = total
+    counts = torch.ones(requests, dtype=torch.int64, device=dev)
+    counts[200] = total - 255
+    starts = torch.nn.functional.pad(torch.cumsum(counts, 0), (1, 0)).to(torch.int32)
+    width = total // block
+    cache = pca.KV4Cache(width, block, kv, dim)
+    x = torch.randn(width * block, kv, dim, device=dev)
+    cache.append(x, x, torch.arange(width * block, dtype=torch.int32, device=dev))
+    table = torch.arange(width, dtype=torch.int32, device=dev).repeat(requests, 1)
+    q = torch.randn(total, heads, dim, device=dev).bfloat16()
+    out = cache.attention(q, table, lens, q_start=starts, window=50)
+    for r in (0, 1, 199, 200, 201, 255):
+        a, b = int(starts[r]), int(starts[r + 1])
+        one = cache.attention(q[a:b], table[r:r + 1], lens[r:r + 1], window=50)
+        assert float((out[a:b] - one).float().abs().max()) <= 2.0 ** -6, r
+
+
+@pytest.mark.gpu
+def test_attention_more_columns_than_a_join(dev):
+    """2^23 columns whose two parts are joined, of which 100 have a query."""
+    print("attention columns", flush=True)
+    requests, kv, heads, dim, block, width = 16384, 8, 64, 64, 16, 600
+    cache = pca.KV4Cache(width, block, kv, dim)
+    x = torch.randn(width * block, kv, dim, device=dev)
+    cache.append(x, x, torch.arange(width * block, dtype=torch.int32, device=dev))
+    table = torch.arange(width, dtype=torch.int32, device=dev).repeat(requests, 1)
+    owner = torch.arange(0, requests, 164, device=dev)[:100]
+    owner[-1] = requests - 1
+    counts = torch.zeros(requests, dtype=torch.int64, device=dev)
+    counts[owner] = 1
+    starts = torch.nn.functional.pad(torch.cumsum(counts, 0), (1, 0)).to(torch.int32)
+    lens = torch.full((requests,), width * block, dtype=torch.int32, device=dev)
+    q = torch.randn(100, heads, dim, device=dev).bfloat16()
+    out = cache.attention(q, table, lens, q_start=starts, max_q=8)
+    want = cache.attention(q, table[:100], lens[:100])
+    assert float((out - want).float().abs().max()) <= 2.0 ** -6
+
+
+@pytest.mark.gpu
+def test_append_more_rows_than_a_launch(dev):
+    """2^27 rows of 256 channels and some (2^24 tokens of 8 heads, one row
+    expanded): the last tokens are written."""
+    print("append rows", flush=True)
+    tokens = (1 << 24) + 5
+    k = torch.randn(1, 1, 256, device=dev).bfloat16().expand(tokens, 8, 256)
+    cache, small = pca.KV4Cache(2, 16, 8, 256), pca.KV4Cache(2, 16, 8, 256)
+    slots = torch.full((tokens,), -1, dtype=torch.int32, device=dev)
+    slots[-20:] = torch.arange(20, dtype=torch.int32, device=dev)
+    cache.append(k, k, slots)
+    small.append(k[:20], k[:20], torch.arange(20, dtype=torch.int32, device=dev))
+    assert torch.equal(cache.pool, small.pool)
