@@ -18,7 +18,8 @@
  * hipStream_t; NULL = default stream), never allocate and never synchronise,
  * so they can be captured in a HIP graph; buffers are the caller's device
  * memory and must stay valid until the stream's work completes.  Calls
- * without a handle run on the current HIP device.
+ * without a handle run on the current HIP device; a handle's are launched on
+ * the device it was created on, to which their buffers and stream belong.
  */
 #ifndef BCONV_Q4_H
 #define BCONV_Q4_H

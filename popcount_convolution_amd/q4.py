@@ -155,8 +155,10 @@ class Q4Linear:
     ``pack_codes``); ``scales``: host float16 ``[out_features,
     ceil(in_features/group)]``; ``zeros``: host uint8 of that shape, or None for
     8; ``bias``: host float32 ``[out_features]`` or None.  ``forward`` takes
-    float32, float16 or bfloat16 rows and sums in float32.
+    float32, float16 or bfloat16 rows on that GPU (``device``) and sums in float32.
     """
+
+    device = None  # where the weights are
 
     def __init__(self, *, in_features: int, out_features: int, weight_words, scales, zeros=None, bias=None,
                  group: int = 128):
@@ -177,7 +179,9 @@ class Q4Linear:
         if zeros is not None and np.asarray(zeros).dtype != np.uint8:
             raise ValueError(f"zeros: dtype {np.asarray(zeros).dtype} is not uint8")
         self.in_features, self.out_features, self.group = in_features, out_features, group
+        torch = _torch or _load_torch()
         self.handle = B.bconv_q4_linear_create(in_features, out_features, group, weight_words, scales, zeros, bias)
+        self.device = torch.device("cuda", torch.cuda.current_device())
 
     def workspace_bytes(self, rows: int, dtype) -> int:
         if _torch is None:
@@ -195,7 +199,7 @@ class Q4Linear:
             raise ValueError(f"input: shape {tuple(shape)} does not end in {self.in_features}")
         code = _dtype_code(x, "input")
         rows, ldx = _row_stride(x, "input")
-        _need_cuda(x, "input")
+        _need_cuda(x, "input", self.device)
         device = x.device
         place, raw = _place(device, stream)
         with place:

@@ -1,0 +1,29 @@
+"""Calls of the 4-bit operators that must be refused on the host, shown without a
+GPU: tensors that exist as shapes, strides and devices alone stand for ones
+that would not fit, or would live on another GPU."""
+
+import pytest
+import torch
+from torch._subclasses.fake_tensor import FakeTensorMode
+
+import popcount_convolution_amd as pca
+
+
+def fake(*shape, dtype=torch.bfloat16, device="cuda:0"):
+    return torch.empty(*shape, dtype=dtype, device=device)
+
+
+def q4_layer(n_in=64, n_out=32):
+    layer = object.__new__(pca.Q4Linear)
+    layer.handle, layer.in_features, layer.out_features, layer.group = None, n_in, n_out, 32
+    layer._needs, layer.device = {}, torch.device("cuda:0")
+    return layer
+
+
+def test_linear_refuses_another_gpu():
+    """Rows on another GPU than the weights', with or without an output there."""
+    with FakeTensorMode():
+        x, out = fake(3, 64, device="cuda:1"), fake(3, 32, device="cuda:1")
+        for kw in ({}, {"out": out}):
+            with pytest.raises(ValueError, match="input: on cuda:1, not on cuda:0"):
+                q4_layer().forward(x, **kw)
