@@ -9,21 +9,20 @@ from torch._subclasses.fake_tensor import FakeTensorMode
 import popcount_convolution_amd as pca
 
 
-def fake(*shape, dtype=torch.bfloat16, device="cuda:0"):
-    return torch.empty(*shape, dtype=dtype, device=device)
+def fake(*shape, dtype=torch.bfloat16):
+    return torch.empty(*shape, dtype=dtype, device="cuda:0")
 
 
-def q4_layer(n_in=64, n_out=32):
+def q4_layer(n_in=64, n_out=32, device="cuda:0"):
     layer = object.__new__(pca.Q4Linear)
     layer.handle, layer.in_features, layer.out_features, layer.group = None, n_in, n_out, 32
-    layer._needs, layer.device = {}, torch.device("cuda:0")
+    layer._needs, layer.device = {}, torch.device(device)
     return layer
 
 
 def test_linear_refuses_another_gpu():
     """Rows on another GPU than the weights', with or without an output there."""
     with FakeTensorMode():
-        x, out = fake(3, 64, device="cuda:1"), fake(3, 32, device="cuda:1")
-        for kw in ({}, {"out": out}):
-            with pytest.raises(ValueError, match="input: on cuda:1, not on cuda:0"):
-                q4_layer().forward(x, **kw)
+        for kw in ({}, {"out": fake(3, 32)}):
+            with pytest.raises(ValueError, match="input: on cuda:0, not on cuda:1"):
+                q4_layer(device="cuda:1").forward(fake(3, 64), **kw)
