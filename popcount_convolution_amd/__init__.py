@@ -78,8 +78,11 @@ class BinaryConvolution:
     ``type`` is ``"xnor"``, ``"and"`` or ``"binary_weights"``; ``weight_bits``
     is a host uint32 array ``[out_c][kernel_h][kernel_w][ceil(in_c/32)]``; the
     scale/bias arrays are host float32 (or None).  ``forward`` takes a CUDA
-    (HIP) float32 NHWC tensor and returns the float32 NHWC output.
+    (HIP) float32 NHWC tensor on that GPU (``device``) and returns the float32
+    NHWC output.
     """
+
+    device = None  # where the weights are
 
     def __init__(self, *, in_h: int, in_w: int, in_c: int, out_c: int, kernel: tuple,
                  stride: tuple = (1, 1), pad: tuple = (0, 0), pad_end=None, type: str = "xnor",
@@ -99,6 +102,8 @@ class BinaryConvolution:
             (BCONV_FLAG_FP4_MFMA if fp4_mfma else BCONV_FLAG_NONE)
         self.handle = bconv_create(self.desc, weight_bits, output_scale, output_bias,
                                    input_scale, input_bias, self.type, self.flags)
+        import torch
+        self.device = torch.device("cuda", torch.cuda.current_device())
         self.in_h, self.in_w = in_h, in_w
         self.in_c, self.out_c, self.out_h, self.out_w = bconv_get_info(self.handle)
 
@@ -140,6 +145,8 @@ class BinaryConvolution:
         import torch
         n = x.shape[0] if isinstance(x, torch.Tensor) and x.dim() == 4 else -1
         check_tensor(x, "input", x_shape(n), x_dtypes)
+        if self.device is not None and x.device != self.device:
+            raise ValueError(f"input: on {x.device}, the layer is on {self.device}")
         s = stream or torch.cuda.current_stream(x.device)
         with torch.cuda.device(x.device), torch.cuda.stream(s):
             if out is None:

@@ -26,3 +26,11 @@ def test_linear_refuses_another_gpu():
         for kw in ({}, {"out": fake(3, 32)}):
             with pytest.raises(ValueError, match="input: on cuda:0, not on cuda:1"):
                 q4_layer(device="cuda:1").forward(fake(3, 64), **kw)
+
+
+def test_convolution_refuses_another_gpu():
+    """The same for the binary layers."""
+    layer = object.__new__(pca.BinaryConvolution)
+    layer.handle, layer.in_h, layer.in_w, layer.in_c, layer.device = None, 4, 4, 8, torch.device("cuda:1")
+    with FakeTensorMode(), pytest.raises(ValueError, match="input: on cuda:0, the layer is on cuda:1"):
+        layer.forward(fake(2, 4, 4, 8, dtype=torch.float32))
