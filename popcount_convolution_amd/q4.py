@@ -87,6 +87,7 @@ def _need_rows(t, name: str, heads: int, dim: int) -> int:
         raise ValueError(f"{name}: shape {tuple(shape)} is not (tokens, {heads}, {dim})")
     if t.stride(2) != 1 and dim > 1:
         raise ValueError(f"{name}: channels must be contiguous (stride {t.stride(2)})")
+    _need_int32(shape[0], name)
     return shape[0]
 
 
@@ -99,7 +100,10 @@ def _need_table(t) -> tuple:
     stride = t.stride()
     if width > 1 and stride[1] != 1 or requests > 1 and stride[0] < width:
         raise ValueError("block_table: rows must be contiguous and must not overlap")
-    return requests, width, stride[0] if requests > 1 else max(width, 1)
+    step = stride[0] if requests > 1 else max(width, 1)
+    _need_int32(requests, "block_table")
+    _need_int32(step, "block_table")  # no less than the width
+    return requests, width, step
 
 
 def _need_workspace(ws, need: int, device) -> None:
@@ -166,6 +170,8 @@ class Q4Linear:
         self._needs: dict = {}  # workspace bytes by (rows, type)
         if group not in (32, 64, 128):
             raise ValueError(f"group: {group} is not 32, 64 or 128")
+        _need_int32(in_features, "in_features")
+        _need_int32(out_features, "out_features")
         groups = -(-in_features // group)
         for name, a, shape in (("weight_words", weight_words, (out_features, -(-in_features // 8))),
                                ("scales", scales, (out_features, groups)), ("zeros", zeros, (out_features, groups)),
@@ -186,6 +192,9 @@ class Q4Linear:
     def workspace_bytes(self, rows: int, dtype) -> int:
         if _torch is None:
             _load_torch()
+        if dtype not in _DTYPES:
+            raise ValueError(f"dtype {dtype} is not one of torch.float32, torch.float16, torch.bfloat16")
+        _need_int32(rows, "rows")
         return B.bconv_q4_linear_workspace_size(self.handle, rows, _DTYPES[dtype])
 
     def forward(self, x, out=None, workspace=None, stream=None):
@@ -199,6 +208,7 @@ class Q4Linear:
             raise ValueError(f"input: shape {tuple(shape)} does not end in {self.in_features}")
         code = _dtype_code(x, "input")
         rows, ldx = _row_stride(x, "input")
+        _need_int32(rows, "input")
         _need_cuda(x, "input", self.device)
         device = x.device
         place, raw = _place(device, stream)
@@ -403,6 +413,7 @@ def build_block_tables(block_table, context_lens, new_lens, free_blocks, free_he
     _need_ints(new_lens, "new_lens", requests, device)
     _need_tensor(free_blocks, "free_blocks")
     free_count = free_blocks.numel()
+    _need_int32(free_count, "free_blocks")
     _need_ints(free_blocks, "free_blocks", free_count, device)
     _need_ints(free_head, "free_head", 1, device)
     if tokens < 0:

@@ -34,3 +34,54 @@ def test_convolution_refuses_another_gpu():
     layer.handle, layer.in_h, layer.in_w, layer.in_c, layer.device = None, 4, 4, 8, torch.device("cuda:1")
     with FakeTensorMode(), pytest.raises(ValueError, match="input: on cuda:0, the layer is on cuda:1"):
         layer.forward(fake(2, 4, 4, 8, dtype=torch.float32))
+
+
+# ------------------------------------- numbers that an int32 does not hold
+# (a C call's would be their low 32 bits: too few rows computed, or another stride)
+
+def i32(*shape):
+    return fake(*shape, dtype=torch.int32)
+
+
+def test_linear_refuses_rows_past_32_bits():
+    with FakeTensorMode():
+        for x in (fake(2 ** 32 + 5, 1), fake(2 ** 16, 2 ** 15, 1)):
+            with pytest.raises(ValueError, match="input: .* is not a 32-bit number"):
+                q4_layer(n_in=1).forward(x)
+    with pytest.raises(ValueError, match="rows: .* is not a 32-bit number"):
+        q4_layer().workspace_bytes(2 ** 32 + 1, torch.float32)
+    with pytest.raises(ValueError, match="dtype"):
+        q4_layer().workspace_bytes(1, torch.float64)
+    for sizes in ({"in_features": 2 ** 32 + 32, "out_features": 1}, {"in_features": 32, "out_features": 2 ** 32 + 1}):
+        with pytest.raises(ValueError, match="features: .* is not a 32-bit number"):
+            pca.Q4Linear(**sizes, weight_words=None, scales=None)
+
+
+def cache():
+    c = object.__new__(pca.KV4Cache)
+    c.kv_heads, c.head_dim, c.block_size, c.device, c._needs = 1, 8, 16, torch.device("cuda:0"), {}
+    return c
+
+
+def test_cache_refuses_tokens_past_32_bits():
+    many = 2 ** 32 + 5
+    with FakeTensorMode():
+        with pytest.raises(ValueError, match="k: .* is not a 32-bit number"):
+            row = fake(1, 1, 8)
+            cache().append(row.expand(many, 1, 8), row.expand(many, 1, 8), i32(many))
+        with pytest.raises(ValueError, match="q: .* is not a 32-bit number"):
+            cache().attention(fake(1, 1, 8).expand(many, 1, 8), i32(1, 2), i32(1))
+        with pytest.raises(ValueError, match="block_table: .* is not a 32-bit number"):
+            cache().attention(fake(2, 1, 8), i32(2, many)[:, :4], i32(2))
+        with pytest.raises(ValueError, match="block_table: .* is not a 32-bit number"):
+            cache().attention(fake(2, 1, 8), i32(1, many), i32(1))
+
+
+def test_block_tables_refuse_numbers_past_32_bits():
+    many = 2 ** 32 + 5
+    with FakeTensorMode():
+        for table, free, name in ((i32(2, many)[:, :4], i32(3), "block_table"), (i32(many, 1), i32(3), "block_table"),
+                                  (i32(2, 4), i32(many), "free_blocks")):
+            n = table.shape[0]
+            with pytest.raises(ValueError, match=name + ": .* is not a 32-bit number"):
+                pca.build_block_tables(table, i32(n), i32(n), free, i32(1), block_size=16, tokens=1)
