@@ -498,9 +498,11 @@ __global__ __launch_bounds__(256, 2) void q4_many_kernel(Q4Args a, Q4Many q)
                 for (int t = 0; t < CB; ++t)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
-                        float scale = (float)s4[i >> 2][i & 3];
-                        if constexpr (DT == BCONV_F32) scale *= xs[t];
-                        acc[r][t][i] = __builtin_fmaf(scale, d[t][i], acc[r][t][i]);
+                        const float scale = (float)s4[i >> 2][i & 3];
+                        // the power of two last: times it alone, the scale could
+                        // become subnormal and lose bits
+                        if constexpr (DT == BCONV_F32) acc[r][t][i] = __builtin_fmaf(scale * d[t][i], xs[t], acc[r][t][i]);
+                        else acc[r][t][i] = __builtin_fmaf(scale, d[t][i], acc[r][t][i]);
                     }
             }
         }

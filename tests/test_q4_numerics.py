@@ -214,3 +214,32 @@ def test_append_more_rows_than_a_launch(dev):
     cache.append(k, k, slots)
     small.append(k[:20], k[:20], torch.arange(20, dtype=torch.int32, device=dev))
     assert torch.equal(cache.pool, small.pool)
+
+
+# ----------------------------------------------------------- small fp32 rows
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("rows,n", [(5, 90), (70, 300), (20, 9000), (50, 9000), (70, 9000)])
+def test_linear_fp32_small_rows(dev, rows, n, group, zeros):
+    """fp32 rows of 1e-26 to 1e-35 times scales of 1e-4, at every batch size: as
+    exact as rows of any other size, as long as the results are normal numbers.
+    2000 terms of random signs: their split to 2^-23 and one fp32 rounding for each
+    of at most 16 + 63 partial sums a result (a matrix instruction adds 16 or 32
+    terms, then groups and splits are added) are below 2^-20 of the results' rms."""
+    print("small rows", rows, n, group, zeros, flush=True)
+    rng = np.random.default_rng(rows + n + group)
+    k = 2000
+    codes = rng.integers(0, 16, (n, k))
+    scales = (rng.uniform(0.5, 1.5, (n, -(-k // group))) * 1e-4).astype(np.float16)
+    zs = rng.integers(6, 10, scales.shape).astype(np.uint8) if zeros else None
+    words = pca.pack_codes(codes)
+    layer = pca.Q4Linear(in_features=k, out_features=n, weight_words=words, scales=scales, zeros=zs, group=group)
+    x = (rng.normal(0, 1, (rows, k)) * 10.0 ** np.linspace(-35, -26, rows)[:, None]).astype(np.float32)
+    want, _ = ref.linear(x.astype(np.float64), words, scales, zs, None, group)
+    err = host(layer.forward(torch.from_numpy(x).to(dev))) - want
+    rms = lambda a: np.sqrt((a ** 2).mean(1))  # noqa: E731
+    assert rms(want).min() > 2.0 ** -126
+    ratio = rms(err) / rms(want)
+    assert (ratio <= 2.0 ** -20).all(), ratio.max()
