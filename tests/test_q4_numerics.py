@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import popcount_convolution_amd as pca
+import q4_precision as prec
 import q4_reference as ref
 
 DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
@@ -243,3 +244,131 @@ def test_linear_fp32_small_rows(dev, rows, n, group, zeros):
     assert rms(want).min() > 2.0 ** -126
     ratio = rms(err) / rms(want)
     assert (ratio <= 2.0 ** -20).all(), ratio.max()
+
+
+# -------------------------------------------------------- ordinary precision
+
+LINEAR = [  # one row and few (1 to 4 output tiles a workgroup, 8 or 16 waves), many (32, 64, 128 rows), split and whole
+    (1, 32, 16, 32, False, False),
+    (1, 4096, 96, 128, False, False),
+    (1, 8200, 8100, 64, True, True),
+    (3, 127, 33, 128, False, True),
+    (7, 2500, 5000, 32, False, False),
+    (13, 5000, 11003, 64, True, True),
+    (16, 256, 16000, 64, True, False),
+    (17, 8200, 4100, 64, True, True),
+    (50, 4100, 4111, 128, True, False),
+    (130, 2049, 3500, 32, True, True),
+    (300, 1100, 3100, 128, False, False),
+    (2000, 300, 1400, 32, False, True),
+]
+
+
+def linear_case(rows, k, n, group, zeros, bias):
+    rng = np.random.default_rng(rows * 1009 + k + n)
+    codes = rng.integers(0, 16, (n, k))
+    shape = (n, -(-k // group))
+    scales = (rng.uniform(0.3, 1.5, shape) * 0.02).astype(np.float16)
+    zs = rng.integers(5, 11, shape).astype(np.uint8) if zeros else None
+    b = rng.normal(0, 1, n).astype(np.float32) if bias else None
+    return pca.pack_codes(codes), scales, zs, b, rng.normal(0, 1, (rows, k)).astype(np.float32)
+
+
+@pytest.mark.parametrize("case", LINEAR[1:4] + LINEAR[-1:])
+def test_linear_bound_tells_one_part_from_two(case):
+    """The bound that the kernels are held to passes two fp16 parts of x and
+    fails one."""
+    *w, x = linear_case(*case)
+    want, bound = prec.linear(x, *w, case[3])
+    for count in (1, 2):
+        top = np.abs(x).max(1, keepdims=True)
+        got = prec.linear(prec.parts(x, count, top), *w, case[3])[0]
+        assert (prec.rms((got - want) / bound) <= 1) == (count == 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("case", LINEAR)
+def test_linear_precision(dev, dtype, case):
+    """fp32: the rms error is that of two-part operands and fp32 sums.  16-bit
+    types: that of one rounding of the result, and 5% (fp32 sums with the codes'
+    offset in them, at most a tenth of fp16's rounding)."""
+    print("linear precision", dtype, case, flush=True)
+    words, scales, zs, b, x = linear_case(*case)
+    rows, k, n, group, *_ = case
+    layer = pca.Q4Linear(in_features=k, out_features=n, weight_words=words, scales=scales, zeros=zs, bias=b,
+                         group=group)
+    x = torch.from_numpy(x).to(dev).to(DT[dtype])
+    want, bound = prec.linear(host(x), words, scales, zs, b, group)
+    err = host(layer.forward(x)) - want
+    if dtype == "f32":
+        ratio = prec.rms(err / bound)
+        assert ratio <= 1, ratio
+    else:
+        best = host(torch.from_numpy(want).to(DT[dtype])) - want
+        assert prec.rms(err) <= 1.05 * prec.rms(best), (prec.rms(err), prec.rms(best))
+
+
+def attention_case(lens, kv, dim, group, seed):
+    """Keys, values and steps of each request in 64 bits, as the cache holds them."""
+    rng = np.random.default_rng(seed)
+    k = [rng.normal(0, 1, (n, kv, dim)).astype(np.float32) for n in lens]
+    v = [rng.normal(0, 1, (n, kv, dim)).astype(np.float32) for n in lens]
+    kx = [ref.quantise(a, group)[3].astype(np.float64) for a in k]
+    vq = [ref.quantise(a, group) for a in v]
+    return rng, k, v, kx, [a[3].astype(np.float64) for a in vq], [a[1].astype(np.float64).max(-1) for a in vq]
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (128, 128), (256, 64)])
+@pytest.mark.parametrize("length", [45, 703])
+def test_attention_bound_tells_one_part_from_two(dim, group, length):
+    """The bound fails queries in one fp16 part, probabilities times steps in one, and
+    passes both in two."""
+    rng, _, _, kx, vx, step = attention_case([length], 1, dim, group, dim + length)
+    q = rng.normal(0, 1.5, (1, 4, dim))
+    want, _, bound, _ = prec.attention(q, kx, vx, step, [length], [1], dim ** -0.5, group)
+    z = np.einsum("hd,td->ht", q[0], kx[0][:, 0]) * dim ** -0.5
+    for count in (1, 2):
+        split = prec.parts(q, count, np.abs(q).max(-1, keepdims=True))
+        got = prec.attention(split, kx, vx, step, [length], [1], dim ** -0.5, group)[0]
+        assert (prec.rms((got - want) / bound) <= 1) == (count == 2)
+        p = np.exp(z - z.max(1, keepdims=True))
+        got = prec.parts(p, count, 1.0) / p.sum(1, keepdims=True) @ vx[0][:, 0]
+        assert (prec.rms((got - want[0]) / bound[0]) <= 1) == (count == 2)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 128), (128, 64), (128, 32), (256, 128), (256, 64),
+                                       (256, 32), (120, 64), (80, 32), (136, 64)])
+@pytest.mark.parametrize("ratio,lens,counts", [(1, [703, 45], [1, 1]), (8, [703, 45], [1, 1]), (4, [6000], [1]),
+                                               (16, [6000], [1]), (2, [300, 37], [20, 37])])
+def test_attention_precision(dev, dtype, dim, group, ratio, lens, counts):
+    """fp32: the rms errors of the result and the log-sum-exp are those of two-part
+    operands and fp32 sums.  fp16: that of one rounding of the result, and 10%
+    (probabilities to 2^-16, a 32nd of it).  bf16: and a quarter (probabilities to
+    2^-11, an eighth of it, in terms of up to a few times the result)."""
+    print("attention precision", dtype, dim, group, ratio, lens, counts, flush=True)
+    kv, block = 2, 16
+    rng, k, v, kx, vx, step = attention_case(lens, kv, dim, group, dim * 31 + group + ratio + sum(lens))
+    per = [-(-n // block) for n in lens]
+    cache = pca.KV4Cache(sum(per), block, kv, dim, group=group)
+    order = rng.permutation(sum(per)).astype(np.int32)
+    table = np.full((len(lens), max(per)), -1, np.int32)
+    for r, n in enumerate(per):
+        table[r, :n] = order[sum(per[:r]):sum(per[:r + 1])]
+        pos = np.arange(lens[r])
+        up = lambda a: torch.from_numpy(a).to(dev)  # noqa: E731
+        cache.append(up(k[r]), up(v[r]), up((table[r, pos // block] * block + pos % block).astype(np.int32)))
+    q = torch.from_numpy(rng.normal(0, 1.5, (sum(counts), kv * ratio, dim)).astype(np.float32)).to(dev).to(DT[dtype])
+    starts = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).to(dev)
+    lse = torch.empty(q.shape[:2], device=dev)
+    out = cache.attention(q, up(table), up(np.array(lens, np.int32)), q_start=starts, max_q=max(counts), lse=lse)
+    want, want_lse, bound, lse_bound = prec.attention(host(q), kx, vx, step, lens, counts, dim ** -0.5, group)
+    err = host(out) - want
+    if dtype == "f32":
+        assert prec.rms(err / bound) <= 1, prec.rms(err / bound)
+        assert prec.rms((host(lse) - want_lse) / lse_bound) <= 1
+    else:
+        best = host(torch.from_numpy(want).to(DT[dtype])) - want
+        assert prec.rms(err) <= {"f16": 1.1, "bf16": 1.25}[dtype] * prec.rms(best), (prec.rms(err), prec.rms(best))
