@@ -75,7 +75,8 @@ bconv_status_t bconv_q4_linear_workspace_size(bconv_q4_linear_t h, int32_t rows,
  * on 16-byte boundaries load wider).  rows == 0 is a no-op.  The workspace is
  * 16-byte aligned and overlaps neither.  bf16 products are exact and summed in fp32 after an
  * offset that is taken out again, so a bf16 row with an infinity gives NaN in
- * every output of that row; fp16 and fp32 rows follow IEEE arithmetic.  An fp32
+ * every output of that row (finite rows, of whatever size, do not); fp16 and fp32
+ * rows follow IEEE arithmetic.  An fp32
  * element enters its products to 2^-24 of itself or 2^-39 of the largest in its
  * 128 inputs, whichever is more.
  * Errors: INVALID_ARGUMENT for a NULL handle or pointer, rows < 0, an unknown
@@ -174,7 +175,7 @@ typedef struct {
     int32_t max_context;         /* most cached tokens of one request (up to 2^30), or 0: the table's width */
     int32_t window;              /* 0: none */
     int32_t dtype;
-    float scale;
+    float scale;                 /* |scale| below 2^115 */
 } bconv_kv4_attention_t;
 
 /* Workspace bytes the call needs (0 is possible); host only. */

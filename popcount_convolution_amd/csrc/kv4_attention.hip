@@ -475,7 +475,7 @@ kv4_attention_kernel(AttnArgs a)
 
     // this lane's columns: row of q, positions seen
     Operand<DT> qf[STEPS];
-    float scale = a.scale_log2;
+    float scale = a.scale_log2 * (1.0f / kUnit<DT>);
     int lo, hi;
     int all_lo = 0, all_hi = 0x7fffffff;  // seen by every column
     {
@@ -515,12 +515,12 @@ kv4_attention_kernel(AttnArgs a)
 
     // sums of q over each group, for the midpoints and the codes' offset (16 in
     // bf16: a product gets -24 of them once it is a lane's own, which takes fewer
-    // registers than starting from them)
+    // registers than starting from them), in units of kUnit as the products are
     float qsum[GROUPS];
 #pragma unroll
     for (int g = 0; g < GROUPS; ++g) {
         f32x4 x = {0, 0, 0, 0};
-        const u32x4 one = constant<DT>(1.0f);
+        const u32x4 one = constant<DT>(kUnit<DT>);
 #pragma unroll
         for (int s = 0; s < PER; ++s) x = mfma_parts<DT>(one, qf[g * PER + s], x);
         qsum[g] = x[0];

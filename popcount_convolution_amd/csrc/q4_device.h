@@ -212,16 +212,21 @@ template <int DT> __device__ __forceinline__ typename Elem<DT>::type round_to(fl
 // Codes to operands.  A stored word holds 8 codes of consecutive k, code 2e at
 // nibble e and code 2e+1 at nibble 4+e, rotated left by 3, so rotating right
 // by 4e brings codes 2e and 2e+1 to bits 3..6 of the two halves, the top four
-// of a bf16's seven mantissa bits: or-ing in the exponent of 16 gives 16 + c.
-// Seven instructions for eight codes.  The same bits in fp16 (ten mantissa
+// of a bf16's seven mantissa bits: or-ing in the exponent of 2^-8 gives (16 + c)
+// 2^-12.  Seven instructions for eight codes.  The same bits in fp16 (ten mantissa
 // bits) under the exponent of 128 give 128 + c.
 //
 // What is left of the offset:
-//   bf16: 16 (the products are exact; the caller takes 16 * sum x out);
+//   bf16: 16 (the products are exact; the caller takes 16 * sum x out).  Products
+//         and what is made of them are in units of kUnit = 2^-12, so that no sum
+//         over a group (at most 128 terms of 31 x each) passes the largest x, and
+//         finite rows keep finite sums; nothing is lost at the other end, since
+//         the matrix cores keep subnormal numbers;
 //   fp16 and fp32: none: a packed subtraction of `zero` leaves the integer
 //         itself, so that no cancellation costs bits.
 constexpr uint32_t kCodeMask = 0x00780078u;
-constexpr uint32_t kBase16 = 0x41804180u;   // bf16 16, 16
+template <int DT> constexpr float kUnit = DT == BCONV_BF16 ? 1.0f / 4096.0f : 1.0f;
+constexpr uint32_t kBase16 = 0x3b803b80u;   // bf16 2^-8, 2^-8: 16 units
 constexpr uint32_t kBase128 = 0x58005800u;  // fp16 128, 128
 
 __device__ __forceinline__ uint32_t rotr(uint32_t w, int n)

@@ -130,10 +130,10 @@ __device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operan
 #pragma unroll
     for (int g = 0; g < 4 / STEPS; ++g) {
         // bf16: the offset 16 + z of the codes leaves -(16 + z) sum x, on the
-        // matrix cores as well (a constant operand times x)
+        // matrix cores as well (a constant operand times x), all in units of kUnit
         f32x4 off = {0, 0, 0, 0};
         if constexpr (DT == BCONV_BF16) {
-            const u32x4 c = constant<DT>(ZP ? -1.0f : -24.0f);
+            const u32x4 c = constant<DT>(ZP ? -kUnit<DT> : -24.0f * kUnit<DT>);
 #pragma unroll
             for (int s = 0; s < STEPS; ++s) off = mfma_parts<DT>(c, x[g * STEPS + s], off);
         }
@@ -170,14 +170,15 @@ __device__ __forceinline__ void chunk_product(const u32x4 (&w)[RT], const Operan
     }
 }
 
-// 4 consecutive outputs of a row, with the bias, as far as there are outputs.
+// 4 consecutive outputs of a row (in units of kUnit), with the bias, as far as
+// there are outputs.
 template <int DT> __device__ __forceinline__ void store_outputs(const Q4Args &a, int m, int o0, f32x4 v)
 {
     typedef typename Elem<DT>::type T;
     T *y = static_cast<T *>(a.y) + (long long)m * a.ldy + o0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-        if (o0 + i < a.n) y[i] = round_to<DT>(v[i] + (a.bias ? a.bias[o0 + i] : 0.0f));
+        if (o0 + i < a.n) y[i] = round_to<DT>(__builtin_fmaf(v[i], 1.0f / kUnit<DT>, a.bias ? a.bias[o0 + i] : 0.0f));
 }
 
 // Few rows of x.  A workgroup takes 16 RT outputs and 16 rows of x; its waves
@@ -263,7 +264,7 @@ __global__ __launch_bounds__(WAVES * 64) void q4_few_kernel(Q4Args a)
 // and the partial sums of the splits.
 struct Q4Many {
     u32x4 *xp;       // [column tiles][chunks * 4][parts][64]
-    float *xs;       // [column tiles][chunks][groups a chunk][16]; bf16: -sum x (times 24 without zero points),
+    float *xs;       // [column tiles][chunks][groups a chunk][16]; bf16: -sum x (times 24 without zero points), in units,
                      // fp32: the power of two to take out of a group's products
     float *sums;     // [splits][column tiles * 16][padded outputs], or nullptr for one split
     int col_tiles;   // padded to the workgroup's
@@ -301,7 +302,7 @@ __global__ __launch_bounds__(256) void q4_pack_kernel(Q4Args a, Q4Many q)
         u32x4 *dst = q.xp + ((long long)tile * a.chunks * 4 + g * STEPS + s) * kSplit<DT> * 64 + lane;
 #pragma unroll
         for (int p = 0; p < kSplit<DT>; ++p) dst[p * 64] = o[s].part[p];
-        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(constant<DT>(ZP ? -1.0f : -24.0f), o[s], sum);
+        if constexpr (DT == BCONV_BF16) sum = mfma_parts<DT>(constant<DT>(ZP ? -kUnit<DT> : -24.0f * kUnit<DT>), o[s], sum);
     }
     if constexpr (DT == BCONV_BF16) xs = sum[0];
     if constexpr (DT != BCONV_F16)

@@ -372,3 +372,56 @@ def test_attention_precision(dev, dtype, dim, group, ratio, lens, counts):
     else:
         best = host(torch.from_numpy(want).to(DT[dtype])) - want
         assert prec.rms(err) <= {"f16": 1.1, "bf16": 1.25}[dtype] * prec.rms(best), (prec.rms(err), prec.rms(best))
+
+
+# ------------------------------------------------- the ends of bf16's range
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("group", [32, 128])
+@pytest.mark.parametrize("rows,n", [(9, 90), (70, 300), (20, 9000), (50, 9000), (70, 9000)])
+def test_linear_bf16_ends(dev, rows, n, group, zeros):
+    """Finite bf16 rows up to the type's largest, of mixed signs and of one, and down
+    to its subnormals: the results are finite, and off by one rounding of theirs and
+    fp32 sums (or of bf16's smallest subnormal steps)."""
+    print("bf16 ends", rows, n, group, zeros, flush=True)
+    rng = np.random.default_rng(rows + n + group)
+    k = 300
+    codes = rng.integers(0, 16, (n, k))
+    scales = (rng.uniform(0.5, 1.5, (n, -(-k // group))) * 1e-4).astype(np.float16)
+    zs = rng.integers(0, 16, scales.shape).astype(np.uint8) if zeros else None
+    words = pca.pack_codes(codes)
+    layer = pca.Q4Linear(in_features=k, out_features=n, weight_words=words, scales=scales, zeros=zs, group=group)
+    x = rng.uniform(0.5, 1, (rows, k)) * rng.choice([-1, 1], (rows, k))
+    x[::3] = np.abs(x[::3])
+    x *= 2.0 ** np.array([128, 127, 124, 118, 112, 0, -100, -112, -120])[np.arange(rows) % 9][:, None]
+    x = torch.from_numpy(np.clip(x, -3.3e38, 3.3e38).astype(np.float32)).to(dev).bfloat16()
+    assert bool(x.isfinite().all())
+    want, bound = prec.linear(host(x), words, scales, zs, None, group)
+    got = host(layer.forward(x))
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= ref.ROUND["bf16"] * np.abs(want) + 8 * bound + 2.0 ** -133).all()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("heads", [2, 16])
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (128, 128), (256, 128)])
+def test_attention_bf16_query_ends(dev, dim, group, heads):
+    """Queries of 2^-110 to bf16's largest with the scale that undoes it give the
+    results of queries of ordinary size, to their roundings: powers of two change
+    nothing else."""
+    print("query ends", dim, group, heads, flush=True)
+    n = 200
+    rng = np.random.default_rng(dim + group + heads)
+    cache = pca.KV4Cache(13, 16, 2, dim, group=group)
+    k, v = (torch.from_numpy(rng.normal(0, 1, (n, 2, dim)).astype(np.float32)).to(dev) for _ in range(2))
+    cache.append(k, v, torch.arange(n, dtype=torch.int32, device=dev))
+    table = torch.arange(13, dtype=torch.int32, device=dev)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=dev)
+    q = torch.from_numpy(rng.uniform(-1, 1, (1, heads, dim))).to(dev).bfloat16()
+    q[0, 0] = q[0, 0].abs()
+    want = cache.attention(q, table, lens, scale=2.0)
+    for e in (-110, -60, 60, 100, 110, 114, 118, 124, 127):
+        big = (q.double() * 2.0 ** e).bfloat16()
+        assert bool(big.isfinite().all())
+        assert torch.equal(cache.attention(big, table, lens, scale=2.0 * 2.0 ** -e), want), e  # a normal number
