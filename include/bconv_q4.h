@@ -141,7 +141,8 @@ bconv_status_t bconv_kv4_layout(const bconv_kv4_desc_t *desc, bconv_kv4_layout_t
  * place, block * block_size + offset; a slot outside the pool (-1 for padding)
  * is not written.  Two tokens must not share a slot.  k_out and v_out, when
  * given, receive the values the cache stands for, in `dtype`, dense
- * [tokens][kv_heads][head_dim], whether or not the token has a slot.
+ * [tokens][kv_heads][head_dim], whether or not the token has a slot; they
+ * overlap neither k, v nor the pool.
  * tokens == 0 is a no-op. */
 bconv_status_t bconv_kv4_append(const bconv_kv4_desc_t *desc, void *stream, void *pool, int32_t tokens,
                                 int32_t dtype, const void *k, int64_t k_token_stride, int64_t k_head_stride,
@@ -163,7 +164,7 @@ typedef struct {
     const void *pool;
     const void *q;               /* [q_tokens][heads][head_dim], strides below (elements) */
     int64_t q_token_stride, q_head_stride;
-    void *out;                   /* same shape and type, dense */
+    void *out;                   /* same shape and type, dense; apart from q, the pool and the workspace */
     float *lse;                  /* [q_tokens][heads] log of the softmax denominators, or NULL */
     const int32_t *block_table;  /* device [requests][table_stride] */
     const int32_t *context_lens; /* device [requests] */
@@ -209,8 +210,8 @@ bconv_status_t bconv_kv4_attention(const bconv_kv4_desc_t *desc, void *stream, c
  *   free_head_out           *free_head + the blocks asked for; more than
  *                           free_count says that some were missing
  * slots, positions, q_start and context_lens_out may each be NULL.  One
- * launch; context_lens and context_lens_out, free_head and free_head_out must
- * be different memory.  requests at most 8192; with 0, slots, positions,
+ * launch; no result may overlap the table or an input (context_lens_out not
+ * context_lens, free_head_out not free_head).  requests at most 8192; with 0, slots, positions,
  * q_start and free_head_out are still written. */
 bconv_status_t bconv_block_tables(void *stream, int32_t requests, int32_t block_size, int32_t *block_table,
                                   int32_t table_width, int32_t table_stride, const int32_t *context_lens,

@@ -172,11 +172,16 @@ extern "C" bconv_status_t bconv_block_tables(void *stream, int32_t requests, int
     if (requests > 0 && (!context_lens || !new_lens || (table_width > 0 && !block_table)))
         return fail(BCONV_ERR_INVALID_ARGUMENT, "block_table, context_lens and new_lens must not be NULL");
     if (free_count > 0 && !free_blocks) return fail(BCONV_ERR_INVALID_ARGUMENT, "free_blocks is NULL");
-    if (free_head == free_head_out)
-        return fail(BCONV_ERR_INVALID_ARGUMENT, "free_head and free_head_out must be different memory");
-    if (context_lens_out && requests > 0 &&
-        bconv::ranges_overlap(context_lens, (size_t)requests * 4, context_lens_out, (size_t)requests * 4))
-        return fail(BCONV_ERR_INVALID_ARGUMENT, "context_lens and context_lens_out overlap");
+    // every workgroup reads the inputs while the first writes results
+    const struct { const int32_t *p; size_t n; } in[] = {
+        {context_lens, (size_t)requests}, {new_lens, (size_t)requests}, {free_blocks, (size_t)free_count}, {free_head, 1},
+        {block_table, requests && table_width ? (size_t)(requests - 1) * table_stride + table_width : 0}},
+        out[] = {{context_lens_out, (size_t)requests}, {q_start, (size_t)requests + 1}, {slots, (size_t)tokens},
+                 {positions, (size_t)tokens}, {free_head_out, 1}};
+    for (const auto &o : out)
+        for (const auto &i : in)
+            if (o.p && i.p && o.n && i.n && bconv::ranges_overlap(i.p, i.n * 4, o.p, o.n * 4))
+                return fail(BCONV_ERR_INVALID_ARGUMENT, "a result overlaps block_table, a length, free_blocks or free_head");
     bconv::TableArgs a{};
     a.requests = requests;
     a.shift = __builtin_ctz((unsigned)block_size);

@@ -85,3 +85,21 @@ def test_block_tables_refuse_numbers_past_32_bits():
             n = table.shape[0]
             with pytest.raises(ValueError, match=name + ": .* is not a 32-bit number"):
                 pca.build_block_tables(table, i32(n), i32(n), free, i32(1), block_size=16, tokens=1)
+
+
+def test_block_tables_refuse_results_over_inputs():
+    """Each result one element into each input, and at its last."""
+    at = dict(table=0x1000, ctx=0x2000, new=0x3000, free=0x4000, head=0x5000)
+    size = dict(table=12, ctx=3, new=3, free=5, head=1)
+    out = dict(lens=0x6000, start=0x7000, slots=0x8000, positions=0x9000, out_head=0xa000)
+
+    def call(**kw):
+        a = {**at, **out, **kw}
+        pca.bconv_block_tables(None, 3, 16, a["table"], 4, 4, a["ctx"], a["new"], a["free"], 5, a["head"],
+                               a["out_head"], 2, a["slots"], a["positions"], a["start"], a["lens"])
+
+    for name in out:
+        for where, base in at.items():
+            for k in (0, size[where] - 1):
+                with pytest.raises(pca.BconvError, match="overlaps"):
+                    call(**{name: base + 4 * k})
