@@ -72,9 +72,14 @@ def _need_ints(t, name: str, count: int, device) -> None:
         _need_dense(t, name, (count,), _torch.int32, device)
 
 
+_INT32_MAX = 0x7fffffff
+
+
 def _need_int32(value, name: str) -> None:
-    """A number that the C side's int32 holds (ctypes would wrap others)."""
-    if not -0x80000000 <= value <= 0x7fffffff:
+    """A number that the C side's int32 holds (ctypes would wrap others).  Sizes
+    of tensors, which are not negative, are compared in place: a call of this costs
+    a decoding step's calls 0.1 us each."""
+    if not -0x80000000 <= value <= _INT32_MAX:
         raise ValueError(f"{name}: {value} is not a 32-bit number")
 
 
@@ -87,7 +92,8 @@ def _need_rows(t, name: str, heads: int, dim: int) -> int:
         raise ValueError(f"{name}: shape {tuple(shape)} is not (tokens, {heads}, {dim})")
     if t.stride(2) != 1 and dim > 1:
         raise ValueError(f"{name}: channels must be contiguous (stride {t.stride(2)})")
-    _need_int32(shape[0], name)
+    if shape[0] > _INT32_MAX:
+        _need_int32(shape[0], name)
     return shape[0]
 
 
@@ -101,8 +107,8 @@ def _need_table(t) -> tuple:
     if width > 1 and stride[1] != 1 or requests > 1 and stride[0] < width:
         raise ValueError("block_table: rows must be contiguous and must not overlap")
     step = stride[0] if requests > 1 else max(width, 1)
-    _need_int32(requests, "block_table")
-    _need_int32(step, "block_table")  # no less than the width
+    if requests > _INT32_MAX or step > _INT32_MAX:  # the step is no less than the width
+        _need_int32(max(requests, step), "block_table")
     return requests, width, step
 
 
@@ -208,9 +214,11 @@ class Q4Linear:
             raise ValueError(f"input: shape {tuple(shape)} does not end in {self.in_features}")
         code = _dtype_code(x, "input")
         rows, ldx = _row_stride(x, "input")
-        _need_int32(rows, "input")
-        _need_cuda(x, "input", self.device)
+        if rows > _INT32_MAX:
+            _need_int32(rows, "input")
         device = x.device
+        if device != self.device:
+            _need_cuda(x, "input", self.device)
         place, raw = _place(device, stream)
         with place:
             out_shape = (*shape[:-1], self.out_features)
@@ -413,7 +421,8 @@ def build_block_tables(block_table, context_lens, new_lens, free_blocks, free_he
     _need_ints(new_lens, "new_lens", requests, device)
     _need_tensor(free_blocks, "free_blocks")
     free_count = free_blocks.numel()
-    _need_int32(free_count, "free_blocks")
+    if free_count > _INT32_MAX:
+        _need_int32(free_count, "free_blocks")
     _need_ints(free_blocks, "free_blocks", free_count, device)
     _need_ints(free_head, "free_head", 1, device)
     if tokens < 0:
