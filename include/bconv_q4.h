@@ -77,8 +77,9 @@ bconv_status_t bconv_q4_linear_workspace_size(bconv_q4_linear_t h, int32_t rows,
  * offset that is taken out again, so a bf16 row with an infinity gives NaN in
  * every output of that row (finite rows, of whatever size, do not); fp16 and fp32
  * rows follow IEEE arithmetic.  An fp32
- * element enters its products to 2^-24 of itself or 2^-39 of the largest in its
- * 128 inputs, whichever is more.
+ * element enters its products to 2^-23 of itself (one bit less than fp32 has) or
+ * 2^-39 of the largest in its 128 inputs, whichever is more: next to inputs 2^16
+ * times larger it loses bits even where their weights are 0.
  * Errors: INVALID_ARGUMENT for a NULL handle or pointer, rows < 0, an unknown
  * dtype, a short stride or overlapping buffers; WORKSPACE for a missing or
  * short workspace; HIP when a launch fails. */
@@ -159,7 +160,12 @@ bconv_status_t bconv_kv4_append(const bconv_kv4_desc_t *desc, void *stream, void
  * - n + j, and with a window w > 0 only the last w of those.  Positions whose
  * block id is outside the pool, or past the table's width, are masked.  A
  * query that sees nothing gives 0 (and lse -inf).  Queries of a request past
- * max_q, and past q_tokens, are not computed. */
+ * max_q, and past q_tokens, are not computed.
+ * Logits, the softmax and all sums are fp32; fp32 queries enter as fp32 rows of a
+ * linear layer do (the largest being the query's own).  A probability times its
+ * value's step meets the code in 11 bits for bf16 results (fewer where the step is
+ * below 2^-19 of the largest that the workgroup's wave has met), 16 bits for fp16
+ * results and 23 bits for fp32 results; what it adds to the denominator is fp32. */
 typedef struct {
     const void *pool;
     const void *q;               /* [q_tokens][heads][head_dim], strides below (elements) */

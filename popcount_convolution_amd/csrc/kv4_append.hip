@@ -58,9 +58,9 @@ struct AppendArgs {
 // DP / 8 lanes a row (token, head, side), 8 channels a lane; since head_dim is
 // a multiple of 8 a lane's channels are all real or all padding.  LG lanes
 // share a group.  Bound by the bytes of x and of the values written back: 8193
-// tokens of 8 heads of 128 channels in bf16, 76.6 MB with the values, 18.5 us
-// (4.1 TB/s; a large copy reaches 4.77).  One decoding step of 32 tokens is a
-// launch (3.3 us).
+// tokens of 8 heads of 128 channels in bf16, 76.6 MB with the values, 19.1 to 19.6 us
+// (3.9 to 4.0 TB/s; a large copy reaches 4.77 to 5.16).  One decoding step of 32
+// tokens is a launch (3.7 us by trace, 3.3 a call in a graph).
 template <int DT, int DP, int LG>
 __global__ __launch_bounds__(256) void kv4_append_kernel(AppendArgs a)
 {

@@ -18,11 +18,13 @@
 // of 64 take about 350 vector and 24 matrix instructions a tile (decoding 120,
 // steps and midpoints 128, softmax 40) for 4.6 KB, 270 vector ones where few
 // columns share their softmax (see Steps).  32 requests of up to 8192 tokens, 32
-// heads over 8, bf16: 48.3 us for 183 MB (3.8 TB/s; a large read reaches 6.05), and
-// 5.7 us for the join of their parts (all of 8192 tokens: 4.4 TB/s with the join); the
+// heads over 8, bf16: 46.3 us for 183 MB (4.0 TB/s; a large read reaches 6.05), and
+// 5.6 us for the join of their parts (all of 8192 tokens: 4.4 TB/s with the join); the
 // rest is the requests' uneven lengths and a workgroup's first loads.  Two requests of
-// 131071 tokens, 16 heads over one, fp16: 15.1 us and 5.1 us for the join (floor
-// 5.5 us).  One of 777 tokens: 7.0 us, a chain of loads (lengths, block ids, keys,
+// 131071 tokens, 16 heads over one, fp16: 15.4 us and 5.2 us for the join (floor
+// 5.5 us).  Four prompts of up to 512 tokens behind up to 2048, 32 heads over 8: 149 us
+// in bf16, 176 in fp16 (floor 32.9): each 16 columns decode the same keys and values
+// anew.  One token of 777: 7.0 us, a chain of loads (lengths, block ids, keys,
 // values).  Registers decide the rest: 128 a wave and four waves a SIMD; spilling
 // 15 of them costs 58 -> 84 us, three waves at 168 registers 66.
 #include <hip/hip_runtime.h>
@@ -127,7 +129,7 @@ __device__ __forceinline__ float lane_groups_sum(float v)
 
 // Type of the operands of V^T P, and parts that a probability, times its value's
 // step, is rounded into: one fp16 (11 bits) for bf16 results, two bf16 (16 bits) for
-// fp16 results, two fp16 (24 bits) for fp32 results.
+// fp16 results, two fp16 (23 bits) for fp32 results.
 //
 // fp16's exponents need these products near 1.
 //   bf16 results: they are taken times 2^lead, a lead that a wave chooses by the

@@ -78,9 +78,10 @@ __device__ __forceinline__ uint32_t lane_groups_max_bits(uint32_t v)
 // normal numbers).
 //
 // A value x times `to` is split into h = fp16(x), l = fp16(x - h): x - h is
-// exact and at most 2^-12 x, so h + l is x to 2^-24, fp32's own rounding, as long
-// as l is a normal number; below that its error is at most 2^-25, that is
-// 2^-(25 + BITS) of the largest value.  Two products then stand for an
+// exact and at most 2^-11 x, a multiple of x's last bit, of which l holds all but
+// the last in the upper half of that range.  So h + l is x to 2^-23 (23 of fp32's 24
+// bits; three values in four are exact), as long as l is a normal number; below that
+// its error is at most 2^-25, that is 2^-(25 + BITS) of the largest value.  Two products then stand for an
 // fp32 product (exact bf16 parts would take three, and 8 instructions a value
 // instead of 3).
 template <int BITS, int LEAST = BITS - 126> struct Range {

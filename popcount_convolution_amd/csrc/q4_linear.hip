@@ -186,10 +186,10 @@ template <int DT> __device__ __forceinline__ void store_outputs(const Q4Args &a,
 // one launch, and with one output tile a workgroup every compute unit has codes
 // to stream from about 4096 outputs on.
 //
-// Bound by the codes' bytes for one row of x (1 x 25088 -> 4096 bf16: 12.6 us for
-// 53 MB, 4.2 TB/s with 2.8 us of launch among them; a large read reaches 6.05),
+// Bound by the codes' bytes for one row of x (1 x 25088 -> 4096 bf16: 12.4 us for
+// 53 MB, 4.3 TB/s with 2.8 us of launch among them; a large read reaches 6.05),
 // by x's operands, which every output tile reads again, for 16 rows (29.6 us).
-// 13 x 5000 -> 11003 bf16 10.5 us; fp32 15.0 us, by the instructions that split x
+// 13 x 5000 -> 11003 bf16 10.5 us, fp16 10.0; fp32 14.7 us, by the instructions that split x
 // (19.8 with exact bf16 codes and three bf16 parts of x; 1 x 25088 -> 4096 26
 // against 39).  Requesting a wave's next chunk before working on this one was
 // slower (13 rows bf16 13.8 us against 12.3): other waves hide the latency, and
@@ -329,11 +329,12 @@ template <int COLS> struct ManyShape {
 // work in them (measured: 12 vector instructions with one 32x32x16, 58 cycles;
 // 6 with one 16x16x32, twice, 68).
 //
-// Bound by instruction issue: 256 x 25088 -> 4096 bf16, 71 us (742 TFLOP/s; a
+// Bound by instruction issue: 256 x 25088 -> 4096 bf16, 71 to 74 us (710 to 742 TFLOP/s; a
 // large library product reaches 1206), matrix cores busy 39% of the cycles and
 // the vector instructions that decode and scale 55%.  Groups of 32 scale four
 // times as often as groups of 128: 124 us.  fp32, two products for each,
-// with the other two launches: 137 us (200 with three bf16 parts; bf16 83).
+// with the other two launches: 135 to 142 us (200 with three bf16 parts; bf16 79 to 83,
+// fp16 76 to 81).
 template <int DT, bool ZP, int STEPS, int COLS>
 __global__ __launch_bounds__(256, 2) void q4_many_kernel(Q4Args a, Q4Many q)
 {

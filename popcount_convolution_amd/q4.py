@@ -338,7 +338,8 @@ class KV4Cache:
         number each.  ``max_context``
         bounds the context lengths (the table's width by default).  ``scale``
         defaults to ``head_dim ** -0.5``; ``window`` > 0 limits a query to that many
-        last positions.  ``lse``: float32 ``[tokens, heads]`` to fill."""
+        last positions.  ``lse``: float32 ``[tokens, heads]`` to fill.  Rows of tokens
+        that ``q_start`` gives to no request are not written."""
         torch = _torch or _load_torch()
         _need_tensor(q, "q")
         shape = q.shape
