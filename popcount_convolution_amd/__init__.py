@@ -9,7 +9,10 @@ stream) and the seeded synthetic workloads (``workloads``).
 
 Next to the binary layers are the 4-bit operators of a language model's
 decoding step (``include/bconv_q4.h``, ``q4``): ``Q4Linear``, ``KV4Cache`` (its
-``append`` and ``attention``) and ``build_block_tables``.
+``append`` and ``attention``) and ``build_block_tables``; and microscaled 4-bit
+floats with layers of experts (``include/bconv_mx4.h``, ``mx4``):
+``mx4_quantize``, ``MX4Linear``, ``MX4Experts`` and ``sort_by_expert``, whose
+``ExpertOrder`` takes rows to the experts and back.
 """
 
 from __future__ import annotations
@@ -33,6 +36,11 @@ from ._binding import (  # noqa: F401  (re-exported C ABI names)
     BCONV_BF16, BCONV_F16, BCONV_F32, bconv_block_tables, bconv_kv4_append, bconv_kv4_attention, bconv_kv4_attention_t,
     bconv_kv4_attention_workspace_size, bconv_kv4_desc_t, bconv_kv4_layout, bconv_q4_linear_create,
     bconv_q4_linear_destroy, bconv_q4_linear_forward, bconv_q4_linear_workspace_size)
+from ._binding import (  # noqa: F401
+    bconv_expert_combine, bconv_expert_combine_backward, bconv_expert_gather, bconv_expert_sort,
+    bconv_expert_sort_workspace_size, bconv_mx4_linear_create, bconv_mx4_linear_desc_t, bconv_mx4_linear_destroy,
+    bconv_mx4_linear_forward, bconv_mx4_linear_workspace_size, bconv_mx4_quantize, bconv_mx4_rows_t)
+from .mx4 import ExpertOrder, MX4Experts, MX4Linear, MX4Tensor, mx4_quantize, sort_by_expert  # noqa: F401
 from .q4 import BlockTables, KV4Cache, Q4Linear, build_block_tables, pack_codes  # noqa: F401
 
 

@@ -103,6 +103,17 @@ class bconv_kv4_attention_t(ctypes.Structure):
                 ("scale", ctypes.c_float)]
 
 
+class bconv_mx4_linear_desc_t(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("experts", "in_features", "out_features")]
+
+
+class bconv_mx4_rows_t(ctypes.Structure):
+    _fields_ = [("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("y", ctypes.c_void_p), ("ldy", ctypes.c_int64), ("x_rows", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("choices", ctypes.c_int32), ("offsets", ctypes.c_void_p),
+                ("order", ctypes.c_void_p)]
+
+
 _lib = None
 
 
@@ -155,6 +166,16 @@ def load_library(path: Optional[str] = None):
         "bconv_kv4_attention": (st, [ctypes.POINTER(bconv_kv4_desc_t), vp, ctypes.POINTER(bconv_kv4_attention_t), vp,
                                      sz]),
         "bconv_block_tables": (st, [vp, i32, i32, vp, i32, i32, vp, vp, vp, i32, vp, vp, i32, vp, vp, vp, vp]),
+        "bconv_mx4_quantize": (st, [vp, i32, i32, i32, vp, i64, vp, vp, vp]),
+        "bconv_mx4_linear_create": (st, [ctypes.POINTER(bconv_mx4_linear_desc_t), vp, vp, vp, vp, ctypes.POINTER(vp)]),
+        "bconv_mx4_linear_workspace_size": (st, [vp, ctypes.POINTER(bconv_mx4_rows_t), ctypes.POINTER(sz)]),
+        "bconv_mx4_linear_forward": (st, [vp, vp, ctypes.POINTER(bconv_mx4_rows_t), vp, sz]),
+        "bconv_mx4_linear_destroy": (st, [vp]),
+        "bconv_expert_sort_workspace_size": (st, [i32, i32, ctypes.POINTER(sz)]),
+        "bconv_expert_sort": (st, [vp, i32, i32, i32, vp, vp, vp, vp, vp, sz]),
+        "bconv_expert_gather": (st, [vp, i32, i32, i32, i32, vp, i64, vp, vp, vp]),
+        "bconv_expert_combine": (st, [vp, i32, i32, i32, i32, vp, i64, vp, i32, vp, vp]),
+        "bconv_expert_combine_backward": (st, [vp, i32, i32, i32, i32, vp, i64, vp, i64, vp, vp, i32, vp, vp, vp]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(lib, name)
@@ -387,5 +408,77 @@ def bconv_block_tables(stream, requests: int, block_size: int, block_table, tabl
         stream, requests, block_size, _ptr(block_table), table_width, table_stride, _ptr(context_lens),
         _ptr(new_lens), _ptr(free_blocks), free_count, _ptr(free_head), _ptr(free_head_out), tokens, _ptr(slots),
         _ptr(positions), _ptr(q_start), _ptr(context_lens_out))
+    if st:
+        _check(st)
+
+
+def bconv_mx4_quantize(stream, rows: int, cols: int, dtype: int, x, ldx: int, codes, scales, values=None) -> None:
+    st = (_lib or load_library()).bconv_mx4_quantize(stream, rows, cols, dtype, _ptr(x), ldx, _ptr(codes),
+                                                     _ptr(scales), _ptr(values))
+    if st:
+        _check(st)
+
+
+def bconv_mx4_linear_create(experts: int, in_features: int, out_features: int, stream, codes, scales, bias=None) -> int:
+    """Device arrays: uint8 codes and scales, float32 bias or None."""
+    desc = bconv_mx4_linear_desc_t(experts, in_features, out_features)
+    h = ctypes.c_void_p()
+    _check(load_library().bconv_mx4_linear_create(ctypes.byref(desc), _ptr(stream), _ptr(codes), _ptr(scales),
+                                                  _ptr(bias), ctypes.byref(h)))
+    return h.value
+
+
+def bconv_mx4_linear_workspace_size(h: int, args: bconv_mx4_rows_t) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().bconv_mx4_linear_workspace_size(h, args, ctypes.byref(b)))
+    return b.value
+
+
+def bconv_mx4_linear_forward(h: int, stream, args: bconv_mx4_rows_t, workspace=None, workspace_bytes: int = 0) -> None:
+    st = (_lib or load_library()).bconv_mx4_linear_forward(h, stream, args, _ptr(workspace), workspace_bytes)
+    if st:
+        _check(st)
+
+
+def bconv_mx4_linear_destroy(h: int) -> None:
+    _check(load_library().bconv_mx4_linear_destroy(h))
+
+
+def bconv_expert_sort_workspace_size(pairs: int, experts: int) -> int:
+    b = ctypes.c_size_t()
+    _check(load_library().bconv_expert_sort_workspace_size(pairs, experts, ctypes.byref(b)))
+    return b.value
+
+
+def bconv_expert_sort(stream, pairs: int, experts: int, id_bytes: int, ids, offsets, order, position, workspace=None,
+                      workspace_bytes: int = 0) -> None:
+    st = (_lib or load_library()).bconv_expert_sort(stream, pairs, experts, id_bytes, _ptr(ids), _ptr(offsets),
+                                                    _ptr(order), _ptr(position), _ptr(workspace), workspace_bytes)
+    if st:
+        _check(st)
+
+
+def bconv_expert_gather(stream, tokens: int, choices: int, width: int, dtype: int, x, ldx: int, order, position,
+                        rows) -> None:
+    st = (_lib or load_library()).bconv_expert_gather(stream, tokens, choices, width, dtype, _ptr(x), ldx, _ptr(order),
+                                                      _ptr(position), _ptr(rows))
+    if st:
+        _check(st)
+
+
+def bconv_expert_combine(stream, tokens: int, choices: int, width: int, dtype: int, rows, ldr: int, position,
+                         weight_dtype: int, weights, y) -> None:
+    st = (_lib or load_library()).bconv_expert_combine(stream, tokens, choices, width, dtype, _ptr(rows), ldr,
+                                                       _ptr(position), weight_dtype, _ptr(weights), _ptr(y))
+    if st:
+        _check(st)
+
+
+def bconv_expert_combine_backward(stream, tokens: int, choices: int, width: int, dtype: int, dy, ldd: int, rows,
+                                  ldr: int, order, position, weight_dtype: int, weights, d_rows,
+                                  d_weights=None) -> None:
+    st = (_lib or load_library()).bconv_expert_combine_backward(
+        stream, tokens, choices, width, dtype, _ptr(dy), ldd, _ptr(rows), ldr, _ptr(order), _ptr(position),
+        weight_dtype, _ptr(weights), _ptr(d_rows), _ptr(d_weights))
     if st:
         _check(st)

@@ -20,7 +20,8 @@ LIB = os.path.join(PKG, "libbconv.so")
 # longest compiles first, so they start before the pool fills
 SOURCES = ("xconv_k3.hip", "xconv_k24.hip", "xconv_k5.hip", "xconv_k1.hip", "bwmma.hip", "i8mma.hip", "gemm.hip", "gemm_f4.hip",
            "xconv.hip", "xconv_small.hip", "bwconv.hip", "bconv.hip", "pack.hip", "prepack.hip", "calib.hip",
-           "q4_linear.hip", "kv4_attention.hip", "kv4_append.hip", "block_tables.hip")
+           "q4_linear.hip", "kv4_attention.hip", "kv4_append.hip", "block_tables.hip", "mx4_linear.hip", "mx4_quantize.hip",
+           "experts.hip")
 ARCH = "gfx950"
 
 HIPCC_FLAGS = [

@@ -1,0 +1,130 @@
+// Device helpers of the microscaled 4-bit operators: blocks of 32 values to
+// codes and a power of two, and the layouts that the kernels share.  Not part
+// of the public ABI.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "bconv_mx4.h"
+#include "q4_device.h"
+
+namespace bconv {
+
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// Inputs of one step of the products: two 16 x 16 x 128 matrix instructions.
+// Lane (row r = lane & 15, lg = lane >> 4) of a step holds the two blocks
+// 64 lg .. 64 lg + 63 of its row, the first for the first instruction.  The sum
+// over k may be taken in any order, as long as both operands agree; this one
+// makes a lane's codes 32 and its scales 2 consecutive bytes of a quantised row.
+constexpr int kStep = BCONV_MX4_PAD;
+
+__host__ __device__ constexpr long long mx4_padded(long long cols)
+{
+    return (cols + BCONV_MX4_PAD - 1) / BCONV_MX4_PAD * BCONV_MX4_PAD;
+}
+
+// 8 consecutive values of one row as loaded.
+template <int DT> struct Eight {
+    u32x4 q[DT == BCONV_F32 ? 2 : 1];
+};
+
+// Those of them that are in the row, zeros for the rest (`left` of them remain).
+template <int DT> __device__ __forceinline__ Eight<DT> load_values(const typename Elem<DT>::type *p, int left, bool vec)
+{
+    Eight<DT> e;
+    if (vec && left >= 8) {
+#pragma unroll
+        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) e.q[i] = reinterpret_cast<const u32x4 *>(p)[i];
+        return e;
+    }
+    if constexpr (DT == BCONV_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e.q[i >> 2][i & 3] = i < left ? __builtin_bit_cast(uint32_t, p[i]) : 0u;
+    } else {
+        const uint16_t *h = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            e.q[0][i] = (2 * i < left ? (uint32_t)h[2 * i] : 0u) | (2 * i + 1 < left ? (uint32_t)h[2 * i + 1] << 16 : 0u);
+    }
+    return e;
+}
+
+// The largest magnitude of some values, as bits that order like it: of fp32, or
+// of the 16-bit type.
+template <int DT> __device__ __forceinline__ uint32_t largest(const Eight<DT> &e)
+{
+    if constexpr (DT == BCONV_F32) {
+        uint32_t m = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = e.q[i >> 2][i & 3] & 0x7fffffffu;
+            m = a > m ? a : m;
+        }
+        return m;
+    } else {
+        u16x2 m = {0, 0};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, (uint32_t)(e.q[0][i] & 0x7fff7fffu)));
+        return m[0] > m[1] ? m[0] : m[1];
+    }
+}
+
+// A block's scale byte from the bits of its largest magnitude: the exponent
+// field of that as fp32, less 2, at least 0; 255 for infinities and NaN.
+template <int DT> __device__ __forceinline__ uint32_t scale_byte(uint32_t top)
+{
+    uint32_t bits = top;
+    if constexpr (DT == BCONV_BF16) bits = top << 16;
+    if constexpr (DT == BCONV_F16)
+        bits = __builtin_bit_cast(uint32_t, (float)__builtin_bit_cast(_Float16, (uint16_t)top));
+    const int field = (int)(bits >> 23);
+    return field == 255 ? 255u : (uint32_t)(field > 2 ? field - 2 : 0);
+}
+
+// Codes of 8 values under a scale byte.  The conversion divides by the power of
+// two of its scale operand's exponent field (0 is 2^-127), rounds to the nearest,
+// ties to even, and saturates: compared with the definition for every exponent.
+template <int DT> __device__ __forceinline__ uint32_t to_codes(const Eight<DT> &e, uint32_t byte)
+{
+    const float s = __builtin_bit_cast(float, byte << 23);
+    uint32_t c = 0;
+    if constexpr (DT == BCONV_F32) {
+        const f32x4 a = __builtin_bit_cast(f32x4, e.q[0]), b = __builtin_bit_cast(f32x4, e.q[1]);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[0], a[1], s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, a[2], a[3], s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, b[0], b[1], s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(c, b[2], b[3], s, 3);
+    } else if constexpr (DT == BCONV_F16) {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, (uint32_t)e.q[0][0]), s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, (uint32_t)e.q[0][1]), s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, (uint32_t)e.q[0][2]), s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_f16(c, __builtin_bit_cast(f16x2, (uint32_t)e.q[0][3]), s, 3);
+    } else {
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)e.q[0][0]), s, 0);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)e.q[0][1]), s, 1);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)e.q[0][2]), s, 2);
+        c = __builtin_amdgcn_cvt_scalef32_pk_fp4_bf16(c, __builtin_bit_cast(bf16x2, (uint32_t)e.q[0][3]), s, 3);
+    }
+    return byte == 255 ? 0u : c;
+}
+
+// D += A B over 128 k of 16 x 16 results; `S` is the byte of the scale operands
+// that belongs to these k.
+template <int S> __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x4 c)
+{
+    const i32x8 a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    // cbsz = blgp = 4: e2m1
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// Launches the quantisation of rows (see bconv_mx4_quantize); arguments are
+// checked by the caller. 
+hipError_t mx4_quantize_rows(hipStream_t s, long long rows, int cols, int dtype, const void *x, long long ldx,
+                             uint8_t *codes, uint8_t *scales, void *values);
+
+}  // namespace bconv
