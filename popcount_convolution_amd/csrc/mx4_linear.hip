@@ -220,26 +220,241 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
     }
 }
 
+// ------------------------------------------------------------------ many rows
+
+// What the many-row kernel takes besides Mx4Args.
+struct Mx4Many {
+    float *sums;  // [splits][rows][padded_n], or nullptr for one split
+    int row_blocks, out_blocks, splits;
+    int padded_n;
+};
+
+// The row block `rb` of the launch: its expert and rows.  Experts' blocks follow each other,
+// those of the rows of no expert come last; f is -1 behind them.
+template <int R> __device__ __forceinline__ int find_rows(const Mx4Args &a, int rb, Span &span)
+{
+    if (!a.offsets) {
+        span.begin = rb * R;
+        span.end = a.rows - span.begin < R ? a.rows : span.begin + R;
+        return 0;
+    }
+    const int lane = threadIdx.x & 63;
+    int before = 0;  // blocks of the experts before these 64
+    for (int f0 = 0; f0 <= a.experts; f0 += 64) {
+        const int f = f0 + lane;
+        const Span s = f <= a.experts ? expert_span(a, f) : Span{0, 0};
+        const int blocks = s.end > s.begin ? (s.end - s.begin + R - 1) / R : 0;
+        int upto = blocks;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int u = __shfl_up(upto, d);
+            if (lane >= d) upto += u;
+        }
+        const unsigned long long past = __ballot(before + upto > rb);
+        if (past) {
+            const int l = __builtin_ctzll(past);
+            span.begin = __builtin_amdgcn_readlane(s.begin, l) + (rb - before - __builtin_amdgcn_readlane(upto - blocks, l)) * R;
+            span.end = __builtin_amdgcn_readlane(s.end, l);
+            if (span.end - span.begin > R) span.end = span.begin + R;
+            return f0 + l;
+        }
+        before += __builtin_amdgcn_readlane(upto, 63);
+    }
+    return -1;
+}
+
+// A workgroup of WM x WN waves takes 16 WM MT rows of x and 16 WN NT outputs; a step
+// of both (128 bytes a row) goes to LDS a step ahead, by loads that pass no registers.
+template <int DT, int WM, int WN, int MT, int NT>
+__global__ __launch_bounds__(WM * WN * 64, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
+{
+    typedef typename Elem<DT>::type T;
+    constexpr int WAVES = WM * WN, R = WM * MT * 16, OT = WN * NT;  // rows of x, output tiles
+    constexpr int XL = R / 8 / WAVES, WL = OT * 2 / WAVES;         // 1 KiB loads a wave
+    static_assert(XL * WAVES * 8 == R && WL * WAVES == OT * 2);
+    struct Stage {
+        u32x4 x[R * 8];    // [row][slot], block b of a step in slot b ^ (row >> 1 & 7)
+        u32x4 w[OT * 128]; // [tile][instruction][lane]
+    };
+    __shared__ Stage stage[2];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int row = lane & 15, lg = lane >> 4;
+
+    // Workgroups go to the XCDs in turn; each takes a run of neighbouring blocks.
+    const int total = gridDim.x;
+    int id = blockIdx.x;
+    {
+        const int xcd = id & 7, each = total >> 3, more = total & 7;
+        id = xcd * each + (xcd < more ? xcd : more) + (id >> 3);
+    }
+    const int blocks = q.row_blocks * q.out_blocks;
+    const int split = id / blocks;
+    id -= split * blocks;
+    constexpr int kGroup = 8;
+    const int group = id / (kGroup * q.out_blocks), g0 = group * kGroup;
+    const int high = q.row_blocks - g0 < kGroup ? q.row_blocks - g0 : kGroup;
+    id -= group * kGroup * q.out_blocks;
+    const int rb = g0 + id % high, ob = id / high;
+    const int tile0 = ob * OT;
+
+    Span span;
+    const int f = find_rows<R>(a, rb, span);
+    if (f < 0) return;
+    if (f == a.experts) {  // rows of no expert
+        for (int e = threadIdx.x; e < (span.end - span.begin) * OT * 16; e += WAVES * 64) {
+            const int o = tile0 * 16 + e % (OT * 16);
+            if (o < a.n) static_cast<T *>(a.y)[(long long)(span.begin + e / (OT * 16)) * a.ldy + o] = (T)0.0f;
+        }
+        return;
+    }
+    const int s_begin = (int)((long long)a.steps * split / q.splits), s_end = (int)((long long)a.steps * (split + 1) / q.splits);
+
+    // where this lane's part of the loads comes from: rows past the last count as the last
+    auto x_row = [&](int r) { return (uint32_t)input_row(a, min(span.begin + r, span.end - 1)); };
+    const uint8_t *xp[XL];
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+        const int r = (j * WAVES + wave) * 8 + (lane >> 3);
+        xp[j] = a.xc + (unsigned long long)x_row(r) * a.steps * 128 + ((lane & 7) ^ (r >> 1 & 7)) * 16;
+    }
+    const u32x4 *wp[WL];
+#pragma unroll
+    for (int j = 0; j < WL; ++j) {
+        const int u = j * WAVES + wave, tile = min(tile0 + (u >> 1), a.tiles - 1);
+        wp[j] = a.codes + (((long long)f * a.tiles + tile) * a.steps * 2 + (u & 1)) * 64 + lane;
+    }
+    const int my_x = wave / WN * MT * 16, my_tile = wave % WN * NT;
+    uint32_t xs_at[MT];
+    const uint16_t *ws_at[NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m) xs_at[m] = x_row(my_x + m * 16 + row) * a.steps * 8 + lg * 2;
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+        ws_at[t] = a.scales + ((long long)f * a.tiles + min(tile0 + my_tile + t, a.tiles - 1)) * a.steps * 64 + lane;
+
+    typedef __attribute__((address_space(3))) void *Lds;
+    uint32_t xs[MT], ws[NT], xn[MT], wn[NT];
+    auto request = [&](int s) {
+        Stage &st = stage[s & 1];
+#pragma unroll
+        for (int j = 0; j < XL; ++j)
+            __builtin_amdgcn_global_load_lds((const void *)(xp[j] + (long long)s * 128), (Lds)(&st.x[(j * WAVES + wave) * 64]), 16, 0, 0);
+#pragma unroll
+        for (int j = 0; j < WL; ++j)
+            __builtin_amdgcn_global_load_lds((const void *)(wp[j] + (long long)s * 128), (Lds)(&st.w[(j * WAVES + wave) * 64]), 16, 0, 0);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xn[m] = *reinterpret_cast<const uint16_t *>(a.xs + (size_t)s * 8 + xs_at[m]);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) wn[t] = ws_at[t][s * 64];
+    };
+    f32x4 acc[MT][NT];
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
+    if (s_begin < s_end) request(s_begin);
+    for (int s = s_begin; s < s_end; ++s) {
+        __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xf << 8));  // vmcnt(0): this step's operands are here
+        __syncthreads();                                          // in every wave, and the other stage is read
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xs[m] = xn[m];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) ws[t] = wn[t];
+        if (s + 1 < s_end) request(s + 1);
+        const Stage &st = stage[s & 1];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            u32x4 w[NT];
+#pragma unroll
+            for (int t = 0; t < NT; ++t) w[t] = st.w[((my_tile + t) * 2 + i) * 64 + lane];
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const int r = my_x + m * 16 + row;
+                const u32x4 x = st.x[r * 8 + ((2 * lg + i) ^ (r >> 1 & 7))];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    acc[m][t] = i ? mfma_mx4<1>(w[t], ws[t], x, xs[m], acc[m][t]) : mfma_mx4<0>(w[t], ws[t], x, xs[m], acc[m][t]);
+            }
+        }
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+        const int i = span.begin + my_x + m * 16 + row;
+        if (i >= span.end) continue;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int o0 = (tile0 + my_tile + t) * 16 + lg * 4;
+            if (q.splits > 1)
+                *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * a.rows + i) * q.padded_n + o0) = acc[m][t];
+            else if (o0 < a.n) store_four<DT>(a, f, i, o0, acc[m][t]);
+        }
+    }
+}
+
+// Adds the splits' sums in order.
+template <int DT> __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args a, Mx4Many q)
+{
+    const int per = (a.n + 3) / 4;
+    const long long id = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (id >= (long long)per * a.rows) return;
+    const int i = (int)(id / per), o0 = (int)(id % per) * 4;
+    const float *p = q.sums + (long long)i * q.padded_n + o0;
+    const long long step = (long long)a.rows * q.padded_n;
+    f32x4 v = *reinterpret_cast<const f32x4 *>(p);
+    for (int s = 1; s < q.splits; ++s) v += *reinterpret_cast<const f32x4 *>(p + s * step);
+    store_four<DT>(a, 0, i, o0, v);
+}
+
 // ------------------------------------------------------------------ dispatch
 
 struct Mx4Plan {
     bool quantise;  // x is quantised by a launch of its own
-    size_t scales_offset, bytes;
+    int shape;      // 0: few rows; rows of x of the many-row kernel's workgroup
+    Mx4Many q;
+    size_t scales_offset, sums_offset, bytes;
 };
 
-Mx4Plan plan_mx4(const Mx4Args &a, bool given)
+Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
 {
     Mx4Plan p{};
-    p.quantise = !given && a.rows > 4;
+    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
+    const int mean = a.rows / a.experts;
+    p.shape = mean > 512 ? 256 : mean > 16 ? 128 : 0;
+    p.quantise = !given && (a.rows > 4 || p.shape);
     if (p.quantise) {
         p.scales_offset = (size_t)a.x_rows * a.steps * (kStep / 2);
-        p.bytes = p.scales_offset + (size_t)a.x_rows * a.steps * (kStep / 32);
+        p.bytes = p.sums_offset = up(p.scales_offset + (size_t)a.x_rows * a.steps * (kStep / 32));
+    }
+    if (p.shape) {
+        const int out_tiles = p.shape / 16;
+        p.q.row_blocks = (a.rows + p.shape - 1) / p.shape + (a.offsets ? a.experts : 0);
+        p.q.out_blocks = (a.tiles + out_tiles - 1) / out_tiles;
+        p.q.padded_n = p.q.out_blocks * p.shape;
+        p.q.splits = 1;
+        if (!a.offsets) {
+            const long long blocks = (long long)p.q.row_blocks * p.q.out_blocks;
+            long long splits = (2LL * cus) / blocks;
+            if (splits > 8) splits = 8;
+            if (splits > a.steps / 4) splits = a.steps / 4;
+            p.q.splits = splits < 1 ? 1 : (int)splits;
+        }
+        if (p.q.splits > 1) p.bytes = p.sums_offset + (size_t)p.q.splits * a.rows * p.q.padded_n * 4;
     }
     return p;
 }
 
-template <int DT> hipError_t run_mx4(const Mx4Args &a, hipStream_t s)
+template <int DT> hipError_t run_mx4(const Mx4Args &a, const Mx4Plan &p, hipStream_t s)
 {
+    if (p.shape) {
+        const dim3 grid((unsigned)((long long)p.q.row_blocks * p.q.out_blocks * p.q.splits));
+        if (p.shape == 256) hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 4, 8, 4>), grid, dim3(512), 0, s, a, p.q);
+        else hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 2, 4, 4>), grid, dim3(256), 0, s, a, p.q);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || p.q.splits == 1) return e;
+        const long long outs = (long long)((a.n + 3) / 4) * a.rows;
+        hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
+        return hipGetLastError();
+    }
     const dim3 grid((a.tiles + 1) / 2, a.offsets ? a.experts + 1 : (a.rows + 15) / 16);
     if (a.x) hipLaunchKernelGGL((mx4_few_kernel<DT, false, 2, 8>), grid, dim3(512), 0, s, a);
     else hipLaunchKernelGGL((mx4_few_kernel<DT, true, 2, 8>), grid, dim3(512), 0, s, a);
@@ -396,7 +611,7 @@ bconv_status_t bconv_mx4_linear_workspace_size(bconv_mx4_linear_t h, const bconv
     const bconv_status_t st = check_sizes(h, args);
     if (st != BCONV_OK) return st;
     if (!bytes) return fail(BCONV_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = args->rows ? bconv::plan_mx4(kernel_args(h, args), !args->x).bytes : 0;
+    *bytes = args->rows ? bconv::plan_mx4(kernel_args(h, args), !args->x, h->cus).bytes : 0;
     return BCONV_OK;
 }
 
@@ -422,7 +637,7 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
     if (((uintptr_t)args->offsets | (uintptr_t)args->order) % 4)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "offsets/order not aligned to an element");
     bconv::Mx4Args a = kernel_args(h, args);
-    const bconv::Mx4Plan p = bconv::plan_mx4(a, !args->x);
+    bconv::Mx4Plan p = bconv::plan_mx4(a, !args->x, h->cus);
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
         return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes, workspace ? workspace_bytes : (size_t)0);
     if (p.bytes > 0 && (uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
@@ -451,10 +666,11 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
         a.xc = codes;
         a.xs = codes + p.scales_offset;
     }
+    p.q.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.sums_offset);
     switch (args->dtype) {
-    case BCONV_F32: e = bconv::run_mx4<BCONV_F32>(a, s); break;
-    case BCONV_F16: e = bconv::run_mx4<BCONV_F16>(a, s); break;
-    default: e = bconv::run_mx4<BCONV_BF16>(a, s); break;
+    case BCONV_F32: e = bconv::run_mx4<BCONV_F32>(a, p, s); break;
+    case BCONV_F16: e = bconv::run_mx4<BCONV_F16>(a, p, s); break;
+    default: e = bconv::run_mx4<BCONV_BF16>(a, p, s); break;
     }
     if (e != hipSuccess) return hip_fail(e, "mx4 linear kernel");
     return BCONV_OK;
