@@ -22,8 +22,7 @@
  * memory and must stay valid until the stream's work completes.  Calls
  * without a handle run on the current HIP device; a handle's are launched on
  * the device it was created on, to which their buffers and stream belong.
- * Elements have any alignment of their own type; 16-byte aligned rows are
- * read and written wider.
+ * Rows may start at any element.
  */
 #ifndef BCONV_MX4_H
 #define BCONV_MX4_H

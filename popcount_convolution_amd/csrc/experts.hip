@@ -182,29 +182,35 @@ struct RowsArgs {
     int tokens, choices, width, pairs;
     int weight_dtype;
     int first;          // token of the launch's first workgroup
-    int vec;            // everything in 16-byte pieces
 };
 
 constexpr int kRowThreads = 256;
 
 template <int DT> constexpr int kPiece = DT == BCONV_F32 ? 4 : 8;  // values of 16 bytes
 
-// V: values a lane moves at once (kPiece or 1).
-template <int DT, int V> struct Part {
-    typename Elem<DT>::type v[V];
-    __device__ __forceinline__ static Part load(const void *base, long long at)
+// What a lane moves at once: 16 bytes of a row, or what is left of it.
+template <int DT> struct Piece {
+    typedef typename Elem<DT>::type T;
+    T v[kPiece<DT>];
+    __device__ __forceinline__ static Piece load(const void *base, long long at, int left)
     {
-        Part p;
-        const typename Elem<DT>::type *s = static_cast<const typename Elem<DT>::type *>(base) + at;
-        if constexpr (V == 1) p.v[0] = *s;
-        else p = __builtin_bit_cast(Part, *reinterpret_cast<const u32x4 *>(s));
+        const T *s = static_cast<const T *>(base) + at;
+        if (left >= kPiece<DT>) return __builtin_bit_cast(Piece, (u32x4)*reinterpret_cast<const u32x4_any *>(s));
+        Piece p;
+#pragma unroll
+        for (int i = 0; i < kPiece<DT>; ++i) p.v[i] = i < left ? s[i] : (T)0.0f;
         return p;
     }
-    __device__ __forceinline__ void store(void *base, long long at) const
+    __device__ __forceinline__ void store(void *base, long long at, int left) const
     {
-        typename Elem<DT>::type *d = static_cast<typename Elem<DT>::type *>(base) + at;
-        if constexpr (V == 1) *d = v[0];
-        else *reinterpret_cast<u32x4 *>(d) = __builtin_bit_cast(u32x4, *this);
+        T *d = static_cast<T *>(base) + at;
+        if (left >= kPiece<DT>) {
+            *reinterpret_cast<u32x4_any *>(d) = __builtin_bit_cast(u32x4, *this);
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < kPiece<DT>; ++i)
+            if (i < left) d[i] = v[i];
     }
 };
 
@@ -231,36 +237,37 @@ __device__ __forceinline__ int place(const RowsArgs &a, long long pair)
 }
 
 // Zeros to the places among those numbered like the token's pairs that are no pair's.
-template <int DT, int V> __device__ __forceinline__ void clear_places(const RowsArgs &a, int t)
+template <int DT> __device__ __forceinline__ void clear_places(const RowsArgs &a, int t)
 {
+    constexpr int V = kPiece<DT>;
+    Piece<DT> zero;
+#pragma unroll
+    for (int i = 0; i < V; ++i) zero.v[i] = (typename Elem<DT>::type)0.0f;
     for (int j = 0; j < a.choices; ++j) {
         const long long p = (long long)t * a.choices + j;
         if (a.order[p] >= 0) continue;
-        for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
-            Part<DT, V> z;
-#pragma unroll
-            for (int i = 0; i < V; ++i) z.v[i] = (typename Elem<DT>::type)0.0f;
-            z.store(a.to, p * a.width + c);
-        }
+        for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) zero.store(a.to, p * a.width + c, a.width - c);
     }
 }
 
 // A workgroup a token: its row is read once and written for each choice.
-template <int DT, int V> __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(RowsArgs a)
+template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(RowsArgs a)
 {
+    constexpr int V = kPiece<DT>;
     const int t = a.first + (int)blockIdx.x;
     for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
-        const Part<DT, V> p = Part<DT, V>::load(a.from, t * a.ld_from + c);
+        const Piece<DT> p = Piece<DT>::load(a.from, t * a.ld_from + c, a.width - c);
         for (int j = 0; j < a.choices; ++j) {
             const int to = place(a, (long long)t * a.choices + j);
-            if (to >= 0) p.store(a.to, (long long)to * a.width + c);
+            if (to >= 0) p.store(a.to, (long long)to * a.width + c, a.width - c);
         }
     }
-    clear_places<DT, V>(a, t);
+    clear_places<DT>(a, t);
 }
 
-template <int DT, int V> __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(RowsArgs a)
+template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(RowsArgs a)
 {
+    constexpr int V = kPiece<DT>;
     const int t = a.first + (int)blockIdx.x;
     for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
         float sum[V];
@@ -271,20 +278,21 @@ template <int DT, int V> __global__ __launch_bounds__(kRowThreads) void expert_c
             const int at = place(a, pair);
             if (at < 0) continue;
             const float w = load_weight(a, pair);
-            const Part<DT, V> p = Part<DT, V>::load(a.from, at * a.ld_from + c);
+            const Piece<DT> p = Piece<DT>::load(a.from, at * a.ld_from + c, a.width - c);
 #pragma unroll
             for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(w, (float)p.v[i], sum[i]);
         }
-        Part<DT, V> y;
+        Piece<DT> y;
 #pragma unroll
         for (int i = 0; i < V; ++i) y.v[i] = (typename Elem<DT>::type)sum[i];
-        y.store(a.to, (long long)t * a.width + c);
+        y.store(a.to, (long long)t * a.width + c, a.width - c);
     }
 }
 
 // A workgroup a token; its choices one after the other.
-template <int DT, int V> __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(RowsArgs a)
+template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(RowsArgs a)
 {
+    constexpr int V = kPiece<DT>;
     __shared__ float part[kRowThreads / 64];
     const int t = a.first + (int)blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int j = 0; j < a.choices; ++j) {
@@ -294,16 +302,16 @@ template <int DT, int V> __global__ __launch_bounds__(kRowThreads) void expert_c
         if (at >= 0) {
             const float w = load_weight(a, pair);
             for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
-                const Part<DT, V> d = Part<DT, V>::load(a.dy, t * a.ld_dy + c);
+                const Piece<DT> d = Piece<DT>::load(a.dy, t * a.ld_dy + c, a.width - c);
                 if (a.d_weights) {
-                    const Part<DT, V> r = Part<DT, V>::load(a.from, at * a.ld_from + c);
+                    const Piece<DT> r = Piece<DT>::load(a.from, at * a.ld_from + c, a.width - c);
 #pragma unroll
                     for (int i = 0; i < V; ++i) dot = __builtin_fmaf((float)d.v[i], (float)r.v[i], dot);
                 }
-                Part<DT, V> g;
+                Piece<DT> g;
 #pragma unroll
                 for (int i = 0; i < V; ++i) g.v[i] = (typename Elem<DT>::type)(w * (float)d.v[i]);
-                g.store(a.to, (long long)at * a.width + c);
+                g.store(a.to, (long long)at * a.width + c, a.width - c);
             }
         }
         if (a.d_weights) {
@@ -319,17 +327,17 @@ template <int DT, int V> __global__ __launch_bounds__(kRowThreads) void expert_c
             __syncthreads();
         }
     }
-    clear_places<DT, V>(a, t);
+    clear_places<DT>(a, t);
 }
 
 enum RowsOp { kGather, kCombine, kCombineBackward };
 
-template <int DT, int V> static void launch_rows(RowsOp op, const RowsArgs &a, unsigned grid, hipStream_t s)
+template <int DT> static void launch_rows(RowsOp op, const RowsArgs &a, unsigned grid, hipStream_t s)
 {
     switch (op) {
-    case kGather: hipLaunchKernelGGL((expert_gather_kernel<DT, V>), dim3(grid), dim3(kRowThreads), 0, s, a); break;
-    case kCombine: hipLaunchKernelGGL((expert_combine_kernel<DT, V>), dim3(grid), dim3(kRowThreads), 0, s, a); break;
-    default: hipLaunchKernelGGL((expert_combine_backward_kernel<DT, V>), dim3(grid), dim3(kRowThreads), 0, s, a);
+    case kGather: hipLaunchKernelGGL((expert_gather_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a); break;
+    case kCombine: hipLaunchKernelGGL((expert_combine_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a); break;
+    default: hipLaunchKernelGGL((expert_combine_backward_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a);
     }
 }
 
@@ -337,8 +345,7 @@ template <int DT> static hipError_t run_rows(RowsOp op, RowsArgs a, hipStream_t 
 {
     return launch_slices(a.tokens, [&](long long first, unsigned grid) {
         a.first = (int)first;
-        if (a.vec) launch_rows<DT, kPiece<DT>>(op, a, grid, s);
-        else launch_rows<DT, 1>(op, a, grid, s);
+        launch_rows<DT>(op, a, grid, s);
     });
 }
 
@@ -391,8 +398,6 @@ bconv_status_t check_rows(int32_t tokens, int32_t choices, int32_t width, int32_
     if (ld < width || ld > (1LL << 40)) return fail(BCONV_ERR_INVALID_ARGUMENT, "%s must be in [width, 2^40]", name);
     return BCONV_OK;
 }
-
-bool wide(const void *p, long long ld, int es) { return (uintptr_t)p % 16 == 0 && ld * es % 16 == 0; }
 
 bconv_status_t finish(bconv::RowsOp op, const bconv::RowsArgs &a, int32_t dtype, void *stream)
 {
@@ -479,7 +484,6 @@ bconv_status_t bconv_expert_gather(void *stream, int32_t tokens, int32_t choices
     a.choices = choices;
     a.width = width;
     a.pairs = (int)pairs;
-    a.vec = wide(x, ldx, es) && wide(rows, width, es);
     return finish(bconv::kGather, a, dtype, stream);
 }
 
@@ -509,7 +513,6 @@ bconv_status_t bconv_expert_combine(void *stream, int32_t tokens, int32_t choice
     a.choices = choices;
     a.width = width;
     a.pairs = (int)pairs;
-    a.vec = wide(rows, ldr, es) && wide(y, width, es);
     return finish(bconv::kCombine, a, dtype, stream);
 }
 
@@ -550,7 +553,6 @@ bconv_status_t bconv_expert_combine_backward(void *stream, int32_t tokens, int32
     a.choices = choices;
     a.width = width;
     a.pairs = (int)pairs;
-    a.vec = wide(dy, ldd, es) && (!d_weights || wide(rows, ldr, es)) && wide(d_rows, width, es);
     return finish(bconv::kCombineBackward, a, dtype, stream);
 }
 

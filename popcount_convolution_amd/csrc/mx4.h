@@ -13,6 +13,11 @@ namespace bconv {
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
+// The same in memory at any element's address: global memory takes wide loads
+// and stores at any alignment, in one instruction.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef u32x2 u32x2_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
 // Inputs of one step of the products: two 16 x 16 x 128 matrix instructions.
 // Lane (row r = lane & 15, lg = lane >> 4) of a step holds the two blocks
@@ -32,12 +37,12 @@ template <int DT> struct Eight {
 };
 
 // Those of them that are in the row, zeros for the rest (`left` of them remain).
-template <int DT> __device__ __forceinline__ Eight<DT> load_values(const typename Elem<DT>::type *p, int left, bool vec)
+template <int DT> __device__ __forceinline__ Eight<DT> load_values(const typename Elem<DT>::type *p, int left)
 {
     Eight<DT> e;
-    if (vec && left >= 8) {
+    if (left >= 8) {
 #pragma unroll
-        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) e.q[i] = reinterpret_cast<const u32x4 *>(p)[i];
+        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) e.q[i] = reinterpret_cast<const u32x4_any *>(p)[i];
         return e;
     }
     if constexpr (DT == BCONV_F32) {

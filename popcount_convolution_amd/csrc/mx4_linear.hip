@@ -28,7 +28,6 @@ struct Mx4Args {
     long long ldx, ldy;
     int rows, x_rows, choices;
     int n, k, tiles, steps, experts;
-    int vec;                 // rows of x are 16-byte aligned
 };
 
 // 8 codes (word j of 16 bytes) of lane (r, lg), instruction i of a step: values
@@ -106,8 +105,19 @@ template <int DT> __device__ __forceinline__ void store_four(const Mx4Args &a, i
     typedef typename Elem<DT>::type T;
     T *y = static_cast<T *>(a.y) + (long long)i * a.ldy + o0;
     const float *b = a.bias ? a.bias + (long long)f * a.n + o0 : nullptr;
+    if (o0 + 4 <= a.n) {
+        if (b) v += *reinterpret_cast<const f32x4_any *>(b);
+        if constexpr (DT == BCONV_F32) {
+            *reinterpret_cast<f32x4_any *>(y) = v;
+        } else {
+            typedef T Pair __attribute__((ext_vector_type(2)));
+            const u32x2 p = {__builtin_bit_cast(uint32_t, (Pair){(T)v[0], (T)v[1]}), __builtin_bit_cast(uint32_t, (Pair){(T)v[2], (T)v[3]})};
+            *reinterpret_cast<u32x2_any *>(y) = p;
+        }
+        return;
+    }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+    for (int j = 0; j < 3; ++j)
         if (o0 + j < a.n) y[j] = (T)(b ? v[j] + b[j] : v[j]);
 }
 
@@ -119,7 +129,7 @@ struct XStep {
 
 // From elements: a lane's two blocks are 64 consecutive values of its row, so
 // that quantising them asks no other lane.
-template <int DT> __device__ __forceinline__ XStep quantised_step(const typename Elem<DT>::type *p, int left, bool vec)
+template <int DT> __device__ __forceinline__ XStep quantised_step(const typename Elem<DT>::type *p, int left)
 {
     XStep x;
     x.s = 0;
@@ -129,7 +139,7 @@ template <int DT> __device__ __forceinline__ XStep quantised_step(const typename
         uint32_t top = 0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            e[j] = load_values<DT>(p + i * 32 + j * 8, left - i * 32 - j * 8, vec);
+            e[j] = load_values<DT>(p + i * 32 + j * 8, left - i * 32 - j * 8);
             const uint32_t t = largest<DT>(e[j]);
             top = t > top ? t : top;
         }
@@ -196,7 +206,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
                     x.s = *reinterpret_cast<const uint16_t *>(a.xs + (xr * a.steps + c) * (kStep / 32) + lg * 2);
                 } else {
                     const int k0 = c * kStep + lg * 64;
-                    x = quantised_step<DT>(static_cast<const T *>(a.x) + xr * a.ldx + k0, a.k - k0, a.vec != 0);
+                    x = quantised_step<DT>(static_cast<const T *>(a.x) + xr * a.ldx + k0, a.k - k0);
                 }
             }
 #pragma unroll
@@ -548,8 +558,6 @@ bconv::Mx4Args kernel_args(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
     a.tiles = h->tiles;
     a.steps = h->steps;
     a.experts = h->desc.experts;
-    const int es = dtype_bytes(args->dtype);
-    a.vec = (uintptr_t)args->x % 16 == 0 && args->ldx * es % 16 == 0;
     return a;
 }
 

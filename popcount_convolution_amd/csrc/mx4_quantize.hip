@@ -22,7 +22,6 @@ struct QuantArgs {
     uint32_t units;    // groups of 8 values of all rows, padding included
     uint32_t per_row;  // of one row
     int cols;
-    int vec, vec_values;
 };
 
 // max over the 4 lanes of a block
@@ -60,11 +59,11 @@ template <int DT> __device__ __forceinline__ Eight<DT> from_codes(uint32_t c, ui
     return e;
 }
 
-template <int DT> __device__ __forceinline__ void store_values(typename Elem<DT>::type *p, const Eight<DT> &e, int left, bool vec)
+template <int DT> __device__ __forceinline__ void store_values(typename Elem<DT>::type *p, const Eight<DT> &e, int left)
 {
-    if (vec && left >= 8) {
+    if (left >= 8) {
 #pragma unroll
-        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) reinterpret_cast<u32x4 *>(p)[i] = e.q[i];
+        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) reinterpret_cast<u32x4_any *>(p)[i] = e.q[i];
         return;
     }
 #pragma unroll
@@ -86,7 +85,7 @@ template <int DT, bool VALUES> __global__ __launch_bounds__(kQuantThreads) void 
         row[j] = unit / a.per_row;
         at[j] = (unit - row[j] * a.per_row) * 8;
         const int left = unit < a.units ? a.cols - (int)at[j] : 0;
-        v[j] = load_values<DT>(static_cast<const T *>(a.x) + (left > 0 ? (long long)row[j] * a.ldx + at[j] : 0), left, a.vec != 0);
+        v[j] = load_values<DT>(static_cast<const T *>(a.x) + (left > 0 ? (long long)row[j] * a.ldx + at[j] : 0), left);
     }
 #pragma unroll
     for (int j = 0; j < kQuantEach; ++j) {
@@ -99,8 +98,7 @@ template <int DT, bool VALUES> __global__ __launch_bounds__(kQuantThreads) void 
         if constexpr (VALUES) {
             const int left = a.cols - (int)at[j];
             if (left > 0)
-                store_values<DT>(static_cast<T *>(a.values) + (long long)row[j] * a.cols + at[j], from_codes<DT>(c, byte), left,
-                                 a.vec_values != 0);
+                store_values<DT>(static_cast<T *>(a.values) + (long long)row[j] * a.cols + at[j], from_codes<DT>(c, byte), left);
         }
     }
 }
@@ -129,8 +127,6 @@ hipError_t mx4_quantize_rows(hipStream_t s, long long rows, int cols, int dtype,
         a.units = (uint32_t)(n * per_row);
         a.per_row = (uint32_t)per_row;
         a.cols = cols;
-        a.vec = (uintptr_t)a.x % 16 == 0 && ldx * es % 16 == 0;
-        a.vec_values = (uintptr_t)a.values % 16 == 0 && (long long)cols * es % 16 == 0;
         switch (dtype) {
         case BCONV_F32: launch_quantize<BCONV_F32>(a, s); break;
         case BCONV_F16: launch_quantize<BCONV_F16>(a, s); break;
