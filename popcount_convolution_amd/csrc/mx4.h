@@ -127,9 +127,80 @@ template <int S> __device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, uint32_t sa,
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a8, b8, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
+// D += A B over 64 k of 32 x 32 results, with byte `S` of the scale operands.
+__device__ __forceinline__ f32x16 mfma_mx4_32(int S, u32x4 a, uint32_t sa, u32x4 b, uint32_t sb, f32x16 c)
+{
+    const i32x8 a8 = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    const i32x8 b8 = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+    switch (S) {  // known where it is called
+    case 0: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 0, (int)sa, 0, (int)sb);
+    case 1: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 1, (int)sa, 1, (int)sb);
+    case 2: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 2, (int)sa, 2, (int)sb);
+    default: return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a8, b8, c, 4, 4, 3, (int)sa, 3, (int)sb);
+    }
+}
+
+// Result rows [begin, end) of expert f; f = experts: those of none.
+struct Span {
+    int begin, end;
+};
+
+__device__ __forceinline__ Span expert_rows(const int *offsets, int experts, int rows, int f)
+{
+    auto inside = [&](int o) { return o < 0 ? 0 : o > rows ? rows : o; };
+    return {inside(offsets[f]), f < experts ? inside(offsets[f + 1]) : rows};
+}
+
+// The rows that a workgroup of a product takes: of expert f (experts: of none).
+struct RowBlock {
+    int f, begin, end, unused;
+};
+
+// Rows of all experts in blocks of up to `size`, expert by expert, those of none
+// last: list[0].f is their number, they follow (at most ceil(rows / size) + experts + 1).
+struct RowBlocks {
+    const int *offsets;
+    RowBlock *list;  // or nullptr: none is wanted
+    int experts, rows, size;
+};
+
+constexpr int kListThreads = 256;
+
+// By one workgroup; a thread takes consecutive experts.
+__device__ __forceinline__ void make_row_blocks(const RowBlocks &b)
+{
+    __shared__ int sums[kListThreads / 64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int each = b.experts / kListThreads + 1, f0 = threadIdx.x * each;
+    int count = 0;
+    for (int f = f0; f < f0 + each && f <= b.experts; ++f) {
+        const Span s = expert_rows(b.offsets, b.experts, b.rows, f);
+        count += s.end > s.begin ? (s.end - s.begin + b.size - 1) / b.size : 0;
+    }
+    int upto = count;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+        const int u = __shfl_up(upto, d);
+        if (lane >= d) upto += u;
+    }
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    int at = upto - count;
+    for (int w = 0; w < wave; ++w) at += sums[w];
+    for (int f = f0; f < f0 + each && f <= b.experts; ++f) {
+        const Span s = expert_rows(b.offsets, b.experts, b.rows, f);
+        for (int r = s.begin; r < s.end; r += b.size) {
+            ++at;
+            b.list[at] = {f, r, s.end - r < b.size ? s.end : r + b.size, 0};
+        }
+    }
+    if (threadIdx.x == kListThreads - 1) b.list[0].f = at;
+}
+
 // Launches the quantisation of rows (see bconv_mx4_quantize); arguments are
-// checked by the caller. 
+// checked by the caller.  The 8 scales of a row's step are together, `srow`
+// bytes from the next row's, `sstep` from the next step's.  One more workgroup makes `blocks`.
 hipError_t mx4_quantize_rows(hipStream_t s, long long rows, int cols, int dtype, const void *x, long long ldx,
-                             uint8_t *codes, uint8_t *scales, void *values);
+                             uint8_t *codes, uint8_t *scales, long long srow, long long sstep, void *values, const RowBlocks &blocks);
 
 }  // namespace bconv

@@ -9,6 +9,7 @@
 #include <hip/hip_runtime.h>
 
 #include <new>
+#include <type_traits>
 
 #include "host.h"
 #include "mx4.h"
@@ -16,13 +17,14 @@
 namespace bconv {
 
 // A layer's weights: [experts][tiles][steps][2][64 lanes][16 bytes], scales
-// [experts][tiles][steps][64 lanes][2 bytes].
+// [experts][tiles][steps][16 outputs][8 blocks].
 struct Mx4Args {
     const u32x4 *codes;
-    const uint16_t *scales;
+    const uint8_t *scales;
     const float *bias;       // [experts][n] or nullptr
     const void *x;           // elements, or nullptr
-    const uint8_t *xc, *xs;  // quantised rows
+    const uint8_t *xc, *xs;  // quantised rows; the scales of a row's step are 8 bytes,
+    long long xs_row, xs_step;  // this far from the next row's and step's
     void *y;
     const int *offsets, *order;
     long long ldx, ldy;
@@ -63,31 +65,20 @@ __global__ void mx4_prepack_scales_kernel(const uint8_t *user, uint8_t *scales, 
     long long id = first + (long long)blockIdx.x * blockDim.x + threadIdx.x;
     if (id >= total) return;
     uint8_t *to = scales + id;
-    const int i = (int)(id & 1), lane = (int)(id >> 1) & 63;
+    const int block = (int)(id & 7), r = (int)(id >> 3) & 15;
     id >>= 7;
     const int step = (int)(id % steps);
     id /= steps;
     const int tile = (int)(id % tiles);
     const long long f = id / tiles;
-    const int o = tile * 16 + (lane & 15), b = step * (kStep / 32) + (lane >> 4) * 2 + i, blocks = (k + 31) / 32;
+    const int o = tile * 16 + r, b = step * (kStep / 32) + block, blocks = (k + 31) / 32;
     *to = o < n && b < blocks ? user[(f * n + o) * blocks + b] : 0;
-}
-
-// Result rows [begin, end) of expert f; of f = experts: those of none.
-struct Span {
-    int begin, end;
-};
-
-__device__ __forceinline__ int clamped_offset(const Mx4Args &a, int f)
-{
-    const int o = a.offsets[f];
-    return o < 0 ? 0 : o > a.rows ? a.rows : o;
 }
 
 __device__ __forceinline__ Span expert_span(const Mx4Args &a, int f)
 {
     if (!a.offsets) return {0, a.rows};
-    return {clamped_offset(a, f), f < a.experts ? clamped_offset(a, f + 1) : a.rows};
+    return expert_rows(a.offsets, a.experts, a.rows, f);
 }
 
 // Input row of result row i (i < rows).
@@ -151,21 +142,21 @@ template <int DT> __device__ __forceinline__ XStep quantised_step(const typename
     return x;
 }
 
-// Few rows of x for the weights.  A workgroup takes 16 RT outputs of one expert and its rows
-// 16 at a time; its waves split the inputs step by step and add their sums in LDS, in
-// a fixed order.
-template <int DT, bool QUANTISED, int RT, int WAVES>
+// Few rows of x for the weights.  A workgroup takes 16 RT outputs of one expert and
+// its rows 16 CT at a time; its waves split the inputs step by step and add their
+// sums in LDS, in a fixed order.
+template <int DT, bool QUANTISED, int RT, int CT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
 {
     typedef typename Elem<DT>::type T;
-    __shared__ f32x4 part[WAVES][RT][64];
+    __shared__ f32x4 part[WAVES][RT * CT][64];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tile0 = blockIdx.x * RT, row = lane & 15, lg = lane >> 4;
     const int f = a.offsets ? blockIdx.y : 0;
     Span span = expert_span(a, f);
-    if (!a.offsets) {  // blockIdx.y counts 16 rows
-        span.begin = blockIdx.y * 16;
-        if (span.end > span.begin + 16) span.end = span.begin + 16;
+    if (!a.offsets) {  // blockIdx.y counts blocks of rows
+        span.begin = blockIdx.y * (16 * CT);
+        if (span.end > span.begin + 16 * CT) span.end = span.begin + 16 * CT;
     }
     if (f == a.experts) {  // rows of no expert
         for (int e = span.begin * RT * 4 + (int)threadIdx.x; e < span.end * RT * 4; e += WAVES * 64) {
@@ -176,19 +167,24 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
         }
         return;
     }
-    for (int m0 = span.begin; m0 < span.end; m0 += 16) {
-        const bool real = m0 + row < span.end;
-        const long long xr = real ? input_row(a, m0 + row) : 0;
-        f32x4 acc[RT];
-        long long first[RT];
+    long long first[RT];
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            acc[r] = f32x4{0, 0, 0, 0};
-            first[r] = ((long long)f * a.tiles + (tile0 + r < a.tiles ? tile0 + r : a.tiles - 1)) * a.steps;
-        }
+    for (int r = 0; r < RT; ++r) first[r] = ((long long)f * a.tiles + (tile0 + r < a.tiles ? tile0 + r : a.tiles - 1)) * a.steps;
+    for (int m0 = span.begin; m0 < span.end; m0 += 16 * CT) {
+        f32x4 acc[RT][CT];
         // Lanes of columns past the last row load nothing: their operands stay 0,
         // and their results are not stored.
-        XStep x = {{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}}, 0};
+        XStep x[CT];
+        long long xr[CT];
+        bool real[CT];
+#pragma unroll
+        for (int t = 0; t < CT; ++t) {
+            real[t] = m0 + t * 16 + row < span.end;
+            xr[t] = real[t] ? input_row(a, m0 + t * 16 + row) : 0;
+            x[t] = {{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}}, 0};
+#pragma unroll
+            for (int r = 0; r < RT; ++r) acc[r][t] = f32x4{0, 0, 0, 0};
+        }
         for (int c = wave; c < a.steps; c += WAVES) {
             u32x4 w[RT][2];
             uint32_t ws[RT];
@@ -196,34 +192,42 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
             for (int r = 0; r < RT; ++r) {
                 w[r][0] = a.codes[(first[r] + c) * 128 + lane];
                 w[r][1] = a.codes[(first[r] + c) * 128 + 64 + lane];
-                ws[r] = a.scales[(first[r] + c) * 64 + lane];
+                ws[r] = *reinterpret_cast<const uint16_t *>(a.scales + (first[r] + c) * 128 + row * 8 + lg * 2);
             }
-            if (real) {
-                if constexpr (QUANTISED) {
-                    const u32x4 *p = reinterpret_cast<const u32x4 *>(a.xc + (xr * a.steps + c) * (kStep / 2) + lg * 32);
-                    x.c[0] = p[0];
-                    x.c[1] = p[1];
-                    x.s = *reinterpret_cast<const uint16_t *>(a.xs + (xr * a.steps + c) * (kStep / 32) + lg * 2);
-                } else {
-                    const int k0 = c * kStep + lg * 64;
-                    x = quantised_step<DT>(static_cast<const T *>(a.x) + xr * a.ldx + k0, a.k - k0);
+#pragma unroll
+            for (int t = 0; t < CT; ++t)
+                if (real[t]) {
+                    if constexpr (QUANTISED) {
+                        const u32x4 *p = reinterpret_cast<const u32x4 *>(a.xc + (xr[t] * a.steps + c) * (kStep / 2) + lg * 32);
+                        x[t].c[0] = p[0];
+                        x[t].c[1] = p[1];
+                        x[t].s = *reinterpret_cast<const uint16_t *>(a.xs + xr[t] * a.xs_row + c * a.xs_step + lg * 2);
+                    } else {
+                        const int k0 = c * kStep + lg * 64;
+                        x[t] = quantised_step<DT>(static_cast<const T *>(a.x) + xr[t] * a.ldx + k0, a.k - k0);
+                    }
                 }
-            }
 #pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r] = mfma_mx4<0>(w[r][0], ws[r], x.c[0], x.s, acc[r]);
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int r = 0; r < RT; ++r) acc[r] = mfma_mx4<1>(w[r][1], ws[r], x.c[1], x.s, acc[r]);
+                for (int r = 0; r < RT; ++r)
+#pragma unroll
+                    for (int t = 0; t < CT; ++t)
+                        acc[r][t] = i ? mfma_mx4<1>(w[r][1], ws[r], x[t].c[1], x[t].s, acc[r][t])
+                                      : mfma_mx4<0>(w[r][0], ws[r], x[t].c[0], x[t].s, acc[r][t]);
         }
 #pragma unroll
-        for (int r = 0; r < RT; ++r) part[wave][r][lane] = acc[r];
-        __syncthreads();
-        for (int e = threadIdx.x; e < RT * 64; e += WAVES * 64) {
-            const int l = e & 63, r = e >> 6;
-            const int i = m0 + (l & 15), o0 = (tile0 + r) * 16 + (l >> 4) * 4;
-            if (i >= span.end || o0 >= a.n) continue;
-            f32x4 v = part[0][r][l];
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int w = 1; w < WAVES; ++w) v += part[w][r][l];
+            for (int t = 0; t < CT; ++t) part[wave][r * CT + t][lane] = acc[r][t];
+        __syncthreads();
+        for (int e = threadIdx.x; e < RT * CT * 64; e += WAVES * 64) {
+            const int l = e & 63, u = e >> 6;
+            const int i = m0 + u % CT * 16 + (l & 15), o0 = (tile0 + u / CT) * 16 + (l >> 4) * 4;
+            if (i >= span.end || o0 >= a.n) continue;
+            f32x4 v = part[0][u][l];
+#pragma unroll
+            for (int w = 1; w < WAVES; ++w) v += part[w][u][l];
             store_four<DT>(a, f, i, o0, v);
         }
         __syncthreads();
@@ -235,81 +239,71 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
 // What the many-row kernel takes besides Mx4Args.
 struct Mx4Many {
     float *sums;  // [splits][rows][padded_n], or nullptr for one split
+    const RowBlock *row_list;  // with experts: what make_row_blocks() makes
     int row_blocks, out_blocks, splits;
     int padded_n;
 };
 
-// The row block `rb` of the launch: its expert and rows.  Experts' blocks follow each other,
-// those of the rows of no expert come last; f is -1 behind them.
-template <int R> __device__ __forceinline__ int find_rows(const Mx4Args &a, int rb, Span &span)
+// The list of row blocks, where no other launch makes it.
+__global__ __launch_bounds__(kListThreads) void mx4_blocks_kernel(RowBlocks b) { make_row_blocks(b); }
+
+template <typename E> struct Values {
+    E v[16 / sizeof(E)];
+};
+
+// s_waitcnt for vector memory alone (and LDS): at most `n` loads outstanding.
+constexpr int vm_wait(int n) { return (n & 15) | (n >> 4 << 14) | (0x7 << 4) | (0x0 << 8); }
+
+constexpr uint32_t kNone = 0x80000000u;  // outside every buffer: a load from there reads no memory and gives 0
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t whole_buffer(const void *p)
 {
-    if (!a.offsets) {
-        span.begin = rb * R;
-        span.end = a.rows - span.begin < R ? a.rows : span.begin + R;
-        return 0;
-    }
-    const int lane = threadIdx.x & 63;
-    int before = 0;  // blocks of the experts before these 64
-    for (int f0 = 0; f0 <= a.experts; f0 += 64) {
-        const int f = f0 + lane;
-        const Span s = f <= a.experts ? expert_span(a, f) : Span{0, 0};
-        const int blocks = s.end > s.begin ? (s.end - s.begin + R - 1) / R : 0;
-        int upto = blocks;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) {
-            const int u = __shfl_up(upto, d);
-            if (lane >= d) upto += u;
-        }
-        const unsigned long long past = __ballot(before + upto > rb);
-        if (past) {
-            const int l = __builtin_ctzll(past);
-            span.begin = __builtin_amdgcn_readlane(s.begin, l) + (rb - before - __builtin_amdgcn_readlane(upto - blocks, l)) * R;
-            span.end = __builtin_amdgcn_readlane(s.end, l);
-            if (span.end - span.begin > R) span.end = span.begin + R;
-            return f0 + l;
-        }
-        before += __builtin_amdgcn_readlane(upto, 63);
-    }
-    return -1;
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, kNone - 1, 0x00020000);
 }
 
-// A workgroup of WM x WN waves takes 16 WM MT rows of x and 16 WN NT outputs; a step
-// of both (128 bytes a row) goes to LDS a step ahead, by loads that pass no registers.
-template <int DT, int WM, int WN, int MT, int NT>
-__global__ __launch_bounds__(WM * WN * 64, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
+template <int DT, int MT, int NT, int WD>
+__global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
 {
     typedef typename Elem<DT>::type T;
-    constexpr int WAVES = WM * WN, R = WM * MT * 16, OT = WN * NT;  // rows of x, output tiles
-    constexpr int XL = R / 8 / WAVES, WL = OT * 2 / WAVES;         // 1 KiB loads a wave
-    static_assert(XL * WAVES * 8 == R && WL * WAVES == OT * 2);
+    constexpr int WAVES = 4, STAGES = 4, R = MT * 32, OT = WAVES * NT * 2;  // rows of x, tiles of 16 outputs
+    constexpr int XL = R / 8 / WAVES, XV = XL + 1, WV = 5 * NT;  // loads of a step: x and its scales, weights and theirs
     struct Stage {
-        u32x4 x[R * 8];    // [row][slot], block b of a step in slot b ^ (row >> 1 & 7)
-        u32x4 w[OT * 128]; // [tile][instruction][lane]
+        u32x4 x[R * 8];        // [row][slot], block b of a step in slot b ^ (row >> 1 & 7)
+        uint32_t xs[R * 2];    // [row][half]
     };
-    __shared__ Stage stage[2];
+    __shared__ union {
+        Stage stage[STAGES];
+        char out[4096 * WAVES];  // results on their way out
+    } lds;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int row = lane & 15, lg = lane >> 4;
+    const int row = lane & 31, half = lane >> 5;
 
     // Workgroups go to the XCDs in turn; each takes a run of neighbouring blocks.
-    const int total = gridDim.x;
+    const int row_blocks = q.row_list ? q.row_list[0].f : q.row_blocks;
+    const int total = row_blocks * q.out_blocks * q.splits;
     int id = blockIdx.x;
+    if (id >= total) return;
     {
         const int xcd = id & 7, each = total >> 3, more = total & 7;
         id = xcd * each + (xcd < more ? xcd : more) + (id >> 3);
     }
-    const int blocks = q.row_blocks * q.out_blocks;
+    const int blocks = row_blocks * q.out_blocks;
     const int split = id / blocks;
     id -= split * blocks;
-    constexpr int kGroup = 8;
+    constexpr int kGroup = 16;
     const int group = id / (kGroup * q.out_blocks), g0 = group * kGroup;
-    const int high = q.row_blocks - g0 < kGroup ? q.row_blocks - g0 : kGroup;
+    const int high = row_blocks - g0 < kGroup ? row_blocks - g0 : kGroup;
     id -= group * kGroup * q.out_blocks;
     const int rb = g0 + id % high, ob = id / high;
     const int tile0 = ob * OT;
 
-    Span span;
-    const int f = find_rows<R>(a, rb, span);
-    if (f < 0) return;
+    Span span = {rb * R, min(rb * R + R, a.rows)};
+    int f = 0;
+    if (q.row_list) {
+        const RowBlock b = q.row_list[1 + rb];
+        f = b.f;
+        span = {b.begin, b.end};
+    }
     if (f == a.experts) {  // rows of no expert
         for (int e = threadIdx.x; e < (span.end - span.begin) * OT * 16; e += WAVES * 64) {
             const int o = tile0 * 16 + e % (OT * 16);
@@ -317,87 +311,196 @@ __global__ __launch_bounds__(WM * WN * 64, 2) void mx4_many_kernel(Mx4Args a, Mx
         }
         return;
     }
-    const int s_begin = (int)((long long)a.steps * split / q.splits), s_end = (int)((long long)a.steps * (split + 1) / q.splits);
+    const int s_begin = __builtin_amdgcn_readfirstlane((int)((long long)a.steps * split / q.splits));
+    const int s_end = __builtin_amdgcn_readfirstlane((int)((long long)a.steps * (split + 1) / q.splits));
 
-    // where this lane's part of the loads comes from: rows past the last count as the last
-    auto x_row = [&](int r) { return (uint32_t)input_row(a, min(span.begin + r, span.end - 1)); };
-    const uint8_t *xp[XL];
+    // Where this lane's part of the loads comes from: rows and tiles past the last
+    // count as the last.  Offsets stay below kNone.
+    const long long x_base = a.choices ? 0 : span.begin;
+    auto x_row = [&](int r) { return (uint32_t)(input_row(a, min(span.begin + r, span.end - 1)) - x_base); };
+    uint32_t xo[XL], xso, wo[NT], wso[NT];
 #pragma unroll
     for (int j = 0; j < XL; ++j) {
         const int r = (j * WAVES + wave) * 8 + (lane >> 3);
-        xp[j] = a.xc + (unsigned long long)x_row(r) * a.steps * 128 + ((lane & 7) ^ (r >> 1 & 7)) * 16;
+        xo[j] = x_row(r) * a.steps * 128 + ((lane & 7) ^ (r >> 1 & 7)) * 16;
     }
-    const u32x4 *wp[WL];
+    const int my_scales = wave % MT * 32;  // with few rows, several waves load the same
+    xso = (uint32_t)(x_row(my_scales + (lane >> 1)) * a.xs_row + (lane & 1) * 4);
+    const int my_tile = tile0 + wave * NT * 2;
 #pragma unroll
-    for (int j = 0; j < WL; ++j) {
-        const int u = j * WAVES + wave, tile = min(tile0 + (u >> 1), a.tiles - 1);
-        wp[j] = a.codes + (((long long)f * a.tiles + tile) * a.steps * 2 + (u & 1)) * 64 + lane;
+    for (int t = 0; t < NT; ++t) {
+        const uint32_t tile = min(my_tile + t * 2 + (row >> 4), a.tiles - 1) - tile0;
+        wo[t] = tile * a.steps * 2048 + half * 512 + (row & 15) * 16;
+        wso[t] = tile * a.steps * 128 + (row & 15) * 8 + half * 4;
     }
-    const int my_x = wave / WN * MT * 16, my_tile = wave % WN * NT;
-    uint32_t xs_at[MT];
-    const uint16_t *ws_at[NT];
-#pragma unroll
-    for (int m = 0; m < MT; ++m) xs_at[m] = x_row(my_x + m * 16 + row) * a.steps * 8 + lg * 2;
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-        ws_at[t] = a.scales + ((long long)f * a.tiles + min(tile0 + my_tile + t, a.tiles - 1)) * a.steps * 64 + lane;
+    const long long first_tile = (long long)f * a.tiles + tile0;
+    const __amdgpu_buffer_rsrc_t rxc = whole_buffer(a.xc + x_base * a.steps * 128), rxs = whole_buffer(a.xs + x_base * a.xs_row);
+    const __amdgpu_buffer_rsrc_t rwc = whole_buffer(a.codes + first_tile * a.steps * 128);
+    const __amdgpu_buffer_rsrc_t rws = whole_buffer(a.scales + first_tile * a.steps * 128);
+    const int xs_step = __builtin_amdgcn_readfirstlane((int)a.xs_step);
 
     typedef __attribute__((address_space(3))) void *Lds;
-    uint32_t xs[MT], ws[NT], xn[MT], wn[NT];
-    auto request = [&](int s) {
-        Stage &st = stage[s & 1];
-#pragma unroll
-        for (int j = 0; j < XL; ++j)
-            __builtin_amdgcn_global_load_lds((const void *)(xp[j] + (long long)s * 128), (Lds)(&st.x[(j * WAVES + wave) * 64]), 16, 0, 0);
-#pragma unroll
-        for (int j = 0; j < WL; ++j)
-            __builtin_amdgcn_global_load_lds((const void *)(wp[j] + (long long)s * 128), (Lds)(&st.w[(j * WAVES + wave) * 64]), 16, 0, 0);
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xn[m] = *reinterpret_cast<const uint16_t *>(a.xs + (size_t)s * 8 + xs_at[m]);
-#pragma unroll
-        for (int t = 0; t < NT; ++t) wn[t] = ws_at[t][s * 64];
+    auto request_x = [&](int s, int slot, int l) {  // one of XV
+        Stage &st = lds.stage[slot];
+        const uint32_t none = s < s_end ? 0 : kNone;
+        if (l == 0)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (Lds)(&st.xs[my_scales * 2]), 4, (int)(xso | none), s * xs_step, 0, 0);
+        else
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rxc, (Lds)(&st.x[((l - 1) * WAVES + wave) * 64]), 16, (int)(xo[l - 1] | none), s * 128, 0, 0);
     };
-    f32x4 acc[MT][NT];
+    u32x4 w[WD + 1][4][NT];
+    uint32_t ws[WD + 1][NT];
+    auto request_w = [&](int s, int set, int l) {  // one of WV
+        const uint32_t none = s < s_end ? 0 : kNone;
+        if (l < NT) ws[set][l] = __builtin_amdgcn_raw_buffer_load_b32(rws, (int)(wso[l] | none), s * 128, 0);
+        else {
+            const int i = (l - NT) / NT, t = (l - NT) % NT;
+            w[set][i][t] = __builtin_amdgcn_raw_buffer_load_b128(rwc, (int)(wo[t] | none), s * 2048 + (i & 1) * 1024 + (i >> 1) * 256, 0);
+        }
+    };
+    f32x16 acc[MT][NT];
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int t = 0; t < NT; ++t) acc[m][t] = f32x4{0, 0, 0, 0};
-    if (s_begin < s_end) request(s_begin);
-    for (int s = s_begin; s < s_end; ++s) {
-        __builtin_amdgcn_s_waitcnt(0 | (0x7 << 4) | (0xf << 8));  // vmcnt(0): this step's operands are here
-        __syncthreads();                                          // in every wave, and the other stage is read
+        for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int m = 0; m < MT; ++m) xs[m] = xn[m];
+            for (int i = 0; i < 16; ++i) acc[m][t][i] = 0.0f;
+    u32x4 x[2][MT];
+    uint32_t xs[2][MT];
+    auto fetch = [&](int slot, int i, int m) {
+        const int r = m * 32 + row;
+        x[i & 1][m] = lds.stage[slot].x[r * 8 + ((4 * half + i) ^ (r >> 1 & 7))];
+    };
+    auto fetch_scale = [&](int slot, int m) { xs[slot & 1][m] = lds.stage[slot].xs[(m * 32 + row) * 2 + half]; };
+    // Step s, whose x is in stage `at` = (s - s_begin) % 4; x of s + 3 and weights of s + WD are requested.
+    auto step = [&](int s, auto AT) {
+        constexpr int at = decltype(AT)::value, next = (at + 1) & 3;
+        constexpr int V = WV + XV, P = MT * NT;  // loads, instructions a phase
 #pragma unroll
-        for (int t = 0; t < NT; ++t) ws[t] = wn[t];
-        if (s + 1 < s_end) request(s + 1);
-        const Stage &st = stage[s & 1];
+        for (int i = 0; i < 4; ++i) {
+            if (i == 3) {
+                // x of the next step is here: all loads but those after it are done
+                __builtin_amdgcn_s_waitcnt(vm_wait((STAGES - 2) * V));
+                __builtin_amdgcn_s_barrier();
+                __builtin_amdgcn_sched_barrier(0);
+            }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            u32x4 w[NT];
+            for (int p = 0; p < P; ++p) {
+                const int m = p / NT, t = p % NT;
+                if (t == 0) {
+                    if (i < 3) fetch(at, i + 1, m);
+                    else {
+                        fetch_scale(next, m);
+                        fetch(next, 0, m);
+                    }
+                }
+                if (i < 3) {
+                    // the loads spread over three phases
 #pragma unroll
-            for (int t = 0; t < NT; ++t) w[t] = st.w[((my_tile + t) * 2 + i) * 64 + lane];
-#pragma unroll
-            for (int m = 0; m < MT; ++m) {
-                const int r = my_x + m * 16 + row;
-                const u32x4 x = st.x[r * 8 + ((2 * lg + i) ^ (r >> 1 & 7))];
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-                    acc[m][t] = i ? mfma_mx4<1>(w[t], ws[t], x, xs[m], acc[m][t]) : mfma_mx4<0>(w[t], ws[t], x, xs[m], acc[m][t]);
+                    for (int l = 0; l < V; ++l)
+                        if (l * 3 * P / V == i * P + p) {
+                            if (l < WV) request_w(s + WD, (at + WD) % (WD + 1), l);
+                            else request_x(s + STAGES - 1, (at + STAGES - 1) & 3, l - WV);
+                        }
+                }
+                acc[m][t] = mfma_mx4_32(i, w[at % (WD + 1)][i][t], ws[at % (WD + 1)][t], x[i & 1][m], xs[at & 1][m], acc[m][t]);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
-    }
+    };
+    static_assert(4 % (WD + 1) == 0 && (STAGES - 2) * (WV + XV) < 64);
+#pragma unroll
+    for (int d = 0; d < STAGES - 1; ++d)
+#pragma unroll
+        for (int l = 0; l < XV; ++l) request_x(s_begin + d, d, l);
+#pragma unroll
+    for (int d = 0; d < WD; ++d)
+#pragma unroll
+        for (int l = 0; l < WV; ++l) request_w(s_begin + d, d, l);
+    __builtin_amdgcn_s_waitcnt(vm_wait(WD * WV));  // x of three steps is here
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-        const int i = span.begin + my_x + m * 16 + row;
-        if (i >= span.end) continue;
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            const int o0 = (tile0 + my_tile + t) * 16 + lg * 4;
-            if (q.splits > 1)
-                *reinterpret_cast<f32x4 *>(q.sums + ((long long)split * a.rows + i) * q.padded_n + o0) = acc[m][t];
-            else if (o0 < a.n) store_four<DT>(a, f, i, o0, acc[m][t]);
+        fetch_scale(0, m);
+        fetch(0, 0, m);
+    }
+    int s = s_begin;
+    for (; s + 4 <= s_end; s += 4) {
+        step(s, std::integral_constant<int, 0>());
+        step(s + 1, std::integral_constant<int, 1>());
+        step(s + 2, std::integral_constant<int, 2>());
+        step(s + 3, std::integral_constant<int, 3>());
+    }
+    if (s < s_end) {
+        step(s, std::integral_constant<int, 0>());
+        if (s + 1 < s_end) {
+            step(s + 1, std::integral_constant<int, 1>());
+            if (s + 2 < s_end) step(s + 2, std::integral_constant<int, 2>());
         }
+    }
+    __builtin_amdgcn_s_waitcnt(vm_wait(0));  // nothing is on its way to LDS any more,
+    __builtin_amdgcn_s_barrier();            // of any wave
+    // Results through LDS, 32 rows of up to 128 bytes a wave at a time, so that they leave as whole lines.
+    const int y0 = my_tile * 16;  // the wave's first output
+    char *out = lds.out + wave * 4096;
+    auto emit = [&](auto TYPE, auto &result, char *to, long long ld, int n) {
+        typedef decltype(TYPE) E;
+        constexpr int TT = sizeof(E) == 2 ? NT : 1, CH = TT * 2 * (int)sizeof(E);  // blocks of 32 outputs, 16-byte pieces a row
+        constexpr int PER = 16 / (int)sizeof(E);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int t0 = 0; t0 < NT; t0 += TT) {
+#pragma unroll
+                for (int t = 0; t < TT; ++t)
+#pragma unroll
+                    for (int v = 0; v < 4; ++v) {  // results 4 v + j are outputs 8 v + 4 half + j of the 32
+                        const f32x4 r = result(m, t0 + t, v);
+                        typedef E E4 __attribute__((ext_vector_type(4)));
+                        const E4 e = {(E)r[0], (E)r[1], (E)r[2], (E)r[3]};
+                        const int at = (t * 32 + v * 8 + half * 4) * (int)sizeof(E);
+                        *reinterpret_cast<E4 *>(out + row * (CH * 16) + (((at >> 4) ^ row) & (CH - 1)) * 16 + (at & 15)) = e;
+                    }
+                __builtin_amdgcn_wave_barrier();
+#pragma unroll
+                for (int k = 0; k < CH / 2; ++k) {
+                    const int r = k * (64 / CH) + lane / CH, c = lane % CH;
+                    const u32x4 e = *reinterpret_cast<const u32x4 *>(out + r * (CH * 16) + ((c ^ r) & (CH - 1)) * 16);
+                    const int i = m * 32 + r, o = y0 + t0 * 32 + c * PER;
+                    if (span.begin + i >= span.end) continue;
+                    char *p = to + ((long long)i * ld + o) * (int)sizeof(E);
+                    if (o + PER <= n) *reinterpret_cast<u32x4_any *>(p) = e;
+                    else
+#pragma unroll
+                        for (int x = 0; x < PER; ++x)
+                            if (o + x < n) reinterpret_cast<E *>(p)[x] = __builtin_bit_cast(Values<E>, e).v[x];
+                }
+                __builtin_amdgcn_wave_barrier();
+            }
+    };
+    if (q.splits > 1) {
+        auto plain = [&](int m, int t, int v) {
+            return f32x4{acc[m][t][4 * v], acc[m][t][4 * v + 1], acc[m][t][4 * v + 2], acc[m][t][4 * v + 3]};
+        };
+        emit(0.0f, plain, reinterpret_cast<char *>(q.sums + ((long long)split * a.rows + span.begin) * q.padded_n), q.padded_n, q.padded_n);
+    } else {
+        f32x4 bias[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+                const int o = y0 + t * 32 + v * 8 + half * 4;
+                bias[t][v] = f32x4{0, 0, 0, 0};
+                if (a.bias)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (o + j < a.n) bias[t][v][j] = a.bias[(long long)f * a.n + o + j];
+            }
+        auto biased = [&](int m, int t, int v) {
+            return f32x4{acc[m][t][4 * v], acc[m][t][4 * v + 1], acc[m][t][4 * v + 2], acc[m][t][4 * v + 3]} + bias[t][v];
+        };
+        emit(T(), biased, reinterpret_cast<char *>(static_cast<T *>(a.y) + (long long)span.begin * a.ldy), a.ldy, a.n);
     }
 }
 
@@ -419,56 +522,81 @@ template <int DT> __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args
 
 struct Mx4Plan {
     bool quantise;  // x is quantised by a launch of its own
-    int shape;      // 0: few rows; rows of x of the many-row kernel's workgroup
+    int many;       // rows of x a workgroup of the many-row kernel takes; 0: the few-row kernel
+    int nt;         // many: blocks of 32 outputs a wave
+    int rt, ct, waves;  // few
     Mx4Many q;
-    size_t scales_offset, sums_offset, bytes;
+    size_t scales_offset, list_offset, sums_offset, bytes;
 };
 
 Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
 {
     Mx4Plan p{};
-    auto up = [](size_t v) { return (v + 255) / 256 * 256; };
     const int mean = a.rows / a.experts;
-    p.shape = mean > 512 ? 256 : mean > 16 ? 128 : 0;
-    p.quantise = !given && (a.rows > 4 || p.shape);
+    p.many = mean > 16 ? 128 : 0;
+    p.quantise = !given && (p.many || a.rows > 4);
+    auto take = [&](size_t n) {
+        const size_t at = p.bytes;
+        p.bytes += (n + 255) / 256 * 256;
+        return at;
+    };
     if (p.quantise) {
-        p.scales_offset = (size_t)a.x_rows * a.steps * (kStep / 2);
-        p.bytes = p.sums_offset = up(p.scales_offset + (size_t)a.x_rows * a.steps * (kStep / 32));
+        take((size_t)a.x_rows * a.steps * (kStep / 2));
+        p.scales_offset = take((size_t)a.x_rows * a.steps * (kStep / 32));
     }
-    if (p.shape) {
-        const int out_tiles = p.shape / 16;
-        p.q.row_blocks = (a.rows + p.shape - 1) / p.shape + (a.offsets ? a.experts : 0);
-        p.q.out_blocks = (a.tiles + out_tiles - 1) / out_tiles;
-        p.q.padded_n = p.q.out_blocks * p.shape;
-        p.q.splits = 1;
-        if (!a.offsets) {
-            const long long blocks = (long long)p.q.row_blocks * p.q.out_blocks;
-            long long splits = (2LL * cus) / blocks;
-            if (splits > 8) splits = 8;
-            if (splits > a.steps / 4) splits = a.steps / 4;
-            p.q.splits = splits < 1 ? 1 : (int)splits;
+    if (!p.many) {
+        p.rt = 2;
+        p.ct = 1;
+        p.waves = 8;
+        return p;
+    }
+    p.q.row_blocks = (a.rows + p.many - 1) / p.many + (a.offsets ? a.experts + 1 : 0);
+    const long long wide = (long long)p.q.row_blocks * ((a.tiles + 15) / 16);
+    p.nt = wide >= cus ? 2 : 1;
+    p.q.out_blocks = (a.tiles + p.nt * 8 - 1) / (p.nt * 8);
+    p.q.padded_n = p.q.out_blocks * p.nt * 128;
+    p.q.splits = 1;
+    if (a.offsets) {
+        p.list_offset = take((size_t)(p.q.row_blocks + 1) * sizeof(RowBlock));
+    } else {
+        long long splits = cus / ((long long)p.q.row_blocks * p.q.out_blocks);
+        if (splits > a.steps / 4) splits = a.steps / 4;
+        if (splits > 8) splits = 8;
+        if (splits > 1) {
+            p.q.splits = (int)splits;
+            p.sums_offset = take((size_t)splits * a.rows * p.q.padded_n * 4);
         }
-        if (p.q.splits > 1) p.bytes = p.sums_offset + (size_t)p.q.splits * a.rows * p.q.padded_n * 4;
     }
     return p;
 }
 
+// The list of row blocks that the plan needs.
+RowBlocks row_blocks(const Mx4Args &a, const Mx4Plan &p)
+{
+    return {a.offsets, const_cast<RowBlock *>(p.q.row_list), a.experts, a.rows, p.many};
+}
+
+template <int DT, bool QUANTISED, int RT, int CT, int WAVES> hipError_t run_few(const Mx4Args &a, hipStream_t s)
+{
+    const dim3 grid((a.tiles + RT - 1) / RT, a.offsets ? a.experts + 1 : (a.rows + 16 * CT - 1) / (16 * CT));
+    hipLaunchKernelGGL((mx4_few_kernel<DT, QUANTISED, RT, CT, WAVES>), grid, dim3(WAVES * 64), 0, s, a);
+    return hipGetLastError();
+}
+
 template <int DT> hipError_t run_mx4(const Mx4Args &a, const Mx4Plan &p, hipStream_t s)
 {
-    if (p.shape) {
+    if (p.many) {
         const dim3 grid((unsigned)((long long)p.q.row_blocks * p.q.out_blocks * p.q.splits));
-        if (p.shape == 256) hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 4, 8, 4>), grid, dim3(512), 0, s, a, p.q);
-        else hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 2, 4, 4>), grid, dim3(256), 0, s, a, p.q);
+        if (p.nt == 2) hipLaunchKernelGGL((mx4_many_kernel<DT, 4, 2, 1>), grid, dim3(256), 0, s, a, p.q);
+        else hipLaunchKernelGGL((mx4_many_kernel<DT, 4, 1, 3>), grid, dim3(256), 0, s, a, p.q);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.q.splits == 1) return e;
         const long long outs = (long long)((a.n + 3) / 4) * a.rows;
         hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
         return hipGetLastError();
     }
-    const dim3 grid((a.tiles + 1) / 2, a.offsets ? a.experts + 1 : (a.rows + 15) / 16);
-    if (a.x) hipLaunchKernelGGL((mx4_few_kernel<DT, false, 2, 8>), grid, dim3(512), 0, s, a);
-    else hipLaunchKernelGGL((mx4_few_kernel<DT, true, 2, 8>), grid, dim3(512), 0, s, a);
-    return hipGetLastError();
+    if (a.x) return run_few<DT, false, 2, 1, 8>(a, s);
+    return run_few<DT, true, 2, 1, 8>(a, s);
 }
 
 }  // namespace bconv
@@ -540,11 +668,13 @@ bconv::Mx4Args kernel_args(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
 {
     bconv::Mx4Args a{};
     a.codes = reinterpret_cast<const bconv::u32x4 *>(h->d_codes);
-    a.scales = reinterpret_cast<const uint16_t *>(h->d_scales);
+    a.scales = h->d_scales;
     a.bias = h->d_bias;
     a.x = args->x;
     a.xc = args->codes;
     a.xs = args->scales;
+    a.xs_row = h->steps * 8LL;
+    a.xs_step = 8;
     a.y = args->y;
     a.offsets = args->offsets;
     a.order = args->order;
@@ -666,15 +796,24 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
     if (guard.err != hipSuccess) return hip_fail(guard.err, "hipSetDevice");
     hipStream_t s = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
+    char *ws = static_cast<char *>(workspace);
+    p.q.sums = reinterpret_cast<float *>(ws + p.sums_offset);
+    if (p.many && a.offsets) p.q.row_list = reinterpret_cast<const bconv::RowBlock *>(ws + p.list_offset);
     if (p.quantise) {
         uint8_t *codes = static_cast<uint8_t *>(workspace);
-        e = bconv::mx4_quantize_rows(s, a.x_rows, k, args->dtype, a.x, a.ldx, codes, codes + p.scales_offset, nullptr);
+        a.xs_row = 8;
+        a.xs_step = a.x_rows * 8LL;
+        e = bconv::mx4_quantize_rows(s, a.x_rows, k, args->dtype, a.x, a.ldx, codes, codes + p.scales_offset, a.xs_row, a.xs_step,
+                                     nullptr, bconv::row_blocks(a, p));
         if (e != hipSuccess) return hip_fail(e, "mx4 quantisation kernel");
         a.x = nullptr;
         a.xc = codes;
         a.xs = codes + p.scales_offset;
+    } else if (p.q.row_list) {
+        hipLaunchKernelGGL(bconv::mx4_blocks_kernel, dim3(1), dim3(bconv::kListThreads), 0, s, bconv::row_blocks(a, p));
+        e = hipGetLastError();
+        if (e != hipSuccess) return hip_fail(e, "mx4 row block kernel");
     }
-    p.q.sums = reinterpret_cast<float *>(static_cast<char *>(workspace) + p.sums_offset);
     switch (args->dtype) {
     case BCONV_F32: e = bconv::run_mx4<BCONV_F32>(a, p, s); break;
     case BCONV_F16: e = bconv::run_mx4<BCONV_F16>(a, p, s); break;

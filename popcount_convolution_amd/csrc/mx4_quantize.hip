@@ -12,6 +12,7 @@
 namespace bconv {
 
 constexpr int kQuantThreads = 256;
+static_assert(kQuantThreads == kListThreads);
 constexpr int kQuantEach = 4;  // groups of 8 values a thread, requested together
 
 struct QuantArgs {
@@ -19,9 +20,12 @@ struct QuantArgs {
     uint8_t *codes, *scales;
     void *values;
     long long ldx;
+    long long srow, sstep;  // bytes between the scales of rows and of steps
     uint32_t units;    // groups of 8 values of all rows, padding included
     uint32_t per_row;  // of one row
     int cols;
+    uint32_t groups;  // workgroups that quantise; one more makes the list
+    RowBlocks list;
 };
 
 // max over the 4 lanes of a block
@@ -77,6 +81,10 @@ template <int DT> __device__ __forceinline__ void store_values(typename Elem<DT>
 template <int DT, bool VALUES> __global__ __launch_bounds__(kQuantThreads) void mx4_quantize_kernel(QuantArgs a)
 {
     typedef typename Elem<DT>::type T;
+    if (blockIdx.x == a.groups) {
+        make_row_blocks(a.list);
+        return;
+    }
     Eight<DT> v[kQuantEach];
     uint32_t row[kQuantEach], at[kQuantEach];
 #pragma unroll
@@ -94,7 +102,7 @@ template <int DT, bool VALUES> __global__ __launch_bounds__(kQuantThreads) void 
         const uint32_t c = to_codes<DT>(v[j], byte);
         if (unit >= a.units) continue;  // whole blocks: units are a multiple of 4
         reinterpret_cast<uint32_t *>(a.codes)[unit] = c;
-        if ((threadIdx.x & 3) == 0) a.scales[unit >> 2] = (uint8_t)byte;
+        if ((threadIdx.x & 3) == 0) a.scales[row[j] * a.srow + (at[j] / kStep) * a.sstep + at[j] / 32 % 8] = (uint8_t)byte;
         if constexpr (VALUES) {
             const int left = a.cols - (int)at[j];
             if (left > 0)
@@ -105,13 +113,14 @@ template <int DT, bool VALUES> __global__ __launch_bounds__(kQuantThreads) void 
 
 template <int DT> static void launch_quantize(const QuantArgs &a, hipStream_t s)
 {
-    const unsigned grid = (a.units + kQuantThreads * kQuantEach - 1) / (kQuantThreads * kQuantEach);
+    const unsigned grid = a.groups + (a.list.list ? 1 : 0);
     if (a.values) hipLaunchKernelGGL((mx4_quantize_kernel<DT, true>), dim3(grid), dim3(kQuantThreads), 0, s, a);
     else hipLaunchKernelGGL((mx4_quantize_kernel<DT, false>), dim3(grid), dim3(kQuantThreads), 0, s, a);
 }
 
 hipError_t mx4_quantize_rows(hipStream_t s, long long rows, int cols, int dtype, const void *x, long long ldx,
-                             uint8_t *codes, uint8_t *scales, void *values)
+                             uint8_t *codes, uint8_t *scales, long long srow, long long sstep, void *values,
+                             const RowBlocks &blocks)
 {
     const int es = dtype == BCONV_F32 ? 4 : 2;
     const long long per_row = mx4_padded(cols) / 8;
@@ -121,12 +130,16 @@ hipError_t mx4_quantize_rows(hipStream_t s, long long rows, int cols, int dtype,
         QuantArgs a{};
         a.x = static_cast<const char *>(x) + first * ldx * es;
         a.codes = codes + first * per_row * 4;
-        a.scales = scales + first * (per_row / 4);
+        a.scales = scales + first * srow;
         a.values = values ? static_cast<char *>(values) + first * cols * es : nullptr;
         a.ldx = ldx;
+        a.srow = srow;
+        a.sstep = sstep;
         a.units = (uint32_t)(n * per_row);
         a.per_row = (uint32_t)per_row;
         a.cols = cols;
+        a.groups = (a.units + kQuantThreads * kQuantEach - 1) / (kQuantThreads * kQuantEach);
+        if (first == 0) a.list = blocks;
         switch (dtype) {
         case BCONV_F32: launch_quantize<BCONV_F32>(a, s); break;
         case BCONV_F16: launch_quantize<BCONV_F16>(a, s); break;
@@ -164,7 +177,7 @@ extern "C" bconv_status_t bconv_mx4_quantize(void *stream, int32_t rows, int32_t
         for (int j = 0; j < i; ++j)
             if (spans[i].n && ranges_overlap(spans[i].p, spans[i].n, spans[j].p, spans[j].n))
                 return fail(BCONV_ERR_INVALID_ARGUMENT, "codes, scales and values must overlap neither x nor each other");
-    const hipError_t e = bconv::mx4_quantize_rows(static_cast<hipStream_t>(stream), rows, cols, dtype, x, ldx, codes, scales, values);
+    const hipError_t e = bconv::mx4_quantize_rows(static_cast<hipStream_t>(stream), rows, cols, dtype, x, ldx, codes, scales, padded / 32, 8, values, bconv::RowBlocks{});
     if (e != hipSuccess) return bconv::hip_fail(e, "mx4 quantisation kernel");
     return BCONV_OK;
 }
