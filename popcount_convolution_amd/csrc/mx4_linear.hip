@@ -520,11 +520,14 @@ template <int DT> __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args
 
 // ------------------------------------------------------------------ dispatch
 
+// Few-row kernels: output tiles, row tiles, waves.
+enum FewVariant { k118, k214, k218, k224, k414, k418, k424 };
+
 struct Mx4Plan {
     bool quantise;  // x is quantised by a launch of its own
     int many;       // rows of x a workgroup of the many-row kernel takes; 0: the few-row kernel
     int nt;         // many: blocks of 32 outputs a wave
-    int rt, ct, waves;  // few
+    FewVariant variant;
     Mx4Many q;
     size_t scales_offset, list_offset, sums_offset, bytes;
 };
@@ -532,9 +535,20 @@ struct Mx4Plan {
 Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
 {
     Mx4Plan p{};
-    const int mean = a.rows / a.experts;
-    p.many = mean > 16 ? 128 : 0;
-    p.quantise = !given && (p.many || a.rows > 4);
+    const int mean = (a.rows + a.experts - 1) / a.experts;
+    // The few-row kernel reads the codes once for 16 or 32 rows, of one layer or of
+    // each expert; the many-row kernel's launches cost some 10 us more.  One layer,
+    // 25088 -> 4096, 32 rows: 16.6 us against 19.4, 64: 22.2 against 20.5; 8192 -> 11008, 32:
+    // 13.7 against 17.3, 48: 19.6 against 18.0; 2048 -> 16384, 128: 14.5 against 21.2;
+    // 4096 -> 4096, 128: 10.0 against 15.7.  64 experts of 2048 -> 2816, 16 rows
+    // each: 34.5 against 39.0, 32: 50.2 against 40.0.
+    const bool many = a.offsets ? mean > 20 : (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << 27;
+    p.many = many ? 128 : 0;
+    // Quantising in the few-row kernel costs every workgroup a little for each step, a launch of its own
+    // 1.2 us and the host's call: 1 row, 4096 -> 4096, 4.6 us against 5.6; 25088 -> 4096, 14.2
+    // against 12.2; 8 rows, 4096 -> 4096, 5.5 against 6.2; 8192 -> 11008, 12.7 against 11.6.
+    // 128 experts of 512 -> 1024, 4 rows each, 9.8 against 11.8; 8 of 4096 -> 4096, 16 rows, 26.4 against 16.5.
+    p.quantise = !given && (many || (a.offsets ? mean > 4 || a.steps > 8 : a.rows > 8 || a.steps > 24));
     auto take = [&](size_t n) {
         const size_t at = p.bytes;
         p.bytes += (n + 255) / 256 * 256;
@@ -544,10 +558,17 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
         take((size_t)a.x_rows * a.steps * (kStep / 2));
         p.scales_offset = take((size_t)a.x_rows * a.steps * (kStep / 32));
     }
-    if (!p.many) {
-        p.rt = 2;
-        p.ct = 1;
-        p.waves = 8;
+    if (!many) {
+        // Output tiles and row tiles a workgroup share their operands, waves the
+        // inputs.  One tile and eight waves while that is two workgroups a
+        // compute unit at most (16 rows of 25088 -> 4096: 14.1 us, two tiles 16.0; of 2048 ->
+        // 16384: two tiles and four waves 7.0, one tile 7.9); more rows share more.
+        const bool small = a.tiles <= 2 * cus, direct = !given && !p.quantise;
+        if (a.offsets) p.variant = direct ? k414 : k224;
+        else if (direct) p.variant = small ? k118 : k418;
+        else if (a.rows <= 16) p.variant = small ? k118 : k214;
+        else if (small && a.rows <= 64) p.variant = a.rows <= 32 ? k218 : k418;
+        else p.variant = k424;
         return p;
     }
     p.q.row_blocks = (a.rows + p.many - 1) / p.many + (a.offsets ? a.experts + 1 : 0);
@@ -595,8 +616,19 @@ template <int DT> hipError_t run_mx4(const Mx4Args &a, const Mx4Plan &p, hipStre
         hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
         return hipGetLastError();
     }
-    if (a.x) return run_few<DT, false, 2, 1, 8>(a, s);
-    return run_few<DT, true, 2, 1, 8>(a, s);
+    if (a.x) switch (p.variant) {
+        case k118: return run_few<DT, false, 1, 1, 8>(a, s);
+        case k414: return run_few<DT, false, 4, 1, 4>(a, s);
+        default: return run_few<DT, false, 4, 1, 8>(a, s);
+        }
+    switch (p.variant) {
+    case k118: return run_few<DT, true, 1, 1, 8>(a, s);
+    case k214: return run_few<DT, true, 2, 1, 4>(a, s);
+    case k218: return run_few<DT, true, 2, 1, 8>(a, s);
+    case k224: return run_few<DT, true, 2, 2, 4>(a, s);
+    case k418: return run_few<DT, true, 4, 1, 8>(a, s);
+    default: return run_few<DT, true, 4, 2, 4>(a, s);
+    }
 }
 
 }  // namespace bconv
