@@ -151,10 +151,14 @@ __device__ __forceinline__ Span expert_rows(const int *offsets, int experts, int
     return {inside(offsets[f]), f < experts ? inside(offsets[f + 1]) : rows};
 }
 
-// The rows that a workgroup of a product takes: of expert f (experts: of none).
+// The rows that a workgroup of a product takes, of expert f (experts: of none),
+// and the blocks that are taken together: `group` / 32 is the first of them,
+// `group` % 32 how many, all of the same expert.
 struct RowBlock {
-    int f, begin, end, unused;
+    int f, begin, end, group;
 };
+
+constexpr int kRowGroup = 16;  // at most
 
 // Rows of all experts in blocks of up to `size`, expert by expert, those of none
 // last: list[0].f is their number, they follow (at most ceil(rows / size) + experts + 1).
@@ -189,10 +193,13 @@ __device__ __forceinline__ void make_row_blocks(const RowBlocks &b)
     for (int w = 0; w < wave; ++w) at += sums[w];
     for (int f = f0; f < f0 + each && f <= b.experts; ++f) {
         const Span s = expert_rows(b.offsets, b.experts, b.rows, f);
-        for (int r = s.begin; r < s.end; r += b.size) {
-            ++at;
-            b.list[at] = {f, r, s.end - r < b.size ? s.end : r + b.size, 0};
+        const int blocks = s.end > s.begin ? (s.end - s.begin + b.size - 1) / b.size : 0;
+        for (int i = 0; i < blocks; ++i) {
+            const int r = s.begin + i * b.size, first = i / kRowGroup * kRowGroup;
+            b.list[1 + at + i] = {f, r, s.end - r < b.size ? s.end : r + b.size,
+                                  (at + first) * 32 + (blocks - first < kRowGroup ? blocks - first : kRowGroup)};
         }
+        at += blocks;
     }
     if (threadIdx.x == kListThreads - 1) b.list[0].f = at;
 }

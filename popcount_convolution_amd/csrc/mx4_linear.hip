@@ -261,56 +261,29 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t whole_buffer(const void *p)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, kNone - 1, 0x00020000);
 }
 
+// LDS of the many-row kernel.
+template <int MT> struct ManyStage {
+    u32x4 x[MT * 32 * 8];      // [row][slot], block b of a step in slot b ^ (row >> 1 & 7)
+    uint32_t xs[MT * 32 * 2];  // [row][half]
+};
+
+constexpr int kStages = 4, kManyRows = 128;
+
+union ManyLds {
+    ManyStage<kManyRows / 32> stage[kStages];
+    char out[4096 * 4];  // results on their way out, a wave's after the other's
+};
+
+// Results of up to 32 MT rows of expert f, 128 NT outputs from tile0 on.
 template <int DT, int MT, int NT, int WD>
-__global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
+__device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, ManyLds &lds, int f, Span span, int tile0, int split)
 {
     typedef typename Elem<DT>::type T;
-    constexpr int WAVES = 4, STAGES = 4, R = MT * 32, OT = WAVES * NT * 2;  // rows of x, tiles of 16 outputs
+    constexpr int WAVES = 4, STAGES = kStages, R = MT * 32;
     constexpr int XL = R / 8 / WAVES, XV = XL + 1, WV = 5 * NT;  // loads of a step: x and its scales, weights and theirs
-    struct Stage {
-        u32x4 x[R * 8];        // [row][slot], block b of a step in slot b ^ (row >> 1 & 7)
-        uint32_t xs[R * 2];    // [row][half]
-    };
-    __shared__ union {
-        Stage stage[STAGES];
-        char out[4096 * WAVES];  // results on their way out
-    } lds;
+    static_assert(R <= kManyRows);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int row = lane & 31, half = lane >> 5;
-
-    // Workgroups go to the XCDs in turn; each takes a run of neighbouring blocks.
-    const int row_blocks = q.row_list ? q.row_list[0].f : q.row_blocks;
-    const int total = row_blocks * q.out_blocks * q.splits;
-    int id = blockIdx.x;
-    if (id >= total) return;
-    {
-        const int xcd = id & 7, each = total >> 3, more = total & 7;
-        id = xcd * each + (xcd < more ? xcd : more) + (id >> 3);
-    }
-    const int blocks = row_blocks * q.out_blocks;
-    const int split = id / blocks;
-    id -= split * blocks;
-    constexpr int kGroup = 16;
-    const int group = id / (kGroup * q.out_blocks), g0 = group * kGroup;
-    const int high = row_blocks - g0 < kGroup ? row_blocks - g0 : kGroup;
-    id -= group * kGroup * q.out_blocks;
-    const int rb = g0 + id % high, ob = id / high;
-    const int tile0 = ob * OT;
-
-    Span span = {rb * R, min(rb * R + R, a.rows)};
-    int f = 0;
-    if (q.row_list) {
-        const RowBlock b = q.row_list[1 + rb];
-        f = b.f;
-        span = {b.begin, b.end};
-    }
-    if (f == a.experts) {  // rows of no expert
-        for (int e = threadIdx.x; e < (span.end - span.begin) * OT * 16; e += WAVES * 64) {
-            const int o = tile0 * 16 + e % (OT * 16);
-            if (o < a.n) static_cast<T *>(a.y)[(long long)(span.begin + e / (OT * 16)) * a.ldy + o] = (T)0.0f;
-        }
-        return;
-    }
     const int s_begin = __builtin_amdgcn_readfirstlane((int)((long long)a.steps * split / q.splits));
     const int s_end = __builtin_amdgcn_readfirstlane((int)((long long)a.steps * (split + 1) / q.splits));
 
@@ -341,7 +314,7 @@ __global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
 
     typedef __attribute__((address_space(3))) void *Lds;
     auto request_x = [&](int s, int slot, int l) {  // one of XV
-        Stage &st = lds.stage[slot];
+        ManyStage<kManyRows / 32> &st = lds.stage[slot];
         const uint32_t none = s < s_end ? 0 : kNone;
         if (l == 0)
             __builtin_amdgcn_raw_ptr_buffer_load_lds(rxs, (Lds)(&st.xs[my_scales * 2]), 4, (int)(xso | none), s * xs_step, 0, 0);
@@ -504,6 +477,57 @@ __global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
     }
 }
 
+template <int DT, int NT, int WD>
+__global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
+{
+    typedef typename Elem<DT>::type T;
+    constexpr int OT = NT * 8;  // tiles of 16 outputs
+    __shared__ ManyLds lds;
+    // Workgroups go to the XCDs in turn; each takes a run of neighbouring blocks.
+    const int row_blocks = q.row_list ? q.row_list[0].f : q.row_blocks;
+    const int total = row_blocks * q.out_blocks * q.splits;
+    int id = blockIdx.x;
+    if (id >= total) return;
+    {
+        const int xcd = id & 7, each = total >> 3, more = total & 7;
+        id = xcd * each + (xcd < more ? xcd : more) + (id >> 3);
+    }
+    const int blocks = row_blocks * q.out_blocks;
+    const int split = id / blocks;
+    id -= split * blocks;
+    // Neighbours share the weights of up to kRowGroup row blocks of one expert,
+    // then its other outputs follow: an L2 reads weights once and the rows of few experts
+    // at a time (groups of 16 blocks of whatever expert read 1.6 times the weights' bytes).
+    int rb = id / q.out_blocks, g0 = rb / kRowGroup * kRowGroup;
+    int high = row_blocks - g0 < kRowGroup ? row_blocks - g0 : kRowGroup;
+    if (q.row_list) {
+        const int g = q.row_list[1 + rb].group;
+        g0 = g >> 5;
+        high = g & 31;
+    }
+    id -= g0 * q.out_blocks;
+    rb = g0 + id % high;
+    const int tile0 = id / high * OT;
+
+    Span span = {rb * kManyRows, min(rb * kManyRows + kManyRows, a.rows)};
+    int f = 0;
+    if (q.row_list) {
+        const RowBlock b = q.row_list[1 + rb];
+        f = b.f;
+        span = {b.begin, b.end};
+    }
+    if (f == a.experts) {  // rows of no expert
+        for (int e = threadIdx.x; e < (span.end - span.begin) * OT * 16; e += 256) {
+            const int o = tile0 * 16 + e % (OT * 16);
+            if (o < a.n) static_cast<T *>(a.y)[(long long)(span.begin + e / (OT * 16)) * a.ldy + o] = (T)0.0f;
+        }
+        return;
+    }
+    if (span.end - span.begin > 64) many_rows<DT, 4, NT, WD>(a, q, lds, f, span, tile0, split);
+    else if (span.end - span.begin > 32) many_rows<DT, 2, NT, WD>(a, q, lds, f, span, tile0, split);
+    else many_rows<DT, 1, NT, WD>(a, q, lds, f, span, tile0, split);
+}
+
 // Adds the splits' sums in order.
 template <int DT> __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args a, Mx4Many q)
 {
@@ -537,13 +561,18 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
     Mx4Plan p{};
     const int mean = (a.rows + a.experts - 1) / a.experts;
     // The few-row kernel reads the codes once for 16 or 32 rows, of one layer or of
-    // each expert; the many-row kernel's launches cost some 10 us more.  One layer,
+    // each expert; the many-row kernel takes 128 rows and its launches cost some 5 to 10 us more.
+    // It pays for many codes read that way, and where its workgroups fill half the card
+    // without splitting the inputs.  One layer,
     // 25088 -> 4096, 32 rows: 16.6 us against 19.4, 64: 22.2 against 20.5; 8192 -> 11008, 32:
-    // 13.7 against 17.3, 48: 19.6 against 18.0; 2048 -> 16384, 128: 14.5 against 21.2;
-    // 4096 -> 4096, 128: 10.0 against 15.7.  64 experts of 2048 -> 2816, 16 rows
+    // 13.7 against 17.3, 48: 19.6 against 18.0; 256 rows of 4096 -> 4096: 13.9 against 20.6; 8192 rows of 512 ->
+    // 512: 15.2 against 10.5; 512 of 1024 -> 4096: 11.2 against 9.5.  64 experts of 2048 -> 2816, 16 rows
     // each: 34.5 against 39.0, 32: 50.2 against 40.0.
-    const bool many = a.offsets ? mean > 20 : (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << 27;
-    p.many = many ? 128 : 0;
+    const long long blocks = (a.rows + 127LL) / 128 * ((a.tiles + 7) / 8);
+    const bool many = a.offsets ? mean > 20
+                                : (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << (a.rows > 32 ? 26 : 27) ||
+                                      (a.rows > 128 && blocks * 2 >= cus);
+    p.many = many ? kManyRows : 0;
     // Quantising in the few-row kernel costs every workgroup a little for each step, a launch of its own
     // 1.2 us and the host's call: 1 row, 4096 -> 4096, 4.6 us against 5.6; 25088 -> 4096, 14.2
     // against 12.2; 8 rows, 4096 -> 4096, 5.5 against 6.2; 8192 -> 11008, 12.7 against 11.6.
@@ -581,7 +610,7 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
         p.list_offset = take((size_t)(p.q.row_blocks + 1) * sizeof(RowBlock));
     } else {
         long long splits = cus / ((long long)p.q.row_blocks * p.q.out_blocks);
-        if (splits > a.steps / 4) splits = a.steps / 4;
+        if (splits > a.steps / 12) splits = a.steps / 12;
         if (splits > 8) splits = 8;
         if (splits > 1) {
             p.q.splits = (int)splits;
@@ -608,8 +637,8 @@ template <int DT> hipError_t run_mx4(const Mx4Args &a, const Mx4Plan &p, hipStre
 {
     if (p.many) {
         const dim3 grid((unsigned)((long long)p.q.row_blocks * p.q.out_blocks * p.q.splits));
-        if (p.nt == 2) hipLaunchKernelGGL((mx4_many_kernel<DT, 4, 2, 1>), grid, dim3(256), 0, s, a, p.q);
-        else hipLaunchKernelGGL((mx4_many_kernel<DT, 4, 1, 3>), grid, dim3(256), 0, s, a, p.q);
+        if (p.nt == 2) hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 1>), grid, dim3(256), 0, s, a, p.q);
+        else hipLaunchKernelGGL((mx4_many_kernel<DT, 1, 3>), grid, dim3(256), 0, s, a, p.q);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess || p.q.splits == 1) return e;
         const long long outs = (long long)((a.n + 3) / 4) * a.rows;
