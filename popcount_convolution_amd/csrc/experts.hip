@@ -250,37 +250,63 @@ template <int DT> __device__ __forceinline__ void clear_places(const RowsArgs &a
     }
 }
 
-// A workgroup a token: its row is read once and written for each choice.
+constexpr int kTogether = 8;  // choices whose rows are in flight at once
+
+// The places of choices j0 .. of a token, -1 for dropped ones and past the last.
+__device__ __forceinline__ void places(const RowsArgs &a, int t, int j0, int (&at)[kTogether])
+{
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j)
+        at[j] = j0 + j < a.choices ? __builtin_amdgcn_readfirstlane(place(a, (long long)t * a.choices + j0 + j)) : -1;
+}
+
+// A workgroup a token: its row is read once for kTogether choices and written for each.
 template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_gather_kernel(RowsArgs a)
 {
     constexpr int V = kPiece<DT>;
     const int t = a.first + (int)blockIdx.x;
-    for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
-        const Piece<DT> p = Piece<DT>::load(a.from, t * a.ld_from + c, a.width - c);
-        for (int j = 0; j < a.choices; ++j) {
-            const int to = place(a, (long long)t * a.choices + j);
-            if (to >= 0) p.store(a.to, (long long)to * a.width + c, a.width - c);
+    for (int j0 = 0; j0 < a.choices; j0 += kTogether) {
+        int at[kTogether];
+        places(a, t, j0, at);
+        for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
+            const Piece<DT> p = Piece<DT>::load(a.from, t * a.ld_from + c, a.width - c);
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+                if (at[j] >= 0) p.store(a.to, (long long)at[j] * a.width + c, a.width - c);
         }
     }
     clear_places<DT>(a, t);
 }
 
-template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(RowsArgs a)
+// A workgroup a token; the rows of kTogether choices are requested before the
+// first is added.  MANY: there are more choices than that.
+template <int DT, bool MANY> __global__ __launch_bounds__(kRowThreads) void expert_combine_kernel(RowsArgs a)
 {
     constexpr int V = kPiece<DT>;
     const int t = a.first + (int)blockIdx.x;
+    int at[kTogether];
+    float w[kTogether];
+    auto choose = [&](int j0) {
+        places(a, t, j0, at);
+#pragma unroll
+        for (int j = 0; j < kTogether; ++j) w[j] = at[j] >= 0 ? load_weight(a, (long long)t * a.choices + j0 + j) : 0.0f;
+    };
+    if constexpr (!MANY) choose(0);
     for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
         float sum[V];
 #pragma unroll
         for (int i = 0; i < V; ++i) sum[i] = 0.0f;
-        for (int j = 0; j < a.choices; ++j) {
-            const long long pair = (long long)t * a.choices + j;
-            const int at = place(a, pair);
-            if (at < 0) continue;
-            const float w = load_weight(a, pair);
-            const Piece<DT> p = Piece<DT>::load(a.from, at * a.ld_from + c, a.width - c);
+        for (int j0 = 0; j0 < (MANY ? a.choices : 1); j0 += kTogether) {
+            if constexpr (MANY) choose(j0);
+            Piece<DT> p[kTogether];
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(w, (float)p.v[i], sum[i]);
+            for (int j = 0; j < kTogether; ++j)
+                if (at[j] >= 0) p[j] = Piece<DT>::load(a.from, at[j] * a.ld_from + c, a.width - c);
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j)
+                if (at[j] >= 0)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) sum[i] = __builtin_fmaf(w[j], (float)p[j].v[i], sum[i]);
         }
         Piece<DT> y;
 #pragma unroll
@@ -289,40 +315,55 @@ template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_
     }
 }
 
-// A workgroup a token; its choices one after the other.
+// A workgroup a token: dy's row is read once for kTogether choices.
 template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(RowsArgs a)
 {
     constexpr int V = kPiece<DT>;
-    __shared__ float part[kRowThreads / 64];
+    __shared__ float part[kRowThreads / 64][kTogether];
     const int t = a.first + (int)blockIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int j = 0; j < a.choices; ++j) {
-        const long long pair = (long long)t * a.choices + j;
-        const int at = place(a, pair);
-        float dot = 0.0f;
-        if (at >= 0) {
-            const float w = load_weight(a, pair);
-            for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
-                const Piece<DT> d = Piece<DT>::load(a.dy, t * a.ld_dy + c, a.width - c);
-                if (a.d_weights) {
-                    const Piece<DT> r = Piece<DT>::load(a.from, at * a.ld_from + c, a.width - c);
+    for (int j0 = 0; j0 < a.choices; j0 += kTogether) {
+        int at[kTogether];
+        float w[kTogether], dot[kTogether];
+        places(a, t, j0, at);
 #pragma unroll
-                    for (int i = 0; i < V; ++i) dot = __builtin_fmaf((float)d.v[i], (float)r.v[i], dot);
-                }
+        for (int j = 0; j < kTogether; ++j) {
+            w[j] = at[j] >= 0 ? load_weight(a, (long long)t * a.choices + j0 + j) : 0.0f;
+            dot[j] = 0.0f;
+        }
+        for (int c = threadIdx.x * V; c < a.width; c += kRowThreads * V) {
+            const int left = a.width - c;
+            const Piece<DT> d = Piece<DT>::load(a.dy, t * a.ld_dy + c, left);
+            Piece<DT> r[kTogether];
+            if (a.d_weights) {
+#pragma unroll
+                for (int j = 0; j < kTogether; ++j)
+                    if (at[j] >= 0) r[j] = Piece<DT>::load(a.from, at[j] * a.ld_from + c, left);
+            }
+#pragma unroll
+            for (int j = 0; j < kTogether; ++j) {
+                if (at[j] < 0) continue;
                 Piece<DT> g;
 #pragma unroll
-                for (int i = 0; i < V; ++i) g.v[i] = (typename Elem<DT>::type)(w * (float)d.v[i]);
-                g.store(a.to, (long long)at * a.width + c, a.width - c);
+                for (int i = 0; i < V; ++i) g.v[i] = (typename Elem<DT>::type)(w[j] * (float)d.v[i]);
+                g.store(a.to, (long long)at[j] * a.width + c, left);
+                if (a.d_weights)
+#pragma unroll
+                    for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf((float)d.v[i], (float)r[j].v[i], dot[j]);
             }
         }
         if (a.d_weights) {
 #pragma unroll
-            for (int d = 32; d > 0; d /= 2) dot += __shfl_xor(dot, d);
-            if (lane == 0) part[wave] = dot;
+            for (int j = 0; j < kTogether; ++j) {
+                if (j0 + j >= a.choices) break;
+#pragma unroll
+                for (int d = 32; d > 0; d /= 2) dot[j] += __shfl_xor(dot[j], d);
+                if (lane == 0) part[wave][j] = dot[j];
+            }
             __syncthreads();
-            if (threadIdx.x == 0) {
-                float sum = part[0];
-                for (int w = 1; w < kRowThreads / 64; ++w) sum += part[w];
-                store_weight(a, pair, sum);
+            if (threadIdx.x < kTogether && j0 + (int)threadIdx.x < a.choices) {
+                float sum = part[0][threadIdx.x];
+                for (int v = 1; v < kRowThreads / 64; ++v) sum += part[v][threadIdx.x];
+                store_weight(a, (long long)t * a.choices + j0 + threadIdx.x, sum);
             }
             __syncthreads();
         }
@@ -336,7 +377,10 @@ template <int DT> static void launch_rows(RowsOp op, const RowsArgs &a, unsigned
 {
     switch (op) {
     case kGather: hipLaunchKernelGGL((expert_gather_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a); break;
-    case kCombine: hipLaunchKernelGGL((expert_combine_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a); break;
+    case kCombine:
+        if (a.choices > kTogether) hipLaunchKernelGGL((expert_combine_kernel<DT, true>), dim3(grid), dim3(kRowThreads), 0, s, a);
+        else hipLaunchKernelGGL((expert_combine_kernel<DT, false>), dim3(grid), dim3(kRowThreads), 0, s, a);
+        break;
     default: hipLaunchKernelGGL((expert_combine_backward_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a);
     }
 }
