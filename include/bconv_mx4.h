@@ -100,14 +100,15 @@ typedef struct {
     const uint8_t *scales;   /*              (16-byte aligned) */
     void *y;                 /* [rows][out_features], row i at y + i*ldy; overlaps nothing else */
     int64_t ldy;             /* >= out_features */
-    int32_t x_rows;          /* input rows */
+    int32_t x_rows;          /* input rows; with offsets, x_rows times in_features (rounded up to a
+                                multiple of 256) is at most 2^32 */
     int32_t rows;            /* result rows */
     int32_t dtype;           /* of x and y */
     int32_t choices;         /* 0: result row i is of input row i (x_rows == rows); otherwise of
                                 order[i] / choices, and x_rows == rows / choices */
     const int32_t *offsets;  /* device [experts + 1]: rows offsets[f] .. offsets[f+1]-1 are expert f's;
                                 NULL for one expert: all rows */
-    const int32_t *order;    /* device [rows], or NULL with choices == 0 */
+    const int32_t *order;    /* device [rows] with choices > 0 (offsets then too), otherwise NULL */
 } bconv_mx4_rows_t;
 
 /* Workspace bytes the call needs (0 is possible); looks at no pointer but whether x is NULL. */

@@ -242,6 +242,7 @@ struct Mx4Many {
     const RowBlock *row_list;  // with experts: what make_row_blocks() makes
     int row_blocks, out_blocks, splits;
     int padded_n;
+    int first;    // the launch's first workgroup
 };
 
 // The list of row blocks, where no other launch makes it.
@@ -486,7 +487,7 @@ __global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
     // Workgroups go to the XCDs in turn; each takes a run of neighbouring blocks.
     const int row_blocks = q.row_list ? q.row_list[0].f : q.row_blocks;
     const int total = row_blocks * q.out_blocks * q.splits;
-    int id = blockIdx.x;
+    int id = q.first + blockIdx.x;
     if (id >= total) return;
     {
         const int xcd = id & 7, each = total >> 3, more = total & 7;
@@ -575,9 +576,9 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
     p.many = many ? kManyRows : 0;
     // Quantising in the few-row kernel costs every workgroup a little for each step, a launch of its own
     // 1.2 us and the host's call: 1 row, 4096 -> 4096, 4.6 us against 5.6; 25088 -> 4096, 14.2
-    // against 12.2; 8 rows, 4096 -> 4096, 5.5 against 6.2; 8192 -> 11008, 12.7 against 11.6.
+    // against 12.2; 12 rows, 4096 -> 4096, 6.4 against 6.4; 16 rows, 2048 -> 2048, 5.0 against 6.1, 6000 -> 1500, 9.1 against 7.4.
     // 128 experts of 512 -> 1024, 4 rows each, 9.8 against 11.8; 8 of 4096 -> 4096, 16 rows, 26.4 against 16.5.
-    p.quantise = !given && (many || (a.offsets ? mean > 4 || a.steps > 8 : a.rows > 8 || a.steps > 24));
+    p.quantise = !given && (many || (a.offsets ? mean > 4 || a.steps > 8 : a.rows > 16 || a.steps > 24 || a.rows * a.steps > 192));
     auto take = [&](size_t n) {
         const size_t at = p.bytes;
         p.bytes += (n + 255) / 256 * 256;
@@ -620,6 +621,16 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
     return p;
 }
 
+// Rows that one set of launches takes: one layer's call of more is several, so that
+// its quantised rows stay below 2 GiB.
+constexpr long long kMaxSteps = 1 << 24;  // rows times steps
+
+int slab_rows(int steps)
+{
+    const long long rows = kMaxSteps / steps / kManyRows * kManyRows;  // steps <= 2^12
+    return (int)(rows < 1 << 18 ? rows : 1 << 18);
+}
+
 // The list of row blocks that the plan needs.
 RowBlocks row_blocks(const Mx4Args &a, const Mx4Plan &p)
 {
@@ -636,10 +647,12 @@ template <int DT, bool QUANTISED, int RT, int CT, int WAVES> hipError_t run_few(
 template <int DT> hipError_t run_mx4(const Mx4Args &a, const Mx4Plan &p, hipStream_t s)
 {
     if (p.many) {
-        const dim3 grid((unsigned)((long long)p.q.row_blocks * p.q.out_blocks * p.q.splits));
-        if (p.nt == 2) hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 1>), grid, dim3(256), 0, s, a, p.q);
-        else hipLaunchKernelGGL((mx4_many_kernel<DT, 1, 3>), grid, dim3(256), 0, s, a, p.q);
-        const hipError_t e = hipGetLastError();
+        Mx4Many q = p.q;
+        const hipError_t e = launch_slices((long long)q.row_blocks * q.out_blocks * q.splits, [&](long long first, unsigned groups) {
+            q.first = (int)first;
+            if (p.nt == 2) hipLaunchKernelGGL((mx4_many_kernel<DT, 2, 1>), dim3(groups), dim3(256), 0, s, a, q);
+            else hipLaunchKernelGGL((mx4_many_kernel<DT, 1, 3>), dim3(groups), dim3(256), 0, s, a, q);
+        });
         if (e != hipSuccess || p.q.splits == 1) return e;
         const long long outs = (long long)((a.n + 3) / 4) * a.rows;
         hipLaunchKernelGGL((mx4_join_kernel<DT>), dim3((unsigned)((outs + 255) / 256)), dim3(256), 0, s, a, p.q);
@@ -713,6 +726,7 @@ template <typename T> bconv_status_t device_alloc(T **p, size_t count)
 }
 
 // What sizes alone decide of a call; workspace_size and forward share it.
+// Offsets of the many-row kernel into quantised rows are 31 bits.
 bconv_status_t check_sizes(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
 {
     if (!h || !args) return fail(BCONV_ERR_INVALID_ARGUMENT, "handle or args is NULL");
@@ -722,7 +736,26 @@ bconv_status_t check_sizes(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
     if (args->choices == 0 ? args->x_rows != args->rows : (long long)args->x_rows * args->choices != args->rows)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "%d rows do not follow from %d input rows and %d choices", args->rows,
                     args->x_rows, args->choices);
+    if ((h->desc.experts > 1 || args->offsets) && (long long)args->x_rows * h->steps > bconv::kMaxSteps)
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "%d input rows of %d values are more than 2^32 values (padded)", args->x_rows,
+                    h->desc.in_features);
     return BCONV_OK;
+}
+
+// Workspace of a call: that of its slabs of rows.
+size_t workspace_of(bconv_mx4_linear_t h, const bconv::Mx4Args &a, bool given)
+{
+    bconv::Mx4Args part = a;
+    const int slab = a.offsets ? a.rows : bconv::slab_rows(a.steps);
+    size_t bytes = 0;
+    for (const int rows : {a.rows < slab ? a.rows : slab, a.rows % slab}) {
+        part.rows = rows;
+        part.x_rows = a.offsets ? a.x_rows : rows;
+        if (rows == 0) continue;
+        const size_t need = bconv::plan_mx4(part, given, h->cus).bytes;
+        bytes = need > bytes ? need : bytes;
+    }
+    return bytes;
 }
 
 bconv::Mx4Args kernel_args(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
@@ -810,7 +843,7 @@ bconv_status_t bconv_mx4_linear_workspace_size(bconv_mx4_linear_t h, const bconv
     const bconv_status_t st = check_sizes(h, args);
     if (st != BCONV_OK) return st;
     if (!bytes) return fail(BCONV_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = args->rows ? bconv::plan_mx4(kernel_args(h, args), !args->x, h->cus).bytes : 0;
+    *bytes = args->rows ? workspace_of(h, kernel_args(h, args), !args->x) : 0;
     return BCONV_OK;
 }
 
@@ -833,54 +866,66 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
     if (!args->offsets && h->desc.experts > 1) return fail(BCONV_ERR_INVALID_ARGUMENT, "offsets is NULL, the layer has experts");
     if ((args->choices > 0) != (args->order != nullptr))
         return fail(BCONV_ERR_INVALID_ARGUMENT, "order must be given with choices, and only then");
+    if (args->order && !args->offsets) return fail(BCONV_ERR_INVALID_ARGUMENT, "order is given without offsets");
     if (((uintptr_t)args->offsets | (uintptr_t)args->order) % 4)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "offsets/order not aligned to an element");
     bconv::Mx4Args a = kernel_args(h, args);
-    bconv::Mx4Plan p = bconv::plan_mx4(a, !args->x, h->cus);
-    if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))
-        return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", p.bytes, workspace ? workspace_bytes : (size_t)0);
-    if (p.bytes > 0 && (uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
+    const size_t need = workspace_of(h, a, !args->x);
+    if (need > 0 && (!workspace || workspace_bytes < need))
+        return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : (size_t)0);
+    if (need > 0 && (uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
     const size_t xc = (size_t)args->x_rows * h->steps * (bconv::kStep / 2), xs = xc / 16;
     const struct { const void *p; size_t n; } in[] = {
         {args->x, args->x ? ((size_t)(args->x_rows - 1) * args->ldx + k) * es : 0}, {args->codes, args->codes ? xc : 0},
         {args->scales, args->scales ? xs : 0}, {args->offsets, args->offsets ? ((size_t)h->desc.experts + 1) * 4 : 0},
         {args->order, args->order ? (size_t)args->rows * 4 : 0}},
-        out[] = {{args->y, ((size_t)(args->rows - 1) * args->ldy + n) * es}, {workspace, p.bytes}};
+        out[] = {{args->y, ((size_t)(args->rows - 1) * args->ldy + n) * es}, {workspace, need}};
     for (const auto &o : out)
         for (const auto &i : in)
             if (o.n && i.n && ranges_overlap(o.p, o.n, i.p, i.n))
                 return fail(BCONV_ERR_INVALID_ARGUMENT, "y or the workspace overlaps x, codes, scales, offsets or order");
-    if (p.bytes && ranges_overlap(out[0].p, out[0].n, workspace, p.bytes))
+    if (need && ranges_overlap(out[0].p, out[0].n, workspace, need))
         return fail(BCONV_ERR_INVALID_ARGUMENT, "y and the workspace overlap");
 
     DeviceGuard guard(h->device);
     if (guard.err != hipSuccess) return hip_fail(guard.err, "hipSetDevice");
     hipStream_t s = static_cast<hipStream_t>(stream);
-    hipError_t e = hipSuccess;
     char *ws = static_cast<char *>(workspace);
-    p.q.sums = reinterpret_cast<float *>(ws + p.sums_offset);
-    if (p.many && a.offsets) p.q.row_list = reinterpret_cast<const bconv::RowBlock *>(ws + p.list_offset);
-    if (p.quantise) {
-        uint8_t *codes = static_cast<uint8_t *>(workspace);
-        a.xs_row = 8;
-        a.xs_step = a.x_rows * 8LL;
-        e = bconv::mx4_quantize_rows(s, a.x_rows, k, args->dtype, a.x, a.ldx, codes, codes + p.scales_offset, a.xs_row, a.xs_step,
-                                     nullptr, bconv::row_blocks(a, p));
-        if (e != hipSuccess) return hip_fail(e, "mx4 quantisation kernel");
-        a.x = nullptr;
-        a.xc = codes;
-        a.xs = codes + p.scales_offset;
-    } else if (p.q.row_list) {
-        hipLaunchKernelGGL(bconv::mx4_blocks_kernel, dim3(1), dim3(bconv::kListThreads), 0, s, bconv::row_blocks(a, p));
-        e = hipGetLastError();
-        if (e != hipSuccess) return hip_fail(e, "mx4 row block kernel");
+    const int slab = a.offsets ? a.rows : bconv::slab_rows(a.steps);
+    for (int64_t first = 0; first < args->rows; first += slab) {
+        if (!a.offsets) {
+            a.rows = a.x_rows = (int)(args->rows - first < slab ? args->rows - first : slab);
+            a.x = args->x ? static_cast<const char *>(args->x) + first * args->ldx * es : nullptr;
+            a.xc = args->codes ? args->codes + first * h->steps * (bconv::kStep / 2) : nullptr;
+            a.xs = args->scales ? args->scales + first * h->steps * (bconv::kStep / 32) : nullptr;
+            a.y = static_cast<char *>(args->y) + first * args->ldy * es;
+        }
+        bconv::Mx4Plan p = bconv::plan_mx4(a, !args->x, h->cus);
+        p.q.sums = reinterpret_cast<float *>(ws + p.sums_offset);
+        if (p.many && a.offsets) p.q.row_list = reinterpret_cast<const bconv::RowBlock *>(ws + p.list_offset);
+        hipError_t e = hipSuccess;
+        if (p.quantise) {
+            uint8_t *codes = reinterpret_cast<uint8_t *>(ws);
+            a.xs_row = 8;
+            a.xs_step = a.x_rows * 8LL;
+            e = bconv::mx4_quantize_rows(s, a.x_rows, k, args->dtype, a.x, a.ldx, codes, codes + p.scales_offset, a.xs_row,
+                                         a.xs_step, nullptr, bconv::row_blocks(a, p));
+            if (e != hipSuccess) return hip_fail(e, "mx4 quantisation kernel");
+            a.x = nullptr;
+            a.xc = codes;
+            a.xs = codes + p.scales_offset;
+        } else if (p.q.row_list) {
+            hipLaunchKernelGGL(bconv::mx4_blocks_kernel, dim3(1), dim3(bconv::kListThreads), 0, s, bconv::row_blocks(a, p));
+            e = hipGetLastError();
+            if (e != hipSuccess) return hip_fail(e, "mx4 row block kernel");
+        }
+        switch (args->dtype) {
+        case BCONV_F32: e = bconv::run_mx4<BCONV_F32>(a, p, s); break;
+        case BCONV_F16: e = bconv::run_mx4<BCONV_F16>(a, p, s); break;
+        default: e = bconv::run_mx4<BCONV_BF16>(a, p, s); break;
+        }
+        if (e != hipSuccess) return hip_fail(e, "mx4 linear kernel");
     }
-    switch (args->dtype) {
-    case BCONV_F32: e = bconv::run_mx4<BCONV_F32>(a, p, s); break;
-    case BCONV_F16: e = bconv::run_mx4<BCONV_F16>(a, p, s); break;
-    default: e = bconv::run_mx4<BCONV_BF16>(a, p, s); break;
-    }
-    if (e != hipSuccess) return hip_fail(e, "mx4 linear kernel");
     return BCONV_OK;
 }
 

@@ -25,8 +25,13 @@ BLOCK = 32   # values that share a power of two
 _PAD = 256   # quantised rows are padded to a multiple of this
 
 
-def _torch():
-    return _q4._torch or _q4._load_torch()
+_torch = None  # the torch module, once a call needs it
+
+
+def _load():
+    global _torch
+    _torch = _q4._torch or _q4._load_torch()
+    return _torch
 
 
 def _padded(cols: int) -> int:
@@ -45,7 +50,7 @@ def mx4_quantize(x, *, values: bool = False, stream=None):
     With ``values`` returns ``(quantised, values)``, the tensor of x's shape and
     type that they stand for.  A 2-d x may have any row stride; others must be
     contiguous.  A block that holds a NaN or an infinity becomes NaN."""
-    torch = _torch()
+    torch = _torch or _load()
     _need_tensor(x, "input")
     shape = x.shape
     if not shape or not 1 <= shape[-1] <= 1 << 20:
@@ -55,12 +60,12 @@ def mx4_quantize(x, *, values: bool = False, stream=None):
     if rows > _INT32_MAX:
         _need_int32(rows, "input")
     _need_cuda(x, "input")
-    cols = shape[-1]
+    *lead, cols = shape
     padded = _padded(cols)
     place, raw = _place(x.device, stream)
     with place:
-        codes = torch.empty((*shape[:-1], padded // 2), dtype=torch.uint8, device=x.device)
-        scales = torch.empty((*shape[:-1], padded // BLOCK), dtype=torch.uint8, device=x.device)
+        codes = x.new_empty((*lead, padded // 2), dtype=torch.uint8)
+        scales = x.new_empty((*lead, padded // BLOCK), dtype=torch.uint8)
         dense = x.new_empty(shape) if values else None
         if rows:
             B.bconv_mx4_quantize(raw, rows, cols, code, x.data_ptr(), ldx, codes.data_ptr(), scales.data_ptr(),
@@ -81,7 +86,7 @@ class _MX4Layer:
             _need_int32(value, name)
             if value < 1:
                 raise ValueError(f"{name}: {value} is not positive")
-        torch = _torch()
+        torch = _torch or _load()
         self.in_features, self.out_features = in_features, out_features
         device = torch.device("cuda", torch.cuda.current_device())
         held = []
@@ -106,7 +111,7 @@ class _MX4Layer:
 
     def _forward(self, x, dtype, out, workspace, stream, rows, out_lead, choices, offsets, order):
         """Product of checked rows: ``rows`` results of shape ``out_lead``."""
-        torch = _q4._torch
+        torch = _torch
         device = self.device
         if type(x) is MX4Tensor:
             if dtype is None:
@@ -133,7 +138,7 @@ class _MX4Layer:
         with place:
             out_shape = (*out_lead, self.out_features)
             if out is None:
-                out = torch.empty(out_shape, dtype=dtype, device=device)
+                out = torch.empty(out_shape, dtype=dtype, device=device) if px is None else x.new_empty(out_shape)
                 ldy = self.out_features
             else:
                 _need_tensor(out, "output")
@@ -316,7 +321,7 @@ def sort_by_expert(expert_ids, experts: int, stream=None) -> ExpertOrder:
     """Sorts the pairs of ``expert_ids`` (int32 or int64 ``[tokens, choices]``, the
     experts that each token chose) by expert, those of an expert in their order.
     Pairs whose id is not in ``[0, experts)`` are dropped."""
-    torch = _torch()
+    torch = _torch or _load()
     _need_tensor(expert_ids, "expert_ids")
     if expert_ids.dtype not in (torch.int32, torch.int64) or expert_ids.dim() != 2 or not expert_ids.shape[1]:
         raise ValueError(f"expert_ids: {expert_ids.dtype} of shape {tuple(expert_ids.shape)} is not int32 or int64 "

@@ -20,7 +20,7 @@ def quantise(x):
     rows, cols = x.shape
     wide = np.zeros((rows, padded(cols)))
     wide[:, :cols] = x
-    blocks = wide.reshape(rows, -1, BLOCK)
+    blocks = wide.reshape(rows, padded(cols) // BLOCK, BLOCK)
     finite = np.isfinite(blocks).all(-1)
     top = np.where(finite, np.abs(np.where(np.isfinite(blocks), blocks, 0)).max(-1), 0)
     _, e = np.frexp(top)                              # top is in [2^(e-1), 2^e)
@@ -30,9 +30,9 @@ def quantise(x):
     for i in range(7):
         middle = (MAGNITUDES[i] + MAGNITUDES[i + 1]) / 2
         index += np.abs(q) >= middle if i % 2 else np.abs(q) > middle   # a tie goes to the even code
-    code = np.where(finite[..., None], index | (np.signbit(q) << 3), 0).reshape(rows, -1).astype(np.uint8)
+    code = np.where(finite[..., None], index | (np.signbit(q) << 3), 0).reshape(wide.shape).astype(np.uint8)
     values = np.ldexp(np.copysign(MAGNITUDES[index], q), e[..., None])
-    values = np.where(finite[..., None], values, np.nan).reshape(rows, -1)[:, :cols]
+    values = np.where(finite[..., None], values, np.nan).reshape(wide.shape)[:, :cols]
     byte = np.where(finite, e + 127, 255).astype(np.uint8)
     return code[:, 0::2] | (code[:, 1::2] << 4), byte, values
 

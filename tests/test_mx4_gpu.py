@@ -158,13 +158,41 @@ def test_linear(dev, dtype, rows, k, n, bias):
     wide = torch.zeros((rows, k + 3), device=dev, dtype=DT[dtype])
     wide[:, 1:k + 1] = x
     buf = torch.full((rows, n + 5), 7.0, device=dev, dtype=DT[dtype])
-    ws = torch.full((1 << 25,), 0xff, dtype=torch.uint8, device=dev)
+    ws = torch.full((1 << 27,), 0xff, dtype=torch.uint8, device=dev)
     layer.forward(wide[:, 1:k + 1], out=buf[:, 2:n + 2], workspace=ws)
     assert torch.equal(buf[:, 2:n + 2], y) and bool((buf[:, :2] == 7).all()) and bool((buf[:, n + 2:] == 7).all())
     # and neither does quantising first
     q = pca.mx4_quantize(x)
     assert torch.equal(layer.forward(q, dtype=DT[dtype]), y)
     layer.close()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,k,n,bias", [
+    (300, 9000, 3000, True),      # two row blocks and a short one, inputs split between workgroups
+    (150, 5000, 5000, False),     # a last block of up to 32 rows
+    (190, 4900, 5003, True),      # of up to 64
+    (129, 6400, 8200, False),     # of one row
+    (1100, 1030, 1111, True),     # workgroups enough without splitting
+    (2600, 260, 4100, True),      # wide workgroups
+    (2050, 1800, 2049, False), (4000, 100, 600, True), (700, 2304, 2300, False)])
+def test_linear_many_rows(dev, dtype, rows, k, n, bias):
+    """Products large enough for the many-row kernel: each shape of its
+    workgroups, short last blocks, tiles past the outputs, steps of 1 to many."""
+    test_linear(dev, dtype, rows, k, n, bias)
+
+
+def test_linear_slabs(dev):
+    """More rows than one set of launches takes."""
+    rng = np.random.default_rng(4)
+    layer, weights = make_linear(rng, 30, 20, True)
+    rows = (1 << 18) + 77
+    x = rows_of(rng, rows, 30, dev, "f16")
+    y = layer.forward(x)
+    for part in (slice(0, 300), slice((1 << 18) - 150, (1 << 18) + 77)):
+        check_product(y[part], x[part], weights, "f16")
+    assert torch.equal(layer.forward(x[1 << 18:]), y[1 << 18:])
+    assert torch.equal(layer.forward(pca.mx4_quantize(x), dtype=torch.float16), y)
 
 
 @pytest.mark.parametrize("rows", [1, 5, 40, 300])
@@ -181,11 +209,10 @@ def test_linear_range(dev, rows):
     check_product(layer.forward(x), x, weights, "f32")
 
 
-@pytest.mark.parametrize("rows", [1, 5, 40, 300])
-def test_linear_nan(dev, rows):
+@pytest.mark.parametrize("rows,k,n", [(1, 700, 90), (5, 700, 90), (40, 700, 90), (300, 700, 90), (600, 700, 1500)])
+def test_linear_nan(dev, rows, k, n):
     """A NaN or an infinity makes its row NaN and no other; a NaN scale of the weights its output."""
     rng = np.random.default_rng(rows)
-    k, n = 700, 90
     codes, scales = ref.random_weights(rng, n, k)
     scales[17, 3] = 255
     layer = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales)
@@ -389,3 +416,139 @@ def test_experts_like_one_layer(dev):
         o = pca.sort_by_expert(torch.zeros((rows, 1), dtype=torch.int64, device=dev), 1)
         want, mass = ref.linear(host(x), codes, scales, None)
         assert (np.abs(host(layer.forward(x, o)) - host(one.forward(x))) <= 2 * ref.linear_bound(want, mass, 400, "f32")).all()
+
+
+@pytest.mark.parametrize("rows", [16, 100])
+def test_experts_one_has_all(dev, rows):
+    """Every token at the last of many experts: its rows are more than one pass of a workgroup takes."""
+    rng = np.random.default_rng(rows)
+    codes, scales = ref.random_weights(rng, 40 * 50, 320)
+    codes, scales = codes.reshape(40, 50, -1), scales.reshape(40, 50, -1)
+    layer = pca.MX4Experts(experts=40, in_features=320, out_features=50, codes=codes, scales=scales)
+    x = rows_of(rng, rows, 320, dev, "f16")
+    o = pca.sort_by_expert(torch.full((rows, 1), 39, dtype=torch.int32, device=dev), 40)
+    check_product(layer.forward(x, o), x, (codes[39], scales[39], None), "f16")
+
+
+# --------------------------------------------------- together, streams, graphs
+
+class Block:
+    """A feed-forward layer of experts as a model would run it."""
+
+    def __init__(self, rng, width, hidden, experts):
+        def layer(n, k):
+            codes, scales = ref.random_weights(rng, experts * n, k, 116, 119)
+            w = codes.reshape(experts, n, -1), scales.reshape(experts, n, -1)
+            return pca.MX4Experts(experts=experts, in_features=k, out_features=n, codes=w[0], scales=w[1]), w
+        self.up, self.up_w = layer(2 * hidden, width)
+        self.down, self.down_w = layer(width, hidden)
+        self.hidden, self.experts = hidden, experts
+
+    def __call__(self, x, ids, weights):
+        order = pca.sort_by_expert(ids, self.experts)
+        both = self.up.forward(x, order)
+        h = torch.nn.functional.silu(both[:, :self.hidden]) * both[:, self.hidden:]
+        rows = self.down.forward(h, order, in_order=True)
+        return order, both, h, rows, order.combine(rows, weights)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("tokens", [1, 30, 500])
+def test_layer_of_experts(dev, dtype, tokens):
+    """Each step of a layer from what the step before it gave."""
+    rng = np.random.default_rng(tokens)
+    width, hidden, experts, choices = 320, 288, 6, 3
+    block = Block(rng, width, hidden, experts)
+    ids = make_ids(rng, tokens, choices, experts, 0.1)
+    offsets, order, position = ref.expert_order(ids, experts)
+    x = rows_of(rng, tokens, width, dev, dtype)
+    weights = torch.from_numpy(rng.random((tokens, choices)).astype(np.float32)).to(dev)
+    o, both, h, rows, y = block(x, torch.from_numpy(ids).to(dev), weights)
+    assert np.array_equal(o.position.cpu().numpy(), position)
+    xs = np.where(order[:, None] >= 0, host(x)[np.maximum(order, 0) // choices], 0)
+    for got, inputs, w in ((both, xs, block.up_w), (rows, host(h), block.down_w)):
+        for e in range(experts):
+            part = slice(offsets[e], offsets[e + 1])
+            want, mass = ref.linear(inputs[part], w[0][e], w[1][e], None)
+            assert (np.abs(host(got)[part] - want) <= ref.linear_bound(want, mass, inputs.shape[1], dtype)).all()
+    assert not host(rows)[offsets[-1]:].any()
+    terms = np.where((position >= 0)[..., None], host(rows)[np.maximum(position, 0)], 0) * host(weights)[..., None]
+    bound = (choices * 2.0 ** -24 * np.abs(terms).sum(1) + ref.HALF_STEP[dtype] * np.abs(terms.sum(1)) * (1 + 2.0 ** -20)
+             + ref.LEAST[dtype])
+    assert (np.abs(host(y) - terms.sum(1)) <= bound).all()
+
+
+@pytest.mark.parametrize("tokens", [3, 300])
+def test_graph_replays(dev, tokens):
+    """A captured layer with changing inputs, between eager work, and two
+    captured graphs in turn."""
+    rng = np.random.default_rng(tokens)
+    block = Block(rng, 320, 288, 6)
+    linear, _ = make_linear(rng, 6000, 3000, True)
+    x = rows_of(rng, tokens, 320, dev, "bf16")
+    wide = rows_of(rng, tokens, 6000, dev, "bf16")
+    ids = torch.from_numpy(make_ids(rng, tokens, 3, 6, 0.1)).to(dev)
+    weights = torch.rand((tokens, 3), device=dev)
+    dy = rows_of(rng, tokens, 320, dev, "bf16")
+
+    def run():
+        o, _, _, rows, y = block(x, ids, weights)
+        return [o.order.clone(), y, *o.combine_backward(dy, rows, weights), o.gather_backward(o.gather(x)), linear.forward(wide),
+                pca.mx4_quantize(x, values=True)[1]]
+
+    run()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()]
+    results = []
+    for g in graphs:
+        with torch.cuda.graph(g, stream=side):
+            results.append(run())
+    for turn in range(4):
+        x.copy_(rows_of(rng, tokens, 320, dev, "bf16"))
+        wide.copy_(rows_of(rng, tokens, 6000, dev, "bf16"))
+        ids.copy_(torch.from_numpy(make_ids(rng, tokens, 3, 6, 0.2)).to(dev))
+        want = run()
+        for g in graphs if turn % 2 else graphs[::-1]:
+            g.replay()
+        torch.cuda.synchronize()
+        for got in results:
+            for a, b in zip(got, want):
+                assert torch.equal(a, b)
+
+
+def test_streams(dev):
+    """Calls on another stream than the current one, two of them at once."""
+    rng = np.random.default_rng(2)
+    block = Block(rng, 320, 288, 6)
+    linear, _ = make_linear(rng, 6000, 3000, True)
+    ids = torch.from_numpy(make_ids(rng, 400, 2, 6)).to(dev)
+    x, wide = rows_of(rng, 400, 320, dev, "bf16"), rows_of(rng, 400, 6000, dev, "bf16")
+    want = pca.sort_by_expert(ids, 6)
+    up, y, q = block.up.forward(x, want), linear.forward(wide), pca.mx4_quantize(wide)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    for s in streams * 3:
+        o = pca.sort_by_expert(ids, 6, stream=s)
+        got.append((o.order, block.up.forward(x, o, stream=s), linear.forward(wide, stream=s),
+                    pca.mx4_quantize(wide, stream=s).codes, o.combine(o.gather(x, stream=s), stream=s)))
+    torch.cuda.synchronize()
+    for order, u, v, codes, back in got:
+        assert torch.equal(order, want.order) and torch.equal(u, up) and torch.equal(v, y) and torch.equal(codes, q.codes)
+        assert torch.equal(back, want.combine(want.gather(x)))
+
+
+def test_results_repeat(dev):
+    """Bit for bit: no sum depends on an order that changes."""
+    rng = np.random.default_rng(6)
+    block = Block(rng, 320, 288, 6)
+    x = rows_of(rng, 700, 320, dev, "f32")
+    ids = torch.from_numpy(make_ids(rng, 700, 4, 6, 0.1)).to(dev)
+    weights = torch.rand((700, 4), device=dev)
+    first = block(x, ids, weights)
+    grads = first[0].combine_backward(x, first[3], weights)
+    for _ in range(3):
+        again = block(x, ids, weights)
+        for a, b in zip((*first[1:], *grads), (*again[1:], *again[0].combine_backward(x, again[3], weights))):
+            assert torch.equal(a, b)
