@@ -111,7 +111,8 @@ typedef struct {
     const int32_t *order;    /* device [rows] with choices > 0 (offsets then too), otherwise NULL */
 } bconv_mx4_rows_t;
 
-/* Workspace bytes the call needs (0 is possible); looks at no pointer but whether x is NULL. */
+/* Workspace bytes the call needs (0 is possible); host only, looks at pointers
+ * only for whether x and offsets are NULL. */
 bconv_status_t bconv_mx4_linear_workspace_size(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args, size_t *bytes);
 
 /* y = the formula above.  offsets and order are those of bconv_expert_sort

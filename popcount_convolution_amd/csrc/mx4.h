@@ -161,12 +161,18 @@ struct RowBlock {
 constexpr int kRowGroup = 16;  // at most
 
 // Rows of all experts in blocks of up to `size`, expert by expert, those of none
-// last: list[0].f is their number, they follow (at most ceil(rows / size) + experts + 1).
+// last: list[0].f is their number, they follow (at most row_blocks_most(); offsets
+// that do not ascend could ask for more, which are left out).
 struct RowBlocks {
     const int *offsets;
     RowBlock *list;  // or nullptr: none is wanted
     int experts, rows, size;
 };
+
+__host__ __device__ inline int row_blocks_most(int rows, int experts, int size)
+{
+    return (rows + size - 1) / size + experts + 1;
+}
 
 constexpr int kListThreads = 256;
 
@@ -191,17 +197,18 @@ __device__ __forceinline__ void make_row_blocks(const RowBlocks &b)
     __syncthreads();
     int at = upto - count;
     for (int w = 0; w < wave; ++w) at += sums[w];
+    const int most = row_blocks_most(b.rows, b.experts, b.size);
     for (int f = f0; f < f0 + each && f <= b.experts; ++f) {
         const Span s = expert_rows(b.offsets, b.experts, b.rows, f);
         const int blocks = s.end > s.begin ? (s.end - s.begin + b.size - 1) / b.size : 0;
-        for (int i = 0; i < blocks; ++i) {
+        for (int i = 0; i < blocks && at + i < most; ++i) {
             const int r = s.begin + i * b.size, first = i / kRowGroup * kRowGroup;
             b.list[1 + at + i] = {f, r, s.end - r < b.size ? s.end : r + b.size,
                                   (at + first) * 32 + (blocks - first < kRowGroup ? blocks - first : kRowGroup)};
         }
         at += blocks;
     }
-    if (threadIdx.x == kListThreads - 1) b.list[0].f = at;
+    if (threadIdx.x == kListThreads - 1) b.list[0].f = at < most ? at : most;
 }
 
 // Launches the quantisation of rows (see bconv_mx4_quantize); arguments are

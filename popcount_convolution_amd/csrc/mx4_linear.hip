@@ -601,7 +601,7 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
         else p.variant = k424;
         return p;
     }
-    p.q.row_blocks = (a.rows + p.many - 1) / p.many + (a.offsets ? a.experts + 1 : 0);
+    p.q.row_blocks = a.offsets ? row_blocks_most(a.rows, a.experts, p.many) : (a.rows + p.many - 1) / p.many;
     const long long wide = (long long)p.q.row_blocks * ((a.tiles + 15) / 16);
     p.nt = wide >= cus ? 2 : 1;
     p.q.out_blocks = (a.tiles + p.nt * 8 - 1) / (p.nt * 8);

@@ -228,9 +228,20 @@ class ExpertOrder:
     int32 ``[tokens, choices]``, each pair's place, -1 where it is dropped."""
 
     def __init__(self, offsets, order, position, experts: int):
+        torch = _torch or _load()
+        _need_tensor(position, "position")
+        if position.dim() != 2 or not position.shape[1]:
+            raise ValueError(f"position: shape {tuple(position.shape)} is not (tokens, choices)")
+        for name, t, shape in (("offsets", offsets, (experts + 1,)), ("order", order, (position.numel(),)),
+                               ("position", position, position.shape)):
+            _need_dense(t, name, shape, torch.int32, position.device)
+        self._set(offsets, order, position, experts)
+
+    def _set(self, offsets, order, position, experts: int):
         self.offsets, self.order, self.position, self.experts = offsets, order, position, experts
         self.tokens, self.choices = position.shape
         self.device = position.device
+        return self
 
     def _rows(self, t, name: str, rows: int, dtype=None):
         """(width, row stride, dtype code) of a tensor ``[rows, width]``."""
@@ -240,8 +251,7 @@ class ExpertOrder:
         code = _dtype_code(t, name)
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
-        if t.device != self.device:
-            _need_cuda(t, name, self.device)
+        _need_cuda(t, name, self.device)
         return t.shape[1], _row_stride(t, name)[1], code
 
     def _weights(self, t):
@@ -317,6 +327,9 @@ class ExpertOrder:
         return d_rows, d_weights
 
 
+_sort_needs: dict = {}  # workspace bytes by (pairs, experts)
+
+
 def sort_by_expert(expert_ids, experts: int, stream=None) -> ExpertOrder:
     """Sorts the pairs of ``expert_ids`` (int32 or int64 ``[tokens, choices]``, the
     experts that each token chose) by expert, those of an expert in their order.
@@ -341,12 +354,17 @@ def sort_by_expert(expert_ids, experts: int, stream=None) -> ExpertOrder:
         # one allocation: offsets, order, positions
         flat = torch.empty(experts + 1 + 2 * pairs, dtype=torch.int32, device=device)
         offsets, order, position = flat.split_with_sizes((experts + 1, pairs, pairs))
-        need = B.bconv_expert_sort_workspace_size(pairs, experts)
+        need = _sort_needs.get((pairs, experts))
+        if need is None:
+            need = B.bconv_expert_sort_workspace_size(pairs, experts)
+            if len(_sort_needs) >= 4096:
+                _sort_needs.clear()
+            _sort_needs[pairs, experts] = need
         workspace = torch.empty(need, dtype=torch.uint8, device=device) if need else None
         base = flat.data_ptr()
         B.bconv_expert_sort(raw, pairs, experts, expert_ids.element_size(), expert_ids.data_ptr(), base,
                             base + 4 * (experts + 1), base + 4 * (experts + 1 + pairs), workspace, need)
-    return ExpertOrder(offsets, order, position.view(tokens, choices), experts)
+    return ExpertOrder.__new__(ExpertOrder)._set(offsets, order, position.view(tokens, choices), experts)
 
 
 class MX4Experts(_MX4Layer):

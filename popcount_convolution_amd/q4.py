@@ -24,12 +24,14 @@ _DTYPES: dict = {}  # torch dtype -> bconv_dtype_t
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _current_device
     import torch
     _DTYPES.update({torch.float32: B.BCONV_F32, torch.float16: B.BCONV_F16, torch.bfloat16: B.BCONV_BF16})
     # the current stream's handle without a Stream object around it, where torch has that
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                           lambda index: torch.cuda.current_stream(index).cuda_stream)
+    # the current device's index, without the check that CUDA is initialised (a device tensor is in hand)
+    _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
     _torch = torch
     return torch
 
@@ -135,7 +137,7 @@ def _place(device, stream):
     """(context to allocate and launch in, raw stream): nothing to enter when
     the call goes to the current device's current stream."""
     if stream is None:
-        if device.index == _torch.cuda.current_device():
+        if device.index == _current_device():
             return _STAY, _raw_stream(device.index)
         stream = _torch.cuda.current_stream(device)
     elif stream.device != device:

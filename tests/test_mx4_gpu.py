@@ -418,6 +418,27 @@ def test_experts_like_one_layer(dev):
         assert (np.abs(host(layer.forward(x, o)) - host(one.forward(x))) <= 2 * ref.linear_bound(want, mass, 400, "f32")).all()
 
 
+def test_experts_offsets_out_of_order(dev):
+    """Offsets and an order that no sort has given stay inside the buffers."""
+    rng = np.random.default_rng(1)
+    codes, scales = ref.random_weights(rng, 6 * 40, 64)
+    layer = pca.MX4Experts(experts=6, in_features=64, out_features=40, codes=codes.reshape(6, 40, -1),
+                           scales=scales.reshape(6, 40, -1))
+    ints = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
+    for tokens in (50, 700):
+        pairs = 2 * tokens
+        x = rows_of(rng, tokens, 64, dev, "bf16")
+        order = torch.randint(-(1 << 30), 1 << 30, (pairs,), device=dev, dtype=torch.int32)
+        position = torch.randint(-(1 << 30), 1 << 30, (tokens, 2), device=dev, dtype=torch.int32)
+        o = pca.ExpertOrder(ints([0, pairs, -5, pairs + 99, 0, pairs, 7]), order, position, 6)
+        buf = torch.full((pairs + 2, 40), 7.0, device=dev, dtype=torch.bfloat16)
+        layer.forward(x, o, out=buf[1:-1])
+        layer.forward(x.repeat(2, 1), o, out=buf[1:-1], in_order=True)
+        o.combine(o.gather(x))
+        torch.cuda.synchronize()
+        assert bool((buf[0] == 7).all()) and bool((buf[-1] == 7).all())
+
+
 @pytest.mark.parametrize("rows", [16, 100])
 def test_experts_one_has_all(dev, rows):
     """Every token at the last of many experts: its rows are more than one pass of a workgroup takes."""
@@ -428,6 +449,95 @@ def test_experts_one_has_all(dev, rows):
     x = rows_of(rng, rows, 320, dev, "f16")
     o = pca.sort_by_expert(torch.full((rows, 1), 39, dtype=torch.int32, device=dev), 40)
     check_product(layer.forward(x, o), x, (codes[39], scales[39], None), "f16")
+
+
+def test_wrappers_refuse(dev):
+    """What the wrappers check once tensors are on the GPU."""
+    rng = np.random.default_rng(0)
+    o = pca.sort_by_expert(torch.zeros((4, 2), dtype=torch.int32, device=dev), 3)
+    x, rows, w = (torch.zeros(s, device=dev) for s in ((4, 10), (8, 10), (4, 2)))
+    layer, _ = make_linear(rng, 64, 10, False)
+    codes, scales = ref.random_weights(rng, 3 * 10, 64)
+    experts = pca.MX4Experts(experts=3, in_features=64, out_features=10, codes=codes.reshape(3, 10, -1),
+                             scales=scales.reshape(3, 10, -1))
+    xs = torch.zeros((4, 64), device=dev, dtype=torch.bfloat16)
+    q = pca.mx4_quantize(xs)
+    for f, match in (
+            (lambda: o.combine(rows, torch.zeros((8, 1), device=dev)), "shape"), (lambda: o.combine(rows, w.double()), "dtype"),
+            (lambda: o.combine(rows, w.t().contiguous().t()), "contiguous"), (lambda: o.combine(rows, w.cpu()), "device"),
+            (lambda: o.combine(rows, w, out=x[:, :9]), "shape"), (lambda: o.gather(x, out=rows.half()), "dtype"),
+            (lambda: o.combine_backward(x, rows[:, :9], w), "values"), (lambda: o.combine_backward(x, rows.half(), w), "dtype"),
+            (lambda: o.combine_backward(x, rows, None, d_weights=w), "without weights"), (lambda: o.gather(x.cpu()), "device"),
+            (lambda: o.gather(torch.zeros((10, 4), device=dev).t()), "strides"),
+            (lambda: layer.forward(xs[:, :63]), "does not end"), (lambda: layer.forward(xs.cpu()), "device"),
+            (lambda: layer.forward(xs, out=torch.zeros((4, 11), device=dev)), "shape"),
+            (lambda: layer.forward(xs, out=torch.zeros((4, 10), device=dev)), "dtype"),
+            (lambda: layer.forward(xs, dtype=torch.float32), "their type"), (lambda: layer.forward(q, dtype=torch.int32), "dtype"),
+            (lambda: layer.forward(pca.MX4Tensor(q.codes, q.scales, 60)), "rows of 60"),
+            (lambda: layer.forward(pca.MX4Tensor(q.codes[:, :64], q.scales, 64)), "codes: shape|scales: shape"),
+            (lambda: layer.forward(pca.MX4Tensor(q.codes, q.scales[:3], 64)), "scales: shape"),
+            (lambda: layer.forward(torch.zeros((300, 64), device=dev, dtype=torch.bfloat16),
+                                   workspace=torch.zeros(8, dtype=torch.uint8, device=dev)), "needed"),
+            (lambda: experts.forward(xs, None), "ExpertOrder"), (lambda: experts.forward(xs[:3], o), "rows"),
+            (lambda: experts.forward(xs, o, in_order=True), "rows"),
+            (lambda: experts.forward(xs, pca.sort_by_expert(torch.zeros((4, 2), dtype=torch.int32, device=dev), 4)), "4 experts"),
+            (lambda: pca.MX4Linear(in_features=64, out_features=10, codes=codes, scales=scales), "shape"),
+            (lambda: pca.MX4Linear(in_features=64, out_features=30, codes=codes.astype(np.int8), scales=scales), "dtype"),
+            (lambda: pca.MX4Linear(in_features=0, out_features=30, codes=codes, scales=scales), "positive"),
+            (lambda: pca.sort_by_expert(torch.zeros((4, 2), dtype=torch.int32, device=dev), 0), "experts"),
+            (lambda: pca.sort_by_expert(torch.zeros((4, 2), dtype=torch.int32, device=dev), 1025), "experts")):
+        with pytest.raises(ValueError, match=match):
+            f()
+    for f in (lambda: o.combine(rows, out=rows[:4]),
+              lambda: experts.forward(xs, o, out=xs.as_strided((8, 10), (32, 1)))):
+        with pytest.raises(pca.BconvError, match="overlap"):
+            f()
+
+
+# -------------------------------------------------------------- far offsets
+
+def test_rows_past_32_bits(dev):
+    """Results of more than 2^32 bytes."""
+    tokens, width = 70001, 32768
+    x = torch.randn((2, width), device=dev).to(torch.bfloat16).repeat_interleave(torch.tensor([tokens - 1, 1], device=dev), 0)
+    ids = torch.zeros((tokens, 1), dtype=torch.int32, device=dev)
+    ids[0] = 1                                                       # the first token's row is the last
+    o = pca.sort_by_expert(ids, 2)
+    rows = o.gather(x)
+    assert torch.equal(rows[-1], x[0]) and torch.equal(rows[-2], x[-1]) and torch.equal(rows[0], x[1])
+    rows[-1] *= 2
+    y = o.combine(rows)
+    assert torch.equal(y[0], x[0] * 2) and torch.equal(y[-1], x[-1]) and torch.equal(y[-2], x[-2])
+    del rows, y
+    q, values = pca.mx4_quantize(x, values=True)
+    want = ref.quantise(host(x[-2:]))
+    assert np.array_equal(q.codes[-2:].cpu().numpy(), want[0]) and np.array_equal(host(values[-2:]), want[2])
+
+
+def test_products_past_32_bits(dev):
+    """Results, and codes of all experts, of more than 2^32 bytes."""
+    rng = np.random.default_rng(9)
+    layer, weights = make_linear(rng, 40, 32771, True)
+    x = rows_of(rng, 66000, 40, dev, "f16")
+    y = layer.forward(x)
+    check_product(y[-130:], x[-130:], weights, "f16")
+    check_product(y[:5], x[:5], weights, "f16")
+    del y
+    layer.close()
+    experts, k, n = 130, 8192, 8200
+    codes = torch.randint(0, 256, (experts, n, k // 2), dtype=torch.uint8, device=dev)
+    scales = torch.randint(118, 122, (experts, n, k // 32), dtype=torch.uint8, device=dev)
+    layer = pca.MX4Experts(experts=experts, in_features=k, out_features=n, codes=codes, scales=scales)
+    for tokens in (2, 30):
+        x = rows_of(rng, tokens, k, dev, "bf16")
+        ids = torch.full((tokens, 100), experts - 1, dtype=torch.int32, device=dev)
+        ids[:, 1:] = -1
+        ids[0, 0] = 0
+        o = pca.sort_by_expert(ids, experts)
+        y = layer.forward(x, o)
+        for e, part in ((0, slice(0, 1)), (experts - 1, slice(1, tokens))):
+            w = codes[e].cpu().numpy(), scales[e].cpu().numpy(), None
+            check_product(y[part], x[0:1] if e == 0 else x[1:], w, "bf16")
 
 
 # --------------------------------------------------- together, streams, graphs
