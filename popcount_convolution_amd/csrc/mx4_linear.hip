@@ -472,10 +472,11 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
             for (int v = 0; v < 4; ++v) {
                 const int o = y0 + t * 32 + v * 8 + half * 4;
                 bias[t][v] = f32x4{0, 0, 0, 0};
-                if (a.bias)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (o + j < a.n) bias[t][v][j] = a.bias[(long long)f * a.n + o + j];
+                if (!a.bias || o >= a.n) continue;
+                const float *b = a.bias + (long long)f * a.n + o;
+                if (o + 4 <= a.n) bias[t][v] = *reinterpret_cast<const f32x4_any *>(b);
+                else
+                    for (int j = 0; j < a.n - o; ++j) bias[t][v][j] = b[j];
             }
         auto biased = [&](int m, int t, int v) {
             return f32x4{acc[m][t][4 * v], acc[m][t][4 * v + 1], acc[m][t][4 * v + 2], acc[m][t][4 * v + 3]} + bias[t][v];
