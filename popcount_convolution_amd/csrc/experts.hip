@@ -319,7 +319,7 @@ template <int DT, bool MANY, bool AWAY> __global__ __launch_bounds__(kRowThreads
 }
 
 // A workgroup a token: dy's row is read once for kTogether choices.
-template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(RowsArgs a)
+template <int DT, bool AWAY> __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(RowsArgs a)
 {
     constexpr int V = kPiece<DT>;
     __shared__ float part[kRowThreads / 64][kTogether];
@@ -348,7 +348,7 @@ template <int DT> __global__ __launch_bounds__(kRowThreads) void expert_combine_
                 Piece<DT> g;
 #pragma unroll
                 for (int i = 0; i < V; ++i) g.v[i] = (typename Elem<DT>::type)(w[j] * (float)d.v[i]);
-                g.store(a.to, (long long)at[j] * a.width + c, left);
+                g.template store<AWAY>(a.to, (long long)at[j] * a.width + c, left);
                 if (a.d_weights)
 #pragma unroll
                     for (int i = 0; i < V; ++i) dot[j] = __builtin_fmaf((float)d.v[i], (float)r[j].v[i], dot[j]);
@@ -384,14 +384,14 @@ template <int DT, bool AWAY> static void launch_rows(RowsOp op, const RowsArgs &
         if (a.choices > kTogether) hipLaunchKernelGGL((expert_combine_kernel<DT, true, AWAY>), dim3(grid), dim3(kRowThreads), 0, s, a);
         else hipLaunchKernelGGL((expert_combine_kernel<DT, false, AWAY>), dim3(grid), dim3(kRowThreads), 0, s, a);
         break;
-    default: hipLaunchKernelGGL((expert_combine_backward_kernel<DT>), dim3(grid), dim3(kRowThreads), 0, s, a);
+    default: hipLaunchKernelGGL((expert_combine_backward_kernel<DT, AWAY>), dim3(grid), dim3(kRowThreads), 0, s, a);
     }
 }
 
 template <int DT> static hipError_t run_rows(RowsOp op, RowsArgs a, hipStream_t s)
 {
     // 32772 rows of 4096 16-bit values gathered: 67 us, 52 past the caches; combined: 64, 50;
-    // 12294 rows of 5003 fp32 values combined: 76, 55 (the gradient's rows, written between reads: 119, 136).
+    // gradients: 138, 130; of 12294 rows of 5003 fp32 values: 135, 115.
     // Smaller results may still be there when they are read; gathered rows that end inside a line are
     // better put together in the caches (5003 fp32 values: 65, 73).
     const int es = DT == BCONV_F32 ? 4 : 2;

@@ -37,12 +37,17 @@ template <int DT> struct Eight {
 };
 
 // Those of them that are in the row, zeros for the rest (`left` of them remain).
-template <int DT> __device__ __forceinline__ Eight<DT> load_values(const typename Elem<DT>::type *p, int left)
+// ONCE: nothing here reads them again.
+template <int DT, bool ONCE = false> __device__ __forceinline__ Eight<DT> load_values(const typename Elem<DT>::type *p, int left)
 {
     Eight<DT> e;
     if (left >= 8) {
 #pragma unroll
-        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) e.q[i] = reinterpret_cast<const u32x4_any *>(p)[i];
+        for (int i = 0; i < (DT == BCONV_F32 ? 2 : 1); ++i) {
+            const u32x4_any *q = reinterpret_cast<const u32x4_any *>(p) + i;
+            if constexpr (ONCE) e.q[i] = __builtin_nontemporal_load(q);
+            else e.q[i] = *q;
+        }
         return e;
     }
     if constexpr (DT == BCONV_F32) {

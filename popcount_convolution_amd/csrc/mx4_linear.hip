@@ -81,12 +81,13 @@ __device__ __forceinline__ Span expert_span(const Mx4Args &a, int f)
     return expert_rows(a.offsets, a.experts, a.rows, f);
 }
 
-// Input row of result row i (i < rows).
-__device__ __forceinline__ int input_row(const Mx4Args &a, int i)
+// Input row of result row i (i < rows): what pair_of() loads, then input_row().
+__device__ __forceinline__ int pair_of(const Mx4Args &a, int i) { return a.choices == 0 ? i : a.order[i]; }
+
+__device__ __forceinline__ int input_row(const Mx4Args &a, int pair)
 {
-    if (a.choices == 0) return i;
-    const int p = a.order[i];
-    const int r = p < 0 ? 0 : p / a.choices;
+    if (a.choices == 0) return pair;
+    const int r = pair < 0 ? 0 : pair / a.choices;
     return r < a.x_rows ? r : a.x_rows - 1;
 }
 
@@ -180,7 +181,7 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
 #pragma unroll
         for (int t = 0; t < CT; ++t) {
             real[t] = m0 + t * 16 + row < span.end;
-            xr[t] = real[t] ? input_row(a, m0 + t * 16 + row) : 0;
+            xr[t] = real[t] ? input_row(a, pair_of(a, m0 + t * 16 + row)) : 0;
             x[t] = {{u32x4{0, 0, 0, 0}, u32x4{0, 0, 0, 0}}, 0};
 #pragma unroll
             for (int r = 0; r < RT; ++r) acc[r][t] = f32x4{0, 0, 0, 0};
@@ -291,15 +292,14 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
     // Where this lane's part of the loads comes from: rows and tiles past the last
     // count as the last.  Offsets stay below kNone.
     const long long x_base = a.choices ? 0 : span.begin;
-    auto x_row = [&](int r) { return (uint32_t)(input_row(a, min(span.begin + r, span.end - 1)) - x_base); };
-    uint32_t xo[XL], xso, wo[NT], wso[NT];
-#pragma unroll
-    for (int j = 0; j < XL; ++j) {
-        const int r = (j * WAVES + wave) * 8 + (lane >> 3);
-        xo[j] = x_row(r) * a.steps * 128 + ((lane & 7) ^ (r >> 1 & 7)) * 16;
-    }
     const int my_scales = wave % MT * 32;  // with few rows, several waves load the same
-    xso = (uint32_t)(x_row(my_scales + (lane >> 1)) * a.xs_row + (lane & 1) * 4);
+    int pair[XL + 1];
+#pragma unroll
+    for (int j = 0; j <= XL; ++j) {
+        const int r = j < XL ? (j * WAVES + wave) * 8 + (lane >> 3) : my_scales + (lane >> 1);
+        pair[j] = pair_of(a, min(span.begin + r, span.end - 1));
+    }
+    uint32_t xo[XL], xso, wo[NT], wso[NT];
     const int my_tile = tile0 + wave * NT * 2;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -383,15 +383,22 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
         }
     };
     static_assert(4 % (WD + 1) == 0 && (STAGES - 2) * (WV + XV) < 64);
-#pragma unroll
-    for (int d = 0; d < STAGES - 1; ++d)
-#pragma unroll
-        for (int l = 0; l < XV; ++l) request_x(s_begin + d, d, l);
+    // the first weights are on their way while the pairs arrive that say which rows of x
 #pragma unroll
     for (int d = 0; d < WD; ++d)
 #pragma unroll
         for (int l = 0; l < WV; ++l) request_w(s_begin + d, d, l);
-    __builtin_amdgcn_s_waitcnt(vm_wait(WD * WV));  // x of three steps is here
+#pragma unroll
+    for (int j = 0; j < XL; ++j) {
+        const int r = (j * WAVES + wave) * 8 + (lane >> 3);
+        xo[j] = (uint32_t)(input_row(a, pair[j]) - x_base) * a.steps * 128 + ((lane & 7) ^ (r >> 1 & 7)) * 16;
+    }
+    xso = (uint32_t)((input_row(a, pair[XL]) - x_base) * a.xs_row + (lane & 1) * 4);
+#pragma unroll
+    for (int d = 0; d < STAGES - 1; ++d)
+#pragma unroll
+        for (int l = 0; l < XV; ++l) request_x(s_begin + d, d, l);
+    __builtin_amdgcn_s_waitcnt(vm_wait(0));  // x of three steps is here
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll

@@ -4,6 +4,10 @@
 // their largest magnitude by two swaps, its exponent is the scale, and the
 // conversion instruction rounds a pair of values under it: about 20 vector
 // instructions for 8 values of 16 bits, next to their 16 bytes.
+//
+// Bound by its bytes: 8193 x 8192 bf16 with the values, 304 MB, 46 us (6.6 TB/s; 51
+// with loads that fill the caches), without them, 170 MB, 28 to 34 us.
+// 32 x 4096: 3.6 us, a launch and one chain of a load and a store.
 #include <hip/hip_runtime.h>
 
 #include "host.h"
@@ -93,7 +97,7 @@ template <int DT, bool VALUES> __global__ __launch_bounds__(kQuantThreads) void 
         row[j] = unit / a.per_row;
         at[j] = (unit - row[j] * a.per_row) * 8;
         const int left = unit < a.units ? a.cols - (int)at[j] : 0;
-        v[j] = load_values<DT>(static_cast<const T *>(a.x) + (left > 0 ? (long long)row[j] * a.ldx + at[j] : 0), left);
+        v[j] = load_values<DT, true>(static_cast<const T *>(a.x) + (left > 0 ? (long long)row[j] * a.ldx + at[j] : 0), left);
     }
 #pragma unroll
     for (int j = 0; j < kQuantEach; ++j) {
