@@ -145,7 +145,13 @@ template <int DT> __device__ __forceinline__ XStep quantised_step(const typename
 
 // Few rows of x for the weights.  A workgroup takes 16 RT outputs of one expert and
 // its rows 16 CT at a time; its waves split the inputs step by step and add their
-// sums in LDS, in a fixed order.
+// sums in LDS, in a fixed order.  The weights go from global memory to the matrix
+// cores without passing LDS, as in memory.
+//
+// Bound by the weights' bytes: 1 x 25088 -> 4096, 54.6 MB, 8.4 to 9.5 us (5.7 to 6.5 TB/s;
+// a large read reaches 5.8), after 2.8 us that quantise the row; 13 x 5000 -> 11003 fp32 6.0 to 7.3 us
+// after 3.6; 32 tokens' 4 of 64 experts of 2048 -> 2816, 170 MB, 26 us (6.5 TB/s, rows quantised here).
+// 512 -> 512: 3.1 us, the launch and a chain of loads.
 template <int DT, bool QUANTISED, int RT, int CT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
 {
@@ -236,6 +242,26 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
 }
 
 // ------------------------------------------------------------------ many rows
+//
+// Four waves lie along the outputs and share 128 rows of x: x goes through LDS,
+// where every wave reads all of it, while a wave's weights are its own and go
+// from global memory to its registers in the order that they were laid out in.
+// x's stages are requested three steps ahead, by loads that pass no registers,
+// weights one step (three, in the narrow shape); the loads, 10 to 15 a step, lie
+// between the matrix instructions one by one, so that neither waits for the
+// other's issue.  32x32x64 instructions: with scales and random codes, one wave a
+// SIMD reaches 6.4 PFLOP/s with them and 4.2 with 16x16x128 (9.1 and 5.1 on zeros:
+// the clock falls with the bits that toggle).
+//
+// Bound by power for large products: 8192 x 8192 -> 8192 bf16, 231 to 280 us (3.9 to
+// 4.8 PFLOP/s, 3.3 to 4 times a large bf16 library product), matrix cores busy 74%
+// of the cycles at 1.3 to 1.5 GHz (an earlier form took as many cycles on zeros, at
+// 2.3 GHz instead of 1.7).  On the way there: both operands in LDS with 16x16x128
+// instructions 435 to 460 us, with 32x32x64 330 to 370, weights in registers 320,
+// results as whole lines 285, a ring of register sets and exact waits 250.
+// For experts by the weights' and results' bytes: 16396 rows of 64 experts, 2048 ->
+// 2816, 300 MB, 66 to 81 us (3.7 to 4.5 TB/s).  256 x 25088 -> 4096, 14 to 22 us, by the
+// latency of the weights, three steps ahead in 256 workgroups.
 
 // What the many-row kernel takes besides Mx4Args.
 struct Mx4Many {
@@ -249,11 +275,11 @@ struct Mx4Many {
 // The list of row blocks, where no other launch makes it.
 __global__ __launch_bounds__(kListThreads) void mx4_blocks_kernel(RowBlocks b) { make_row_blocks(b); }
 
-template <typename E> struct Values {
+template <typename E> struct Values {  // of 16 bytes
     E v[16 / sizeof(E)];
 };
 
-// s_waitcnt for vector memory alone (and LDS): at most `n` loads outstanding.
+// s_waitcnt: at most `n` vector loads outstanding, no LDS read.
 constexpr int vm_wait(int n) { return (n & 15) | (n >> 4 << 14) | (0x7 << 4) | (0x0 << 8); }
 
 constexpr uint32_t kNone = 0x80000000u;  // outside every buffer: a load from there reads no memory and gives 0
@@ -545,7 +571,7 @@ __global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
     else many_rows<DT, 1, NT, WD>(a, q, lds, f, span, tile0, split);
 }
 
-// Adds the splits' sums in order.
+// Adds the splits' sums in order.  Bound by its bytes: 4 sums of 256 x 4096, 19 MB, 4.0 to 5.0 us.
 template <int DT> __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args a, Mx4Many q)
 {
     const int per = (a.n + 3) / 4;
@@ -577,23 +603,25 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
 {
     Mx4Plan p{};
     const int mean = (a.rows + a.experts - 1) / a.experts;
-    // The few-row kernel reads the codes once for 16 or 32 rows, of one layer or of
-    // each expert; the many-row kernel takes 128 rows and its launches cost some 5 to 10 us more.
-    // It pays for many codes read that way, and where its workgroups fill half the card
-    // without splitting the inputs.  One layer,
-    // 25088 -> 4096, 32 rows: 16.6 us against 19.4, 64: 22.2 against 20.5; 8192 -> 11008, 32:
-    // 13.7 against 17.3, 48: 19.6 against 18.0; 256 rows of 4096 -> 4096: 13.9 against 20.6; 8192 rows of 512 ->
-    // 512: 15.2 against 10.5; 512 of 1024 -> 4096: 11.2 against 9.5.  64 experts of 2048 -> 2816, 16 rows
-    // each: 34.5 against 39.0, 32: 50.2 against 40.0.
+    // The few-row kernel reads the codes once for 16 or 32 rows, of one layer or
+    // of each expert; the many-row kernel takes 128 rows and its launches cost 5 to
+    // 10 us more.  It pays for many codes read that way, and where its workgroups
+    // fill half the card without splitting the inputs.  One layer, few against many:
+    // 25088 -> 4096, 32 rows 16.6 us and 19.4, 64 rows 22.2 and 20.5; 12000 -> 6000,
+    // 40 rows 25.9 and 16.6; 8192 -> 11008, 32 rows 13.7 and 17.3, 48 rows 19.6 and 18.0;
+    // 4096 -> 1024, 512 rows 11.0 and 16.0; 512 -> 512, 8192 rows 15.2 and 10.5; 1024 ->
+    // 4096, 512 rows 11.2 and 9.5.  64 experts of 2048 -> 2816, 16 rows each 34.5 and
+    // 39.0, 32 rows each 50.2 and 40.0.
     const long long blocks = (a.rows + 127LL) / 128 * ((a.tiles + 7) / 8);
     const bool many = a.offsets ? mean > 20
                                 : (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << (a.rows > 32 ? 26 : 27) ||
                                       (a.rows > 128 && blocks * 2 >= cus);
     p.many = many ? kManyRows : 0;
-    // Quantising in the few-row kernel costs every workgroup a little for each step, a launch of its own
-    // 1.2 us and the host's call: 1 row, 4096 -> 4096, 4.6 us against 5.6; 25088 -> 4096, 14.2
-    // against 12.2; 12 rows, 4096 -> 4096, 6.4 against 6.4; 16 rows, 2048 -> 2048, 5.0 against 6.1, 6000 -> 1500, 9.1 against 7.4.
-    // 128 experts of 512 -> 1024, 4 rows each, 9.8 against 11.8; 8 of 4096 -> 4096, 16 rows, 26.4 against 16.5.
+    // Quantising in the few-row kernel costs every workgroup a little for each step,
+    // a launch of its own 1.2 us and the host's call.  There against in a launch: 1 row,
+    // 4096 -> 4096, 4.6 us and 5.6, 25088 -> 4096 14.2 and 12.2; 12 rows, 4096 -> 4096, 6.4
+    // and 6.4; 16 rows, 2048 -> 2048, 5.0 and 6.1, 6000 -> 1500 9.1 and 7.4.  128 experts of
+    // 512 -> 1024, 4 rows each, 9.8 and 11.8; 8 of 4096 -> 4096, 16 rows each, 26.4 and 16.5.
     p.quantise = !given && (many || (a.offsets ? mean > 4 || a.steps > 8 : a.rows > 16 || a.steps > 24 || a.rows * a.steps > 192));
     auto take = [&](size_t n) {
         const size_t at = p.bytes;
@@ -606,9 +634,11 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
     }
     if (!many) {
         // Output tiles and row tiles a workgroup share their operands, waves the
-        // inputs.  One tile and eight waves while that is two workgroups a
-        // compute unit at most (16 rows of 25088 -> 4096: 14.1 us, two tiles 16.0; of 2048 ->
-        // 16384: two tiles and four waves 7.0, one tile 7.9); more rows share more.
+        // inputs.  One tile and eight waves while that is two workgroups a compute
+        // unit at most (16 rows of 25088 -> 4096: 14.1 us, two tiles 16.0; of 2048 ->
+        // 16384: two tiles and four waves 7.0, one tile 7.9); more rows share more (32 rows of
+        // 8192 -> 11008: four and two tiles 14.3, two tiles 16.7; 128 of 4096 -> 4096: 10.0 and 11.4).
+        // Experts: two and two tiles (16 rows each of 8 of 4096 -> 4096: 16.5; four and two 17.1).
         const bool small = a.tiles <= 2 * cus, direct = !given && !p.quantise;
         if (a.offsets) p.variant = direct ? k414 : k224;
         else if (direct) p.variant = small ? k118 : k418;
@@ -618,6 +648,8 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
         return p;
     }
     p.q.row_blocks = a.offsets ? row_blocks_most(a.rows, a.experts, p.many) : (a.rows + p.many - 1) / p.many;
+    // 256 outputs a workgroup where that fills the card (8192 x 8192 -> 8192: 321 us, 128 outputs 382; 16396 rows
+    // of 64 experts: 73, 91); otherwise 128 and weights requested three steps ahead (256 x 25088 -> 4096: 28.2, 30.9).
     const long long wide = (long long)p.q.row_blocks * ((a.tiles + 15) / 16);
     p.nt = wide >= cus ? 2 : 1;
     p.q.out_blocks = (a.tiles + p.nt * 8 - 1) / (p.nt * 8);
@@ -626,6 +658,8 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
     if (a.offsets) {
         p.list_offset = take((size_t)(p.q.row_blocks + 1) * sizeof(RowBlock));
     } else {
+        // a workgroup a compute unit, at least 12 steps each: joining the sums costs 5 us and more (256 x 4096 ->
+        // 4096, 16 steps: two splits 15.7, one 13.5; 200 x 8192 -> 2048, 32 steps: two splits 17.2, one 18.9)
         long long splits = cus / ((long long)p.q.row_blocks * p.q.out_blocks);
         if (splits > a.steps / 12) splits = a.steps / 12;
         if (splits > 8) splits = 8;
