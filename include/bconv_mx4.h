@@ -22,7 +22,7 @@
  * memory and must stay valid until the stream's work completes.  Calls
  * without a handle run on the current HIP device; a handle's are launched on
  * the device it was created on, to which their buffers and stream belong.
- * Rows may start at any element.
+ * Rows may start at any element; row strides are at most 2^30 elements.
  */
 #ifndef BCONV_MX4_H
 #define BCONV_MX4_H

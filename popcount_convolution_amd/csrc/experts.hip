@@ -464,7 +464,7 @@ bconv_status_t check_rows(int32_t tokens, int32_t choices, int32_t width, int32_
     if (tokens < 0 || choices < 1 || (long long)tokens * choices > kMaxPairs)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "tokens >= 0, choices >= 1 and tokens*choices <= 2^27 are needed");
     if (width < 1 || width > (1 << 20)) return fail(BCONV_ERR_INVALID_ARGUMENT, "width must be in [1, %d]", 1 << 20);
-    if (ld < width || ld > (1LL << 40)) return fail(BCONV_ERR_INVALID_ARGUMENT, "%s must be in [width, 2^40]", name);
+    if (ld < width || ld > bconv::kMaxStride) return fail(BCONV_ERR_INVALID_ARGUMENT, "%s must be in [width, 2^30]", name);
     return BCONV_OK;
 }
 

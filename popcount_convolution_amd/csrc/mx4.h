@@ -31,6 +31,9 @@ __host__ __device__ constexpr long long mx4_padded(long long cols)
     return (cols + BCONV_MX4_PAD - 1) / BCONV_MX4_PAD * BCONV_MX4_PAD;
 }
 
+// Elements between rows at most: the bytes of a call's rows stay below 2^63.
+constexpr long long kMaxStride = 1LL << 30;
+
 // 8 consecutive values of one row as loaded.
 template <int DT> struct Eight {
     u32x4 q[DT == BCONV_F32 ? 2 : 1];
@@ -206,10 +209,11 @@ __device__ __forceinline__ void make_row_blocks(const RowBlocks &b)
     for (int f = f0; f < f0 + each && f <= b.experts; ++f) {
         const Span s = expert_rows(b.offsets, b.experts, b.rows, f);
         const int blocks = s.end > s.begin ? (s.end - s.begin + b.size - 1) / b.size : 0;
-        for (int i = 0; i < blocks && at + i < most; ++i) {
+        const int held = blocks < most - at ? blocks : most - at;
+        for (int i = 0; i < held; ++i) {
             const int r = s.begin + i * b.size, first = i / kRowGroup * kRowGroup;
             b.list[1 + at + i] = {f, r, s.end - r < b.size ? s.end : r + b.size,
-                                  (at + first) * 32 + (blocks - first < kRowGroup ? blocks - first : kRowGroup)};
+                                  (at + first) * 32 + (held - first < kRowGroup ? held - first : kRowGroup)};
         }
         at += blocks;
     }

@@ -907,9 +907,9 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
     if (!args->y || (!args->x && (!args->codes || !args->scales)))
         return fail(BCONV_ERR_INVALID_ARGUMENT, "y and x (or codes and scales) must not be NULL");
     if (args->x && (args->codes || args->scales)) return fail(BCONV_ERR_INVALID_ARGUMENT, "x and codes are both given");
-    if (args->ldy < n || args->ldy > (1LL << 40)) return fail(BCONV_ERR_INVALID_ARGUMENT, "ldy must be in [out_features, 2^40]");
-    if (args->x && (args->ldx < k || args->ldx > (1LL << 40)))
-        return fail(BCONV_ERR_INVALID_ARGUMENT, "ldx must be in [in_features, 2^40]");
+    if (args->ldy < n || args->ldy > bconv::kMaxStride) return fail(BCONV_ERR_INVALID_ARGUMENT, "ldy must be in [out_features, 2^30]");
+    if (args->x && (args->ldx < k || args->ldx > bconv::kMaxStride))
+        return fail(BCONV_ERR_INVALID_ARGUMENT, "ldx must be in [in_features, 2^30]");
     if (((uintptr_t)args->x | (uintptr_t)args->y) % es) return fail(BCONV_ERR_INVALID_ARGUMENT, "x/y not aligned to an element");
     if ((uintptr_t)args->codes % 16 || (uintptr_t)args->scales % 8)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "codes must be 16-byte aligned, scales 8-byte");

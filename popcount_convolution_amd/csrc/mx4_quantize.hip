@@ -167,7 +167,7 @@ extern "C" bconv_status_t bconv_mx4_quantize(void *stream, int32_t rows, int32_t
     if (!es) return fail(BCONV_ERR_INVALID_ARGUMENT, "unknown dtype %d", dtype);
     if (rows < 0) return fail(BCONV_ERR_INVALID_ARGUMENT, "rows must be >= 0");
     if (cols < 1 || cols > (1 << 20)) return fail(BCONV_ERR_INVALID_ARGUMENT, "cols must be in [1, %d]", 1 << 20);
-    if (ldx < cols || ldx > (1LL << 40)) return fail(BCONV_ERR_INVALID_ARGUMENT, "ldx must be in [cols, 2^40]");
+    if (ldx < cols || ldx > bconv::kMaxStride) return fail(BCONV_ERR_INVALID_ARGUMENT, "ldx must be in [cols, 2^30]");
     if (rows == 0) return BCONV_OK;
     if (!x || !codes || !scales) return fail(BCONV_ERR_INVALID_ARGUMENT, "x, codes and scales must not be NULL");
     if (((uintptr_t)x | (uintptr_t)values) % es) return fail(BCONV_ERR_INVALID_ARGUMENT, "x/values not aligned to an element");

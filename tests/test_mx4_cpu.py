@@ -51,7 +51,7 @@ X, C, S, V = 1 << 20, 2 << 20, 3 << 20, 4 << 20
 
 
 @pytest.mark.parametrize("change", [
-    dict(rows=-1), dict(cols=0), dict(cols=(1 << 20) + 1), dict(dtype=3), dict(dtype=-1), dict(ldx=99), dict(ldx=(1 << 40) + 1),
+    dict(rows=-1), dict(cols=0), dict(cols=(1 << 20) + 1), dict(dtype=3), dict(dtype=-1), dict(ldx=99), dict(ldx=(1 << 30) + 1),
     dict(x=None), dict(codes=None), dict(scales=None), dict(x=X + 1), dict(codes=C + 8), dict(scales=S + 4), dict(values=V + 1),
     dict(codes=X), dict(scales=X), dict(values=X), dict(values=C), dict(scales=C)])
 def test_quantize_refuses(lib, change):
@@ -110,7 +110,7 @@ COMMON = [dict(tokens=-1), dict(choices=0), dict(tokens=1 << 20, choices=1 << 8)
 
 
 @pytest.mark.parametrize("change", COMMON + [
-    dict(ldx=9), dict(ldx=(1 << 40) + 1), dict(x=None), dict(order=None), dict(rows=None), dict(x=X + 1), dict(rows=C + 1),
+    dict(ldx=9), dict(ldx=(1 << 30) + 1), dict(x=None), dict(order=None), dict(rows=None), dict(x=X + 1), dict(rows=C + 1),
     dict(order=S + 1), dict(rows=X), dict(rows=S), dict(rows=V)])
 def test_gather_refuses(lib, change):
     a = dict(stream=None, tokens=5, choices=2, width=10, dtype=BF16, x=X, ldx=10, order=S, position=V, rows=C)

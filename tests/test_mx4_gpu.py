@@ -425,7 +425,7 @@ def test_experts_offsets_out_of_order(dev):
     layer = pca.MX4Experts(experts=6, in_features=64, out_features=40, codes=codes.reshape(6, 40, -1),
                            scales=scales.reshape(6, 40, -1))
     ints = lambda a: torch.tensor(a, dtype=torch.int32, device=dev)  # noqa: E731
-    for tokens in (50, 700):
+    for tokens in (50, 700, 5000):
         pairs = 2 * tokens
         x = rows_of(rng, tokens, 64, dev, "bf16")
         order = torch.randint(-(1 << 30), 1 << 30, (pairs,), device=dev, dtype=torch.int32)
