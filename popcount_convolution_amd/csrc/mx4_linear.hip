@@ -372,15 +372,20 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
         x[i & 1][m] = lds.stage[slot].x[r * 8 + ((4 * half + i) ^ (r >> 1 & 7))];
     };
     auto fetch_scale = [&](int slot, int m) { xs[slot & 1][m] = lds.stage[slot].xs[(m * 32 + row) * 2 + half]; };
-    // Step s, whose x is in stage `at` = (s - s_begin) % 4; x of s + 3 and weights of s + WD are requested.
-    auto step = [&](int s, auto AT) {
-        constexpr int at = decltype(AT)::value, next = (at + 1) & 3;
-        constexpr int V = WV + XV, P = MT * NT;  // loads, instructions a phase
+    // Step s, whose x is in stage `at` = (s - s_begin) % 4.  LEFT: the steps that
+    // may still follow, as far as that is known: x of s + 3 and weights of s + WD are
+    // requested where there can be such a step.  What the wait counts has to be
+    // issued as written: a load whose result no step uses would be dropped.
+    constexpr int V = WV + XV, P = MT * NT;  // loads of a whole step, instructions a phase
+    auto step = [&](int s, auto AT, auto LEFT) {
+        constexpr int at = decltype(AT)::value, next = (at + 1) & 3, left = decltype(LEFT)::value;
+        constexpr int loads = (left >= WD ? WV : 0) + (left >= STAGES - 1 ? XV : 0);
+        constexpr int before = at > 0 && left < STAGES - 1 ? (left + 1 >= WD ? WV : 0) : V;  // loads of the step before
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (i == 3) {
+            if (i == 3 && left > 0) {
                 // x of the next step is here: all loads but those after it are done
-                __builtin_amdgcn_s_waitcnt(vm_wait((STAGES - 2) * V));
+                __builtin_amdgcn_s_waitcnt(vm_wait(before + loads));
                 __builtin_amdgcn_s_barrier();
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -389,7 +394,7 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
                 const int m = p / NT, t = p % NT;
                 if (t == 0) {
                     if (i < 3) fetch(at, i + 1, m);
-                    else {
+                    else if (left > 0) {
                         fetch_scale(next, m);
                         fetch(next, 0, m);
                     }
@@ -399,8 +404,11 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
 #pragma unroll
                     for (int l = 0; l < V; ++l)
                         if (l * 3 * P / V == i * P + p) {
-                            if (l < WV) request_w(s + WD, (at + WD) % (WD + 1), l);
-                            else request_x(s + STAGES - 1, (at + STAGES - 1) & 3, l - WV);
+                            if (l < WV) {
+                                if constexpr (left >= WD) request_w(s + WD, (at + WD) % (WD + 1), l);
+                            } else if constexpr (left >= STAGES - 1) {
+                                request_x(s + STAGES - 1, (at + STAGES - 1) & 3, l - WV);
+                            }
                         }
                 }
                 acc[m][t] = mfma_mx4_32(i, w[at % (WD + 1)][i][t], ws[at % (WD + 1)][t], x[i & 1][m], xs[at & 1][m], acc[m][t]);
@@ -408,7 +416,7 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
             }
         }
     };
-    static_assert(4 % (WD + 1) == 0 && (STAGES - 2) * (WV + XV) < 64);
+    static_assert(4 % (WD + 1) == 0 && WD < STAGES && 2 * V < 64);
     // the first weights are on their way while the pairs arrive that say which rows of x
 #pragma unroll
     for (int d = 0; d < WD; ++d)
@@ -432,18 +440,22 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
         fetch_scale(0, m);
         fetch(0, 0, m);
     }
+    typedef std::integral_constant<int, 0> I0;
+    typedef std::integral_constant<int, 1> I1;
+    typedef std::integral_constant<int, 2> I2;
+    typedef std::integral_constant<int, 3> I3;
     int s = s_begin;
-    for (; s + 4 <= s_end; s += 4) {
-        step(s, std::integral_constant<int, 0>());
-        step(s + 1, std::integral_constant<int, 1>());
-        step(s + 2, std::integral_constant<int, 2>());
-        step(s + 3, std::integral_constant<int, 3>());
+    for (; s + 4 <= s_end; s += 4) {  // up to three more may follow the last
+        step(s, I0(), I3());
+        step(s + 1, I1(), I3());
+        step(s + 2, I2(), I3());
+        step(s + 3, I3(), I3());
     }
     if (s < s_end) {
-        step(s, std::integral_constant<int, 0>());
+        step(s, I0(), I2());
         if (s + 1 < s_end) {
-            step(s + 1, std::integral_constant<int, 1>());
-            if (s + 2 < s_end) step(s + 2, std::integral_constant<int, 2>());
+            step(s + 1, I1(), I1());
+            if (s + 2 < s_end) step(s + 2, I2(), I0());
         }
     }
     __builtin_amdgcn_s_waitcnt(vm_wait(0));  // nothing is on its way to LDS any more,
