@@ -241,24 +241,29 @@ class ExpertOrder:
         self.offsets, self.order, self.position, self.experts = offsets, order, position, experts
         self.tokens, self.choices = position.shape
         self.device = position.device
+        self._index = self.device.index  # None, as no tensor's get_device(), off the GPU
         return self
 
     def _rows(self, t, name: str, rows: int, dtype=None):
         """(width, row stride, dtype code) of a tensor ``[rows, width]``."""
         _need_tensor(t, name)
-        if t.dim() != 2 or t.shape[0] != rows or not 1 <= t.shape[1] <= 1 << 20:
-            raise ValueError(f"{name}: shape {tuple(t.shape)} is not ({rows}, 1 to {1 << 20})")
+        shape = t.shape
+        if len(shape) != 2 or shape[0] != rows or not 1 <= shape[1] <= 1 << 20:
+            raise ValueError(f"{name}: shape {tuple(shape)} is not ({rows}, 1 to {1 << 20})")
         code = _dtype_code(t, name)
         if dtype is not None and t.dtype != dtype:
             raise ValueError(f"{name}: dtype {t.dtype} is not {dtype}")
-        _need_cuda(t, name, self.device)
-        return t.shape[1], _row_stride(t, name)[1], code
+        if t.get_device() != self._index:
+            _need_cuda(t, name, self.device)
+        width = shape[1]
+        return width, width if t.is_contiguous() else _row_stride(t, name)[1], code
 
     def _weights(self, t):
         """Type code of the weights ``[tokens, choices]``."""
         _need_tensor(t, "weights")
         code = _dtype_code(t, "weights")
-        _need_dense(t, "weights", self.position.shape, t.dtype, self.device)
+        if t.shape != self.position.shape or not t.is_contiguous() or t.get_device() != self._index:
+            _need_dense(t, "weights", self.position.shape, t.dtype, self.device)
         return code
 
     def _result(self, out, name: str, shape, like):
