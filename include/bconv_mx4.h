@@ -102,7 +102,7 @@ typedef struct {
     int64_t ldy;             /* >= out_features */
     int32_t x_rows;          /* input rows; with offsets, x_rows times in_features (rounded up to a
                                 multiple of 256) is at most 2^32 */
-    int32_t rows;            /* result rows */
+    int32_t rows;            /* result rows; with offsets at most 2^27 */
     int32_t dtype;           /* of x and y */
     int32_t choices;         /* 0: result row i is of input row i (x_rows == rows); otherwise of
                                 order[i] / choices, and x_rows == rows / choices */

@@ -424,14 +424,13 @@ namespace {
 
 using bconv::fail;
 using bconv::hip_fail;
+using bconv::kMaxPairs;
 using bconv::ranges_overlap;
 
 int bytes_of(int32_t dtype)
 {
     return dtype == BCONV_F32 ? 4 : dtype == BCONV_F16 || dtype == BCONV_BF16 ? 2 : 0;
 }
-
-constexpr long long kMaxPairs = 1LL << 27;
 
 bconv_status_t check_sort(int32_t pairs, int32_t experts)
 {

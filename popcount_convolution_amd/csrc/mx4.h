@@ -34,6 +34,9 @@ __host__ __device__ constexpr long long mx4_padded(long long cols)
 // Elements between rows at most: the bytes of a call's rows stay below 2^63.
 constexpr long long kMaxStride = 1LL << 30;
 
+// (token, choice) pairs of a call at most, so rows of experts too.
+constexpr long long kMaxPairs = 1LL << 27;
+
 // 8 consecutive values of one row as loaded.
 template <int DT> struct Eight {
     u32x4 q[DT == BCONV_F32 ? 2 : 1];

@@ -788,7 +788,8 @@ template <typename T> bconv_status_t device_alloc(T **p, size_t count)
 }
 
 // What sizes alone decide of a call; workspace_size and forward share it.
-// Offsets of the many-row kernel into quantised rows are 31 bits.
+// Offsets of the many-row kernel into quantised rows are 31 bits; as many rows as
+// can be sorted leave room for what int32 counts of rows and their blocks add.
 bconv_status_t check_sizes(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
 {
     if (!h || !args) return fail(BCONV_ERR_INVALID_ARGUMENT, "handle or args is NULL");
@@ -798,7 +799,9 @@ bconv_status_t check_sizes(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
     if (args->choices == 0 ? args->x_rows != args->rows : (long long)args->x_rows * args->choices != args->rows)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "%d rows do not follow from %d input rows and %d choices", args->rows,
                     args->x_rows, args->choices);
-    if ((h->desc.experts > 1 || args->offsets) && (long long)args->x_rows * h->steps > bconv::kMaxSteps)
+    if (!args->offsets && h->desc.experts == 1) return BCONV_OK;  // slabs of rows
+    if (args->rows > bconv::kMaxPairs) return fail(BCONV_ERR_INVALID_ARGUMENT, "%d rows of experts are more than 2^27", args->rows);
+    if ((long long)args->x_rows * h->steps > bconv::kMaxSteps)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "%d input rows of %d values are more than 2^32 values (padded)", args->x_rows,
                     h->desc.in_features);
     return BCONV_OK;
