@@ -282,11 +282,13 @@ template <typename E> struct Values {  // of 16 bytes
 // s_waitcnt: at most `n` vector loads outstanding, no LDS read.
 constexpr int vm_wait(int n) { return (n & 15) | (n >> 4 << 14) | (0x7 << 4) | (0x0 << 8); }
 
-constexpr uint32_t kNone = 0x80000000u;  // outside every buffer: a load from there reads no memory and gives 0
+// Bytes of every buffer, so that an offset from there on reads no memory and gives
+// 0.  Quantised rows may fill it: with a byte less, the last codes of the last row read as 0.
+constexpr uint32_t kNone = 0x80000000u;
 
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t whole_buffer(const void *p)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, kNone - 1, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, kNone, 0x00020000);
 }
 
 // LDS of the many-row kernel.

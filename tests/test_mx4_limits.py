@@ -42,3 +42,26 @@ def test_more_rows_than_can_be_sorted(dev, experts, x_rows, choices):
         assert e.value.status == pca.BCONV_ERR_INVALID_ARGUMENT
     args.rows, args.choices, args.x_rows = 1 << 27, 1 << 27, 1
     assert pca.bconv_mx4_linear_workspace_size(layer.handle, args) > 1 << 24  # the list of 2^20 row blocks
+
+
+def test_most_input_rows(dev):
+    """2^32 input values, as many as a layer of experts takes: the last codes end
+    at byte 2^31 of the quantised rows, and the last row has its large values there."""
+    tokens, k, n = 1 << 20, 4096, 20
+    layer, codes, scales = make_experts(2, k, n)
+    x = torch.randn((tokens, k), device=dev, dtype=torch.bfloat16)
+    x[-1, -8:] = 500 + 100 * torch.arange(8, device=dev)
+    ids = torch.zeros((tokens, 1), dtype=torch.int32, device=dev)
+    ids[::3] = 1
+    order = pca.sort_by_expert(ids, 2)
+    q = pca.mx4_quantize(x)
+    assert q.codes.numel() == 1 << 31
+    y = layer.forward(q, order, dtype=torch.float32)
+    assert torch.equal(layer.forward(x, order), y.to(torch.bfloat16))
+    at = order.position[-40:, 0].long()
+    rows, got = x[-40:].to(torch.float64).cpu().numpy(), y[at].to(torch.float64).cpu().numpy()
+    for e in range(2):
+        mine = (ids[-40:, 0] == e).cpu().numpy()
+        want, mass = ref.linear(rows[mine], codes[e], scales[e], None)
+        ok = (np.abs(got[mine] - want) <= ref.linear_bound(want, mass, k, "f32")).all(1)
+        assert ok.all(), np.nonzero(mine)[0][~ok] - 40
