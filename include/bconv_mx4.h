@@ -98,7 +98,8 @@ typedef struct {
     int64_t ldx;             /* >= in_features */
     const uint8_t *codes;    /* with x NULL: input rows as bconv_mx4_quantize lays them out */
     const uint8_t *scales;   /*              (16-byte aligned) */
-    void *y;                 /* [rows][out_features], row i at y + i*ldy; overlaps nothing else */
+    void *y;                 /* [rows][out_features], row i at y + i*ldy; overlaps nothing else (y and x may be
+                                columns of one buffer: the same stride, no element of both) */
     int64_t ldy;             /* >= out_features */
     int32_t x_rows;          /* input rows; with offsets, x_rows times in_features (rounded up to a
                                 multiple of 256) is at most 2^32 */

@@ -85,4 +85,18 @@ inline bool ranges_overlap(const void *a, size_t an, const void *b, size_t bn)
     return a0 < b0 + bn && b0 < a0 + an;
 }
 
+// Whether rows of x (k wide, ldx apart) and of y (n wide, ldy apart), elements of
+// `es` bytes, share an element.  Columns of one buffer (equal strides) lie inside
+// each other's extent without sharing any.
+inline bool rows_overlap(const void *x, int64_t ldx, int k, int x_rows, const void *y, int64_t ldy, int n, int y_rows, int es)
+{
+    const size_t xb = ((size_t)(x_rows - 1) * ldx + k) * es, yb = ((size_t)(y_rows - 1) * ldy + n) * es;
+    if (!ranges_overlap(x, xb, y, yb)) return false;
+    const intptr_t apart = (intptr_t)((uintptr_t)y - (uintptr_t)x);
+    if (ldx != ldy || apart % es) return true;
+    int64_t d = apart / es % ldx;  // y's first column among x's
+    if (d < 0) d += ldx;
+    return d < k || d + n > ldx;
+}
+
 }  // namespace bconv

@@ -754,6 +754,7 @@ using bconv::DeviceGuard;
 using bconv::fail;
 using bconv::hip_fail;
 using bconv::ranges_overlap;
+using bconv::rows_overlap;
 
 constexpr int32_t kMaxFeatures = 1 << 20;
 
@@ -942,15 +943,17 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
         return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : (size_t)0);
     if (need > 0 && (uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
     const size_t xc = (size_t)args->x_rows * h->steps * (bconv::kStep / 2), xs = xc / 16;
-    const struct { const void *p; size_t n; } in[] = {
-        {args->x, args->x ? ((size_t)(args->x_rows - 1) * args->ldx + k) * es : 0}, {args->codes, args->codes ? xc : 0},
-        {args->scales, args->scales ? xs : 0}, {args->offsets, args->offsets ? ((size_t)h->desc.experts + 1) * 4 : 0},
-        {args->order, args->order ? (size_t)args->rows * 4 : 0}},
-        out[] = {{args->y, ((size_t)(args->rows - 1) * args->ldy + n) * es}, {workspace, need}};
+    struct Extent { const void *p; size_t n; };
+    const Extent in[] = {
+        {args->codes, args->codes ? xc : 0}, {args->scales, args->scales ? xs : 0},
+        {args->offsets, args->offsets ? ((size_t)h->desc.experts + 1) * 4 : 0}, {args->order, args->order ? (size_t)args->rows * 4 : 0}};
+    const Extent x = {args->x, args->x ? ((size_t)(args->x_rows - 1) * args->ldx + k) * es : 0};
+    const Extent out[] = {{args->y, ((size_t)(args->rows - 1) * args->ldy + n) * es}, {workspace, need}};
+    bool overlap = x.n && rows_overlap(args->x, args->ldx, k, args->x_rows, args->y, args->ldy, n, args->rows, es);
+    overlap = overlap || (x.n && need && ranges_overlap(x.p, x.n, workspace, need));
     for (const auto &o : out)
-        for (const auto &i : in)
-            if (o.n && i.n && ranges_overlap(o.p, o.n, i.p, i.n))
-                return fail(BCONV_ERR_INVALID_ARGUMENT, "y or the workspace overlaps x, codes, scales, offsets or order");
+        for (const auto &i : in) overlap = overlap || (o.n && i.n && ranges_overlap(o.p, o.n, i.p, i.n));
+    if (overlap) return fail(BCONV_ERR_INVALID_ARGUMENT, "y or the workspace overlaps x, codes, scales, offsets or order");
     if (need && ranges_overlap(out[0].p, out[0].n, workspace, need))
         return fail(BCONV_ERR_INVALID_ARGUMENT, "y and the workspace overlap");
 

@@ -689,6 +689,7 @@ using bconv::DeviceGuard;
 using bconv::fail;
 using bconv::hip_fail;
 using bconv::ranges_overlap;
+using bconv::rows_overlap;
 using bconv::upload;
 
 constexpr int32_t kMaxFeatures = 1 << 20;
@@ -711,20 +712,6 @@ void release(bconv_q4_linear *h)
     for (void *p : ptrs)
         if (p) (void)hipFree(p);
     delete h;
-}
-
-// Whether rows of x (k wide, ldx apart) and of y (n wide, ldy apart) share an
-// element.  Columns of one buffer (equal strides) lie inside each other's
-// extent without sharing any.
-bool rows_overlap(const void *x, int64_t ldx, int k, const void *y, int64_t ldy, int n, int rows, int es)
-{
-    const size_t xb = ((size_t)(rows - 1) * ldx + k) * es, yb = ((size_t)(rows - 1) * ldy + n) * es;
-    if (!ranges_overlap(x, xb, y, yb)) return false;
-    const intptr_t apart = (intptr_t)((uintptr_t)y - (uintptr_t)x);
-    if (ldx != ldy || apart % es) return true;
-    int64_t d = apart / es % ldx;  // y's first column among x's
-    if (d < 0) d += ldx;
-    return d < k || d + n > ldx;
 }
 
 int dtype_bytes(int32_t dtype)
@@ -823,7 +810,7 @@ bconv_status_t bconv_q4_linear_forward(bconv_q4_linear_t h, void *stream, int32_
     if (ldx > (1LL << 40) || ldy > (1LL << 40)) return fail(BCONV_ERR_INVALID_ARGUMENT, "ldx/ldy too large");
     if (((uintptr_t)x | (uintptr_t)y) % es) return fail(BCONV_ERR_INVALID_ARGUMENT, "x/y not aligned to an element");
     const size_t xb = ((size_t)(rows - 1) * ldx + k) * es, yb = ((size_t)(rows - 1) * ldy + n) * es;
-    if (rows_overlap(x, ldx, k, y, ldy, n, rows, es)) return fail(BCONV_ERR_INVALID_ARGUMENT, "x and y overlap");
+    if (rows_overlap(x, ldx, k, rows, y, ldy, n, rows, es)) return fail(BCONV_ERR_INVALID_ARGUMENT, "x and y overlap");
     const int slab = bconv::slab_rows(h->chunks, h->per_chunk);
     bconv::Q4Plan p = bconv::plan_linear(rows < slab ? rows : slab, dtype, h->tiles, h->chunks, h->per_chunk, h->cus);
     if (p.bytes > 0 && (!workspace || workspace_bytes < p.bytes))

@@ -65,3 +65,57 @@ def test_most_input_rows(dev):
         want, mass = ref.linear(rows[mine], codes[e], scales[e], None)
         ok = (np.abs(got[mine] - want) <= ref.linear_bound(want, mass, k, "f32")).all(1)
         assert ok.all(), np.nonzero(mine)[0][~ok] - 40
+
+
+DT = {"f32": torch.float32, "f16": torch.float16, "bf16": torch.bfloat16}
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows", [1, 3, 40, 300])
+def test_columns_of_one_buffer(dev, dtype, rows):
+    """Inputs and results side by side in one buffer, in both orders, give what
+    buffers of their own do; columns that share one element are refused."""
+    k, n, gap = 200, 51, 3
+    layer, _, _ = make_experts(2, k, n)
+    codes, scales = ref.random_weights(np.random.default_rng(1), n, k)
+    linear = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales)
+    ids = (torch.arange(rows, dtype=torch.int32, device=dev) % 2).view(rows, 1)
+    order = pca.sort_by_expert(ids, 2)
+    values = torch.randn((rows, k), device=dev).to(DT[dtype])
+    forwards = (linear.forward, lambda x, out=None: layer.forward(x, order, out=out),
+                lambda x, out=None: layer.forward(x, order, out=out, in_order=True))
+    for forward in forwards:
+        want = forward(values)
+        for x0, y0 in ((0, k), (n, 0), (n + gap, 1), (1, k + gap)):
+            buf = torch.full((rows, k + n + gap + 2), 7.0, device=dev, dtype=DT[dtype])
+            x, y = buf[:, x0:x0 + k], buf[:, y0:y0 + n]
+            x.copy_(values)
+            forward(x, out=y)
+            assert torch.equal(y, want) and torch.equal(x, values)
+            rest = torch.ones(buf.shape[1], dtype=torch.bool, device=dev)
+            rest[x0:x0 + k] = rest[y0:y0 + n] = False
+            assert bool((buf[:, rest] == 7).all())
+        buf = torch.zeros((rows + 1, k + n + 2), device=dev, dtype=DT[dtype])
+        for x0, y0 in ((0, k - 1), (n, 1), (0, 0)):
+            with pytest.raises(pca.BconvError, match="overlap"):
+                forward(buf[:rows, x0:x0 + k], out=buf[:rows, y0:y0 + n])
+        if rows > 1:
+            # a result that ends in the next row's inputs; one of another stride between the inputs
+            for stride, y0 in ((k + n + 2, k + 3), (n + 1, k)):
+                with pytest.raises(pca.BconvError, match="overlap"):
+                    forward(buf[:rows, :k], out=buf.as_strided((rows, n), (stride, 1), y0))
+
+
+def test_columns_of_one_buffer_of_tokens(dev):
+    """As many columns of results as inputs, for tokens with several experts each:
+    more result rows than input rows, in the same columns' stride."""
+    tokens, choices, k, n = 30, 3, 96, 40
+    layer, _, _ = make_experts(4, k, n)
+    ids = torch.randint(0, 4, (tokens, choices), device=dev)
+    order = pca.sort_by_expert(ids, 4)
+    buf = torch.zeros((tokens * choices, k + n), device=dev)
+    buf[:tokens, :k] = torch.randn((tokens, k), device=dev)
+    want = layer.forward(buf[:tokens, :k].contiguous(), order)
+    x = buf[:tokens, :k].clone()
+    layer.forward(buf[:tokens, :k], order, out=buf[:, k:])
+    assert torch.equal(buf[:, k:], want) and torch.equal(buf[:tokens, :k], x) and not bool(buf[tokens:, :k].any())
