@@ -23,6 +23,7 @@ from .q4 import (_INT32_MAX, _DTYPES, _dtype_code, _need_cuda, _need_dense, _nee
 
 BLOCK = 32   # values that share a power of two
 _PAD = 256   # quantised rows are padded to a multiple of this
+_MOST_PAIRS = 1 << 27  # (token, choice) pairs of an order
 
 
 _torch = None  # the torch module, once a call needs it
@@ -235,6 +236,8 @@ class ExpertOrder:
         for name, t, shape in (("offsets", offsets, (experts + 1,)), ("order", order, (position.numel(),)),
                                ("position", position, position.shape)):
             _need_dense(t, name, shape, torch.int32, position.device)
+        if position.numel() > _MOST_PAIRS:
+            raise ValueError(f"position: {position.numel()} pairs are more than 2^27")
         self._set(offsets, order, position, experts)
 
     def _set(self, offsets, order, position, experts: int):
