@@ -166,3 +166,33 @@ def test_row_blocks_of_every_size(dev, dtype, k, n, bias, dropped):
     assert torch.equal(layer.forward(gathered, o, in_order=True), y)
     assert torch.equal(layer.forward(pca.mx4_quantize(x), o, dtype=DT[dtype]), y)
     assert torch.equal(layer.forward(pca.mx4_quantize(gathered), o, in_order=True, dtype=DT[dtype]), y)
+
+
+@pytest.mark.parametrize("counts", [(0, 0, 0), (0, 5, 0), (3, 0, 4)])
+def test_order_is_checked(dev, counts):
+    """Tensors of an order on the GPU, each with one thing wrong; a right one works."""
+    flat = np.repeat(np.arange(3), counts)
+    if flat.size % 2:
+        flat = np.append(flat, -1)
+    tokens = flat.size // 2
+    offsets, order, position = (torch.from_numpy(a).to(dev) for a in ref.expert_order(flat.reshape(tokens, 2), 3))
+    x = torch.arange(tokens, device=dev, dtype=torch.float32).view(tokens, 1).expand(tokens, 5).contiguous()
+    got = pca.ExpertOrder(offsets, order, position, 3).gather(x)
+    assert torch.equal(got, torch.where((order >= 0)[:, None], x[order.clamp(min=0) // 2] if tokens else got, 0.0))
+    ints = lambda *s: torch.zeros(s, dtype=torch.int32, device=dev)  # noqa: E731
+    for bad, match in (
+            ((ints(3), order, position), "^offsets: shape \\(3,\\) != \\(4,\\)"), ((offsets.long(), order, position), "^offsets: dtype"),
+            ((ints(8)[::2], order, position), "^offsets: .*contiguous"), ((offsets.cpu(), order, position), "^offsets: .*device"),
+            ((offsets, ints(2 * tokens + 1), position), "^order: shape"), ((offsets, order.long(), position), "^order: dtype"),
+            ((offsets, order, ints(2 * tokens)), "^position: shape"), ((offsets, order, position.long()), "^position: dtype"),
+            ((offsets, order, ints(tokens, 0)), "^position: shape"), ((offsets, order, None), "^position: a torch tensor"),
+            ((None, order, position), "^offsets: a torch tensor"), ((offsets, None, position), "^order: a torch tensor")):
+        with pytest.raises(ValueError, match=match):
+            pca.ExpertOrder(*bad, 3)
+    if tokens > 1:
+        for bad, match in (((offsets, ints(4 * tokens)[::2], position), "^order: .*contiguous"),
+                           ((offsets, order.cpu(), position), "^order: .*device"),
+                           ((offsets, order, ints(2, tokens).t()), "^position: .*contiguous"),
+                           ((offsets, order, position.cpu()), "on cuda:0, not on cpu|^position: .*device")):
+            with pytest.raises(ValueError, match=match):
+                pca.ExpertOrder(*bad, 3)
