@@ -167,6 +167,19 @@ class _MX4Layer:
             B.bconv_mx4_linear_forward(self.handle, raw, args, workspace.data_ptr() if need else None, need)
         return out
 
+    def _workspace_bytes(self, rows: int, x_rows: int, choices: int, dtype, quantised: bool, experts: bool) -> int:
+        if _torch is None:
+            _load()
+        code = _DTYPES.get(dtype)
+        if code is None:
+            raise ValueError(f"dtype {dtype} is not one of torch.float32, torch.float16, torch.bfloat16")
+        _need_int32(rows, "rows")
+        given = 16  # any address: of pointers, only whether they are there counts
+        args = B.bconv_mx4_rows_t(None if quantised else given, 0, given if quantised else None,
+                                  given if quantised else None, None, 0, x_rows, rows, code, choices,
+                                  given if experts else None, given if choices else None)
+        return B.bconv_mx4_linear_workspace_size(self.handle, args)
+
     def _input_shape(self, x):
         """Shape of the input's rows, without their values."""
         if type(x) is MX4Tensor:
@@ -204,6 +217,11 @@ class MX4Linear(_MX4Layer):
 
     def __init__(self, *, in_features: int, out_features: int, codes, scales, bias=None):
         self._create(1, in_features, out_features, (out_features,), codes, scales, bias)
+
+    def workspace_bytes(self, rows: int, dtype, *, quantised: bool = False) -> int:
+        """Bytes of the workspace of a call with ``rows`` rows and results of
+        ``dtype``, from an ``MX4Tensor`` if ``quantised``."""
+        return self._workspace_bytes(rows, rows, 0, dtype, quantised, False)
 
     def forward(self, x, out=None, *, dtype=None, workspace=None, stream=None):
         """``[..., in_features]`` rows of float32, float16 or bfloat16 ->
@@ -386,6 +404,15 @@ class MX4Experts(_MX4Layer):
     def __init__(self, *, experts: int, in_features: int, out_features: int, codes, scales, bias=None):
         self.experts = experts
         self._create(experts, in_features, out_features, (experts, out_features), codes, scales, bias)
+
+    def workspace_bytes(self, tokens: int, choices: int, dtype, *, in_order: bool = False, quantised: bool = False) -> int:
+        """Bytes of the workspace of a call with an order of ``tokens`` times
+        ``choices`` pairs and results of ``dtype``, from an ``MX4Tensor`` if ``quantised``."""
+        _need_int32(tokens, "tokens")
+        if not 1 <= choices <= _INT32_MAX:
+            raise ValueError(f"choices: {choices} is not in [1, {_INT32_MAX}]")
+        rows = tokens * choices
+        return self._workspace_bytes(rows, rows if in_order else tokens, 0 if in_order else choices, dtype, quantised, True)
 
     def forward(self, x, order: ExpertOrder, out=None, *, in_order: bool = False, dtype=None, workspace=None,
                 stream=None):

@@ -28,3 +28,25 @@ def test_order_takes_as_many_pairs_as_a_sort():
     with FakeTensorMode():
         o = pca.ExpertOrder(i32(4), i32(2 ** 27), i32(2 ** 24, 8), 3)
     assert (o.tokens, o.choices, o.experts) == (2 ** 24, 8, 3)
+
+
+def layer(cls):
+    made = object.__new__(cls)
+    made.handle = None
+    return made
+
+
+def test_workspace_bytes_refuses():
+    linear, experts = layer(pca.MX4Linear), layer(pca.MX4Experts)
+    for f, match in ((lambda: linear.workspace_bytes(2 ** 32 + 1, torch.float32), "rows: .* is not a 32-bit number"),
+                     (lambda: linear.workspace_bytes(1, torch.float64), "dtype"),
+                     (lambda: experts.workspace_bytes(2 ** 32 + 1, 1, torch.float32), "tokens: .* is not a 32-bit number"),
+                     (lambda: experts.workspace_bytes(2 ** 20, 2 ** 12 + 1, torch.float32), "rows: .* is not a 32-bit number"),
+                     (lambda: experts.workspace_bytes(5, 0, torch.float32), "choices: 0"),
+                     (lambda: experts.workspace_bytes(5, 2 ** 32 + 1, torch.float32), "choices"),
+                     (lambda: experts.workspace_bytes(5, 2, torch.int32), "dtype")):
+        with pytest.raises(ValueError, match=match):
+            f()
+    for f in (lambda: linear.workspace_bytes(1, torch.float32), lambda: experts.workspace_bytes(5, 2, torch.float32)):
+        with pytest.raises(pca.BconvError, match="handle"):  # a closed layer
+            f()

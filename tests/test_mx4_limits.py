@@ -119,3 +119,35 @@ def test_columns_of_one_buffer_of_tokens(dev):
     x = buf[:tokens, :k].clone()
     layer.forward(buf[:tokens, :k], order, out=buf[:, k:])
     assert torch.equal(buf[:, k:], want) and torch.equal(buf[:tokens, :k], x) and not bool(buf[tokens:, :k].any())
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("tokens,choices,k,n", [(1, 1, 64, 16), (3, 2, 5000, 40), (20, 4, 600, 70), (300, 2, 9000, 30), (700, 3, 300, 600)])
+def test_workspace_of_the_size_that_is_asked_for(dev, dtype, tokens, choices, k, n):
+    """workspace_bytes() is what calls need: as much gives the same results as none
+    given, a byte less is refused."""
+    layer, _, _ = make_experts(3, k, n)
+    codes, scales = ref.random_weights(np.random.default_rng(1), n, k)
+    linear = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales)
+    x = torch.randn((tokens, k), device=dev).to(DT[dtype])
+    order = pca.sort_by_expert(torch.randint(0, 3, (tokens, choices), device=dev), 3)
+    rows = order.gather(x)
+    q, qr = pca.mx4_quantize(x), pca.mx4_quantize(rows)
+    sizes = set()
+    for need, forward in (
+            (linear.workspace_bytes(tokens, DT[dtype]), lambda **a: linear.forward(x, **a)),
+            (linear.workspace_bytes(tokens, DT[dtype], quantised=True), lambda **a: linear.forward(q, dtype=DT[dtype], **a)),
+            (layer.workspace_bytes(tokens, choices, DT[dtype]), lambda **a: layer.forward(x, order, **a)),
+            (layer.workspace_bytes(tokens, choices, DT[dtype], quantised=True),
+             lambda **a: layer.forward(q, order, dtype=DT[dtype], **a)),
+            (layer.workspace_bytes(tokens, choices, DT[dtype], in_order=True), lambda **a: layer.forward(rows, order, in_order=True, **a)),
+            (layer.workspace_bytes(tokens, choices, DT[dtype], in_order=True, quantised=True),
+             lambda **a: layer.forward(qr, order, in_order=True, dtype=DT[dtype], **a))):
+        sizes.add(need)
+        want = forward()
+        ws = torch.full((need + 64,), 0xff, dtype=torch.uint8, device=dev)
+        assert torch.equal(forward(workspace=ws[:need]), want) and bool((ws[need:] == 255).all())
+        if need:
+            with pytest.raises(ValueError, match=f"{need - 1} bytes given, {need} needed"):
+                forward(workspace=ws[:need - 1])
+    assert (sizes == {0}) == (tokens == 1)
