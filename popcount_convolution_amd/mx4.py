@@ -8,6 +8,9 @@ of both).  As in ``q4``, torch provides device memory and the current stream;
 every step runs in the kernels of ``libbconv.so`` (``include/bconv_mx4.h``
 documents formats and formulas), tensors are checked before anything is
 launched, and what a call allocates is allocated on the stream it launches on.
+No call here is part of torch's autograd: results carry no gradient, also where
+an input requires one.  Gradients are calls of their own, of the gather and the
+combination; the products have none.
 """
 
 from __future__ import annotations
@@ -40,7 +43,9 @@ def _padded(cols: int) -> int:
 
 
 class MX4Tensor(NamedTuple):
-    """Quantised rows: what ``mx4_quantize`` returns and linear layers take."""
+    """Quantised rows: what ``mx4_quantize`` returns and linear layers take.  Layers'
+    weights are held without the padding: ``codes[..., :ceil(cols / 2)]`` and
+    ``scales[..., :ceil(cols / 32)]`` of quantised rows of weights."""
     codes: object   # uint8 [..., padded / 2], value 2 i of a row in the low half of byte i
     scales: object  # uint8 [..., padded / 32], exponent + 127 of a block of 32 values; 255: NaN
     cols: int       # values of a row; padded is that, rounded up to a multiple of 256 with zeros
@@ -306,13 +311,16 @@ class ExpertOrder:
         return out
 
     def gather_backward(self, d_rows, out=None, stream=None):
-        """Gradient of ``gather``: that of its rows -> that of the tokens' rows."""
+        """Gradient of ``gather``: that of its rows -> that of the tokens' rows.  (Of
+        gathered rows that went through experts with gradients: those of
+        ``MX4Experts`` have none, and take the tokens' rows themselves.)"""
         return self.combine(d_rows, None, out=out, stream=stream)
 
     def combine(self, rows, weights=None, out=None, stream=None):
         """Rows in the experts' order -> ``[tokens, width]``, the sum of each token's
         rows times its ``weights`` (``[tokens, choices]`` of float32, float16 or
-        bfloat16; None for 1), without the dropped ones."""
+        bfloat16; None for 1), without the dropped ones.  The result carries no
+        gradient: a router learns from ``combine_backward``."""
         width, ldr, code = self._rows(rows, "rows", self.tokens * self.choices)
         weight_code = 0 if weights is None else self._weights(weights)
         place, raw = _place(self.device, stream)
