@@ -613,7 +613,7 @@ struct Mx4Plan {
     size_t scales_offset, list_offset, sums_offset, bytes;
 };
 
-Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
+Mx4Plan plan_mx4(const Mx4Args &a, int dtype, bool given, int cus)
 {
     Mx4Plan p{};
     const int mean = (a.rows + a.experts - 1) / a.experts;
@@ -631,12 +631,38 @@ Mx4Plan plan_mx4(const Mx4Args &a, bool given, int cus)
                                 : (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << (a.rows > 32 ? 26 : 27) ||
                                       (a.rows > 128 && blocks * 2 >= cus);
     p.many = many ? kManyRows : 0;
-    // Quantising in the few-row kernel costs every workgroup a little for each step,
-    // a launch of its own 1.2 us and the host's call.  There against in a launch: 1 row,
-    // 4096 -> 4096, 4.6 us and 5.6, 25088 -> 4096 14.2 and 12.2; 12 rows, 4096 -> 4096, 6.4
-    // and 6.4; 16 rows, 2048 -> 2048, 5.0 and 6.1, 6000 -> 1500 9.1 and 7.4.  128 experts of
-    // 512 -> 1024, 4 rows each, 9.8 and 11.8; 8 of 4096 -> 4096, 16 rows each, 26.4 and 16.5.
-    p.quantise = !given && (many || (a.offsets ? mean > 4 || a.steps > 8 : a.rows > 16 || a.steps > 24 || a.rows * a.steps > 192));
+    // Quantising in the few-row kernel costs every workgroup a little for each step, more
+    // in fp32; a launch of its own costs 1.2 to 2 us and the host's call.  There against in
+    // a launch, us in a captured graph, weights that are in no cache:
+    //   one layer, 4096 and 11008 outputs     bf16                   fp32
+    //     1 row, 13 steps                   5.0  6.3   8.0  9.5    5.4 6.0    9.4  9.4
+    //     1 row, 16                         5.2  6.2   8.7  9.6    5.9 6.0   10.4  9.4
+    //     1 row, 24                         7.5  7.8  11.6 11.6    9.2 8.0   13.6 11.7
+    //     1 row, 32                         9.0  8.6  14.4 13.6   11.0 9.0   17.1 13.9
+    //     12 rows, 8                        5.0  6.4   7.2  8.2    6.3 6.8    8.5  8.7
+    //     8 rows, 13                        5.6  6.6   9.6  9.9    7.9 7.0   11.1 10.3
+    //     12 rows, 13                       6.7  6.8  10.6 10.2    9.0 7.1   12.6 10.6
+    //     12 rows, 16                       6.8  7.0  11.5 10.5   10.0 7.4   13.9 10.9
+    //   experts x outputs, rows each, steps
+    //     8 x 4096, 1, 8 and 2, 16          9.3 10.2  17.2 17.4   11.4 10.7  19.6 17.9
+    //     16 x 1024, 2, 8 and 16            7.8  8.7  12.6 11.5    8.5  9.3  13.7 12.3
+    //     8 x 4096, 8 and 12, 8            12.0 13.0  16.8 12.9   14.2 13.4  15.8 13.7
+    //     64 x 1024, 8 and 12, 2            9.0 10.9  11.4 11.6   10.5 11.3  14.3 12.0
+    //     128 x 1024, 12 and 16, 2         16.8 16.6  19.7 17.8   21.3 17.3  26.4 18.6
+    //   the more workgroups, the more of them quantise the same rows: 2 rows each,
+    //     16 x 1024, 8 (8192 cells)         7.8  8.7               8.5  9.3
+    //     128 x 256, 8 (16384)             10.5 12.2              12.2 12.7
+    //     64 x 2816, 2 (22528)             16.4 18.2              21.1 18.3
+    //     128 x 1024, 4 (32768)            16.9 18.3              22.2 19.2
+    //     128 x 1024, 8 (65536)            28.0 27.0              32.9 27.5
+    //     64 x 2816, 8 (90112)             34.2 33.4              44.7 35.6
+    // Of 1250 such points the form taken is 0.4% slower than the better one on average,
+    // 23% at worst (128 x 256, 12 rows each of 4 steps, fp32: 13.7 and 11.1).
+    const bool fp32 = dtype == BCONV_F32;
+    const long long cells = (long long)a.experts * a.tiles * a.steps;  // 2 KiB of codes each
+    const bool apart = a.offsets ? a.steps > 9 || mean > 12 || mean * a.steps > 64 || cells > (fp32 ? 1 << 13 : 1 << 15)
+                                 : a.rows > 16 || a.steps > (fp32 ? 13 : 20) || a.rows * a.steps > (fp32 ? 96 : 160);
+    p.quantise = !given && (many || apart);
     auto take = [&](size_t n) {
         const size_t at = p.bytes;
         p.bytes += (n + 255) / 256 * 256;
@@ -811,7 +837,7 @@ bconv_status_t check_sizes(bconv_mx4_linear_t h, const bconv_mx4_rows_t *args)
 }
 
 // Workspace of a call: that of its slabs of rows.
-size_t workspace_of(bconv_mx4_linear_t h, const bconv::Mx4Args &a, bool given)
+size_t workspace_of(bconv_mx4_linear_t h, const bconv::Mx4Args &a, int dtype, bool given)
 {
     bconv::Mx4Args part = a;
     const int slab = a.offsets ? a.rows : bconv::slab_rows(a.steps);
@@ -820,7 +846,7 @@ size_t workspace_of(bconv_mx4_linear_t h, const bconv::Mx4Args &a, bool given)
         part.rows = rows;
         part.x_rows = a.offsets ? a.x_rows : rows;
         if (rows == 0) continue;
-        const size_t need = bconv::plan_mx4(part, given, h->cus).bytes;
+        const size_t need = bconv::plan_mx4(part, dtype, given, h->cus).bytes;
         bytes = need > bytes ? need : bytes;
     }
     return bytes;
@@ -911,7 +937,7 @@ bconv_status_t bconv_mx4_linear_workspace_size(bconv_mx4_linear_t h, const bconv
     const bconv_status_t st = check_sizes(h, args);
     if (st != BCONV_OK) return st;
     if (!bytes) return fail(BCONV_ERR_INVALID_ARGUMENT, "bytes is NULL");
-    *bytes = args->rows ? workspace_of(h, kernel_args(h, args), !args->x) : 0;
+    *bytes = args->rows ? workspace_of(h, kernel_args(h, args), args->dtype, !args->x) : 0;
     return BCONV_OK;
 }
 
@@ -938,7 +964,7 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
     if (((uintptr_t)args->offsets | (uintptr_t)args->order) % 4)
         return fail(BCONV_ERR_INVALID_ARGUMENT, "offsets/order not aligned to an element");
     bconv::Mx4Args a = kernel_args(h, args);
-    const size_t need = workspace_of(h, a, !args->x);
+    const size_t need = workspace_of(h, a, args->dtype, !args->x);
     if (need > 0 && (!workspace || workspace_bytes < need))
         return fail(BCONV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : (size_t)0);
     if (need > 0 && (uintptr_t)workspace % 16) return fail(BCONV_ERR_INVALID_ARGUMENT, "workspace must be 16-byte aligned");
@@ -970,7 +996,7 @@ bconv_status_t bconv_mx4_linear_forward(bconv_mx4_linear_t h, void *stream, cons
             a.xs = args->scales ? args->scales + first * h->steps * (bconv::kStep / 32) : nullptr;
             a.y = static_cast<char *>(args->y) + first * args->ldy * es;
         }
-        bconv::Mx4Plan p = bconv::plan_mx4(a, !args->x, h->cus);
+        bconv::Mx4Plan p = bconv::plan_mx4(a, args->dtype, !args->x, h->cus);
         p.q.sums = reinterpret_cast<float *>(ws + p.sums_offset);
         if (p.many && a.offsets) p.q.row_list = reinterpret_cast<const bconv::RowBlock *>(ws + p.list_offset);
         hipError_t e = hipSuccess;

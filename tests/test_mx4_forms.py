@@ -196,3 +196,47 @@ def test_order_is_checked(dev, counts):
                            ((offsets, order, position.cpu()), "on cuda:0, not on cpu|^position: .*device")):
             with pytest.raises(ValueError, match=match):
                 pca.ExpertOrder(*bad, 3)
+
+
+# Rows quantised in the products and in a launch before them, a few of each expert.
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("experts,each,k,n", [
+    (8, 12, 500, 300), (8, 13, 500, 300), (5, 8, 2048, 260), (5, 9, 2048, 260), (16, 3, 2304, 70), (16, 3, 2305, 70),
+    (6, 12, 1281, 1030), (128, 2, 1024, 256), (128, 2, 1030, 272), (64, 2, 2000, 1030), (3, 16, 257, 2100)])
+def test_few_rows_of_each_expert(dev, dtype, experts, each, k, n):
+    say("few rows each", dtype, experts, each, k, n)
+    rng = np.random.default_rng(experts * each + k)
+    layer, codes, scales, b = make_experts(rng, experts, k, n, True)
+    counts = rng.multinomial(experts * each, np.ones(experts) / experts)
+    flat = rng.permutation(np.repeat(np.arange(experts), counts))
+    choices = 2 if flat.size % 2 == 0 else 1
+    ids = flat.reshape(-1, choices)
+    offsets, order, _ = ref.expert_order(ids, experts)
+    o = pca.sort_by_expert(torch.from_numpy(ids).to(dev), experts)
+    x = random((ids.shape[0], k), dev, dtype, 7, 1)
+    y = layer.forward(x, o)
+    xs = host(x)[order // choices]
+    for e in range(experts):
+        part = slice(offsets[e], offsets[e + 1])
+        want, mass = ref.linear(xs[part], codes[e], scales[e], b[e])
+        assert (np.abs(host(y[part]) - want) <= ref.linear_bound(want, mass, k, dtype)).all(), e
+    assert torch.equal(layer.forward(pca.mx4_quantize(x), o, dtype=DT[dtype]), y)
+    assert torch.equal(layer.forward(o.gather(x), o, in_order=True), y)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,k,n", [
+    (1, 3328, 300), (1, 3329, 300), (1, 5120, 300), (1, 5121, 300), (12, 2048, 70), (13, 2048, 70), (8, 5120, 50), (8, 5121, 50),
+    (7, 3300, 8300), (16, 1500, 8300), (16, 2600, 8300), (2, 2048, 16411)])
+def test_few_rows_of_one_layer(dev, dtype, rows, k, n):
+    say("few rows", dtype, rows, k, n)
+    rng = np.random.default_rng(rows * 7 + k)
+    codes, scales = ref.random_weights(rng, n, k)
+    b = rng.normal(0, 1, n).astype(np.float32)
+    layer = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales, bias=b)
+    x = random((rows, k), dev, dtype, 8, 1)
+    want, mass = ref.linear(host(x), codes, scales, b)
+    bound = ref.linear_bound(want, mass, k, dtype)
+    assert (np.abs(host(layer.forward(x)) - want) <= bound).all()
+    # from quantised rows the inputs may be split between other numbers of waves
+    assert (np.abs(host(layer.forward(pca.mx4_quantize(x), dtype=DT[dtype])) - want) <= bound).all()
