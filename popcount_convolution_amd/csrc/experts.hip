@@ -327,7 +327,8 @@ template <int DT, bool MANY, bool AWAY> __global__ __launch_bounds__(kRowThreads
 
 // A workgroup a token: dy's row is read once for kTogether choices; or, with
 // few tokens, one for each choice (gridDim.y of them).  Bound by its bytes: 2049 tokens
-// with 6 rows of 5003 fp32 values, 533 MB, 117 to 134 us (4.0 to 4.6 TB/s).
+// with 6 rows of 5003 fp32 values, 533 MB, 118 us again and again (4.5 TB/s), 135
+// with the tokens' gradient between.
 template <int DT, bool AWAY> __global__ __launch_bounds__(kRowThreads) void expert_combine_backward_kernel(RowsArgs a)
 {
     constexpr int V = kPiece<DT>;
@@ -401,10 +402,12 @@ template <int DT, bool AWAY> static void launch_rows(RowsOp op, const RowsArgs &
 
 template <int DT> static hipError_t run_rows(RowsOp op, RowsArgs a, hipStream_t s)
 {
-    // 32772 rows of 4096 16-bit values gathered: 67 us, 52 past the caches; combined: 64, 50;
-    // gradients: 138, 130; of 12294 rows of 5003 fp32 values: 135, 115.
-    // Smaller results may still be there when they are read; gathered rows that end inside a line are
-    // better put together in the caches (5003 fp32 values: 65, 73).
+    // Through the caches and past them: 32772 rows of 4096 bf16 values gathered 67.5 us, 52.4; combined 64.4, 51.6;
+    // gradients 146, 140; 12294 rows of 5003 fp32 values combined 45.3, 44.7, gradients 134, 118; 16392 of 4096
+    // bf16 gradients 72, 53.  The next kernel pays part of it: with one that reads the result, gathered 156, 159,
+    // combined (and added to as many rows) 97, 103, gradients and the tokens' 213, 203; 190, 191; 101, 98.
+    // 8200 rows of 4096 (64 MiB): 15.1, 18.2; 15.2, 15.1; 29.3, 28.9, with the next 37, 41; 20.4, 20.5; 43, 46.
+    // Gathered rows that end inside a line are better put together in the caches (5003 fp32 values: 66, 73).
     const int es = DT == BCONV_F32 ? 4 : 2;
     const bool away = (long long)a.pairs * a.width * es > 1LL << 26 && (op != kGather || a.width * es % 128 == 0);
     // 64 tokens of 8 rows of 7168 bf16 values: gradients 15.2 us, 10.1 shared, combined 8.7, 7.6; 256 of 4096: 11.4, 13.7.

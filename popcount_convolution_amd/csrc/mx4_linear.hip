@@ -148,9 +148,10 @@ template <int DT> __device__ __forceinline__ XStep quantised_step(const typename
 // sums in LDS, in a fixed order.  The weights go from global memory to the matrix
 // cores without passing LDS, as in memory.
 //
-// Bound by the weights' bytes: 1 x 25088 -> 4096, 54.6 MB, 8.4 to 9.5 us (5.7 to 6.5 TB/s;
-// a large read reaches 5.8), after 2.8 us that quantise the row; 13 x 5000 -> 11003 fp32 6.0 to 7.3 us
-// after 3.6; 32 tokens' 4 of 64 experts of 2048 -> 2816, 170 MB, 26 us (6.5 TB/s, rows quantised here).
+// Bound by the weights' bytes: 1 x 25088 -> 4096, 54.6 MB, 9.4 to 9.5 us (5.7 to 5.8 TB/s;
+// a large read reaches 5.8), after 2.9 us that quantise the row; 13 x 5000 -> 11003 fp32, 30 MB, 6.2 to 7.2 us
+// (4.2 to 4.9 TB/s: a wave has one step's loads in flight) after 3.8; 32 tokens' 4 of 64 experts of 2048 -> 2816,
+// of which they choose 44, 135 MB, 20 to 22 us (6.1 to 6.8 TB/s, some of it in the memory-side cache) after 2.5 to 4.
 // 512 -> 512: 3.1 us, the launch and a chain of loads.
 template <int DT, bool QUANTISED, int RT, int CT, int WAVES>
 __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
@@ -254,14 +255,14 @@ __global__ __launch_bounds__(WAVES * 64) void mx4_few_kernel(Mx4Args a)
 // the clock falls with the bits that toggle).
 //
 // Bound by power for large products: 8192 x 8192 -> 8192 bf16, 231 to 280 us (3.9 to
-// 4.8 PFLOP/s, 3.3 to 4 times a large bf16 library product), matrix cores busy 74%
+// 4.8 PFLOP/s, 3.3 to 4 times a large bf16 library product), matrix cores busy 71 to 74%
 // of the cycles at 1.3 to 1.5 GHz (an earlier form took as many cycles on zeros, at
 // 2.3 GHz instead of 1.7).  On the way there: both operands in LDS with 16x16x128
 // instructions 435 to 460 us, with 32x32x64 330 to 370, weights in registers 320,
 // results as whole lines 285, a ring of register sets and exact waits 250.
 // For experts by the weights' and results' bytes: 16396 rows of 64 experts, 2048 ->
-// 2816, 300 MB, 66 to 81 us (3.7 to 4.5 TB/s).  256 x 25088 -> 4096, 14 to 22 us, by the
-// latency of the weights, three steps ahead in 256 workgroups.
+// 2816, 327 MB moved, 67 to 77 us (4.2 to 4.9 TB/s, a copy's rate).  256 x 25088 -> 4096, 19 to 21 us, by the
+// latency of the weights, three steps ahead in 256 workgroups of one wave a SIMD.
 
 // What the many-row kernel takes besides Mx4Args.
 struct Mx4Many {
@@ -528,8 +529,10 @@ __device__ __forceinline__ void many_rows(const Mx4Args &a, const Mx4Many &q, Ma
         auto biased = [&](int m, int t, int v) {
             return f32x4{acc[m][t][4 * v], acc[m][t][4 * v + 1], acc[m][t][4 * v + 2], acc[m][t][4 * v + 3]} + bias[t][v];
         };
-        // past the caches, whose room the weights and x of other workgroups need (the prompt of 16396 rows, 64 experts of
-        // 2048 -> 2816: 81 us, 66 so; 16384 rows of one such layer: 58, 51)
+        // past the caches, whose room the weights and x of other workgroups need (quantise and product of 16396 rows, 64
+        // experts of 2048 -> 2816: 86 us, 73 so; 4096 rows, 16 of 1024 -> 1408: 16.7, 15.6), at any size: with a kernel
+        // that reads the results next, 128 and 131; 28.1 and 24.3; 1024 rows, 8 of 2048 -> 2816 19.2 and 18.9; one layer, 512 x
+        // 1024 -> 4096 14.4 and 14.7, 2048 x 4096 -> 4096 38.2 and 37.7, 8192 x 8192 -> 8192 350 and 328
         emit(T(), std::true_type(), biased, reinterpret_cast<char *>(static_cast<T *>(a.y) + (long long)span.begin * a.ldy), a.ldy, a.n);
     }
 }
@@ -585,7 +588,7 @@ __global__ __launch_bounds__(256, 2) void mx4_many_kernel(Mx4Args a, Mx4Many q)
     else many_rows<DT, 1, NT, WD>(a, q, lds, f, span, tile0, split);
 }
 
-// Adds the splits' sums in order.  Bound by its bytes: 4 sums of 256 x 4096, 19 MB, 4.0 to 5.0 us.
+// Adds the splits' sums in order.  Bound by its bytes: 4 sums of 256 x 4096, 19 MB, 4.0 to 4.2 us.
 template <int DT> __global__ __launch_bounds__(256) void mx4_join_kernel(Mx4Args a, Mx4Many q)
 {
     const int per = (a.n + 3) / 4;
