@@ -151,3 +151,124 @@ def test_workspace_of_the_size_that_is_asked_for(dev, dtype, tokens, choices, k,
             with pytest.raises(ValueError, match=f"{need - 1} bytes given, {need} needed"):
                 forward(workspace=ws[:need - 1])
     assert (sizes == {0}) == (tokens == 1)
+
+
+# ---------------------------------------------------------- the largest sizes
+
+def check_some(y, x, codes, scales, bias, dtype, rows, outs):
+    """The results of some rows and outputs."""
+    got = y[rows][:, outs].to(torch.float64).cpu().numpy()
+    want, mass = ref.linear(x[rows].to(torch.float64).cpu().numpy(), codes[outs], scales[outs], None if bias is None else bias[outs])
+    assert (np.abs(got - want) <= ref.linear_bound(want, mass, x.shape[1], dtype)).all()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows,k,n", [(1, 1 << 20, 16), (5, (1 << 20) - 1, 40), (20, 1 << 20, 33), (150, 1 << 20, 20), (1, 32, 1 << 20),
+                                      (3, 300, (1 << 20) - 5), (40, 33, 1 << 20), (200, 257, 1 << 20)])
+def test_widest_layers(dev, dtype, rows, k, n):
+    rng = np.random.default_rng(rows)
+    codes, scales = ref.random_weights(rng, n, k)
+    bias = rng.normal(0, 1, n).astype(np.float32)
+    layer = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales, bias=bias)
+    x = torch.randn((rows, k), device=dev).to(DT[dtype])
+    y = layer.forward(x)
+    some = np.unique(np.concatenate([[0, n - 1, n // 2], rng.integers(0, n, 50)]))
+    check_some(y, x, codes, scales, bias, dtype, np.unique([0, rows // 2, rows - 1]), some)
+    q = layer.forward(pca.mx4_quantize(x), dtype=DT[dtype])
+    check_some(q, x, codes, scales, bias, dtype, np.unique([0, rows // 2, rows - 1]), some)
+
+
+@pytest.mark.parametrize("tokens,choices,k,n", [(1, 1, 40, 33), (700, 3, 40, 33), (3000, 8, 70, 300)])
+def test_most_experts(dev, tokens, choices, k, n):
+    layer, codes, scales = make_experts(1024, k, n, 3)
+    rng = np.random.default_rng(tokens)
+    ids = np.where(rng.random((tokens, choices)) < 0.3, 1023, rng.integers(-1, 1025, (tokens, choices)))
+    ids[0, 0] = 1023
+    offsets, order, _ = ref.expert_order(ids, 1024)
+    o = pca.sort_by_expert(torch.from_numpy(ids).to(dev), 1024)
+    assert np.array_equal(o.offsets.cpu().numpy(), offsets)
+    x = torch.randn((tokens, k), device=dev)
+    y, xs = layer.forward(x, o).to(torch.float64).cpu().numpy(), x.to(torch.float64).cpu().numpy()[np.maximum(order, 0) // choices]
+    for e in range(1024):
+        part = slice(offsets[e], offsets[e + 1])
+        want, mass = ref.linear(xs[part], codes[e], scales[e], None)
+        assert (np.abs(y[part] - want) <= ref.linear_bound(want, mass, k, "f32")).all(), e
+    assert not y[offsets[-1]:].any()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+def test_quantise_in_slices(dev, dtype):
+    """More rows than one launch quantises."""
+    rows, cols = (1 << 25) + 3, 3
+    x = torch.randn((rows, cols), device=dev).to(DT[dtype])
+    q, values = pca.mx4_quantize(x, values=True)
+    for part in (slice(0, 40), slice((1 << 25) - 40, rows), slice(12345678, 12345700)):
+        codes, scales, want = ref.quantise(x[part].to(torch.float64).cpu().numpy())
+        assert np.array_equal(q.codes[part].cpu().numpy(), codes) and np.array_equal(q.scales[part].cpu().numpy(), scales)
+        assert np.array_equal(values[part].to(torch.float64).cpu().numpy(), want)
+    # a value of fewer bits than it was made of stays what it is when it is quantised again
+    assert torch.equal(pca.mx4_quantize(values, values=True)[1], values)
+
+
+@pytest.mark.parametrize("choices", [1, 8])
+def test_most_pairs(dev, choices):
+    """2^27 pairs sorted, and rows of one value moved there and back."""
+    tokens, experts = (1 << 27) // choices, 7
+    ids = torch.randint(-1, experts, (tokens, choices), dtype=torch.int32, device=dev)
+    o = pca.sort_by_expert(ids, experts)
+    flat = ids.view(-1)
+    key = torch.where(flat < 0, experts, flat)
+    want = torch.sort(key.to(torch.int16), stable=True)[1].to(torch.int32)
+    counts = torch.bincount(key, minlength=experts + 1)
+    offsets = torch.cumsum(counts, 0) - counts
+    assert torch.equal(o.offsets.long(), offsets)
+    kept = int(offsets[-1])
+    assert torch.equal(o.order[:kept], want[:kept]) and bool((o.order[kept:] == -1).all())
+    del key, counts
+    position = o.position.view(-1)
+    assert bool((position[flat < 0] == -1).all())
+    assert torch.equal(position[want[:kept].long()], torch.arange(kept, dtype=torch.int32, device=dev))
+    x = torch.randint(-8, 9, (tokens, 1), device=dev).to(torch.bfloat16)
+    rows = o.gather(x)
+    assert torch.equal(rows[:kept, 0], x[want[:kept].long() // choices, 0]) and not bool(rows[kept:].any())
+    times = (ids >= 0).sum(1, keepdim=True)
+    assert torch.equal(o.combine(rows), (x.float() * times).to(torch.bfloat16))  # whole numbers up to 64
+    d_rows, d_weights = o.combine_backward(x, rows, (ids >= 0).to(torch.bfloat16))
+    assert torch.equal(d_rows, rows)
+    assert torch.equal(d_weights, torch.where(ids >= 0, x.float() ** 2, 0).to(torch.bfloat16))
+
+
+@pytest.mark.parametrize("tokens,choices", [(1, 3), (130, 2), (3, 1)])
+def test_widest_rows(dev, tokens, choices):
+    width = 1 << 20
+    ids = torch.randint(0, 3, (tokens, choices), device=dev)
+    ids[-1, 0] = 5
+    o = pca.sort_by_expert(ids, 3)
+    x = torch.randint(-4, 5, (tokens, width), device=dev).to(torch.float16)
+    rows = o.gather(x)
+    order = o.order.long()
+    assert torch.equal(rows, torch.where((order >= 0)[:, None], x[order.clamp(min=0) // choices], 0))
+    times = (ids < 3).sum(1, keepdim=True)
+    assert torch.equal(o.combine(rows), x * times)
+    weights = torch.randint(-2, 3, (tokens, choices), device=dev).float()
+    d_rows, d_weights = o.combine_backward(x, rows, weights)
+    assert torch.equal(d_rows, torch.where((order >= 0)[:, None], x[order.clamp(min=0) // choices] * weights.view(-1)[order.clamp(min=0), None].half(), 0))
+    # whole numbers up to 2^24: exact in fp32 in any order
+    assert torch.equal(d_weights.double(), torch.where(ids < 3, (x.double() ** 2).sum(1, keepdim=True), 0.0))
+
+
+# ----------------------------------------------------- powers of two at the ends
+
+@pytest.mark.parametrize("rows", [1, 5, 40, 300])
+@pytest.mark.parametrize("low,x_exponent", [(0, 110), (3, 118), (250, -149), (247, -120), (251, -127)])
+def test_range_of_the_powers(dev, rows, low, x_exponent):
+    """Weights' powers of 2^-127 up, times the largest x, and of 2^124 down, times
+    subnormal ones: their products are ordinary numbers."""
+    rng = np.random.default_rng(rows + low)
+    k, n = 640, 70
+    codes, scales = ref.random_weights(rng, n, k, low, low + 3)
+    layer = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales)
+    x = torch.from_numpy(np.ldexp(rng.integers(-15, 16, (rows, k)).astype(np.float64), x_exponent).astype(np.float32)).to(dev)
+    assert bool(x.isfinite().all())
+    for y in (layer.forward(x), layer.forward(pca.mx4_quantize(x), dtype=torch.float32)):
+        check_some(y, x, codes, scales, None, "f32", np.arange(rows), np.arange(n))
