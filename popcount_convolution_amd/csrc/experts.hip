@@ -407,6 +407,8 @@ template <int DT> static hipError_t run_rows(RowsOp op, RowsArgs a, hipStream_t 
     // bf16 gradients 72, 53.  The next kernel pays part of it: with one that reads the result, gathered 156, 159,
     // combined (and added to as many rows) 97, 103, gradients and the tokens' 213, 203; 190, 191; 101, 98.
     // 8200 rows of 4096 (64 MiB): 15.1, 18.2; 15.2, 15.1; 29.3, 28.9, with the next 37, 41; 20.4, 20.5; 43, 46.
+    // A combination goes by the rows that it reads, not the fewer that it stores: 41 MB of 246 between gradients, the pass of
+    // both 193, 191; 16 MB of 134 alone 28.1, 28.3, with a kernel that reads them 36.7, 37.7.
     // Gathered rows that end inside a line are better put together in the caches (5003 fp32 values: 66, 73).
     const int es = DT == BCONV_F32 ? 4 : 2;
     const bool away = (long long)a.pairs * a.width * es > 1LL << 26 && (op != kGather || a.width * es % 128 == 0);
