@@ -243,7 +243,7 @@ class MX4Linear(_MX4Layer):
 
 
 class ExpertOrder:
-    """(token, choice) pairs in the order of their experts, from
+    """(token, choice) pairs in the order of their experts (2^27 at most), from
     ``sort_by_expert``, and what takes rows there and back.
 
     ``offsets``: int32 ``[experts + 1]``, where each expert's pairs start (the last:
