@@ -646,6 +646,10 @@ Mx4Plan plan_mx4(const Mx4Args &a, int dtype, bool given, int cus)
     //     8 rows, 13                        5.6  6.6   9.6  9.9    7.9 7.0   11.1 10.3
     //     12 rows, 13                       6.7  6.8  10.6 10.2    9.0 7.1   12.6 10.6
     //     12 rows, 16                       6.8  7.0  11.5 10.5   10.0 7.4   13.9 10.9
+    //   of more outputs than the card takes four tiles a compute unit at once
+    //     16384: 1 row, 4 and 16 steps      5.0  6.4  10.5 10.8    5.3 6.4   11.7 10.6
+    //     17408                             7.3  7.0  15.4 12.8    7.8 7.1   18.4 12.6
+    //     65536: 1 row, 1 and 8 steps       9.6  7.3  20.8 16.8   10.1 7.3   23.3 16.8
     //   experts x outputs, rows each, steps
     //     8 x 4096, 1, 8 and 2, 16          9.3 10.2  17.2 17.4   11.4 10.7  19.6 17.9
     //     16 x 1024, 2, 8 and 16            7.8  8.7  12.6 11.5    8.5  9.3  13.7 12.3
@@ -659,12 +663,13 @@ Mx4Plan plan_mx4(const Mx4Args &a, int dtype, bool given, int cus)
     //     128 x 1024, 4 (32768)            16.9 18.3              22.2 19.2
     //     128 x 1024, 8 (65536)            28.0 27.0              32.9 27.5
     //     64 x 2816, 8 (90112)             34.2 33.4              44.7 35.6
-    // Of 1250 such points the form taken is 0.4% slower than the better one on average,
+    // Of 1814 such points the form taken is 0.3% slower than the better one on average,
     // 23% at worst (128 x 256, 12 rows each of 4 steps, fp32: 13.7 and 11.1).
     const bool fp32 = dtype == BCONV_F32;
     const long long cells = (long long)a.experts * a.tiles * a.steps;  // 2 KiB of codes each
     const bool apart = a.offsets ? a.steps > 9 || mean > 12 || mean * a.steps > 64 || cells > (fp32 ? 1 << 13 : 1 << 15)
-                                 : a.rows > 16 || a.steps > (fp32 ? 13 : 20) || a.rows * a.steps > (fp32 ? 96 : 160);
+                                 : a.rows > 16 || a.tiles > 4 * cus || a.steps > (fp32 ? 13 : 20) ||
+                                       a.rows * a.steps > (fp32 ? 96 : 160);
     p.quantise = !given && (many || apart);
     auto take = [&](size_t n) {
         const size_t at = p.bytes;

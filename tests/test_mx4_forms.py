@@ -240,3 +240,10 @@ def test_few_rows_of_one_layer(dev, dtype, rows, k, n):
     assert (np.abs(host(layer.forward(x)) - want) <= bound).all()
     # from quantised rows the inputs may be split between other numbers of waves
     assert (np.abs(host(layer.forward(pca.mx4_quantize(x), dtype=DT[dtype])) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,k,n", [(1, 300, 16384), (3, 300, 16385), (16, 40, 16400), (9, 2049, 16400)])
+def test_few_rows_of_many_outputs(dev, dtype, rows, k, n):
+    """Around as many outputs as compute units take at once, from where on rows are quantised in a launch."""
+    test_few_rows_of_one_layer(dev, dtype, rows, k, n)
