@@ -627,11 +627,15 @@ Mx4Plan plan_mx4(const Mx4Args &a, int dtype, bool given, int cus)
     // 25088 -> 4096, 32 rows 16.6 us and 19.4, 64 rows 22.2 and 20.5; 12000 -> 6000,
     // 40 rows 25.9 and 16.6; 8192 -> 11008, 32 rows 13.7 and 17.3, 48 rows 19.6 and 18.0;
     // 4096 -> 1024, 512 rows 11.0 and 16.0; 512 -> 512, 8192 rows 15.2 and 10.5; 1024 ->
-    // 4096, 512 rows 11.2 and 9.5.  64 experts of 2048 -> 2816, 16 rows each 34.5 and
+    // 4096, 512 rows 11.2 and 9.5.  Up to 16 rows the codes are read once by either: 16384 ->
+    // 16384, 1 row 28.3 and 33.1, 16 rows 29.0 and 33.8; 25088 -> 11008, 1 row 30.6 and 33.4, 16 rows
+    // 35.9 and 34.4; 12288 -> 49152, 1 row 56.3 and 60.9, 16 rows 59.5 and 63.6; 32768 -> 32768 within 1%; 17
+    // to 32 rows there 31.0 to 31.7 and 33.9 to 35.0; 34.9 to 38.9 and 34.6 to 36.2; 60.1 to 62.4 and 63.8 to 64.7; 16384 ->
+    // 8192 25.0 to 25.9 and 22.5 to 23.0.  64 experts of 2048 -> 2816, 16 rows each 34.5 and
     // 39.0, 32 rows each 50.2 and 40.0.
     const long long blocks = (a.rows + 127LL) / 128 * ((a.tiles + 7) / 8);
     const bool many = a.offsets ? mean > 20
-                                : (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << (a.rows > 32 ? 26 : 27) ||
+                                : (a.rows > 16 && (a.rows + 15LL) / 16 * a.tiles * a.steps * 2048 > 1LL << (a.rows > 32 ? 26 : 27)) ||
                                       (a.rows > 128 && blocks * 2 >= cus);
     p.many = many ? kManyRows : 0;
     // Quantising in the few-row kernel costs every workgroup a little for each step, more

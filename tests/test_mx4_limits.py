@@ -272,3 +272,17 @@ def test_range_of_the_powers(dev, rows, low, x_exponent):
     assert bool(x.isfinite().all())
     for y in (layer.forward(x), layer.forward(pca.mx4_quantize(x), dtype=torch.float32)):
         check_some(y, x, codes, scales, None, "f32", np.arange(rows), np.arange(n))
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("rows", [1, 16, 17])
+def test_few_rows_of_a_large_layer(dev, dtype, rows):
+    """More than 128 MiB of codes: read once for up to 16 rows, from 17 on by the kernel of many rows."""
+    k, n = 16640, 16400
+    rng = np.random.default_rng(rows)
+    codes, scales = ref.random_weights(rng, n, k)
+    layer = pca.MX4Linear(in_features=k, out_features=n, codes=codes, scales=scales)
+    x = torch.randn((rows, k), device=dev).to(DT[dtype])
+    some = np.unique(np.concatenate([[0, n - 1], rng.integers(0, n, 50)]))
+    for y in (layer.forward(x), layer.forward(pca.mx4_quantize(x), dtype=DT[dtype])):
+        check_some(y, x, codes, scales, None, dtype, np.arange(rows), some)
